@@ -88,6 +88,28 @@ class GroupInfo(ctypes.Structure):
                 ("split_b", ctypes.c_int32), ("lane", ctypes.c_int32)]
 
 
+class RmsNorm(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("h", ctypes.c_void_p), ("y", ctypes.c_void_p), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("rstd", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("ld_x", ctypes.c_int64), ("ld_residual", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("pad_", ctypes.c_int32)]
+
+
+class RmsNormGrad(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("h", ctypes.c_void_p), ("dh", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("rstd", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+                ("dweight", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("first", ctypes.c_int32),
+                ("pad_", ctypes.c_int32)]
+
+
+class MxMatrix(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("layout", ctypes.c_int32), ("pad_", ctypes.c_int32)]
+
+
 # every symbol include/sshdp.h declares, with its argument and return types
 _P = ctypes.c_void_p
 SIGNATURES = {
@@ -117,6 +139,21 @@ SIGNATURES = {
                                    ctypes.c_int64, _P], ctypes.c_int),
     "sshdp_gemm_bf16_nt": ([_P, _P, _P, _P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                             ctypes.c_float, ctypes.c_float, ctypes.c_int32, _P], ctypes.c_int),
+    "sshdp_grad_workspace": ([_P, ctypes.POINTER(ctypes.c_int64)], ctypes.c_int),
+    "sshdp_grad_sumsq": ([_P, _P, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "sshdp_grad_clip": ([_P, _P, _P, _P, ctypes.c_float, _P, _P], ctypes.c_int),
+    "sshdp_grad_clip_norm": ([_P, _P, _P, ctypes.c_float, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "sshdp_quant_mxfp8": ([_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P, _P, _P, _P, _P],
+                          ctypes.c_int),
+    "sshdp_rmsnorm_mxfp8": ([ctypes.POINTER(RmsNorm), _P], ctypes.c_int),
+    "sshdp_rmsnorm_backward_workspace": ([ctypes.c_int64, ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)],
+                                         ctypes.c_int),
+    "sshdp_rmsnorm_backward": ([ctypes.POINTER(RmsNormGrad), _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "sshdp_plan_mx_matrix": ([_P, ctypes.c_int32, _P, _P, ctypes.POINTER(MxMatrix)], ctypes.c_int),
+    "sshdp_gemm_mxfp8_workspace": ([ctypes.POINTER(MxMatrix), ctypes.POINTER(MxMatrix), ctypes.c_int32,
+                                    ctypes.POINTER(ctypes.c_int64)], ctypes.c_int),
+    "sshdp_gemm_mxfp8": ([ctypes.POINTER(MxMatrix), ctypes.POINTER(MxMatrix), ctypes.c_int32, _P, _P, ctypes.c_int32,
+                          ctypes.c_int64, _P, ctypes.c_size_t, _P], ctypes.c_int),
     "sshdp_ns_executed": ([_P, _P, ctypes.c_size_t, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_double),
                            _P], ctypes.c_int),
     "sshdp_profile_enable": ([_P, ctypes.c_int32], ctypes.c_int),
@@ -239,6 +276,14 @@ class Plan:
         _check(lib().sshdp_plan_node(self.handle, i, ctypes.byref(a), ctypes.byref(g)), "sshdp_plan_node")
         return a.value, g.value
 
+    def mx_matrix(self, i, codes, scales):
+        """Node i's MXFP8 region inside the codes and scales roots, as an operand of gemm_mxfp8."""
+        m = MxMatrix()
+        _check(lib().sshdp_plan_mx_matrix(self.handle, i, _ptr(codes), _ptr(scales), ctypes.byref(m)),
+               "sshdp_plan_mx_matrix")
+        m._keep = (codes, scales)
+        return m
+
     def ns_executed(self, workspace, workspace_bytes, stream=None):
         """(units per group, MFMA flops) the Newton-Schulz tiles executed in the
         last Muon call that used this workspace (units with all-zero momentum
@@ -321,6 +366,86 @@ def rs_reduce(inputs, in_dtype, out, out_mode, n, seed=0, ctr=0, g0=0, stream=No
 def rs_accumulate(inputs, in_dtype, g, n, first, stream=None):
     _check(lib().sshdp_rs_accumulate(_ptr_array(inputs), len(inputs), RS_DTYPE[in_dtype], _ptr(g), int(n),
                                      int(bool(first)), _stream(stream)), "sshdp_rs_accumulate")
+
+
+DTYPE = {"fp32": 0, "bf16": 1}      # SSHDP_DTYPE_*
+GEMM_OP = {"nt": 0, "nn": 1}
+# an unknown name becomes a value the library rejects (ARG)
+
+
+def grad_workspace(plan):
+    n = ctypes.c_int64()
+    _check(lib().sshdp_grad_workspace(plan.handle, ctypes.byref(n)), "sshdp_grad_workspace")
+    return n.value
+
+
+def grad_sumsq(plan, grad, sumsq, workspace, workspace_bytes, stream=None):
+    _check(lib().sshdp_grad_sumsq(plan.handle, _ptr(grad), _ptr(sumsq), _ptr(workspace), int(workspace_bytes),
+                                  _stream(stream)), "sshdp_grad_sumsq")
+
+
+def grad_clip(plan, grad, out, sumsq, max_norm, stats, stream=None):
+    _check(lib().sshdp_grad_clip(plan.handle, _ptr(grad), _ptr(out), _ptr(sumsq), max_norm, _ptr(stats),
+                                 _stream(stream)), "sshdp_grad_clip")
+
+
+def grad_clip_norm(plan, grad, out, max_norm, stats, workspace, workspace_bytes, stream=None):
+    """out = grad * min(1, max_norm / norm) over the plan's units; stats[0:2] = norm, factor."""
+    _check(lib().sshdp_grad_clip_norm(plan.handle, _ptr(grad), _ptr(out), max_norm, _ptr(stats), _ptr(workspace),
+                                      int(workspace_bytes), _stream(stream)), "sshdp_grad_clip_norm")
+
+
+def quant_mxfp8(src, dtype, rows, cols, codes=None, scales=None, codes_t=None, scales_t=None, ld=None, stream=None):
+    """MXFP8 of src along its rows (codes, scales) and/or its columns (codes_t, scales_t: the transpose)."""
+    _check(lib().sshdp_quant_mxfp8(_ptr(src), DTYPE.get(dtype, -1), rows, cols, cols if ld is None else ld,
+                                   _ptr(codes), _ptr(scales), _ptr(codes_t), _ptr(scales_t), _stream(stream)),
+           "sshdp_quant_mxfp8")
+
+
+def rmsnorm_mxfp8(x, weight, rows, cols, dtype="bf16", weight_dtype="fp32", residual=None, h=None, y=None, codes=None,
+                  scales=None, rstd=None, eps=1e-6, ld_x=None, ld_residual=None, stream=None):
+    a = RmsNorm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(h), _ptr(y), _ptr(codes), _ptr(scales), _ptr(rstd), rows,
+                cols, cols if ld_x is None else ld_x, cols if ld_residual is None else ld_residual,
+                DTYPE.get(dtype, -1), DTYPE.get(weight_dtype, -1), eps, 0)
+    _check(lib().sshdp_rmsnorm_mxfp8(ctypes.byref(a), _stream(stream)), "sshdp_rmsnorm_mxfp8")
+
+
+def rmsnorm_backward_workspace(rows, cols):
+    n = ctypes.c_int64()
+    _check(lib().sshdp_rmsnorm_backward_workspace(rows, cols, ctypes.byref(n)), "sshdp_rmsnorm_backward_workspace")
+    return n.value
+
+
+def rmsnorm_backward(dy, h, weight, rstd, dx, dweight, rows, cols, dtype="bf16", weight_dtype="fp32", dh=None,
+                     first=True, workspace=None, workspace_bytes=0, stream=None):
+    a = RmsNormGrad(_ptr(dy), _ptr(h), _ptr(dh), _ptr(weight), _ptr(rstd), _ptr(dx), _ptr(dweight), rows, cols,
+                    DTYPE.get(dtype, -1), DTYPE.get(weight_dtype, -1), int(bool(first)), 0)
+    _check(lib().sshdp_rmsnorm_backward(ctypes.byref(a), _ptr(workspace), int(workspace_bytes), _stream(stream)),
+           "sshdp_rmsnorm_backward")
+
+
+def mx_matrix(codes, scales, rows, cols, layout="rowmajor"):
+    """A dense rows x cols MXFP8 matrix and its scales, an operand of gemm_mxfp8."""
+    m = MxMatrix(_ptr(codes), _ptr(scales), rows, cols, LAYOUT.get(layout, -1), 0)
+    m._keep = (codes, scales)
+    return m
+
+
+def gemm_mxfp8_workspace(a, b, op="nt"):
+    n = ctypes.c_int64()
+    _check(lib().sshdp_gemm_mxfp8_workspace(ctypes.byref(a), ctypes.byref(b), GEMM_OP.get(op, -1), ctypes.byref(n)),
+           "sshdp_gemm_mxfp8_workspace")
+    return n.value
+
+
+def gemm_mxfp8(a, b, out, out_dtype="bf16", op="nt", addend=None, ld_out=None, workspace=None, workspace_bytes=0,
+               stream=None):
+    """out = A B^T (op "nt") or A B (op "nn", B in 32 x 32 blocks), plus addend (float32 output)."""
+    if ld_out is None:
+        ld_out = b.cols if op == "nn" else b.rows
+    _check(lib().sshdp_gemm_mxfp8(ctypes.byref(a), ctypes.byref(b), GEMM_OP.get(op, -1), _ptr(addend), _ptr(out),
+                                  DTYPE.get(out_dtype, -1), ld_out, _ptr(workspace), int(workspace_bytes),
+                                  _stream(stream)), "sshdp_gemm_mxfp8")
 
 
 def _ref(x):

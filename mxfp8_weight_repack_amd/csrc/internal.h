@@ -114,6 +114,14 @@ struct CChunk {
   int32_t pad_;
 };
 
+// Gradient-norm work item: a contiguous run of unit elements (<= kChunk) after
+// merging units that touch (head views that tile their matrix become one run).
+struct GChunk {
+  int64_t base;
+  int32_t n;
+  int32_t pad_;
+};
+
 struct DeviceTables {
   MuonUnit *munits = nullptr;
   F0Tile *f0tiles = nullptr;
@@ -123,6 +131,7 @@ struct DeviceTables {
   QChunk *qchunks = nullptr;
   Q32Tile *q32tiles = nullptr;
   CChunk *cchunks = nullptr;
+  GChunk *gchunks = nullptr;
   NsGroupDev *ns_groups = nullptr;
   NsTile *ns_tiles[kMaxLanes][3][2] = {};   // [lane][stage: Gram, poly, update][tile: 128, 256]
   int32_t *norm_units = nullptr;
@@ -134,6 +143,7 @@ struct sshdp_plan {
   int64_t root_numel = 0;
   sshdp_plan_opts opts{};
   std::vector<int64_t> node_abs;
+  std::vector<sshdp_node> nodes;        // the caller's data tree (shapes of the MXFP8 regions)
   std::vector<int32_t> node_group;
   std::vector<sshdp::MuonUnit> munits;
   std::vector<sshdp::F0Tile> f0tiles;
@@ -159,6 +169,7 @@ struct sshdp_plan {
   int64_t n_qchunks_fused = 0;
   std::vector<sshdp::Q32Tile> q32tiles; // BLOCK32X32 layout: all requant work
   std::vector<sshdp::CChunk> cchunks;   // BF16 regions
+  std::vector<sshdp::GChunk> gchunks;   // every unit element exactly once (gradient norm and clip)
   size_t ws_uscale = 0, ws_partials = 0, ws_bytes = 0;
   sshdp_plan_stats stats{};
   bool host_only = true;
@@ -194,4 +205,31 @@ hipError_t launch_rs_reduce(const void *const *inputs, int n_in, int in_bf16, vo
                             uint64_t seed, uint64_t ctr, int64_t g0, hipStream_t s);
 hipError_t launch_rs_accumulate(const void *const *inputs, int n_in, int in_bf16, float *g, int64_t n, int first,
                                 hipStream_t s);
+
+// Operators around the update (k_grad.hip, k_rows.hip, k_gemm_mx.hip).
+int64_t grad_partials(int64_t chunks);               // doubles of partial sums one norm writes
+hipError_t launch_grad_partials(const sshdp_plan &p, const float *g, double *partials, hipStream_t s);
+hipError_t launch_grad_total(const sshdp_plan &p, const double *partials, double *sumsq, hipStream_t s);
+// parts: n_parts partial sums of squares (one: an already joined sum)
+hipError_t launch_grad_scale(const sshdp_plan &p, const float *g, float *out, const double *parts, int64_t n_parts,
+                             float max_norm, float *stats, hipStream_t s);
+hipError_t launch_quant_rows(const void *src, bool bf16, int64_t rows, int64_t cols, int64_t ld, uint8_t *codes,
+                             uint8_t *scales, hipStream_t s);
+hipError_t launch_quant_tiles(const void *src, bool bf16, int64_t rows, int64_t cols, int64_t ld, uint8_t *codes,
+                              uint8_t *scales, uint8_t *codes_t, uint8_t *scales_t, hipStream_t s);
+hipError_t launch_rmsnorm(const sshdp_rmsnorm &a, hipStream_t s);
+int64_t rmsnorm_partials(int64_t rows, int64_t cols);   // partial rows of the weight gradient
+hipError_t launch_rmsnorm_backward(const sshdp_rmsnorm_grad &a, float *partials, hipStream_t s);
+// One product: out[m][n] = sum_k A[m][k] B[n][k] (nn: B[k][n]) (+ addend[m][n])
+struct GemmMx {
+  const uint8_t *a, *as, *b, *bs;
+  int32_t la, lb;                     // scale layouts
+  int64_t m, n, k;
+  const float *addend;
+  void *out;
+  int64_t ld;
+  bool nn, bf16;
+};
+int64_t gemm_mx_workspace(int64_t m, int64_t n, int64_t k, bool nn);
+hipError_t launch_gemm_mx(const GemmMx &g, void *ws, hipStream_t s);
 }  // namespace sshdp

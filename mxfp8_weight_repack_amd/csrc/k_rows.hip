@@ -1,0 +1,408 @@
+// k_rows.hip -- MXFP8 quantisation of any matrix (along rows, along columns, or
+// both), and the residual RMS norm with MXFP8 output and its gradient.
+//
+// All of them are bound by HBM: each element is read once and each result
+// written once, in 16-byte loads and 8- or 16-byte stores.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "mx_rows.h"
+
+namespace sshdp {
+namespace {
+
+// ------------------------------------------------------------------ along rows
+
+// One 8-element run per lane; a row is cols / 8 runs and 4 of them one block, so
+// runs of all rows are numbered through and blocks never leave their 4 lanes.
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_quant_rows(const void *src, int64_t runs, int runs_per_row, int64_t ld,
+                                                    uint8_t *codes, uint8_t *scales) {
+  // `runs` is a multiple of 4, so a block's lanes leave the loop together and the
+  // shuffles of the others never need them
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < runs; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / runs_per_row;
+    const int64_t at = row * ld + (i - row * runs_per_row) * 8;
+    float v[8];
+    unpack8<BF16>(load8<BF16>(src, at), v);
+    const uint32_t sb = mx_scale_byte(mx_amax4(v));
+    *reinterpret_cast<u32x2_t *>(codes + i * 8) = mx_encode8(v, sb);
+    if ((i & 3) == 0) scales[i >> 2] = (uint8_t)sb;
+  }
+}
+
+// --------------------------------------------------- along columns, or both ways
+
+constexpr int kQtRows = 128, kQtCols = 128;          // tile of one workgroup
+
+// A 128 x 128 tile goes through LDS as float32.  Reading it: a row's 128 elements
+// are 16 lanes' 8 each (full 256- or 512-byte lines).  Along columns a lane then
+// takes one column's 32 rows, so a block is one lane's and needs no exchange; 4
+// consecutive lanes take the 4 row groups of a column, i.e. 128 consecutive bytes
+// of codes_t.  LDS columns are rotated by the row group (element (r, c) sits at
+// column c ^ 16 * (r / 32)), so the 4 groups x 16 columns a wave reads at one step
+// fall on all 64 banks.  Rows past the end count as zeros.
+template <bool BF16, bool ROWS>
+__global__ __launch_bounds__(256) void k_quant_tiles(const void *src, int64_t rows, int64_t cols, int64_t ld,
+                                                     uint8_t *codes, uint8_t *scales, uint8_t *codes_t,
+                                                     uint8_t *scales_t, int64_t tiles_c) {
+  __shared__ float sm[kQtRows * kQtCols];
+  const int t = threadIdx.x;
+  const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
+  const int64_t r0 = tr * kQtRows, c0 = tc * kQtCols;
+  const int lc = (t & 15) * 8, lr = t >> 4;
+  const bool in_c = c0 + lc < cols;                   // cols % 32 == 0: whole blocks in or out
+  Raw8<BF16> raw[kQtRows / 16];
+#pragma unroll
+  for (int p = 0; p < kQtRows / 16; ++p) {
+    const int64_t r = r0 + lr + 16 * p;
+    raw[p] = Raw8<BF16>{};
+    if (in_c && r < rows) raw[p] = load8<BF16>(src, r * ld + c0 + lc);
+  }
+#pragma unroll
+  for (int p = 0; p < kQtRows / 16; ++p) {
+    const int rr = lr + 16 * p;
+    float v[8];
+    unpack8<BF16>(raw[p], v);
+    if (ROWS) {
+      const uint32_t sb = mx_scale_byte(mx_amax4(v));
+      if (in_c && r0 + rr < rows) {
+        const int64_t e = (r0 + rr) * cols + c0 + lc;
+        *reinterpret_cast<u32x2_t *>(codes + e) = mx_encode8(v, sb);
+        if ((t & 3) == 0) scales[e >> 5] = (uint8_t)sb;
+      }
+    }
+    float4 *d = reinterpret_cast<float4 *>(sm + rr * kQtCols + (lc ^ ((rr >> 5) << 4)));
+    d[0] = make_float4(v[0], v[1], v[2], v[3]);
+    d[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+  __syncthreads();
+  const int64_t rp = (rows + 31) / 32 * 32;
+  const int grp = t & 3;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = (t >> 2) + 64 * h;
+    const int64_t r = r0 + 32 * grp;
+    float v[32];
+    uint32_t a = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      v[j] = sm[(32 * grp + j) * kQtCols + (c ^ (grp << 4))];
+      a = max(a, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    }
+    if (c0 + c >= cols || r >= rp) continue;
+    const uint32_t sb = mx_scale_byte(a);
+    u32x4r_t w[2];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      w[j >> 2][j & 3] = mx_encode4(make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]), sb);
+    if (sb == 0xFFu && r + 32 > rows) {               // the missing rows' codes stay 0 in a NaN block too
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (r + j >= rows) w[j >> 4][(j >> 2) & 3] &= ~(0xFFu << (8 * (j & 3)));
+    }
+    const int64_t e = (c0 + c) * rp + r;
+    u32x4r_t *o = reinterpret_cast<u32x4r_t *>(codes_t + e);
+    o[0] = w[0];
+    o[1] = w[1];
+    scales_t[e >> 5] = (uint8_t)sb;
+  }
+}
+
+// -------------------------------------------------------------- residual RMS norm
+
+// Row layout of the norm kernels: WPR waves share a row, lane l of wave w holds
+// the 8-element runs w * 64 + l + c * WPR * 64, c < NCH.  Rows of up to 512 * NCH
+// elements take one wave, so a workgroup of 4 waves needs no barrier at all.
+template <int WPR, int NCH>
+struct RowCfg {
+  static constexpr int kWpr = WPR, kNch = NCH;
+  static constexpr int kThreads = WPR > 4 ? 64 * WPR : 256;
+  static constexpr int kRows = kThreads / 64 / WPR;    // rows a workgroup works on at once
+};
+
+// Sum over a row's lanes: a butterfly in the wave, then the waves in order.
+template <int WPR>
+__device__ __forceinline__ double row_sum(double v, double *sm) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  if (WPR > 1) {
+    const int w = threadIdx.x >> 6, first = w / WPR * WPR;
+    __syncthreads();                                   // the previous row's sums have been read
+    if ((threadIdx.x & 63) == 0) sm[w] = v;
+    __syncthreads();
+    v = 0.0;
+#pragma unroll
+    for (int k = 0; k < WPR; ++k) v += sm[first + k];
+  }
+  return v;
+}
+
+template <bool BF16, bool WBF16, class C>
+__global__ __launch_bounds__(C::kThreads) void k_rmsnorm(sshdp_rmsnorm a) {
+  __shared__ double sm[C::kThreads / 64];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int sub = wave / C::kWpr, run0 = (wave % C::kWpr) * 64 + lane;
+  const int runs = (int)(a.cols >> 3);
+  float w[C::kNch][8];
+#pragma unroll
+  for (int c = 0; c < C::kNch; ++c) {
+    const int run = run0 + c * C::kWpr * 64;
+    Raw8<WBF16> r{};
+    if (run < runs) r = load8<WBF16>(a.weight, run * 8);
+    unpack8<WBF16>(r, w[c]);
+  }
+  // the loop bound is the same for all waves of a workgroup (barriers inside)
+  for (int64_t g = blockIdx.x; g * C::kRows < a.rows; g += gridDim.x) {
+    const int64_t row = g * C::kRows + sub;
+    const bool live = row < a.rows;
+    float h[C::kNch][8];
+    double s = 0.0;
+    Raw8<BF16> rx[C::kNch], rr[C::kNch];
+#pragma unroll
+    for (int c = 0; c < C::kNch; ++c) {
+      const int run = run0 + c * C::kWpr * 64;
+      rx[c] = Raw8<BF16>{};
+      rr[c] = Raw8<BF16>{};
+      if (live && run < runs) {
+        rx[c] = load8<BF16>(a.x, row * a.ld_x + run * 8);
+        if (a.residual) rr[c] = load8<BF16>(a.residual, row * a.ld_residual + run * 8);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < C::kNch; ++c) {
+      const int run = run0 + c * C::kWpr * 64;
+      unpack8<BF16>(rx[c], h[c]);
+      if (a.residual) {
+        float r[8];
+        unpack8<BF16>(rr[c], r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[c][j] += r[j];
+        const Raw8<BF16> p = pack8<BF16>(h[c]);         // h as stored is what the norm sees
+        unpack8<BF16>(p, h[c]);
+        if (a.h && live && run < runs) store8<BF16>(a.h, row * a.cols + run * 8, p);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s = fma((double)h[c][j], (double)h[c][j], s);
+    }
+    s = row_sum<C::kWpr>(s, sm);
+    const double rstd = 1.0 / sqrt(s / (double)a.cols + (double)a.eps);
+    if (a.rstd && live && run0 == 0) a.rstd[row] = (float)rstd;
+#pragma unroll
+    for (int c = 0; c < C::kNch; ++c) {
+      const int run = run0 + c * C::kWpr * 64;
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = (float)((double)h[c][j] * rstd * (double)w[c][j]);
+      if (a.codes) {
+        const uint32_t sb = mx_scale_byte(mx_amax4(y));
+        if (live && run < runs) {
+          const int64_t e = row * a.cols + run * 8;
+          *reinterpret_cast<u32x2_t *>(a.codes + e) = mx_encode8(y, sb);
+          if ((lane & 3) == 0) a.scales[e >> 5] = (uint8_t)sb;
+        }
+      }
+      if (a.y && live && run < runs) store8<BF16>(a.y, row * a.cols + run * 8, pack8<BF16>(y));
+    }
+  }
+}
+
+// --------------------------------------------------------------------- its gradient
+
+// Workgroups keep their columns' weight-gradient sums in registers over all their
+// rows and leave one partial row each; k_dweight adds the partial rows.
+template <bool BF16, bool WBF16, class C>
+__global__ __launch_bounds__(C::kThreads) void k_rmsnorm_grad(sshdp_rmsnorm_grad a, float *partials) {
+  __shared__ double sm[C::kThreads / 64];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int sub = wave / C::kWpr, run0 = (wave % C::kWpr) * 64 + lane;
+  const int runs = (int)(a.cols >> 3);
+  float w[C::kNch][8], dw[C::kNch][8];
+#pragma unroll
+  for (int c = 0; c < C::kNch; ++c) {
+    const int run = run0 + c * C::kWpr * 64;
+    Raw8<WBF16> r{};
+    if (run < runs) r = load8<WBF16>(a.weight, run * 8);
+    unpack8<WBF16>(r, w[c]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[c][j] = 0.f;
+  }
+  for (int64_t g = blockIdx.x; g * C::kRows < a.rows; g += gridDim.x) {
+    const int64_t row = g * C::kRows + sub;
+    const bool live = row < a.rows;
+    Raw8<BF16> ry[C::kNch], rh[C::kNch], rd[C::kNch];
+#pragma unroll
+    for (int c = 0; c < C::kNch; ++c) {
+      const int run = run0 + c * C::kWpr * 64;
+      ry[c] = Raw8<BF16>{};
+      rh[c] = Raw8<BF16>{};
+      rd[c] = Raw8<BF16>{};
+      if (live && run < runs) {
+        const int64_t e = row * a.cols + run * 8;
+        ry[c] = load8<BF16>(a.dy, e);
+        rh[c] = load8<BF16>(a.h, e);
+        if (a.dh) rd[c] = load8<BF16>(a.dh, e);
+      }
+    }
+    const float rstd = live ? a.rstd[row] : 0.f;
+    float s = 0.f;
+#pragma unroll
+    for (int c = 0; c < C::kNch; ++c) {
+      float dy[8], h[8];
+      unpack8<BF16>(ry[c], dy);
+      unpack8<BF16>(rh[c], h);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float xhat = h[j] * rstd;
+        s = fmaf(w[c][j] * dy[j], xhat, s);
+        dw[c][j] = fmaf(dy[j], xhat, dw[c][j]);
+      }
+    }
+    const float mean = (float)(row_sum<C::kWpr>((double)s, sm) / (double)a.cols);
+#pragma unroll
+    for (int c = 0; c < C::kNch; ++c) {
+      const int run = run0 + c * C::kWpr * 64;
+      float dy[8], h[8], dx[8];
+      unpack8<BF16>(ry[c], dy);
+      unpack8<BF16>(rh[c], h);
+      unpack8<BF16>(rd[c], dx);                          // zeros without dh
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dx[j] = fmaf(rstd, fmaf(-mean, h[j] * rstd, w[c][j] * dy[j]), dx[j]);
+      if (live && run < runs) store8<BF16>(a.dx, row * a.cols + run * 8, pack8<BF16>(dx));
+    }
+  }
+  // one partial row per row slot of the workgroup
+#pragma unroll
+  for (int c = 0; c < C::kNch; ++c) {
+    const int run = run0 + c * C::kWpr * 64;
+    if (run < runs) {
+      float4 *p = reinterpret_cast<float4 *>(partials + ((int64_t)blockIdx.x * C::kRows + sub) * a.cols + run * 8);
+      p[0] = make_float4(dw[c][0], dw[c][1], dw[c][2], dw[c][3]);
+      p[1] = make_float4(dw[c][4], dw[c][5], dw[c][6], dw[c][7]);
+    }
+  }
+}
+
+// dweight = (first ? 0 : dweight) + sum of the partial rows: 32 columns per
+// workgroup, 32 row slices added in slice order.
+__global__ __launch_bounds__(1024) void k_dweight(const float *partials, int64_t n, int64_t cols, int first,
+                                                  float *dweight) {
+  __shared__ float sm[32][33];
+  const int c = threadIdx.x & 31, sl = threadIdx.x >> 5;
+  const int64_t col = (int64_t)blockIdx.x * 32 + c;      // cols % 32 == 0
+  float s = 0.f;
+  for (int64_t i = sl; i < n; i += 32) s += partials[i * cols + col];
+  sm[sl][c] = s;
+  __syncthreads();
+  if (sl == 0) {
+    float v = first ? 0.f : dweight[col];
+    s = 0.f;
+    for (int k = 0; k < 32; ++k) s += sm[k][c];
+    dweight[col] = v + s;
+  }
+}
+
+using R1x1 = RowCfg<1, 1>;
+using R1x2 = RowCfg<1, 2>;
+using R1x4 = RowCfg<1, 4>;
+using R4x2 = RowCfg<4, 2>;
+using R4x4 = RowCfg<4, 4>;
+using R16x2 = RowCfg<16, 2>;
+using R16x4 = RowCfg<16, 4>;
+
+// Calls f with the row layout for `cols`: the fewest waves per row whose
+// registers hold it.
+template <class F>
+void with_rows(int64_t cols, F f) {
+  if (cols <= 512) f(R1x1{});
+  else if (cols <= 1024) f(R1x2{});
+  else if (cols <= 2048) f(R1x4{});
+  else if (cols <= 4096) f(R4x2{});
+  else if (cols <= 8192) f(R4x4{});
+  else if (cols <= 16384) f(R16x2{});
+  else f(R16x4{});
+}
+
+constexpr int64_t kNormGroups = 2048;                  // workgroups of the forward at most
+constexpr int64_t kGradRows = 1024;                    // partial rows of the weight gradient at most
+
+template <class C>
+int64_t norm_groups(int64_t rows, int64_t most) {
+  return std::max<int64_t>(1, std::min((rows + C::kRows - 1) / C::kRows, most));
+}
+
+template <class C>
+hipError_t rmsnorm(const sshdp_rmsnorm &a, hipStream_t s) {
+  const dim3 grid((unsigned)norm_groups<C>(a.rows, kNormGroups)), block(C::kThreads);
+  const bool b = a.dtype == SSHDP_DTYPE_BF16, wb = a.weight_dtype == SSHDP_DTYPE_BF16;
+  if (b && wb) hipLaunchKernelGGL((k_rmsnorm<true, true, C>), grid, block, 0, s, a);
+  else if (b) hipLaunchKernelGGL((k_rmsnorm<true, false, C>), grid, block, 0, s, a);
+  else if (wb) hipLaunchKernelGGL((k_rmsnorm<false, true, C>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_rmsnorm<false, false, C>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+template <class C>
+hipError_t rmsnorm_grad(const sshdp_rmsnorm_grad &a, float *partials, hipStream_t s) {
+  const dim3 grid((unsigned)norm_groups<C>(a.rows, kGradRows / C::kRows)), block(C::kThreads);
+  const bool b = a.dtype == SSHDP_DTYPE_BF16, wb = a.weight_dtype == SSHDP_DTYPE_BF16;
+  if (b && wb) hipLaunchKernelGGL((k_rmsnorm_grad<true, true, C>), grid, block, 0, s, a, partials);
+  else if (b) hipLaunchKernelGGL((k_rmsnorm_grad<true, false, C>), grid, block, 0, s, a, partials);
+  else if (wb) hipLaunchKernelGGL((k_rmsnorm_grad<false, true, C>), grid, block, 0, s, a, partials);
+  else hipLaunchKernelGGL((k_rmsnorm_grad<false, false, C>), grid, block, 0, s, a, partials);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quant_rows(const void *src, bool bf16, int64_t rows, int64_t cols, int64_t ld, uint8_t *codes,
+                             uint8_t *scales, hipStream_t s) {
+  const int64_t runs = rows * (cols / 8);
+  const dim3 grid((unsigned)std::min<int64_t>((runs + 255) / 256, 1 << 20)), block(256);
+  if (bf16) hipLaunchKernelGGL((k_quant_rows<true>), grid, block, 0, s, src, runs, (int)(cols / 8), ld, codes, scales);
+  else hipLaunchKernelGGL((k_quant_rows<false>), grid, block, 0, s, src, runs, (int)(cols / 8), ld, codes, scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_quant_tiles(const void *src, bool bf16, int64_t rows, int64_t cols, int64_t ld, uint8_t *codes,
+                              uint8_t *scales, uint8_t *codes_t, uint8_t *scales_t, hipStream_t s) {
+  const int64_t tiles_c = (cols + kQtCols - 1) / kQtCols;
+  const dim3 grid((unsigned)((rows + kQtRows - 1) / kQtRows * tiles_c)), block(256);
+#define SSHDP_QT(B, R) \
+  hipLaunchKernelGGL((k_quant_tiles<B, R>), grid, block, 0, s, src, rows, cols, ld, codes, scales, codes_t, scales_t, \
+                     tiles_c)
+  if (bf16 && codes) SSHDP_QT(true, true);
+  else if (bf16) SSHDP_QT(true, false);
+  else if (codes) SSHDP_QT(false, true);
+  else SSHDP_QT(false, false);
+#undef SSHDP_QT
+  return hipGetLastError();
+}
+
+hipError_t launch_rmsnorm(const sshdp_rmsnorm &a, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  with_rows(a.cols, [&](auto c) { e = rmsnorm<decltype(c)>(a, s); });
+  return e;
+}
+
+int64_t rmsnorm_partials(int64_t rows, int64_t cols) {
+  int64_t n = 0;
+  with_rows(cols, [&](auto c) {
+    using C = decltype(c);
+    n = norm_groups<C>(rows, kGradRows / C::kRows) * C::kRows;
+  });
+  return n;
+}
+
+hipError_t launch_rmsnorm_backward(const sshdp_rmsnorm_grad &a, float *partials, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  if (a.rows) with_rows(a.cols, [&](auto c) { e = rmsnorm_grad<decltype(c)>(a, partials, s); });
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_dweight, dim3((unsigned)(a.cols / 32)), dim3(1024), 0, s, partials,
+                     a.rows ? rmsnorm_partials(a.rows, a.cols) : 0, a.cols, a.first, a.dweight);
+  return hipGetLastError();
+}
+
+}  // namespace sshdp

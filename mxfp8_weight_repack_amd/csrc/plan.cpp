@@ -558,6 +558,14 @@ void build_elementwise(sshdp_plan &p, const sshdp_node *nodes, int32_t n) {
   p.qchunks = fused;
   p.qchunks.insert(p.qchunks.end(), plain.begin(), plain.end());
   p.stats.n_quant_regions = (int32_t)p.qregions.size();
+  // the gradient norm's runs: unit runs that touch are one, then cut into chunks
+  for (size_t i = 0; i < units.size();) {
+    const int64_t a = units[i].start;
+    int64_t e = a;
+    for (; i < units.size() && units[i].start == e; ++i) e += units[i].len;
+    for (int64_t pos = a; pos < e; pos += kChunk)
+      p.gchunks.push_back({pos, (int32_t)std::min<int64_t>(kChunk, e - pos), 0});
+  }
   for (const Interval &iv : units) {
     if (iv.opt != SSHDP_OPT_ADAMW) continue;
     for (int64_t s = iv.start; s < iv.start + iv.len; s += kChunk) {
@@ -574,7 +582,7 @@ size_t table_bytes(const std::vector<T> &v) { return round_up((int64_t)(v.size()
 int upload(sshdp_plan &p) {
   const size_t total = table_bytes(p.munits) + table_bytes(p.f0tiles) + table_bytes(p.aseg_all) +
                        table_bytes(p.aseg_unfused) + table_bytes(p.qregions) + table_bytes(p.qchunks) +
-                       table_bytes(p.q32tiles) + table_bytes(p.cchunks) + table_bytes(p.ns_groups) +
+                       table_bytes(p.q32tiles) + table_bytes(p.cchunks) + table_bytes(p.gchunks) + table_bytes(p.ns_groups) +
                        table_bytes(p.norm_units) + 256;
   size_t tiles_total = 0;
   for (auto &ln : p.ns_tiles)
@@ -599,6 +607,7 @@ int upload(sshdp_plan &p) {
   put(p.qchunks, p.d.qchunks);
   put(p.q32tiles, p.d.q32tiles);
   put(p.cchunks, p.d.cchunks);
+  put(p.gchunks, p.d.gchunks);
   put(p.ns_groups, p.d.ns_groups);
   put(p.norm_units, p.d.norm_units);
   for (int ln = 0; ln < kMaxLanes; ++ln)
@@ -674,6 +683,7 @@ int sshdp_plan_views(const sshdp_node *nodes, int32_t n_nodes, int64_t root_nume
   p->root_numel = root_numel;
   p->opts = o;
   p->node_abs = abs;
+  p->nodes.assign(nodes, nodes + n_nodes);
   p->stats.root_numel = root_numel;
   p->stats.scale_bytes = o.scale_layout == SSHDP_SCALE_BLOCK32X32 ? (root_numel + 1023) / 1024 : (root_numel + 31) / 32;
   p->stats.n_nodes = n_nodes;

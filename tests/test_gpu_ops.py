@@ -1,0 +1,446 @@
+"""GPU parity of the operators around the update -- gradient norm and clip, MXFP8
+quantisation, residual RMS norm and its gradient, MXFP8 products -- against
+float64 references (tests/ops_ref.py) and the oracle's codes, at sizes and
+values where they can go wrong."""
+
+import numpy as np
+import pytest
+
+import mxfp8_weight_repack_amd as sh
+import ops_ref as R
+from gpu_util import say
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    sh.lib()
+
+
+def stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def dev(a, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    return t if dtype is None else t.to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+
+
+def host(t):
+    torch.cuda.synchronize()
+    return t.float().cpu().numpy() if t.dtype == torch.bfloat16 else t.cpu().numpy()
+
+
+def buf(*shape, dtype=torch.uint8, fill=0xA5):
+    return torch.full(shape, fill, dtype=dtype, device="cuda")
+
+
+def work(n):
+    """Workspace of exactly n bytes with stale contents (0xFF: NaN as floats)."""
+    return buf(max(n, 16), fill=0xFF)
+
+
+# ------------------------------------------------------------------ norm and clip
+
+def unit(offset, rows, cols, stride=None, opt="adamw", parent=-1):
+    return dict(parent=parent, offset=offset, rows=rows, cols=cols, row_stride=stride or cols, is_unit=True,
+                optimizer=opt, quantize=None)
+
+
+def _unit_mask(nodes, n):
+    m = np.zeros(n, bool)
+    for d in nodes:
+        for i in range(d["rows"]):
+            m[d["offset"] + i * d["row_stride"]:d["offset"] + i * d["row_stride"] + d["cols"]] = True
+    return m
+
+
+TREES = {
+    "one element": ([unit(5, 1, 1)], 8),
+    "whole root": ([unit(0, 1, 4096)], 4096),
+    "odd runs": ([unit(1, 1, 3), unit(7, 1, 4097), unit(4105, 1, 2), unit(4200, 1, 8191)], 13000),
+    "touching heads": ([unit(64 * h, 96, 64, 256, opt="muon") for h in range(4)], 96 * 256),
+    "strided, gaps": ([unit(3, 50, 33, 41), unit(2100, 7, 5, 9), unit(2304, 64, 64, opt="muon")], 8192),
+    "many": ([unit(40 * i, 1, 1 + (7 * i) % 40) for i in range(500)], 20000),
+    "large": ([unit(0, 1, 9_000_001), unit(9_000_004, 3000, 1000)], 12_000_016),
+}
+
+
+def _clip(nodes, n, g, max_norm, in_place=False, split=False):
+    plan = sh.Plan(nodes, n)
+    gd = dev(g)
+    out = gd if in_place else torch.full_like(gd, 7.0)
+    stats = buf(2, dtype=torch.float32, fill=-1.0)
+    nb = sh.grad_workspace(plan)
+    ws = work(nb)
+    if split:
+        s = buf(2, dtype=torch.float64, fill=-1.0)
+        sh.grad_sumsq(plan, gd, s, ws, nb, stream())
+        sh.grad_clip(plan, gd, out, s, max_norm, stats, stream())
+    else:
+        sh.grad_clip_norm(plan, gd, out, max_norm, stats, ws, nb, stream())
+    return host(out), host(stats)
+
+
+@pytest.mark.parametrize("max_norm", [0.37, 1e6])
+@pytest.mark.parametrize("tree", sorted(TREES))
+def test_clip_against_float64(tree, max_norm):
+    say(f"clip {tree} max {max_norm}")
+    nodes, n = TREES[tree]
+    rng = np.random.default_rng(len(tree))
+    g = rng.standard_normal(n).astype(np.float32)
+    mask = _unit_mask(nodes, n)
+    g[~mask] = np.nan                                  # gaps are neither read ...
+    norm = np.sqrt(np.sum(g[mask].astype(np.float64) ** 2))
+    coef = float(np.float32(max_norm)) / norm if norm > np.float32(max_norm) else 1.0
+    for kw in (dict(), dict(in_place=True), dict(split=True)):
+        out, stats = _clip(nodes, n, g, max_norm, **kw)
+        # one rounding to float32 each; float64 sums add less than 1% of one
+        assert abs(stats[0] - norm) <= 1.01 * R.U * norm
+        assert abs(stats[1] - coef) <= 1.01 * R.U * coef
+        ref = g[mask].astype(np.float64) * coef
+        assert np.all(np.abs(out[mask] - ref) <= 2.02 * R.U * np.abs(ref) + 2.0 ** -149)
+        rest = out[~mask]                              # ... nor written
+        assert np.all(np.isnan(rest)) if kw.get("in_place") else np.all(rest == 7.0)
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e30, 3e38])
+def test_clip_of_extreme_gradients(scale):
+    """Squares far outside float32's range: the norm is exact, the clip finite."""
+    say(f"clip scale {scale}")
+    n = 5000
+    g = (np.random.default_rng(1).uniform(-1, 1, n) * scale).astype(np.float32)
+    norm = np.sqrt(np.sum(g.astype(np.float64) ** 2))
+    out, stats = _clip([unit(0, 1, n)], n, g, 1.0)
+    want = np.float32(norm) if norm <= np.finfo(np.float32).max else np.inf
+    assert stats[0] == want or abs(stats[0] - norm) <= 1.01 * R.U * norm
+    coef = 1.0 / norm if norm > 1 else 1.0
+    # a coefficient below float32's normal range is off by half its smallest step
+    bound = 2.02 * R.U * np.abs(g * coef) + np.abs(g.astype(np.float64)) * 2.0 ** -150 + 2.0 ** -149
+    assert np.all(np.abs(out - g.astype(np.float64) * coef) <= bound)
+
+
+@pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
+def test_clip_of_non_finite_gradients(bad):
+    say(f"clip with {bad}")
+    g = np.random.default_rng(2).standard_normal(6000).astype(np.float32)
+    g[4321] = bad
+    out, stats = _clip([unit(0, 1, 6000)], 6000, g, 1.0)
+    ok = np.arange(6000) != 4321
+    if np.isnan(bad):
+        assert np.isnan(stats[0]) and stats[1] == 1.0 and np.array_equal(out[ok], g[ok])
+    else:
+        assert np.isinf(stats[0]) and stats[1] == 0.0 and np.all(out[ok] == 0)
+    assert np.isnan(out[4321])
+
+
+def test_clip_is_reproducible():
+    nodes, n = TREES["large"]
+    g = np.random.default_rng(3).standard_normal(n).astype(np.float32)
+    a, sa = _clip(nodes, n, g, 1.0)
+    b, sb = _clip(nodes, n, g, 1.0)
+    c, sc = _clip(nodes, n, g, 1.0, split=True)
+    assert np.array_equal(a, b, equal_nan=True) and np.array_equal(sa, sb)
+    assert np.array_equal(a, c, equal_nan=True) and np.array_equal(sa, sc)
+
+
+# ---------------------------------------------------------------------- quantising
+
+def _matrix(rng, r, c, dtype, special=True):
+    x = (rng.standard_normal((r, c)) * np.exp(rng.standard_normal((r, 1)))).astype(np.float32)
+    x = R.as_dtype(x, dtype)
+    if special and r * c >= 32 * 8:
+        f = x.reshape(-1)
+        f[rng.integers(0, f.size, 12)] = [np.nan, np.inf, -np.inf, -0.0, 0.0, 448.0, 449.0, 1e-40, -1e-45, 3e38,
+                                          2.0 ** -126, -448.0 * 2.0 ** -20]
+        x[:, :32] = np.where(rng.random((r, 1)) < 0.3, 0, x[:, :32])
+        x = R.as_dtype(x, dtype)
+    return x
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows,cols,ld", [(1, 32, 32), (1, 4096, 4096), (31, 96, 104), (32, 128, 128), (33, 160, 160),
+                                          (127, 1056, 1064), (129, 256, 512), (300, 64, 64), (1000, 2048, 2048)])
+def test_quant_bit_exact(rows, cols, ld, dtype):
+    say(f"quant {rows}x{cols} ld {ld} {dtype}")
+    rng = np.random.default_rng(rows * 7 + cols)
+    x = _matrix(rng, rows, cols, dtype)
+    full = np.full((rows, ld), np.nan, np.float32)
+    full[:, :cols] = x
+    src = dev(full, dtype)
+    qc, qs = R.quant_rows(x)
+    tc, ts = R.quant_cols(x)
+    for along in ("rows", "cols", "both"):
+        c = s = ct = st = None
+        if along != "cols":
+            c, s = buf(rows * cols + 64), buf(rows * cols // 32 + 64)
+        if along != "rows":
+            ct, st = buf(tc.size + 64), buf(ts.size + 64)
+        sh.quant_mxfp8(src, dtype, rows, cols, c, s, ct, st, ld=ld, stream=stream())
+        for got, ref in ((c, qc), (s, qs), (ct, tc), (st, ts)):
+            if got is None:
+                continue
+            got = host(got)
+            assert np.array_equal(got[:ref.size], ref.reshape(-1)), along
+            assert np.all(got[ref.size:] == 0xA5)      # nothing behind the last row
+
+
+# ------------------------------------------------------------------------ RMS norm
+
+NORM_SIZES = [(1, 32), (1, 8192), (3, 512), (5, 544), (7, 1056), (130, 2048), (33, 2080), (2, 4128), (9, 8224),
+              (3, 16416), (2, 32768), (2500, 64)]
+
+
+@pytest.mark.parametrize("dtype,wdtype", [("bf16", "fp32"), ("fp32", "fp32"), ("fp32", "bf16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("rows,cols", NORM_SIZES)
+def test_rmsnorm_codes_bit_exact(rows, cols, dtype, wdtype):
+    say(f"rmsnorm {rows}x{cols} {dtype}/{wdtype}")
+    rng = np.random.default_rng(rows + cols)
+    ldx, ldr = cols + 8, cols + 16
+    x = np.full((rows, ldx), np.nan, np.float32)
+    r = np.full((rows, ldr), np.nan, np.float32)
+    x[:, :cols] = _matrix(rng, rows, cols, dtype, special=False)
+    r[:, :cols] = _matrix(rng, rows, cols, dtype, special=False)
+    if rows > 2:
+        x[1, :cols] = 0
+        r[1, :cols] = 0                                # a row of zeros: eps alone
+    w = R.as_dtype(1 + 0.2 * rng.standard_normal(cols), wdtype)
+    for residual in (True, False):
+        eps = 1e-5
+        h, rstd, y = R.rmsnorm(x[:, :cols], r[:, :cols] if residual else None, w, eps, dtype)
+        qc, qs = R.quant_rows(y)
+        td = torch.bfloat16 if dtype == "bf16" else torch.float32
+        hd, yd = buf(rows + 1, cols, dtype=td, fill=3.0), buf(rows + 1, cols, dtype=td, fill=3.0)
+        c, s, rs = buf(rows + 1, cols), buf(rows + 1, cols // 32), buf(rows + 1, dtype=torch.float32, fill=3.0)
+        sh.rmsnorm_mxfp8(dev(x, dtype), dev(w, wdtype), rows, cols, dtype=dtype, weight_dtype=wdtype,
+                         residual=dev(r, dtype) if residual else None, h=hd if residual else None, y=yd, codes=c,
+                         scales=s, rstd=rs, eps=eps, ld_x=ldx, ld_residual=ldr, stream=stream())
+        if residual:
+            assert np.array_equal(host(hd)[:rows], h) and np.all(host(hd)[rows] == 3.0)
+        assert np.array_equal(host(c)[:rows], qc) and np.all(host(c)[rows] == 0xA5)
+        assert np.array_equal(host(s)[:rows], qs) and np.all(host(s)[rows] == 0xA5)
+        assert np.all(np.abs(host(rs)[:rows] - rstd) <= 1.01 * R.U * rstd) and host(rs)[rows] == 3.0
+        # y in float32 may differ where the float64 product sits within its own error of a rounding border
+        yr = R.as_dtype(y, dtype)
+        assert np.all(np.abs(host(yd)[:rows] - yr) <= 2 * R.HALF[dtype] * np.abs(yr)) and np.all(host(yd)[rows] == 3.0)
+        assert np.mean(host(yd)[:rows] != yr) <= 1e-4
+
+
+def test_rmsnorm_in_place_and_alone():
+    """h may be the residual itself; each output may be asked for alone."""
+    rng = np.random.default_rng(5)
+    rows, cols = 37, 1056
+    x, r = (_matrix(rng, rows, cols, "bf16", special=False) for _ in range(2))
+    w = np.ones(cols, np.float32)
+    h, rstd, y = R.rmsnorm(x, r, w, 1e-6, "bf16")
+    rd = dev(r, "bf16")
+    sh.rmsnorm_mxfp8(dev(x, "bf16"), dev(w), rows, cols, residual=rd, h=rd, stream=stream())
+    assert np.array_equal(host(rd), h)
+    rs = buf(rows, dtype=torch.float32, fill=0)
+    sh.rmsnorm_mxfp8(rd, dev(w), rows, cols, rstd=rs, stream=stream())
+    assert np.all(np.abs(host(rs) - rstd) <= 1.01 * R.U * rstd)
+    yd = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    sh.rmsnorm_mxfp8(rd, dev(w), rows, cols, y=yd, stream=stream())
+    assert np.array_equal(host(yd), R.as_dtype(y, "bf16"))
+
+
+def test_rmsnorm_of_non_finite_rows():
+    rng = np.random.default_rng(6)
+    rows, cols = 6, 256
+    x = rng.standard_normal((rows, cols)).astype(np.float32)
+    x[1, 40], x[2, 70], x[3, :] = np.nan, np.inf, 0.0
+    x[4] *= 1e30                                       # squares beyond float32
+    x[5] *= 1e-30
+    w = np.ones(cols, np.float32)
+    for eps in (1e-6, 0.0):
+        h, rstd, y = R.rmsnorm(x, None, w, eps, "fp32")
+        qc, qs = R.quant_rows(y)
+        c, s = buf(rows, cols), buf(rows, cols // 32)
+        sh.rmsnorm_mxfp8(dev(x), dev(w), rows, cols, dtype="fp32", codes=c, scales=s, eps=eps, stream=stream())
+        assert np.array_equal(host(c), qc) and np.array_equal(host(s), qs), eps
+
+
+@pytest.mark.parametrize("dtype,wdtype", [("bf16", "fp32"), ("fp32", "fp32"), ("fp32", "bf16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("rows,cols", NORM_SIZES + [(4100, 96)])
+def test_rmsnorm_backward_against_float64(rows, cols, dtype, wdtype):
+    say(f"rmsnorm backward {rows}x{cols} {dtype}/{wdtype}")
+    rng = np.random.default_rng(rows * 3 + cols)
+    dy, h, dh = (_matrix(rng, rows, cols, dtype, special=False) for _ in range(3))
+    w = R.as_dtype(1 + 0.2 * rng.standard_normal(cols), wdtype)
+    rstd = R.rmsnorm(h, None, w, 1e-6, dtype)[1].astype(np.float32)
+    nb = sh.rmsnorm_backward_workspace(rows, cols)
+    base = rng.standard_normal(cols).astype(np.float32)
+    td = torch.bfloat16 if dtype == "bf16" else torch.float32
+    for through, first in ((True, True), (False, False)):
+        dx, bdx, dw, bdw = R.rmsnorm_grad(dy, h, w, rstd, dh if through else None, dtype)
+        dxd, dwd = buf(rows + 1, cols, dtype=td, fill=3.0), dev(np.concatenate([base, [9.0]]).astype(np.float32))
+        sh.rmsnorm_backward(dev(dy, dtype), dev(h, dtype), dev(w, wdtype), dev(rstd), dxd, dwd, rows, cols,
+                            dtype=dtype, weight_dtype=wdtype, dh=dev(dh, dtype) if through else None, first=first,
+                            workspace=work(nb), workspace_bytes=nb, stream=stream())
+        got = host(dxd)
+        assert np.all(np.abs(got[:rows] - dx) <= bdx) and np.all(got[rows] == 3.0)
+        if not first:
+            dw, bdw = dw + base, bdw + R.U * (np.abs(dw + base) + np.abs(base))
+        got = host(dwd)
+        assert np.all(np.abs(got[:cols] - dw) <= bdw) and got[cols] == 9.0
+
+
+def test_rmsnorm_backward_in_place_and_empty():
+    rng = np.random.default_rng(8)
+    rows, cols = 20, 96
+    dy, h, dh = (_matrix(rng, rows, cols, "fp32", special=False) for _ in range(3))
+    w = np.ones(cols, np.float32)
+    rstd = R.rmsnorm(h, None, w, 1e-6, "fp32")[1].astype(np.float32)
+    dx, bdx, _, _ = R.rmsnorm_grad(dy, h, w, rstd, dh, "fp32")
+    nb = sh.rmsnorm_backward_workspace(rows, cols)
+    dwd = torch.zeros(cols, device="cuda")
+    d = dev(dy)
+    sh.rmsnorm_backward(d, dev(h), dev(w), dev(rstd), d, dwd, rows, cols, dtype="fp32", dh=dev(dh), workspace=work(nb),
+                        workspace_bytes=nb, stream=stream())
+    assert np.all(np.abs(host(d) - dx) <= bdx)
+    before = host(dwd).copy()
+    sh.rmsnorm_backward(None, None, None, None, None, dwd, 0, cols, first=False, stream=stream())
+    assert np.array_equal(host(dwd), before)
+    sh.rmsnorm_backward(None, None, None, None, None, dwd, 0, cols, first=True, stream=stream())
+    assert np.all(host(dwd) == 0)
+
+
+# ------------------------------------------------------------------------ products
+
+def _operand(rng, rows, cols, layout, exact):
+    """codes, flat scales and float64 values; `exact`: small whole numbers under
+    scales 1 and 2, so that every partial sum is a whole number below 2^24 and
+    the float32 result must be the exact one."""
+    if exact:
+        v = rng.choice(np.array([0x00, 0x38, 0x40, 0x44, 0xB8, 0xC0, 0x48], np.uint8), (rows, cols))   # 0 1 2 3 -1 -2 4
+        n = {"block32x32": (rows // 32) * (cols // 32)}.get(layout, rows * cols // 32)
+        s = rng.choice(np.array([127, 128], np.uint8), max(n, 1))
+        return v, s, R.decode(v, s, layout)
+    w = (rng.standard_normal((rows, cols)) * np.exp(rng.standard_normal((rows, 1)))).astype(np.float32)
+    c, s = R.quant_weight(w, layout)
+    return c, s, R.decode(c, s, layout)
+
+
+def _gemm(a, b, m, n, out_dtype, op="nt", addend=None, pad=0, layouts=("rowmajor", "rowmajor"), in_place=False):
+    (ac, as_), (bc, bs) = a, b
+    A = sh.mx_matrix(dev(ac), dev(as_), ac.shape[0], ac.shape[1], layouts[0])
+    B = sh.mx_matrix(dev(bc), dev(bs), bc.shape[0], bc.shape[1], layouts[1])
+    td = torch.bfloat16 if out_dtype == "bf16" else torch.float32
+    out = buf(m + 1, n + pad, dtype=td, fill=3.0)
+    ad = None
+    if addend is not None:
+        full = np.full((m + 1, n + pad), 3.0, np.float32)
+        full[:m, :n] = addend
+        ad = dev(full)
+        if in_place:
+            out = ad
+    nb = sh.gemm_mxfp8_workspace(A, B, op=op)
+    sh.gemm_mxfp8(A, B, out, out_dtype, op=op, addend=ad, ld_out=n + pad, workspace=work(nb) if nb else None,
+                  workspace_bytes=nb, stream=stream())
+    o = host(out)
+    assert np.all(o[m] == 3.0) and np.all(o[:, n:] == 3.0)      # nothing behind the last row or column
+    return o[:m, :n]
+
+
+SHAPES = [(1, 1, 32), (1, 64, 64), (1, 2048, 2048), (3, 33, 160), (16, 128, 4096), (17, 100, 96), (31, 257, 1056),
+          (64, 96, 512), (65, 300, 288), (100, 1000, 1000 // 32 * 32), (127, 129, 128), (256, 256, 256),
+          (300, 520, 640), (513, 384, 2048), (1030, 777, 224)]
+
+
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_gemm_nt_exact_sums(m, n, k):
+    """Whole-number operands: the float32 output must equal the exact sum."""
+    say(f"gemm nt exact {m}x{n}x{k}")
+    rng = np.random.default_rng(m + n + k)
+    ac, as_, a = _operand(rng, m, k, "rowmajor", True)
+    bc, bs, b = _operand(rng, n, k, "rowmajor", True)
+    add = rng.integers(-50, 50, (m, n)).astype(np.float32)
+    assert np.array_equal(_gemm((ac, as_), (bc, bs), m, n, "fp32"), a @ b.T)
+    assert np.array_equal(_gemm((ac, as_), (bc, bs), m, n, "fp32", addend=add, pad=4), a @ b.T + add)
+    assert np.array_equal(_gemm((ac, as_), (bc, bs), m, n, "fp32", addend=add, pad=7, in_place=True), a @ b.T + add)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 32, 32), (2, 64, 128), (33, 96, 256), (130, 544, 96), (257, 256, 1024),
+                                   (64, 2048, 512), (600, 320, 288)])
+def test_gemm_nn_exact_sums(m, n, k):
+    say(f"gemm nn exact {m}x{n}x{k}")
+    rng = np.random.default_rng(m + n + k)
+    ac, as_, a = _operand(rng, m, k, "rowmajor", True)
+    bc, bs, b = _operand(rng, k, n, "block32x32", True)
+    lay = ("rowmajor", "block32x32")
+    assert np.array_equal(_gemm((ac, as_), (bc, bs), m, n, "fp32", "nn", layouts=lay), a @ b)
+    add = rng.integers(-50, 50, (m, n)).astype(np.float32)
+    assert np.array_equal(_gemm((ac, as_), (bc, bs), m, n, "fp32", "nn", addend=add, pad=3, layouts=lay), a @ b + add)
+
+
+@pytest.mark.parametrize("la,lb", [("rowmajor", "tile32x4"), ("rowmajor", "block32x32"), ("tile32x4", "rowmajor"),
+                                   ("block32x32", "tile32x4"), ("tile32x4", "block32x32")])
+@pytest.mark.parametrize("m,n,k", [(32, 64, 128), (96, 160, 512), (288, 544, 640), (32, 2048, 1152)])
+def test_gemm_scale_layouts_exact(m, n, k, la, lb):
+    say(f"gemm layouts {la} {lb} {m}x{n}x{k}")
+    rng = np.random.default_rng(m + n + k)
+    ac, as_, a = _operand(rng, m, k, la, True)
+    bc, bs, b = _operand(rng, n, k, lb, True)
+    assert np.array_equal(_gemm((ac, as_), (bc, bs), m, n, "fp32", layouts=(la, lb)), a @ b.T)
+
+
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_gemm_nt_against_float64(m, n, k, out):
+    say(f"gemm nt {m}x{n}x{k} {out}")
+    rng = np.random.default_rng(m * 5 + n + k)
+    ac, as_, a = _operand(rng, m, k, "rowmajor", False)
+    bc, bs, b = _operand(rng, n, k, "rowmajor", False)
+    ref, bound = R.product(a, b, None, out)
+    got = _gemm((ac, as_), (bc, bs), m, n, out, pad=5)
+    assert np.all(np.abs(got - ref) <= bound)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 64, 256), (130, 544, 96), (300, 320, 1024)])
+def test_gemm_nn_against_float64(m, n, k):
+    say(f"gemm nn {m}x{n}x{k}")
+    rng = np.random.default_rng(m * 5 + n + k)
+    ac, as_, a = _operand(rng, m, k, "rowmajor", False)
+    bc, bs, b = _operand(rng, k, n, "block32x32", False)
+    for out in ("fp32", "bf16"):
+        ref, bound = R.product(a, b.T, None, out)
+        got = _gemm((ac, as_), (bc, bs), m, n, out, "nn", layouts=("rowmajor", "block32x32"))
+        assert np.all(np.abs(got - ref) <= bound)
+
+
+@pytest.mark.parametrize("m", [2, 40, 300])
+def test_gemm_nan_blocks_and_extreme_scales(m):
+    """A NaN block spoils its row (and column) alone; scales at both ends of E8M0."""
+    say(f"gemm NaN blocks m {m}")
+    rng = np.random.default_rng(m)
+    n, k = 96, 384
+    ac, as_, a = _operand(rng, m, k, "rowmajor", True)
+    bc, bs, b = _operand(rng, n, k, "rowmajor", True)
+    sa, sb = as_.reshape(m, k // 32), bs.reshape(n, k // 32)
+    sa[1, :], sb[:, :] = 250, 10                       # 2^123 * 2^-117: finite products
+    ac[1, 5 * 32:6 * 32], sa[1, 5] = 0, 0
+    a, b = R.decode(ac, sa, "rowmajor"), R.decode(bc, sb, "rowmajor")
+    got = _gemm((ac, sa), (bc, sb), m, n, "fp32")
+    ref, bound = R.product(a, b, None, "fp32")
+    assert np.all(np.abs(got - ref) <= bound)
+    sa[0, 3], sb[7, 2] = 255, 255
+    got = _gemm((ac, sa), (bc, sb), m, n, "fp32")
+    bad = np.zeros((m, n), bool)
+    bad[0, :], bad[:, 7] = True, True
+    assert np.all(np.isnan(got[bad])) and np.array_equal(got[~bad], _gemm((ac, sa), (bc, np.where(sb == 255, 10, sb)),
+                                                                          m, n, "fp32")[~bad])
+
+
+def test_gemm_empty_sizes():
+    rng = np.random.default_rng(0)
+    z = np.zeros((0, 64), np.uint8)
+    ac, as_, a = _operand(rng, 5, 64, "rowmajor", True)
+    assert _gemm((z, z.reshape(-1)), (ac, as_), 0, 5, "bf16").shape == (0, 5)
+    k0 = np.zeros((5, 0), np.uint8), np.zeros(0, np.uint8)
+    add = rng.standard_normal((5, 5)).astype(np.float32)
+    assert np.all(_gemm(k0, k0, 5, 5, "bf16", pad=3) == 0)
+    assert np.array_equal(_gemm(k0, k0, 5, 5, "fp32", addend=add, in_place=True), add)
