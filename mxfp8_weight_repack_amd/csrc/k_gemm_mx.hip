@@ -125,11 +125,406 @@ __global__ __launch_bounds__(64) void k_gemm_mx_16(GemmMx p, int64_t tiles_n) {
   }
 }
 
+// ------------------------------------------------------------------ tiled products
+//
+// A workgroup makes a TN x TM block of the output (n x m), its waves WN x WM of them
+// (TN / WN) x (TM / WM) each, 128 k per step.  Operands go from memory to LDS with
+// buffer loads (no registers in between), two stages, each 128-byte row's 16-byte
+// chunks XOR-swizzled; the buffer resources end with the operand's last row, so
+// rows past it read as zeros, and chunks past K are sent out of range.
+//
+// Scales: every 4 steps a thread loads one row's 16 scale bytes (4 steps x 4
+// blocks), four steps ahead, and a 4 x 4 byte transpose across the lanes 16 and 32
+// apart turns each step's 4 bytes into the word the matrix instruction wants: lane
+// 16 g + r holds block g's byte of the rows r, 16 + r, 32 + r, 48 + r of its 64-row
+// group, picked by the instruction's byte select.
+
+constexpr int kBufWord3 = 0x00020000;                // raw gfx9-family buffer resource
+constexpr int kRowB = 128;                           // bytes (= k) of a stage row
+
+template <int TN_, int TM_, int WN_, int WM_>
+struct Tile {
+  static constexpr int TN = TN_, TM = TM_, WN = WN_, WM = WM_, NW = WN * WM, NT = 64 * NW;
+  static constexpr int FP = TN / WN / 16, FQ = TM / WM / 16;     // 16-row fragments of a wave: n side, m side
+  static constexpr int SEGP = TN * kRowB, SEGQ = TM * kRowB, STAGE = SEGP + SEGQ;
+  static constexpr int NIP = SEGP / 1024 / NW, NIQ = SEGQ / 1024 / NW;   // buffer loads per wave and stage
+  static constexpr int GRPS = (TN + TM) / 64;                   // 64-row scale groups, n side first
+  static constexpr int RING = 2 * 4 * GRPS * 64 * 4;            // scale words: 2 x 4 steps
+  static constexpr int EPI = TM * (TN + 8) * 2;                 // bfloat16 output tile
+  static constexpr int LDS = 2 * STAGE + RING > EPI ? 2 * STAGE + RING : EPI;
+  static_assert(FP % 4 == 0 && FQ == 4 && NT == TN + TM, "a thread per scale row, 64-row groups");
+};
+
+// Chunk swizzle of a stage row: 8 consecutive rows, one LDS pass, hit 8 different chunks.
+__device__ __forceinline__ int swz(int r) { return r & 7; }
+
+// Bytes (row j = lane / 16, block g) -> lane 16 g + r holds block g's bytes of rows j = 0..3.
+__device__ __forceinline__ uint32_t lane_transpose(uint32_t x, int lane) {
+  auto a = __builtin_amdgcn_permlane32_swap(x, x, false, false);      // [0]: lanes 0..31 twice, [1]: 32..63
+  x = __builtin_amdgcn_perm(a[1], a[0], lane < 32 ? 0x05040100u : 0x07060302u);
+  auto b = __builtin_amdgcn_permlane16_swap(x, x, false, false);      // [0]: even rows of 16 twice, [1]: odd
+  return __builtin_amdgcn_perm(b[1], b[0], lane & 16 ? 0x07030501u : 0x06020400u);
+}
+
+// One 8-bit matrix instruction; ip, iq: byte selects of the scale words (constants once unrolled).
+template <int IP, int IQ>
+__device__ __forceinline__ f32x4_t mx_mma(const i32x8_t &p, const i32x8_t &q, const f32x4_t &c, int sp, int sq) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q, c, 0, 0, IP, sp, IQ, sq);
+}
+template <int IP>
+__device__ __forceinline__ f32x4_t mx_mma_q(int iq, const i32x8_t &p, const i32x8_t &q, const f32x4_t &c, int sp, int sq) {
+  switch (iq) {
+    case 0: return mx_mma<IP, 0>(p, q, c, sp, sq);
+    case 1: return mx_mma<IP, 1>(p, q, c, sp, sq);
+    case 2: return mx_mma<IP, 2>(p, q, c, sp, sq);
+    default: return mx_mma<IP, 3>(p, q, c, sp, sq);
+  }
+}
+__device__ __forceinline__ f32x4_t mx_mma_pq(int ip, int iq, const i32x8_t &p, const i32x8_t &q, const f32x4_t &c,
+                                             int sp, int sq) {
+  switch (ip) {
+    case 0: return mx_mma_q<0>(iq, p, q, c, sp, sq);
+    case 1: return mx_mma_q<1>(iq, p, q, c, sp, sq);
+    case 2: return mx_mma_q<2>(iq, p, q, c, sp, sq);
+    default: return mx_mma_q<3>(iq, p, q, c, sp, sq);
+  }
+}
+
+// Workgroup id -> output tile.  Workgroup i runs on XCD i % 8, each with its own L2:
+// each XCD gets one contiguous eighth of an order that walks the tiles in strips of
+// 8 along m, so the 32 workgroups an XCD runs at once share 8 x 4 operand panels.
+__device__ __forceinline__ void tile_of(int64_t id, int64_t tiles_m, int64_t tiles_n, int64_t &tm, int64_t &tn) {
+  const int64_t total = tiles_m * tiles_n, q = total >> 3, rem = total & 7, x = id & 7;
+  const int64_t pos = x * q + min(x, rem) + (id >> 3);
+  const int64_t strip = pos / (8 * tiles_n), in = pos - strip * 8 * tiles_n;
+  const int64_t h = min<int64_t>(8, tiles_m - strip * 8);
+  tn = in / h;
+  tm = strip * 8 + in - tn * h;
+}
+
+// The operand stages' addressing, shared by both matrix forms.
+template <class C, bool NN>
+struct Loader {
+  const GemmMx &p;
+  int64_t n0, m0;
+  int nk;
+  int wave, lane;
+  int voffp, voffq, tailp, tailq;                    // lane byte offsets; the tail step's
+  const uint8_t *gp, *gq;
+  const uint8_t *sbase;                              // scales: the wave's 64-row group ...
+  int soff, xstep, xlane, xmax, xmul, tshift;        // ... and the lane's address in it
+  uint32_t psel;
+
+  __device__ __forceinline__ Loader(const GemmMx &p_, int64_t n0_, int64_t m0_) : p(p_), n0(n0_), m0(m0_) {
+    const int t = threadIdx.x;
+    lane = t & 63;
+    wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    nk = (int)((p.k + kRowB - 1) / kRowB);
+    const int kt = (int)(p.k - (int64_t)(nk - 1) * kRowB);    // k of the last step (a multiple of 32)
+    const int row = 8 * wave + (lane >> 3), chunk = (lane & 7) ^ swz(row);
+    voffq = row * (int)p.k + chunk * 16;
+    tailq = chunk * 16 < kt ? voffq : INT32_MAX - 15;
+    gq = p.a + m0 * p.k;
+    if (NN) {
+      // stage rows are k, 256-byte rows of TN columns; chunk c of row k at c ^ (k & 7)
+      constexpr int CPR = C::TN / 16, RPI = 64 / CPR;
+      const int kr = RPI * wave + lane / CPR, c = (lane % CPR) ^ (kr & 7);
+      voffp = n0 + c * 16 < p.n ? kr * (int)p.n + c * 16 : INT32_MAX - 15;
+      tailp = voffp;                                  // k rows past K are past the resource
+      gp = p.b + n0;
+    } else {
+      voffp = voffq;
+      tailp = tailq;
+      gp = p.b + n0 * p.k;
+    }
+    // Scales: wave = 64-row group, n side first.  A lane reads one row's 4 bytes of a step
+    // at sbase + soff + min(step * xstep + xlane, xmax) * xmul.  Rows past the end repeat
+    // the last one: their codes are zeros and their results unused.
+    const bool ps = wave < C::TN / 64;
+    const int layout = ps ? p.lb : p.la, KB = (int)(p.k >> 5);
+    const int64_t r0 = ps ? n0 + 64 * wave : m0 + 64 * (wave - C::TN / 64);
+    // the group's first row, or the last row's block of 32 where the group is past the end
+    const int64_t rl = (ps ? p.n : p.m) - 1, rb = min(r0, rl & ~(int64_t)31);
+    const int rr = (int)min<int64_t>(lane, rl - rb);
+    sbase = ps ? p.bs : p.as;
+    xmul = 1;
+    xlane = 0;
+    tshift = 0;
+    psel = 0;
+    if (NN && ps) {
+      // the group's 64 columns are two blocks: lane 16 g + r reads 4 neighbouring columns'
+      // blocks in block row 4 step + g and keeps its two
+      const int NB = (int)(p.n >> 5), nb = min((int)(n0 >> 5) + 2 * wave, NB - 1), first = min(nb, NB - 4);
+      sbase += first;
+      soff = 0;
+      xstep = 4;
+      xlane = lane >> 4;
+      xmax = KB - 1;
+      xmul = NB;
+      psel = (uint32_t)(nb - first) * 0x0101u + (uint32_t)min(nb - first + 1, 3) * 0x01010000u;
+    } else if (layout == SSHDP_SCALE_TILE32X4) {
+      sbase += (rb >> 5) * (KB >> 2) * 128;
+      soff = (rr >> 5) * (KB >> 2) * 128 + (rr & 31) * 4;
+      xstep = 128;
+      xmax = ((KB >> 2) - 1) * 128;
+    } else {
+      const int sh = layout == SSHDP_SCALE_ROWMAJOR ? 0 : 5;
+      sbase += (rb >> sh) * KB;
+      soff = (rr >> sh) * KB;
+      xstep = 4;
+      xmax = KB - 4;
+      tshift = 8;
+    }
+  }
+
+  // stages: n side 0, n side 1, m side 0, m side 1 (so a stage is an immediate offset of its LDS reads)
+  __device__ __forceinline__ void load(char *smem, int stage, int kt) const {
+    const bool last = kt == nk - 1;
+    const int vp = last ? tailp : voffp, vq = last ? tailq : voffq;
+    char *sp = smem + stage * C::SEGP + wave * 1024, *sq = smem + 2 * C::SEGP + stage * C::SEGQ + wave * 1024;
+    const int64_t k0 = (int64_t)kt * kRowB;
+    if (NN) {
+      constexpr int RPI = 64 / (C::TN / 16);
+      const int64_t left = (p.k - k0 < kRowB ? p.k - k0 : (int64_t)kRowB) * p.n - n0;
+      const __amdgpu_buffer_rsrc_t r =
+          __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(gp + k0 * p.n), 0, (int)left, kBufWord3);
+#pragma unroll
+      for (int i = 0; i < C::NIP; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(sp + i * C::NW * 1024), 16,
+                                                 vp, i * RPI * C::NW * (int)p.n, 0, 0);
+    } else {
+      const int64_t rows = p.n - n0 < C::TN ? p.n - n0 : (int64_t)C::TN;
+      const __amdgpu_buffer_rsrc_t r =
+          __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(gp), 0, (int)(rows * p.k), kBufWord3);
+#pragma unroll
+      for (int i = 0; i < C::NIP; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(sp + i * C::NW * 1024), 16,
+                                                 vp, i * 8 * C::NW * (int)p.k + (int)k0, 0, 0);
+    }
+    const int64_t rows = p.m - m0 < C::TM ? p.m - m0 : (int64_t)C::TM;
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(gq), 0, (int)(rows * p.k), kBufWord3);
+#pragma unroll
+    for (int i = 0; i < C::NIQ; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(sq + i * C::NW * 1024), 16, vq,
+                                               i * 8 * C::NW * (int)p.k + (int)k0, 0, 0);
+  }
+
+  // The words of this wave's 64 scale rows for steps 4 q .. 4 q + 3, as they lie in
+  // memory.  No branches: control flow here would let the compiler move matrix
+  // instructions of one phase past the next one's barrier.
+  __device__ __forceinline__ u32x4_t scales(int q) const {
+    u32x4_t w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int x = (4 * q + j) * xstep + xlane;
+      uint32_t v;
+      __builtin_memcpy(&v, sbase + (uint32_t)(soff + min(x, xmax) * xmul), 4);   // any alignment
+      w[j] = v;
+    }
+    return w;
+  }
+  // One step's word for the matrix instruction: lane 16 g + r gets block g's bytes of the
+  // rows r, 16 + r, 32 + r, 48 + r.
+  __device__ __forceinline__ uint32_t scale_word(uint32_t x, int step) const {
+    // the last word of a row whose blocks are no multiple of 4 was read from its last 4
+    // bytes; what the shift brings in scales codes that are all zero
+    const uint32_t t = lane_transpose(x >> min(max(step * xstep - xmax, 0) * tshift, 24), lane);
+    return NN && wave < C::TN / 64 ? __builtin_amdgcn_perm(x, x, psel) : t;
+  }
+};
+
+template <class C, bool NN>
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_gemm_mx8(GemmMx p, int64_t tiles_m,
+                                                                                             int64_t tiles_n) {
+  __shared__ __align__(1024) char smem[C::LDS];
+  int64_t tm, tn;
+  tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int64_t n0 = tn * C::TN, m0 = tm * C::TM;
+  const Loader<C, NN> ld(p, n0, m0);
+  const int lane = ld.lane, wave = ld.wave, wn = wave / C::WM, wm = wave % C::WM;
+  const int r = lane & 15, g = lane >> 4;
+  uint32_t *ring = reinterpret_cast<uint32_t *>(smem + 2 * C::STAGE);
+  constexpr int FP = C::FP, FQ = C::FQ, HP = FP / 2, HQ = FQ / 2;
+
+  // fragment addresses: row 16 i + r of the wave's panel, chunks g and 4 + g
+  const int cof = (g ^ swz(r)) * 16;
+  const int rowp = (wn * (C::TN / C::WN) + r) * kRowB + cof, rowq = 2 * C::SEGP + (wm * (C::TM / C::WM) + r) * kRowB + cof;
+  // NN: fragment i's 16 columns are one chunk of each k row; a transposing read hands
+  // a lane one column's 8 k (rows kb .. kb + 7), read 16 bytes a row by lane pairs
+  const int trp = (16 * g + (r >> 1)) * C::TN + ((r >> 1) << 4) + 8 * (r & 1) + wn * (C::TN / C::WN);
+
+  f32x4_t acc[FP][FQ];
+#pragma unroll
+  for (int i = 0; i < FP; ++i)
+#pragma unroll
+    for (int j = 0; j < FQ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  auto ldp = [&](int stage, int i) __attribute__((always_inline)) {
+    i32x8_t v;
+    const char *st = smem + stage * C::SEGP;
+    if (NN) {
+      typedef int i32x2_t __attribute__((ext_vector_type(2)));
+      typedef __attribute__((address_space(3))) i32x2_t lds_i32x2_t;
+      const char *a = st + (trp ^ (i << 4));
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const i32x2_t w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2_t *)(a + ((h >> 1) * 64 + (h & 1) * 8) * C::TN));
+        v[2 * h] = w[0];
+        v[2 * h + 1] = w[1];
+      }
+    } else {
+      const u32x4_t x = *reinterpret_cast<const u32x4_t *>(st + rowp + i * 16 * kRowB);
+      const u32x4_t y = *reinterpret_cast<const u32x4_t *>(st + (rowp ^ 64) + i * 16 * kRowB);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = (int)x[k], v[4 + k] = (int)y[k];
+    }
+    return v;
+  };
+  auto ldq = [&](int stage, int j) __attribute__((always_inline)) {
+    i32x8_t v;
+    const char *st = smem + stage * C::SEGQ + j * 16 * kRowB;
+    const u32x4_t x = *reinterpret_cast<const u32x4_t *>(st + rowq);
+    const u32x4_t y = *reinterpret_cast<const u32x4_t *>(st + (rowq ^ 64));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = (int)x[k], v[4 + k] = (int)y[k];
+    return v;
+  };
+  auto lds_scale = [&](int kt, int grp) __attribute__((always_inline)) {
+    return (int)ring[((kt & 7) * C::GRPS + grp) * 64 + lane];
+  };
+  const int gp = wn * (FP / 4), gq = C::TN / 64 + wm;
+
+  // Fragments in registers: P holds half of the n side, its slots reloaded with the other
+  // half right after their last use; Q0 or Q2 (by turns) and Q1 the m side's two pairs.
+  i32x8_t P[HP], Q0[HQ], Q1[HQ], Q2[HQ];
+  int sp[2][FP / 4], sq[2];
+  auto put_scales = [&](const u32x4_t &w, int q) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      ring[((4 * (q & 1) + j) * C::GRPS + wave) * 64 + lane] = ld.scale_word(w[j], 4 * q + j);
+  };
+
+  const int nk = ld.nk;
+  u32x4_t sw = ld.scales(0);
+  ld.load(smem, 0, 0);
+  put_scales(sw, 0);
+  ld.load(smem, 1, nk > 1 ? 1 : 0);
+  sw = ld.scales(1);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(0) : "memory");
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < HP; ++i) P[i] = ldp(0, i);
+#pragma unroll
+  for (int j = 0; j < HQ; ++j) Q0[j] = ldq(0, j);
+#pragma unroll
+  for (int i = 0; i < FP / 4; ++i) sp[0][i] = lds_scale(0, gp + i);
+  sq[0] = lds_scale(0, gq);
+
+  constexpr int RP = NN ? 4 : 2;                      // LDS reads of an n-side fragment
+  // A quarter of a step: HP x HQ matrix instructions with n-side fragments i0 .. and
+  // m-side fragments j0 ...  After a fragment's last use `reload` fills its slot; `nr`
+  // other LDS reads are spread between the instructions.
+  auto mma = [&](int i0, i32x8_t(&Q)[HQ], int j0, const int (&s)[FP / 4], int t, int nr, bool roll, auto reload)
+                 __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < HP; ++i) {
+#pragma unroll
+      for (int j = 0; j < HQ; ++j)
+        acc[i0 + i][j0 + j] = mx_mma_pq((i0 + i) & 3, j0 + j, P[i], Q[j], acc[i0 + i][j0 + j], s[(i0 + i) >> 2], t);
+      if (roll) P[i] = reload(i);
+    }
+#pragma unroll
+    for (int i = 0; i < HP * HQ; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (i < nr) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (roll && i % HQ == HQ - 1) __builtin_amdgcn_sched_group_barrier(0x100, RP, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto none = [](int) { return i32x8_t{}; };
+  // One step: the m side's first pair is in QX, its second goes to Q1, the next step's
+  // first to QZ.
+  auto step = [&](int kt, int q, int phase, i32x8_t(&QX)[HQ], i32x8_t(&QZ)[HQ], const int (&s)[FP / 4], int t,
+                  int (&sn)[FP / 4], int &tn_) __attribute__((always_inline)) {
+    const int stage = phase & 1;
+#pragma unroll
+    for (int j = 0; j < HQ; ++j) Q1[j] = ldq(stage, HQ + j);
+    mma(0, QX, 0, s, t, 2 * HQ, false, none);
+    mma(0, Q1, HQ, s, t, 0, true, [&](int i) __attribute__((always_inline)) { return ldp(stage, HP + i); });
+    // every wave has read this step's stage, and the next one has landed
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __syncthreads();
+    // near the end the reload repeats the last step into a stage nobody reads again
+    ld.load(smem, stage, kt + 2 < nk ? kt + 2 : nk - 1);
+    if (phase == 2) put_scales(sw, q + 1);
+    if (phase == 3) sw = ld.scales(q + 2);
+#pragma unroll
+    for (int j = 0; j < HQ; ++j) QZ[j] = ldq(stage ^ 1, j);
+#pragma unroll
+    for (int i = 0; i < FP / 4; ++i) sn[i] = lds_scale(kt + 1, gp + i);
+    tn_ = lds_scale(kt + 1, gq);
+    mma(HP, Q1, HQ, s, t, 2 * HQ + FP / 4 + 1, false, none);
+    mma(HP, QX, 0, s, t, 0, true, [&](int i) __attribute__((always_inline)) { return ldp(stage ^ 1, i); });
+  };
+  for (int kt = 0, q = 0;; kt += 4, ++q) {
+    step(kt, q, 0, Q0, Q2, sp[0], sq[0], sp[1], sq[1]);
+    if (kt + 1 >= nk) break;
+    step(kt + 1, q, 1, Q2, Q0, sp[1], sq[1], sp[0], sq[0]);
+    if (kt + 2 >= nk) break;
+    step(kt + 2, q, 2, Q0, Q2, sp[0], sq[0], sp[1], sq[1]);
+    if (kt + 3 >= nk) break;
+    step(kt + 3, q, 3, Q2, Q0, sp[1], sq[1], sp[0], sq[0]);
+    if (kt + 4 >= nk) break;
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // the trailing reloads
+  __syncthreads();
+
+  // bfloat16 tile through LDS (rows m), then whole rows of 16-byte stores
+  uint16_t *lt = reinterpret_cast<uint16_t *>(smem);
+  constexpr int LP = C::TN + 8;
+#pragma unroll
+  for (int i = 0; i < FP; ++i)
+#pragma unroll
+    for (int j = 0; j < FQ; ++j) {
+      const f32x4_t &v = acc[i][j];
+      uint2 *d = reinterpret_cast<uint2 *>(lt + (wm * (C::TM / C::WM) + 16 * j + r) * LP + wn * (C::TN / C::WN) + 16 * i + 4 * g);
+      *d = make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
+    }
+  __syncthreads();
+  uint16_t *out = static_cast<uint16_t *>(p.out);
+  constexpr int CH = C::TN / 8;
+  for (int id = threadIdx.x; id < C::TM * CH; id += C::NT) {
+    const int row = id / CH, c = (id - row * CH) * 8;
+    const int64_t m = m0 + row, n = n0 + c;
+    if (m >= p.m || n >= p.n) continue;
+    const u32x4_t v = *reinterpret_cast<const u32x4_t *>(lt + row * LP + c);
+    uint16_t *o = out + m * p.ld + n;
+    if (n + 8 <= p.n && p.ld % 8 == 0) {
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t *>(o));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (n + k < p.n) o[k] = (uint16_t)(v[k >> 1] >> (16 * (k & 1)));
+    }
+  }
+}
+
+using T256 = Tile<256, 256, 2, 4>;
+
+template <class C, bool NN>
+hipError_t gemm8(const GemmMx &g, hipStream_t s) {
+  const int64_t tm = (g.m + C::TM - 1) / C::TM, tn = (g.n + C::TN - 1) / C::TN;
+  hipLaunchKernelGGL((k_gemm_mx8<C, NN>), dim3((unsigned)(tm * tn)), dim3(C::NT), 0, s, g, tm, tn);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 int64_t gemm_mx_workspace(int64_t, int64_t, int64_t, bool) { return 0; }
 
 hipError_t launch_gemm_mx(const GemmMx &g, void *, hipStream_t s) {
+  if (g.bf16 && g.k >= 128 && g.m >= 128 && g.n >= 128) return g.nn ? gemm8<T256, true>(g, s) : gemm8<T256, false>(g, s);
   const int64_t tm = (g.m + 15) / 16, tn = (g.n + 15) / 16;
   const dim3 grid((unsigned)(tm * tn)), block(64);
   if (g.nn && g.bf16) hipLaunchKernelGGL((k_gemm_mx_16<true, true>), grid, block, 0, s, g, tn);
