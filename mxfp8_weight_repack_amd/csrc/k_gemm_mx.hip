@@ -51,13 +51,17 @@ __device__ __forceinline__ int64_t scale_index(int layout, int64_t r, int64_t kb
 
 // 8 codes (two words) times 2^(byte - 127), as bfloat16, exact.  The conversion reads
 // the scale's exponent bits, so byte << 23 is E8M0 from 2^-127 (0) to NaN (255).
-__device__ __forceinline__ bf16x8_t to_bf16(int w0, int w1, uint32_t byte) {
+__device__ __forceinline__ u32x4_t to_bf16(int w0, int w1, uint32_t byte) {
   const float s = __uint_as_float(byte << 23);
   bf16x2_t v[4] = {__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, false),
                    __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, true),
                    __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, false),
                    __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, true)};
-  return __builtin_bit_cast(bf16x8_t, v);
+  return __builtin_bit_cast(u32x4_t, v);
+}
+
+__device__ __forceinline__ f32x4_t mma_bf16(const u32x4_t &p, const u32x4_t &q, const f32x4_t &c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, p), __builtin_bit_cast(bf16x8_t, q), c, 0, 0, 0);
 }
 
 // One wave, one 16 x 16 block of the output, operands straight from memory.
@@ -105,8 +109,7 @@ __global__ __launch_bounds__(64) void k_gemm_mx_16(GemmMx p, int64_t tiles_n) {
         const int sa = scale_a(kb + 2 * h + (g >> 1)), sb = scale_b(kb + 2 * h + (g >> 1));
 #pragma unroll
         for (int j = 4 * h; j < 4 * h + 4; j += 2)
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(to_bf16(b[j], b[j + 1], sb), to_bf16(a[j], a[j + 1], sa), acc,
-                                                        0, 0, 0);
+          acc = mma_bf16(to_bf16(b[j], b[j + 1], sb), to_bf16(a[j], a[j + 1], sa), acc);
       }
     }
   }
@@ -202,6 +205,11 @@ __device__ __forceinline__ void tile_of(int64_t id, int64_t tiles_m, int64_t til
   tm = strip * 8 + in - tn * h;
 }
 
+// 16 bytes per lane from memory straight to LDS, lane i at dst + 16 i.
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, char *dst, int voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 16, voff, soff, 0, 0);
+}
+
 // The operand stages' addressing, shared by both matrix forms.
 template <class C, bool NN>
 struct Loader {
@@ -290,24 +298,24 @@ struct Loader {
           __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(gp + k0 * p.n), 0, (int)left, kBufWord3);
 #pragma unroll
       for (int i = 0; i < C::NIP; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(sp + i * C::NW * 1024), 16,
-                                                 vp, i * RPI * C::NW * (int)p.n, 0, 0);
+        dma16(r, sp + i * C::NW * 1024,
+                                                 vp, i * RPI * C::NW * (int)p.n);
     } else {
       const int64_t rows = p.n - n0 < C::TN ? p.n - n0 : (int64_t)C::TN;
       const __amdgpu_buffer_rsrc_t r =
           __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(gp), 0, (int)(rows * p.k), kBufWord3);
 #pragma unroll
       for (int i = 0; i < C::NIP; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(sp + i * C::NW * 1024), 16,
-                                                 vp, i * 8 * C::NW * (int)p.k + (int)k0, 0, 0);
+        dma16(r, sp + i * C::NW * 1024,
+                                                 vp, i * 8 * C::NW * (int)p.k + (int)k0);
     }
     const int64_t rows = p.m - m0 < C::TM ? p.m - m0 : (int64_t)C::TM;
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(gq), 0, (int)(rows * p.k), kBufWord3);
 #pragma unroll
     for (int i = 0; i < C::NIQ; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)(sq + i * C::NW * 1024), 16, vq,
-                                               i * 8 * C::NW * (int)p.k + (int)k0, 0, 0);
+      dma16(r, sq + i * C::NW * 1024, vq,
+                                               i * 8 * C::NW * (int)p.k + (int)k0);
   }
 
   // The words of this wave's 64 scale rows for steps 4 q .. 4 q + 3, as they lie in
@@ -510,12 +518,183 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
   }
 }
 
+// Four consecutive n of one row m: float32 result, the addend joined in.  `vec`: rows
+// are 16-byte multiples, so four in range go out together.
+__device__ __forceinline__ void store_f32(const GemmMx &p, float *out, int64_t m, int64_t n, f32x4_t v, bool vec) {
+  if (m >= p.m || n >= p.n) return;
+  const int64_t e = m * p.ld + n;
+  if (vec && n + 4 <= p.n) {
+    if (p.addend) v += *reinterpret_cast<const f32x4_t *>(p.addend + e);
+    *reinterpret_cast<f32x4_t *>(out + e) = v;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (n + k < p.n) out[e + k] = p.addend ? v[k] + p.addend[e + k] : v[k];
+  }
+}
+
+// Float32 output: the same tiles, stages and scale words, with operands converted to
+// bfloat16 on their way from LDS to the matrix instructions.  A half step is one 16-byte
+// chunk per lane (64 k): its m-side fragments stay converted while the n side's pass by,
+// one converted (8 conversions) beside the previous one's 2 x FQ matrix instructions.
+template <class C, bool NN>
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_gemm_mx16(GemmMx p, int64_t tiles_m,
+                                                                                              int64_t tiles_n) {
+  __shared__ __align__(1024) char smem[C::LDS];
+  int64_t tm, tn;
+  tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int64_t n0 = tn * C::TN, m0 = tm * C::TM;
+  const Loader<C, NN> ld(p, n0, m0);
+  const int lane = ld.lane, wave = ld.wave, wn = wave / C::WM, wm = wave % C::WM;
+  const int r = lane & 15, g = lane >> 4;
+  uint32_t *ring = reinterpret_cast<uint32_t *>(smem + 2 * C::STAGE);
+  constexpr int FP = C::FP, FQ = C::FQ;
+  const int cof = (g ^ swz(r)) * 16;
+  const int rowp = (wn * (C::TN / C::WN) + r) * kRowB + cof, rowq = 2 * C::SEGP + (wm * (C::TM / C::WM) + r) * kRowB + cof;
+  const int trp = (16 * g + (r >> 1)) * C::TN + ((r >> 1) << 4) + 8 * (r & 1) + wn * (C::TN / C::WN);
+
+  f32x4_t acc[FP][FQ];
+#pragma unroll
+  for (int i = 0; i < FP; ++i)
+#pragma unroll
+    for (int j = 0; j < FQ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  auto ldp = [&](int stage, int h, int i) __attribute__((always_inline)) {
+    const char *st = smem + stage * C::SEGP;
+    if (NN) {
+      typedef int i32x2_t __attribute__((ext_vector_type(2)));
+      typedef __attribute__((address_space(3))) i32x2_t lds_i32x2_t;
+      const char *a = st + (trp ^ (i << 4)) + h * 64 * C::TN;
+      const i32x2_t x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2_t *)a);
+      const i32x2_t y = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2_t *)(a + 8 * C::TN));
+      return u32x4_t{(uint32_t)x[0], (uint32_t)x[1], (uint32_t)y[0], (uint32_t)y[1]};
+    }
+    return *reinterpret_cast<const u32x4_t *>(st + (rowp ^ (h << 6)) + i * 16 * kRowB);
+  };
+  auto ldq = [&](int stage, int h, int j) __attribute__((always_inline)) {
+    return *reinterpret_cast<const u32x4_t *>(smem + stage * C::SEGQ + (rowq ^ (h << 6)) + j * 16 * kRowB);
+  };
+  // half h of lane (r, g) lies in block 2 h + g / 2
+  const int sl = ((g >> 1) << 4) + r;
+  auto lds_scale = [&](int kt, int h, int grp) __attribute__((always_inline)) {
+    return ring[((kt & 7) * C::GRPS + grp) * 64 + 32 * h + sl];
+  };
+  auto convert = [&](const u32x4_t &x, uint32_t word, int byte, u32x4_t(&out)[2]) __attribute__((always_inline)) {
+    const uint32_t e = (word >> (8 * byte)) & 0xFFu;
+    out[0] = to_bf16((int)x[0], (int)x[1], e);
+    out[1] = to_bf16((int)x[2], (int)x[3], e);
+  };
+  const int gp = wn * (FP / 4), gq = C::TN / 64 + wm;
+  auto put_scales = [&](const u32x4_t &w, int q) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      ring[((4 * (q & 1) + j) * C::GRPS + wave) * 64 + lane] = ld.scale_word(w[j], 4 * q + j);
+  };
+
+  const int nk = ld.nk;
+  u32x4_t sw = ld.scales(0);
+  ld.load(smem, 0, 0);
+  put_scales(sw, 0);
+  ld.load(smem, 1, nk > 1 ? 1 : 0);
+  sw = ld.scales(1);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+
+  u32x4_t P[2], Q[FQ];                                // raw: the next two n-side fragments, the next half's m side
+  u32x4_t pc[2][2], qc[FQ][2];                       // converted: this and the next n-side fragment, the m side
+  uint32_t sp[2][FP / 4], sq[2];                      // scale words of this half and the next
+#pragma unroll
+  for (int i = 0; i < FP / 4; ++i) sp[0][i] = lds_scale(0, 0, gp + i);
+  sq[0] = lds_scale(0, 0, gq);
+#pragma unroll
+  for (int j = 0; j < FQ; ++j) Q[j] = ldq(0, 0, j);
+  P[0] = ldp(0, 0, 0);
+  P[1] = ldp(0, 0, 1);
+#pragma unroll
+  for (int j = 0; j < FQ; ++j) convert(Q[j], sq[0], j, qc[j]);
+  convert(P[0], sp[0][0], 0, pc[0]);
+
+  // Half a step.  Two fragments ahead are read, one ahead is converted; with the last
+  // two of the second half, which read the next stage, comes the step's barrier.
+  auto half = [&](int kt, int q, int phase, int h) __attribute__((always_inline)) {
+    const int stage = phase & 1, ns = h ? stage ^ 1 : stage, nh = h ^ 1, nkt = kt + h;
+    auto one = [&](int i) __attribute__((always_inline)) {
+      // fragment i + 1's conversion, then its slot takes fragment i + 3
+      if (i == FP - 2) {
+        if (h) {
+          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+          __syncthreads();                            // this stage is read, the next has landed
+          ld.load(smem, stage, kt + 2 < nk ? kt + 2 : nk - 1);
+          if (phase == 2) put_scales(sw, q + 1);
+          if (phase == 3) sw = ld.scales(q + 2);
+        }
+#pragma unroll
+        for (int k = 0; k < FP / 4; ++k) sp[nh][k] = lds_scale(nkt, nh, gp + k);
+        sq[nh] = lds_scale(nkt, nh, gq);
+#pragma unroll
+        for (int j = 0; j < FQ; ++j) Q[j] = ldq(ns, nh, j);
+      }
+      P[i & 1] = i + 2 < FP ? ldp(stage, h, i + 2) : ldp(ns, nh, i + 2 - FP);
+      if (i + 1 < FP) convert(P[(i + 1) & 1], sp[h][(i + 1) >> 2], (i + 1) & 3, pc[(i + 1) & 1]);
+      else convert(P[0], sp[nh][0], 0, pc[0]);
+#pragma unroll
+      for (int j = 0; j < FQ; ++j) {
+        acc[i][j] = mma_bf16(pc[i & 1][0], qc[j][0], acc[i][j]);
+        acc[i][j] = mma_bf16(pc[i & 1][1], qc[j][1], acc[i][j]);
+        if (i == FP - 1) convert(Q[j], sq[nh], j, qc[j]);
+      }
+      if (i == FP - 1) {
+#pragma unroll
+        for (int k = 0; k < 2 * FQ; ++k) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
+        }
+      } else {
+        __builtin_amdgcn_sched_group_barrier(0x100, NN ? 2 : 1, 0);
+#pragma unroll
+        for (int k = 0; k < 2 * FQ; ++k) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);
+          if (k & 1) __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);
+          if (i == FP - 2) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+#pragma unroll
+    for (int i = 0; i < FP; ++i) one(i);
+  };
+  for (int kt = 0, q = 0;; kt += 4, ++q) {
+    half(kt, q, 0, 0);
+    half(kt, q, 0, 1);
+    if (kt + 1 >= nk) break;
+    half(kt + 1, q, 1, 0);
+    half(kt + 1, q, 1, 1);
+    if (kt + 2 >= nk) break;
+    half(kt + 2, q, 2, 0);
+    half(kt + 2, q, 2, 1);
+    if (kt + 3 >= nk) break;
+    half(kt + 3, q, 3, 0);
+    half(kt + 3, q, 3, 1);
+    if (kt + 4 >= nk) break;
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // the trailing reloads
+  float *out = static_cast<float *>(p.out);
+  const bool vec = p.ld % 4 == 0;
+#pragma unroll
+  for (int j = 0; j < FQ; ++j)
+#pragma unroll
+    for (int i = 0; i < FP; ++i)
+      store_f32(p, out, m0 + wm * (C::TM / C::WM) + 16 * j + r, n0 + wn * (C::TN / C::WN) + 16 * i + 4 * g, acc[i][j], vec);
+}
+
 using T256 = Tile<256, 256, 2, 4>;
 
 template <class C, bool NN>
-hipError_t gemm8(const GemmMx &g, hipStream_t s) {
+hipError_t gemm_tiled(const GemmMx &g, hipStream_t s) {
   const int64_t tm = (g.m + C::TM - 1) / C::TM, tn = (g.n + C::TN - 1) / C::TN;
-  hipLaunchKernelGGL((k_gemm_mx8<C, NN>), dim3((unsigned)(tm * tn)), dim3(C::NT), 0, s, g, tm, tn);
+  if (g.bf16) hipLaunchKernelGGL((k_gemm_mx8<C, NN>), dim3((unsigned)(tm * tn)), dim3(C::NT), 0, s, g, tm, tn);
+  else hipLaunchKernelGGL((k_gemm_mx16<C, NN>), dim3((unsigned)(tm * tn)), dim3(C::NT), 0, s, g, tm, tn);
   return hipGetLastError();
 }
 
@@ -524,7 +703,7 @@ hipError_t gemm8(const GemmMx &g, hipStream_t s) {
 int64_t gemm_mx_workspace(int64_t, int64_t, int64_t, bool) { return 0; }
 
 hipError_t launch_gemm_mx(const GemmMx &g, void *, hipStream_t s) {
-  if (g.bf16 && g.k >= 128 && g.m >= 128 && g.n >= 128) return g.nn ? gemm8<T256, true>(g, s) : gemm8<T256, false>(g, s);
+  if (g.k >= 128 && g.m >= 128 && g.n >= 128) return g.nn ? gemm_tiled<T256, true>(g, s) : gemm_tiled<T256, false>(g, s);
   const int64_t tm = (g.m + 15) / 16, tn = (g.n + 15) / 16;
   const dim3 grid((unsigned)(tm * tn)), block(64);
   if (g.nn && g.bf16) hipLaunchKernelGGL((k_gemm_mx_16<true, true>), grid, block, 0, s, g, tn);
