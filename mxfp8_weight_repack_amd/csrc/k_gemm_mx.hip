@@ -25,6 +25,8 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cstdlib>
+#include <cstdio>
 
 #include "internal.h"
 
@@ -42,13 +44,6 @@ __device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
 }
 
-// Index of the scale byte of row `r`'s block kb in a matrix with KB blocks a row.
-__device__ __forceinline__ int64_t scale_index(int layout, int64_t r, int64_t kb, int64_t KB) {
-  if (layout == SSHDP_SCALE_ROWMAJOR) return r * KB + kb;
-  if (layout == SSHDP_SCALE_TILE32X4) return ((r >> 5) * (KB >> 2) + (kb >> 2)) * 128 + (r & 31) * 4 + (kb & 3);
-  return (r >> 5) * KB + kb;
-}
-
 // 8 codes (two words) times 2^(byte - 127), as bfloat16, exact.  The conversion reads
 // the scale's exponent bits, so byte << 23 is E8M0 from 2^-127 (0) to NaN (255).
 __device__ __forceinline__ u32x4_t to_bf16(int w0, int w1, uint32_t byte) {
@@ -64,67 +59,176 @@ __device__ __forceinline__ f32x4_t mma_bf16(const u32x4_t &p, const u32x4_t &q, 
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, p), __builtin_bit_cast(bf16x8_t, q), c, 0, 0, 0);
 }
 
-// One wave, one 16 x 16 block of the output, operands straight from memory.
-template <bool NN, bool BF16>
-__global__ __launch_bounds__(64) void k_gemm_mx_16(GemmMx p, int64_t tiles_n) {
-  const int l = threadIdx.x, r = l & 15, g = l >> 4;
-  const int64_t m = blockIdx.x / tiles_n * 16 + r, n = blockIdx.x % tiles_n * 16 + r;
-  const bool in_m = m < p.m, in_n = n < p.n;
-  const int64_t KB = p.k >> 5;
-  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t k0 = 0; k0 < p.k; k0 += 128) {
-    i32x8_t a = {0, 0, 0, 0, 0, 0, 0, 0}, b = a;
+// Four consecutive n of one row m: float32 result, the addend joined in.  `vec`: rows
+// are 16-byte multiples, so four in range go out together.
+__device__ __forceinline__ void store_f32(const GemmMx &p, float *out, int64_t m, int64_t n, f32x4_t v, bool vec) {
+  if (m >= p.m || n >= p.n) return;
+  const int64_t e = m * p.ld + n;
+  if (vec && n + 4 <= p.n) {
+    if (p.addend) v += *reinterpret_cast<const f32x4_t *>(p.addend + e);
+    *reinterpret_cast<f32x4_t *>(out + e) = v;
+  } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t k = k0 + 64 * h + 16 * g;          // K % 32 == 0: a chunk is in or out as a whole
-      if (k < p.k && in_m) {
-        const u32x4_t v = *reinterpret_cast<const u32x4_t *>(p.a + m * p.k + k);
+    for (int k = 0; k < 4; ++k)
+      if (n + k < p.n) out[e + k] = p.addend ? v[k] + p.addend[e + k] : v[k];
+  }
+}
+
+__device__ __forceinline__ void store_bf16(const GemmMx &p, int64_t m, int64_t n, const f32x4_t &v, bool vec) {
+  if (m >= p.m || n >= p.n) return;
+  uint16_t *o = static_cast<uint16_t *>(p.out) + m * p.ld + n;
+  const uint32_t x = pk_bf16(v[0], v[1]), y = pk_bf16(v[2], v[3]);
+  if (vec && n + 4 <= p.n) {
+    *reinterpret_cast<uint2 *>(o) = make_uint2(x, y);
+  } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) a[4 * h + j] = (int)v[j];
-      }
-      if (k < p.k && in_n) {
-        if (NN) {
+    for (int k = 0; k < 4; ++k)
+      if (n + k < p.n) o[k] = (uint16_t)((k < 2 ? x : y) >> (16 * (k & 1)));
+  }
+}
+
+// ------------------------------------------------------------------- few-row products
+
+// out of p.m rows for a few m (one token to a small batch), and whatever the tiles below do
+// not take: bound by reading B once.  A workgroup's W waves share 16 * NF columns n and
+// split K among them, one 128-k step in W each, so together they read runs of W * 128
+// bytes of B's rows; codes go straight from memory to the matrix instructions, UN steps'
+// loads in flight per wave.  MT * 16 rows of m at a time (grid.y); rows past the end
+// repeat the last one.  The waves' sums meet in LDS and are added in wave order.
+template <bool NN, bool BF16, int W, int NF, int MT, int UN, int ROT>
+__global__ __launch_bounds__(64 * W) void k_gemm_mx_rows(GemmMx p) {
+  __shared__ __align__(16) f32x4_t part[W][NF * MT][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int64_t nb = (int64_t)blockIdx.x * 16 * NF, mb = (int64_t)blockIdx.y * 16 * MT;
+  const int KB = (int)(p.k >> 5), nk = (int)((p.k + 127) / 128);
+  const uint8_t *pb[NF], *pa[MT], *sb[NF], *sa[MT];
+  int tb, ta;                                        // scale bytes: block kb of the row at (kb / 4) * t + kb % 4
+  auto row_scales = [](const uint8_t *s, int layout, int64_t row, int KB_, int &t) __attribute__((always_inline)) {
+    t = layout == SSHDP_SCALE_TILE32X4 ? 128 : 4;
+    if (layout == SSHDP_SCALE_TILE32X4) return s + (row >> 5) * (KB_ >> 2) * 128 + (row & 31) * 4;
+    return s + (layout == SSHDP_SCALE_ROWMAJOR ? row : row >> 5) * KB_;
+  };
+  int64_t nr[NF];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) b[4 * h + (j >> 2)] |= (int)p.b[(k + j) * p.n + n] << (8 * (j & 3));
-        } else {
-          const u32x4_t v = *reinterpret_cast<const u32x4_t *>(p.b + n * p.k + k);
+  for (int i = 0; i < NF; ++i) {
+    nr[i] = min(nb + 16 * i + r, p.n - 1);
+    pb[i] = NN ? p.b + nr[i] : p.b + nr[i] * p.k;
+    sb[i] = NN ? p.bs + (nr[i] >> 5) : row_scales(p.bs, p.lb, nr[i], KB, tb);
+  }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) b[4 * h + j] = (int)v[j];
-        }
-      }
-    }
-    auto scale_a = [&](int64_t kb) -> int {            // 2^-127 beside codes that are all zero
-      return kb < KB && in_m ? p.as[scale_index(p.la, m, kb, KB)] : 0;
-    };
-    auto scale_b = [&](int64_t kb) -> int {
-      if (!(kb < KB && in_n)) return 0;
-      return NN ? p.bs[kb * (p.n >> 5) + (n >> 5)] : p.bs[scale_index(p.lb, n, kb, KB)];
-    };
-    const int64_t kb = k0 >> 5;
-    if (BF16) {
-      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, acc, 0, 0, 0, scale_b(kb + g), 0, scale_a(kb + g));
-    } else {
+  for (int j = 0; j < MT; ++j) {
+    const int64_t m = min(mb + 16 * j + r, p.m - 1);
+    pa[j] = p.a + m * p.k;
+    sa[j] = row_scales(p.as, p.la, m, KB, ta);
+  }
+  f32x4_t acc[NF][MT];
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  // Steps and chunks past K load nothing and add zeros.
+  struct Step {
+    i32x8_t b[NF], a[MT];
+    uint32_t wb[NF], wa[MT];                         // 8-bit form: block g's byte; else blocks g / 2 and 2 + g / 2
+  };
+  auto fetch = [&](Step &st, int kt) __attribute__((always_inline)) {
+    auto chunks = [&](const uint8_t *q) __attribute__((always_inline)) {
+      i32x8_t v = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int sa = scale_a(kb + 2 * h + (g >> 1)), sb = scale_b(kb + 2 * h + (g >> 1));
+        const int64_t k = (int64_t)kt * 128 + 64 * h + 16 * g;
+        if (k < p.k) {
+          const u32x4_t x = *reinterpret_cast<const u32x4_t *>(q + k);
 #pragma unroll
-        for (int j = 4 * h; j < 4 * h + 4; j += 2)
-          acc = mma_bf16(to_bf16(b[j], b[j + 1], sb), to_bf16(a[j], a[j + 1], sa), acc);
+          for (int j = 0; j < 4; ++j) v[4 * h + j] = (int)x[j];
+        }
+      }
+      return v;
+    };
+    auto byte = [&](const uint8_t *s, int t, int blk) __attribute__((always_inline)) {
+      const int kb = 4 * kt + blk;
+      return kb < KB ? (uint32_t)s[(kb >> 2) * t + (kb & 3)] : 0u;
+    };
+    auto byte_nn = [&](const uint8_t *s, int blk) __attribute__((always_inline)) {
+      const int kb = 4 * kt + blk;
+      return kb < KB ? (uint32_t)s[(int64_t)kb * (p.n >> 5)] : 0u;
+    };
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+      if (NN) {
+        st.b[i] = i32x8_t{0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const int64_t k = (int64_t)kt * 128 + 64 * (c >> 4) + 16 * g + (c & 15);
+          if (k < p.k) st.b[i][c >> 2] |= (int)pb[i][k * p.n] << (8 * (c & 3));
+        }
+        st.wb[i] = BF16 ? byte_nn(sb[i], g) : byte_nn(sb[i], g >> 1) | byte_nn(sb[i], 2 + (g >> 1)) << 8;
+      } else {
+        st.b[i] = chunks(pb[i]);
+        st.wb[i] = BF16 ? byte(sb[i], tb, g) : byte(sb[i], tb, g >> 1) | byte(sb[i], tb, 2 + (g >> 1)) << 8;
       }
     }
-  }
-  // every lane takes part in the matrix instructions: none may sink below the branch
-  asm volatile("" : "+v"(acc));
-  const int64_t n0 = blockIdx.x % tiles_n * 16 + 4 * g;
-  if (!in_m) return;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (n0 + j >= p.n) break;
-    const int64_t e = m * p.ld + n0 + j;
-    float v = acc[j];
-    if (p.addend) v += p.addend[e];
-    if (BF16) static_cast<uint16_t *>(p.out)[e] = (uint16_t)pk_bf16(v, 0.f);
-    else static_cast<float *>(p.out)[e] = v;
+    for (int j = 0; j < MT; ++j) {
+      st.a[j] = chunks(pa[j]);
+      st.wa[j] = BF16 ? byte(sa[j], ta, g) : byte(sa[j], ta, g >> 1) | byte(sa[j], ta, 2 + (g >> 1)) << 8;
+    }
+  };
+  auto multiply = [&](const Step &st) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        if (BF16) {
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(st.b[i], st.a[j], acc[i][j], 0, 0, 0, (int)st.wb[i], 0,
+                                                                       (int)st.wa[j]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            acc[i][j] = mma_bf16(to_bf16(st.b[i][2 * c], st.b[i][2 * c + 1], (st.wb[i] >> (8 * (c >> 1))) & 0xFFu),
+                                 to_bf16(st.a[j][2 * c], st.a[j][2 * c + 1], (st.wa[j] >> (8 * (c >> 1))) & 0xFFu),
+                                 acc[i][j]);
+        }
+      }
+  };
+  Step st[2][UN];
+  const int rot = ROT ? (int)((blockIdx.x * ROT) % max(nk / (W * UN), 1)) * (W * UN) : 0;
+  auto at = [&](int k0) { const int x = k0 + rot; return ROT ? (x < nk ? x : x - nk) : x; };
+  (void)at;
+#pragma unroll
+  for (int u = 0; u < UN; ++u) fetch(st[0][u], wave + rot + u * W);
+  for (int k0 = wave;;) {
+#pragma unroll
+    for (int u = 0; u < UN; ++u) fetch(st[1][u], at(k0 + UN * W) + u * W);
+#pragma unroll
+    for (int u = 0; u < UN; ++u) multiply(st[0][u]);
+    k0 += UN * W;
+    if (k0 >= nk) break;
+#pragma unroll
+    for (int u = 0; u < UN; ++u) fetch(st[0][u], at(k0 + UN * W) + u * W);
+#pragma unroll
+    for (int u = 0; u < UN; ++u) multiply(st[1][u]);
+    k0 += UN * W;
+    if (k0 >= nk) break;
+  }
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) asm volatile("" : "+v"(acc[i][j]));
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) part[wave][i * MT + j][lane] = acc[i][j];
+  __syncthreads();
+  const bool vec = p.ld % 4 == 0;
+  for (int f = wave; f < NF * MT; f += W) {
+    f32x4_t v = part[0][f][lane];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += part[w][f][lane];
+    const int64_t n = nb + 16 * (f / MT) + 4 * g, m = mb + 16 * (f % MT) + r;
+    if (BF16) store_bf16(p, m, n, v, vec);
+    else store_f32(p, static_cast<float *>(p.out), m, n, v, vec);
   }
 }
 
@@ -205,6 +309,13 @@ __device__ __forceinline__ void tile_of(int64_t id, int64_t tiles_m, int64_t til
   tm = strip * 8 + in - tn * h;
 }
 
+// All of a workgroup's LDS accesses and its loads but the newest `LEFT` are done.  (The
+// barrier builtin would wait for those as well.)
+template <int LEFT>
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
+}
+
 // 16 bytes per lane from memory straight to LDS, lane i at dst + 16 i.
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, char *dst, int voff, int soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 16, voff, soff, 0, 0);
@@ -215,34 +326,37 @@ template <class C, bool NN>
 struct Loader {
   const GemmMx &p;
   int64_t n0, m0;
-  int nk;
+  int kt0, nk, last;                                 // this workgroup's steps: kt0 .. kt0 + nk - 1; the matrix's last
   int wave, lane;
-  int voffp, voffq, tailp, tailq;                    // lane byte offsets; the tail step's
+  int voffp, voffq;                                  // lane byte offsets
+  bool inp, inq;                                     // whether the lane's chunk lies inside the last step
   const uint8_t *gp, *gq;
   const uint8_t *sbase;                              // scales: the wave's 64-row group ...
   int soff, xstep, xlane, xmax, xmul, tshift;        // ... and the lane's address in it
+  bool xwords;                                       // a step's words lie apart: 4-byte loads
   uint32_t psel;
 
-  __device__ __forceinline__ Loader(const GemmMx &p_, int64_t n0_, int64_t m0_) : p(p_), n0(n0_), m0(m0_) {
+  __device__ __forceinline__ Loader(const GemmMx &p_, int64_t n0_, int64_t m0_, int kt0_, int nk_)
+      : p(p_), n0(n0_), m0(m0_), kt0(kt0_), nk(nk_) {
     const int t = threadIdx.x;
     lane = t & 63;
     wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    nk = (int)((p.k + kRowB - 1) / kRowB);
-    const int kt = (int)(p.k - (int64_t)(nk - 1) * kRowB);    // k of the last step (a multiple of 32)
+    last = (int)((p.k + kRowB - 1) / kRowB) - 1;
+    const int kt = (int)(p.k - (int64_t)last * kRowB);        // k of the last step (a multiple of 32)
     const int row = 8 * wave + (lane >> 3), chunk = (lane & 7) ^ swz(row);
     voffq = row * (int)p.k + chunk * 16;
-    tailq = chunk * 16 < kt ? voffq : INT32_MAX - 15;
+    inq = chunk * 16 < kt;
     gq = p.a + m0 * p.k;
     if (NN) {
       // stage rows are k, 256-byte rows of TN columns; chunk c of row k at c ^ (k & 7)
       constexpr int CPR = C::TN / 16, RPI = 64 / CPR;
       const int kr = RPI * wave + lane / CPR, c = (lane % CPR) ^ (kr & 7);
       voffp = n0 + c * 16 < p.n ? kr * (int)p.n + c * 16 : INT32_MAX - 15;
-      tailp = voffp;                                  // k rows past K are past the resource
+      inp = true;                                     // k rows past K are past the resource
       gp = p.b + n0;
     } else {
       voffp = voffq;
-      tailp = tailq;
+      inp = inq;
       gp = p.b + n0 * p.k;
     }
     // Scales: wave = 64-row group, n side first.  A lane reads one row's 4 bytes of a step
@@ -259,6 +373,7 @@ struct Loader {
     xlane = 0;
     tshift = 0;
     psel = 0;
+    xwords = true;
     if (NN && ps) {
       // the group's 64 columns are two blocks: lane 16 g + r reads 4 neighbouring columns'
       // blocks in block row 4 step + g and keeps its two
@@ -282,14 +397,18 @@ struct Loader {
       xstep = 4;
       xmax = KB - 4;
       tshift = 8;
+      xwords = false;
     }
   }
 
-  // stages: n side 0, n side 1, m side 0, m side 1 (so a stage is an immediate offset of its LDS reads)
-  __device__ __forceinline__ void load(char *smem, int stage, int kt) const {
-    const bool last = kt == nk - 1;
-    const int vp = last ? tailp : voffp, vq = last ? tailq : voffq;
-    char *sp = smem + stage * C::SEGP + wave * 1024, *sq = smem + 2 * C::SEGP + stage * C::SEGQ + wave * 1024;
+  // Stages: n side 0, n side 1, m side 0, m side 1 (so a stage is an immediate offset of
+  // its LDS reads).  The two sides' loads are issued apart, among matrix instructions: a
+  // wave issues in order, and the 8 of one step back to back hold up everything behind
+  // them for as long as all waves' loads take to issue.
+  __device__ __forceinline__ void load_p(char *smem, int stage, int kt) const {
+    kt += kt0;
+    const int v = kt < last || inp ? voffp : INT32_MAX - 15;
+    char *sp = smem + stage * C::SEGP + wave * 1024;
     const int64_t k0 = (int64_t)kt * kRowB;
     if (NN) {
       constexpr int RPI = 64 / (C::TN / 16);
@@ -297,59 +416,111 @@ struct Loader {
       const __amdgpu_buffer_rsrc_t r =
           __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(gp + k0 * p.n), 0, (int)left, kBufWord3);
 #pragma unroll
-      for (int i = 0; i < C::NIP; ++i)
-        dma16(r, sp + i * C::NW * 1024,
-                                                 vp, i * RPI * C::NW * (int)p.n);
+      for (int i = 0; i < C::NIP; ++i) dma16(r, sp + i * C::NW * 1024, v, i * RPI * C::NW * (int)p.n);
     } else {
       const int64_t rows = p.n - n0 < C::TN ? p.n - n0 : (int64_t)C::TN;
       const __amdgpu_buffer_rsrc_t r =
           __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(gp), 0, (int)(rows * p.k), kBufWord3);
 #pragma unroll
-      for (int i = 0; i < C::NIP; ++i)
-        dma16(r, sp + i * C::NW * 1024,
-                                                 vp, i * 8 * C::NW * (int)p.k + (int)k0);
+      for (int i = 0; i < C::NIP; ++i) dma16(r, sp + i * C::NW * 1024, v, i * 8 * C::NW * (int)p.k + (int)k0);
     }
+  }
+  __device__ __forceinline__ void load_q(char *smem, int stage, int kt) const {
+    kt += kt0;
+    const int v = kt < last || inq ? voffq : INT32_MAX - 15;
+    char *sq = smem + 2 * C::SEGP + stage * C::SEGQ + wave * 1024;
     const int64_t rows = p.m - m0 < C::TM ? p.m - m0 : (int64_t)C::TM;
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(gq), 0, (int)(rows * p.k), kBufWord3);
 #pragma unroll
-    for (int i = 0; i < C::NIQ; ++i)
-      dma16(r, sq + i * C::NW * 1024, vq,
-                                               i * 8 * C::NW * (int)p.k + (int)k0);
+    for (int i = 0; i < C::NIQ; ++i) dma16(r, sq + i * C::NW * 1024, v, i * 8 * C::NW * (int)p.k + kt * kRowB);
   }
 
-  // The words of this wave's 64 scale rows for steps 4 q .. 4 q + 3, as they lie in
-  // memory.  No branches: control flow here would let the compiler move matrix
-  // instructions of one phase past the next one's barrier.
+  // The bytes of this wave's 64 scale rows for steps 4 q .. 4 q + 3 as they lie in memory,
+  // lane = row.  Row-contiguous layouts take one 16-byte load (each lane another line, so
+  // loads are what counts), from the row's last 16 bytes where fewer are left; SHORT
+  // matrices (up to 4 steps, one quad) have too few bytes in a row for that.
+  template <bool SHORT>
   __device__ __forceinline__ u32x4_t scales(int q) const {
     u32x4_t w;
+    if (SHORT || xwords) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int x = (4 * q + j) * xstep + xlane;
-      uint32_t v;
-      __builtin_memcpy(&v, sbase + (uint32_t)(soff + min(x, xmax) * xmul), 4);   // any alignment
-      w[j] = v;
+      for (int j = 0; j < 4; ++j) {
+        const int x = (kt0 + 4 * q + j) * xstep + xlane;
+        uint32_t v;
+        __builtin_memcpy(&v, sbase + (uint32_t)(soff + min(x, xmax) * xmul), 4);   // any alignment
+        w[j] = v;
+      }
+    } else {
+      __builtin_memcpy(&w, sbase + (uint32_t)(soff + min((kt0 + 4 * q) * 4, xmax - 12)), 16);
     }
     return w;
   }
-  // One step's word for the matrix instruction: lane 16 g + r gets block g's bytes of the
-  // rows r, 16 + r, 32 + r, 48 + r.
-  __device__ __forceinline__ uint32_t scale_word(uint32_t x, int step) const {
-    // the last word of a row whose blocks are no multiple of 4 was read from its last 4
-    // bytes; what the shift brings in scales codes that are all zero
-    const uint32_t t = lane_transpose(x >> min(max(step * xstep - xmax, 0) * tshift, 24), lane);
-    return NN && wave < C::TN / 64 ? __builtin_amdgcn_perm(x, x, psel) : t;
+  // Step 4 q + j's word for the matrix instruction: lane 16 g + r gets block g's bytes of
+  // the rows r, 16 + r, 32 + r, 48 + r.
+  template <bool SHORT>
+  __device__ __forceinline__ void scale_words(const u32x4_t &raw, int q, uint32_t (&out)[4]) const {
+    u32x4_t w = raw;
+    // what was read from before its place moves down (no branches here: see pin below);
+    // zeros come in beside codes that are all zero
+    if (SHORT) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] >>= min(max((kt0 + 4 * q + j) * xstep - xmax, 0) * tshift, 24);
+    } else {
+      const int d = min(max((kt0 + 4 * q) * 4 - (xmax - 12), 0), 15) * tshift;
+      const uint64_t lo = w[0] | (uint64_t)w[1] << 32, hi = w[2] | (uint64_t)w[3] << 32;
+      const uint64_t hs = hi >> (d & 63), ls = (lo >> (d & 63)) | (hi << 1 << (63 - (d & 63)));
+      w[0] = (uint32_t)(d < 64 ? ls : hs);
+      w[1] = (uint32_t)((d < 64 ? ls : hs) >> 32);
+      w[2] = (uint32_t)(d < 64 ? hs : 0);
+      w[3] = (uint32_t)((d < 64 ? hs : 0) >> 32);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      out[j] = NN && wave < C::TN / 64 ? __builtin_amdgcn_perm(w[j], w[j], psel) : lane_transpose(w[j], lane);
   }
 };
 
-template <class C, bool NN>
+
+// One K split's sums of a tile, dense M x N4 float32 per split (N4: N to a multiple of 4).
+template <class C>
+__device__ __forceinline__ void store_part(const GemmMx &p, float *parts, int64_t n0, int64_t m0, int wn, int wm, int lane,
+                                           const f32x4_t (&acc)[C::FP][C::FQ]) {
+  const int64_t n4 = (p.n + 3) & ~(int64_t)3;
+  float *o = parts + (int64_t)blockIdx.y * p.m * n4;
+#pragma unroll
+  for (int j = 0; j < C::FQ; ++j)
+#pragma unroll
+    for (int i = 0; i < C::FP; ++i) {
+      const int64_t m = m0 + wm * (C::TM / C::WM) + 16 * j + (lane & 15), n = n0 + wn * (C::TN / C::WN) + 16 * i + 4 * (lane >> 4);
+      if (m < p.m && n < n4) *reinterpret_cast<f32x4_t *>(o + m * n4 + n) = acc[i][j];
+    }
+}
+
+// The splits' sums added in split order, 4 consecutive n per thread.
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_gemm_mx_join(GemmMx p, const float *parts, int splits) {
+  const int64_t n4 = (p.n + 3) & ~(int64_t)3, words = p.m * (n4 >> 2);
+  const bool vec = p.ld % 4 == 0;
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < words; i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / (n4 >> 2), n = (i - m * (n4 >> 2)) * 4;
+    const f32x4_t *q = reinterpret_cast<const f32x4_t *>(parts) + i;
+    f32x4_t v = q[0];
+    for (int s = 1; s < splits; ++s) v += q[s * words];
+    if (BF16) store_bf16(p, m, n, v, vec);
+    else store_f32(p, static_cast<float *>(p.out), m, n, v, vec);
+  }
+}
+
+template <class C, bool NN, bool SHORT>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_gemm_mx8(GemmMx p, int64_t tiles_m,
-                                                                                             int64_t tiles_n) {
+                                                                                             int64_t tiles_n, int steps, float *parts) {
   __shared__ __align__(1024) char smem[C::LDS];
   int64_t tm, tn;
   tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
   const int64_t n0 = tn * C::TN, m0 = tm * C::TM;
-  const Loader<C, NN> ld(p, n0, m0);
+  const int kt0 = (int)blockIdx.y * steps;
+  const Loader<C, NN> ld(p, n0, m0, kt0, min(steps, (int)((p.k + kRowB - 1) / kRowB) - kt0));
   const int lane = ld.lane, wave = ld.wave, wn = wave / C::WM, wm = wave % C::WM;
   const int r = lane & 15, g = lane >> 4;
   uint32_t *ring = reinterpret_cast<uint32_t *>(smem + 2 * C::STAGE);
@@ -404,21 +575,32 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
   const int gp = wn * (FP / 4), gq = C::TN / 64 + wm;
 
   // Fragments in registers: P holds half of the n side, its slots reloaded with the other
-  // half right after their last use; Q0 or Q2 (by turns) and Q1 the m side's two pairs.
-  i32x8_t P[HP], Q0[HQ], Q1[HQ], Q2[HQ];
+  // half right after their last use; Q0 and Q1 (by turns) the m side's first pair and second.
+  i32x8_t P[HP], Q0[HQ], Q1[HQ];
   int sp[2][FP / 4], sq[2];
-  auto put_scales = [&](const u32x4_t &w, int q) __attribute__((always_inline)) {
+  auto put_scales = [&](const u32x4_t &raw, int q) __attribute__((always_inline)) {
+    uint32_t w[4];
+    ld.template scale_words<SHORT>(raw, q, w);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      ring[((4 * (q & 1) + j) * C::GRPS + wave) * 64 + lane] = ld.scale_word(w[j], 4 * q + j);
+    for (int j = 0; j < 4; ++j) ring[((4 * (q & 1) + j) * C::GRPS + wave) * 64 + lane] = w[j];
+  };
+  // Control flow keeps nothing from moving matrix instructions to where their sums are
+  // next used, past a barrier: this pins them.
+  auto pin = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < FP; ++i)
+#pragma unroll
+      for (int j = 0; j < FQ; ++j) asm volatile("" : "+v"(acc[i][j]));
   };
 
   const int nk = ld.nk;
-  u32x4_t sw = ld.scales(0);
-  ld.load(smem, 0, 0);
+  u32x4_t sw = ld.template scales<SHORT>(0);
+  ld.load_p(smem, 0, 0);
+  ld.load_q(smem, 0, 0);
   put_scales(sw, 0);
-  ld.load(smem, 1, nk > 1 ? 1 : 0);
-  sw = ld.scales(1);
+  ld.load_p(smem, 1, nk > 1 ? 1 : 0);
+  ld.load_q(smem, 1, nk > 1 ? 1 : 0);
+  if (!SHORT) sw = ld.template scales<false>(1);
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(0) : "memory");
   __syncthreads();
 #pragma unroll
@@ -432,8 +614,8 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
   constexpr int RP = NN ? 4 : 2;                      // LDS reads of an n-side fragment
   // A quarter of a step: HP x HQ matrix instructions with n-side fragments i0 .. and
   // m-side fragments j0 ...  After a fragment's last use `reload` fills its slot; `nr`
-  // other LDS reads are spread between the instructions.
-  auto mma = [&](int i0, i32x8_t(&Q)[HQ], int j0, const int (&s)[FP / 4], int t, int nr, bool roll, auto reload)
+  // other LDS reads and `nv` loads to LDS are spread between the instructions.
+  auto mma = [&](int i0, i32x8_t(&Q)[HQ], int j0, const int (&s)[FP / 4], int t, int nr, int nv, bool roll, auto reload)
                  __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < HP; ++i) {
@@ -446,48 +628,59 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
     for (int i = 0; i < HP * HQ; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       if (i < nr) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (i % 2 == 0 && i / 2 < nv) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
       if (roll && i % HQ == HQ - 1) __builtin_amdgcn_sched_group_barrier(0x100, RP, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
   auto none = [](int) { return i32x8_t{}; };
-  // One step: the m side's first pair is in QX, its second goes to Q1, the next step's
-  // first to QZ.
-  auto step = [&](int kt, int q, int phase, i32x8_t(&QX)[HQ], i32x8_t(&QZ)[HQ], const int (&s)[FP / 4], int t,
+  // One step: the m side's first pair is in QX, its second goes to QY, then the next
+  // step's first.
+  auto step = [&](int kt, int q, int phase, i32x8_t(&QX)[HQ], i32x8_t(&QY)[HQ], const int (&s)[FP / 4], int t,
                   int (&sn)[FP / 4], int &tn_) __attribute__((always_inline)) {
     const int stage = phase & 1;
 #pragma unroll
-    for (int j = 0; j < HQ; ++j) Q1[j] = ldq(stage, HQ + j);
-    mma(0, QX, 0, s, t, 2 * HQ, false, none);
-    mma(0, Q1, HQ, s, t, 0, true, [&](int i) __attribute__((always_inline)) { return ldp(stage, HP + i); });
-    // every wave has read this step's stage, and the next one has landed
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __syncthreads();
+    for (int j = 0; j < HQ; ++j) QY[j] = ldq(stage, HQ + j);
+    mma(0, QX, 0, s, t, 2 * HQ, 0, false, none);
+    mma(0, QY, HQ, s, t, 0, 0, true, [&](int i) __attribute__((always_inline)) { return ldp(stage, HP + i); });
+    // every wave has read this step's stage, and the next one has landed (phase 3: but for
+    // the scales' load of the step before, 4 loads where their words lie apart)
+    if (!SHORT && phase == 3) stage_barrier<1>();
+    else stage_barrier<0>();
     // near the end the reload repeats the last step into a stage nobody reads again
-    ld.load(smem, stage, kt + 2 < nk ? kt + 2 : nk - 1);
-    if (phase == 2) put_scales(sw, q + 1);
-    if (phase == 3) sw = ld.scales(q + 2);
-#pragma unroll
-    for (int j = 0; j < HQ; ++j) QZ[j] = ldq(stage ^ 1, j);
+    ld.load_p(smem, stage, kt + 2 < nk ? kt + 2 : nk - 1);
+    if (!SHORT && phase == 2) put_scales(sw, q + 1);
 #pragma unroll
     for (int i = 0; i < FP / 4; ++i) sn[i] = lds_scale(kt + 1, gp + i);
     tn_ = lds_scale(kt + 1, gq);
-    mma(HP, Q1, HQ, s, t, 2 * HQ + FP / 4 + 1, false, none);
-    mma(HP, QX, 0, s, t, 0, true, [&](int i) __attribute__((always_inline)) { return ldp(stage ^ 1, i); });
+    mma(HP, QY, HQ, s, t, FP / 4 + 1, C::NIP, false, none);
+    ld.load_q(smem, stage, kt + 2 < nk ? kt + 2 : nk - 1);
+#pragma unroll
+    for (int j = 0; j < HQ; ++j) QY[j] = ldq(stage ^ 1, j);
+    mma(HP, QX, 0, s, t, 2 * HQ, C::NIQ, true, [&](int i) __attribute__((always_inline)) { return ldp(stage ^ 1, i); });
+    // last of the step's loads, so the next barrier's wait can leave it in flight
+    if (!SHORT && phase == 2) {
+      pin();
+      sw = ld.template scales<false>(q + 2);
+    }
   };
   for (int kt = 0, q = 0;; kt += 4, ++q) {
-    step(kt, q, 0, Q0, Q2, sp[0], sq[0], sp[1], sq[1]);
+    step(kt, q, 0, Q0, Q1, sp[0], sq[0], sp[1], sq[1]);
     if (kt + 1 >= nk) break;
-    step(kt + 1, q, 1, Q2, Q0, sp[1], sq[1], sp[0], sq[0]);
+    step(kt + 1, q, 1, Q1, Q0, sp[1], sq[1], sp[0], sq[0]);
     if (kt + 2 >= nk) break;
-    step(kt + 2, q, 2, Q0, Q2, sp[0], sq[0], sp[1], sq[1]);
+    step(kt + 2, q, 2, Q0, Q1, sp[0], sq[0], sp[1], sq[1]);
     if (kt + 3 >= nk) break;
-    step(kt + 3, q, 3, Q2, Q0, sp[1], sq[1], sp[0], sq[0]);
+    step(kt + 3, q, 3, Q1, Q0, sp[1], sq[1], sp[0], sq[0]);
     if (kt + 4 >= nk) break;
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // the trailing reloads
   __syncthreads();
 
+  if (parts) {
+    store_part<C>(p, parts, n0, m0, wn, wm, lane, acc);
+    return;
+  }
   // bfloat16 tile through LDS (rows m), then whole rows of 16-byte stores
   uint16_t *lt = reinterpret_cast<uint16_t *>(smem);
   constexpr int LP = C::TN + 8;
@@ -518,33 +711,19 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
   }
 }
 
-// Four consecutive n of one row m: float32 result, the addend joined in.  `vec`: rows
-// are 16-byte multiples, so four in range go out together.
-__device__ __forceinline__ void store_f32(const GemmMx &p, float *out, int64_t m, int64_t n, f32x4_t v, bool vec) {
-  if (m >= p.m || n >= p.n) return;
-  const int64_t e = m * p.ld + n;
-  if (vec && n + 4 <= p.n) {
-    if (p.addend) v += *reinterpret_cast<const f32x4_t *>(p.addend + e);
-    *reinterpret_cast<f32x4_t *>(out + e) = v;
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (n + k < p.n) out[e + k] = p.addend ? v[k] + p.addend[e + k] : v[k];
-  }
-}
-
 // Float32 output: the same tiles, stages and scale words, with operands converted to
 // bfloat16 on their way from LDS to the matrix instructions.  A half step is one 16-byte
 // chunk per lane (64 k): its m-side fragments stay converted while the n side's pass by,
 // one converted (8 conversions) beside the previous one's 2 x FQ matrix instructions.
-template <class C, bool NN>
+template <class C, bool NN, bool SHORT>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_gemm_mx16(GemmMx p, int64_t tiles_m,
-                                                                                              int64_t tiles_n) {
+                                                                                              int64_t tiles_n, int steps, float *parts) {
   __shared__ __align__(1024) char smem[C::LDS];
   int64_t tm, tn;
   tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
   const int64_t n0 = tn * C::TN, m0 = tm * C::TM;
-  const Loader<C, NN> ld(p, n0, m0);
+  const int kt0 = (int)blockIdx.y * steps;
+  const Loader<C, NN> ld(p, n0, m0, kt0, min(steps, (int)((p.k + kRowB - 1) / kRowB) - kt0));
   const int lane = ld.lane, wave = ld.wave, wn = wave / C::WM, wm = wave % C::WM;
   const int r = lane & 15, g = lane >> 4;
   uint32_t *ring = reinterpret_cast<uint32_t *>(smem + 2 * C::STAGE);
@@ -585,18 +764,29 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
     out[1] = to_bf16((int)x[2], (int)x[3], e);
   };
   const int gp = wn * (FP / 4), gq = C::TN / 64 + wm;
-  auto put_scales = [&](const u32x4_t &w, int q) __attribute__((always_inline)) {
+  auto put_scales = [&](const u32x4_t &raw, int q) __attribute__((always_inline)) {
+    uint32_t w[4];
+    ld.template scale_words<SHORT>(raw, q, w);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      ring[((4 * (q & 1) + j) * C::GRPS + wave) * 64 + lane] = ld.scale_word(w[j], 4 * q + j);
+    for (int j = 0; j < 4; ++j) ring[((4 * (q & 1) + j) * C::GRPS + wave) * 64 + lane] = w[j];
+  };
+  // Control flow keeps nothing from moving matrix instructions to where their sums are
+  // next used, past a barrier: this pins them.
+  auto pin = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < FP; ++i)
+#pragma unroll
+      for (int j = 0; j < FQ; ++j) asm volatile("" : "+v"(acc[i][j]));
   };
 
   const int nk = ld.nk;
-  u32x4_t sw = ld.scales(0);
-  ld.load(smem, 0, 0);
+  u32x4_t sw = ld.template scales<SHORT>(0);
+  ld.load_p(smem, 0, 0);
+  ld.load_q(smem, 0, 0);
   put_scales(sw, 0);
-  ld.load(smem, 1, nk > 1 ? 1 : 0);
-  sw = ld.scales(1);
+  ld.load_p(smem, 1, nk > 1 ? 1 : 0);
+  ld.load_q(smem, 1, nk > 1 ? 1 : 0);
+  if (!SHORT) sw = ld.template scales<false>(1);
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
 
@@ -622,11 +812,10 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
       // fragment i + 1's conversion, then its slot takes fragment i + 3
       if (i == FP - 2) {
         if (h) {
-          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-          __syncthreads();                            // this stage is read, the next has landed
-          ld.load(smem, stage, kt + 2 < nk ? kt + 2 : nk - 1);
-          if (phase == 2) put_scales(sw, q + 1);
-          if (phase == 3) sw = ld.scales(q + 2);
+          if (!SHORT && phase == 3) stage_barrier<1>();
+          else stage_barrier<0>();                    // this stage is read, the next has landed
+          ld.load_p(smem, stage, kt + 2 < nk ? kt + 2 : nk - 1);
+          if (!SHORT && phase == 2) put_scales(sw, q + 1);
         }
 #pragma unroll
         for (int k = 0; k < FP / 4; ++k) sp[nh][k] = lds_scale(nkt, nh, gp + k);
@@ -634,6 +823,7 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
 #pragma unroll
         for (int j = 0; j < FQ; ++j) Q[j] = ldq(ns, nh, j);
       }
+      if (i == FP - 1 && h) ld.load_q(smem, stage, kt + 2 < nk ? kt + 2 : nk - 1);
       P[i & 1] = i + 2 < FP ? ldp(stage, h, i + 2) : ldp(ns, nh, i + 2 - FP);
       if (i + 1 < FP) convert(P[(i + 1) & 1], sp[h][(i + 1) >> 2], (i + 1) & 3, pc[(i + 1) & 1]);
       else convert(P[0], sp[nh][0], 0, pc[0]);
@@ -648,6 +838,7 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
         for (int k = 0; k < 2 * FQ; ++k) {
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
           __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
+          if (h && k % 2 == 0 && k / 2 < C::NIQ) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
         }
       } else {
         __builtin_amdgcn_sched_group_barrier(0x100, NN ? 2 : 1, 0);
@@ -657,12 +848,17 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
           __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);
           if (k & 1) __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);
           if (i == FP - 2) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          if (i == FP - 2 && h && k % 2 == 0 && k / 2 < C::NIP) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
     };
 #pragma unroll
     for (int i = 0; i < FP; ++i) one(i);
+    if (!SHORT && phase == 2 && h) {
+      pin();
+      sw = ld.template scales<false>(q + 2);
+    }
   };
   for (int kt = 0, q = 0;; kt += 4, ++q) {
     half(kt, q, 0, 0);
@@ -679,6 +875,10 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
     if (kt + 4 >= nk) break;
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // the trailing reloads
+  if (parts) {
+    store_part<C>(p, parts, n0, m0, wn, wm, lane, acc);
+    return;
+  }
   float *out = static_cast<float *>(p.out);
   const bool vec = p.ld % 4 == 0;
 #pragma unroll
@@ -689,28 +889,77 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
 }
 
 using T256 = Tile<256, 256, 2, 4>;
+using T128 = Tile<128, 128, 2, 2>;
 
 template <class C, bool NN>
-hipError_t gemm_tiled(const GemmMx &g, hipStream_t s) {
+hipError_t gemm_tiled(const GemmMx &g, int splits, int steps, float *parts, hipStream_t s) {
   const int64_t tm = (g.m + C::TM - 1) / C::TM, tn = (g.n + C::TN - 1) / C::TN;
-  if (g.bf16) hipLaunchKernelGGL((k_gemm_mx8<C, NN>), dim3((unsigned)(tm * tn)), dim3(C::NT), 0, s, g, tm, tn);
-  else hipLaunchKernelGGL((k_gemm_mx16<C, NN>), dim3((unsigned)(tm * tn)), dim3(C::NT), 0, s, g, tm, tn);
+  const dim3 grid((unsigned)(tm * tn), (unsigned)splits), block(C::NT);
+  if (splits == 1) parts = nullptr;
+  const bool sh = g.k <= 4 * kRowB;
+  if (g.bf16 && sh) hipLaunchKernelGGL((k_gemm_mx8<C, NN, true>), grid, block, 0, s, g, tm, tn, steps, parts);
+  else if (g.bf16) hipLaunchKernelGGL((k_gemm_mx8<C, NN, false>), grid, block, 0, s, g, tm, tn, steps, parts);
+  else if (sh) hipLaunchKernelGGL((k_gemm_mx16<C, NN, true>), grid, block, 0, s, g, tm, tn, steps, parts);
+  else hipLaunchKernelGGL((k_gemm_mx16<C, NN, false>), grid, block, 0, s, g, tm, tn, steps, parts);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || splits == 1) return e;
+  const int64_t words = g.m * ((g.n + 3) / 4);
+  const dim3 jgrid((unsigned)std::min<int64_t>((words + 255) / 256, 8192)), jblock(256);
+  if (g.bf16) hipLaunchKernelGGL((k_gemm_mx_join<true>), jgrid, jblock, 0, s, g, parts, splits);
+  else hipLaunchKernelGGL((k_gemm_mx_join<false>), jgrid, jblock, 0, s, g, parts, splits);
   return hipGetLastError();
+}
+
+template <bool NN, bool BF16, int W, int NF, int MT, int UN, int ROT = 0>
+hipError_t gemm_rows(const GemmMx &g, hipStream_t s) {
+  const dim3 grid((unsigned)((g.n + 16 * NF - 1) / (16 * NF)), (unsigned)((g.m + 16 * MT - 1) / (16 * MT)));
+  hipLaunchKernelGGL((k_gemm_mx_rows<NN, BF16, W, NF, MT, UN, ROT>), grid, dim3(64 * W), 0, s, g);
+  return hipGetLastError();
+}
+
+// How a product runs: few-row kernel (tile 0), or tiles of 256 or 128 with K in `splits`
+// runs of `steps` 128-k steps (a multiple of 4: scale words come 4 steps at a time).
+struct Shape {
+  int tile, splits, steps;
+};
+
+Shape shape_of(int64_t m, int64_t n, int64_t k, bool nn) {
+  if (k < 128 || n < 128 || (m <= 64 && !nn && !getenv("MX_TILE"))) return {0, 1, 0};
+  const int nk = (int)((k + kRowB - 1) / kRowB);
+  if (const char *e = getenv("MX_TILE")) { int t = 256, sp = 1; sscanf(e, "%d,%d", &t, &sp); if (!t) return {0, 1, 0}; int st = ((nk + sp - 1) / sp + 3) / 4 * 4; return {t, (nk + st - 1) / st, st}; }
+  return {256, 1, nk};
 }
 
 }  // namespace
 
-int64_t gemm_mx_workspace(int64_t, int64_t, int64_t, bool) { return 0; }
+int64_t gemm_mx_workspace(int64_t m, int64_t n, int64_t k, bool nn) {
+  const Shape sh = shape_of(m, n, k, nn);
+  return sh.splits > 1 ? sh.splits * m * ((n + 3) / 4 * 4) * (int64_t)sizeof(float) : 0;
+}
 
-hipError_t launch_gemm_mx(const GemmMx &g, void *, hipStream_t s) {
-  if (g.k >= 128 && g.m >= 128 && g.n >= 128) return g.nn ? gemm_tiled<T256, true>(g, s) : gemm_tiled<T256, false>(g, s);
-  const int64_t tm = (g.m + 15) / 16, tn = (g.n + 15) / 16;
-  const dim3 grid((unsigned)(tm * tn)), block(64);
-  if (g.nn && g.bf16) hipLaunchKernelGGL((k_gemm_mx_16<true, true>), grid, block, 0, s, g, tn);
-  else if (g.nn) hipLaunchKernelGGL((k_gemm_mx_16<true, false>), grid, block, 0, s, g, tn);
-  else if (g.bf16) hipLaunchKernelGGL((k_gemm_mx_16<false, true>), grid, block, 0, s, g, tn);
-  else hipLaunchKernelGGL((k_gemm_mx_16<false, false>), grid, block, 0, s, g, tn);
-  return hipGetLastError();
+hipError_t launch_gemm_mx(const GemmMx &g, void *ws, hipStream_t s) {
+  const Shape sh = shape_of(g.m, g.n, g.k, g.nn);
+  float *parts = static_cast<float *>(ws);
+  if (sh.tile == 256)
+    return g.nn ? gemm_tiled<T256, true>(g, sh.splits, sh.steps, parts, s)
+                : gemm_tiled<T256, false>(g, sh.splits, sh.steps, parts, s);
+  if (sh.tile == 128)
+    return g.nn ? gemm_tiled<T128, true>(g, sh.splits, sh.steps, parts, s)
+                : gemm_tiled<T128, false>(g, sh.splits, sh.steps, parts, s);
+  if (g.nn) return g.bf16 ? gemm_rows<true, true, 4, 1, 1, 1>(g, s) : gemm_rows<true, false, 4, 1, 1, 1>(g, s);
+  if (const char *e = getenv("MX_ROWS")) { int c = atoi(e);
+    if (c == 1) return gemm_rows<false, true, 8, 1, 1, 2>(g, s);
+    if (c == 2) return gemm_rows<false, true, 8, 1, 1, 1>(g, s);
+    if (c == 3) return gemm_rows<false, true, 4, 1, 1, 2>(g, s);
+    if (c == 4) return gemm_rows<false, true, 16, 1, 1, 1>(g, s);
+    if (c == 5) return gemm_rows<false, true, 8, 1, 1, 1, 1>(g, s);
+    if (c == 6) return gemm_rows<false, true, 8, 1, 1, 2, 1>(g, s);
+    if (c == 7) return gemm_rows<false, true, 8, 2, 1, 1>(g, s);
+    if (c == 8) return gemm_rows<false, true, 8, 1, 1, 3>(g, s);
+  }
+  if (g.m <= 16) return g.bf16 ? gemm_rows<false, true, 8, 1, 1, 1>(g, s) : gemm_rows<false, false, 8, 1, 1, 1>(g, s);
+  if (g.m <= 32) return g.bf16 ? gemm_rows<false, true, 8, 1, 2, 1>(g, s) : gemm_rows<false, false, 8, 1, 2, 1>(g, s);
+  return g.bf16 ? gemm_rows<false, true, 8, 2, 4, 1>(g, s) : gemm_rows<false, false, 8, 2, 4, 1>(g, s);
 }
 
 }  // namespace sshdp
