@@ -25,8 +25,6 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <cstdlib>
-#include <cstdio>
 
 #include "internal.h"
 
@@ -95,7 +93,7 @@ __device__ __forceinline__ void store_bf16(const GemmMx &p, int64_t m, int64_t n
 // bytes of B's rows; codes go straight from memory to the matrix instructions, UN steps'
 // loads in flight per wave.  MT * 16 rows of m at a time (grid.y); rows past the end
 // repeat the last one.  The waves' sums meet in LDS and are added in wave order.
-template <bool NN, bool BF16, int W, int NF, int MT, int UN, int ROT>
+template <bool NN, bool BF16, int W, int NF, int MT, int UN>
 __global__ __launch_bounds__(64 * W) void k_gemm_mx_rows(GemmMx p) {
   __shared__ __align__(16) f32x4_t part[W][NF * MT][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -193,20 +191,17 @@ __global__ __launch_bounds__(64 * W) void k_gemm_mx_rows(GemmMx p) {
       }
   };
   Step st[2][UN];
-  const int rot = ROT ? (int)((blockIdx.x * ROT) % max(nk / (W * UN), 1)) * (W * UN) : 0;
-  auto at = [&](int k0) { const int x = k0 + rot; return ROT ? (x < nk ? x : x - nk) : x; };
-  (void)at;
 #pragma unroll
-  for (int u = 0; u < UN; ++u) fetch(st[0][u], wave + rot + u * W);
+  for (int u = 0; u < UN; ++u) fetch(st[0][u], wave + u * W);
   for (int k0 = wave;;) {
 #pragma unroll
-    for (int u = 0; u < UN; ++u) fetch(st[1][u], at(k0 + UN * W) + u * W);
+    for (int u = 0; u < UN; ++u) fetch(st[1][u], k0 + UN * W + u * W);
 #pragma unroll
     for (int u = 0; u < UN; ++u) multiply(st[0][u]);
     k0 += UN * W;
     if (k0 >= nk) break;
 #pragma unroll
-    for (int u = 0; u < UN; ++u) fetch(st[0][u], at(k0 + UN * W) + u * W);
+    for (int u = 0; u < UN; ++u) fetch(st[0][u], k0 + UN * W + u * W);
 #pragma unroll
     for (int u = 0; u < UN; ++u) multiply(st[1][u]);
     k0 += UN * W;
@@ -249,17 +244,19 @@ __global__ __launch_bounds__(64 * W) void k_gemm_mx_rows(GemmMx p) {
 constexpr int kBufWord3 = 0x00020000;                // raw gfx9-family buffer resource
 constexpr int kRowB = 128;                           // bytes (= k) of a stage row
 
-template <int TN_, int TM_, int WN_, int WM_>
+template <int TN_, int TM_, int WN_, int WM_, int NST_>
 struct Tile {
-  static constexpr int TN = TN_, TM = TM_, WN = WN_, WM = WM_, NW = WN * WM, NT = 64 * NW;
+  static constexpr int TN = TN_, TM = TM_, WN = WN_, WM = WM_, NW = WN * WM, NT = 64 * NW, NST = NST_;
   static constexpr int FP = TN / WN / 16, FQ = TM / WM / 16;     // 16-row fragments of a wave: n side, m side
   static constexpr int SEGP = TN * kRowB, SEGQ = TM * kRowB, STAGE = SEGP + SEGQ;
   static constexpr int NIP = SEGP / 1024 / NW, NIQ = SEGQ / 1024 / NW;   // buffer loads per wave and stage
   static constexpr int GRPS = (TN + TM) / 64;                   // 64-row scale groups, n side first
   static constexpr int RING = 2 * 4 * GRPS * 64 * 4;            // scale words: 2 x 4 steps
   static constexpr int EPI = TM * (TN + 8) * 2;                 // bfloat16 output tile
-  static constexpr int LDS = 2 * STAGE + RING > EPI ? 2 * STAGE + RING : EPI;
+  static constexpr int LDS = NST * STAGE + RING > EPI ? NST * STAGE + RING : EPI;
+  static constexpr int WPS = NT * (163840 / LDS) / 256;         // waves per SIMD
   static_assert(FP % 4 == 0 && FQ == 4 && NT == TN + TM, "a thread per scale row, 64-row groups");
+  static_assert((NST == 2 || NST == 4) && (NST - 1) * SEGP + SEGP / WN <= 65536, "stages are LDS read offsets");
 };
 
 // Chunk swizzle of a stage row: 8 consecutive rows, one LDS pass, hit 8 different chunks.
@@ -309,11 +306,12 @@ __device__ __forceinline__ void tile_of(int64_t id, int64_t tiles_m, int64_t til
   tm = strip * 8 + in - tn * h;
 }
 
-// All of a workgroup's LDS accesses and its loads but the newest `LEFT` are done.  (The
-// barrier builtin would wait for those as well.)
-template <int LEFT>
-__device__ __forceinline__ void stage_barrier() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
+// All of a workgroup's LDS accesses are done, and its loads but the newest LEFT, one more
+// if `scales` (a constant once unrolled).  The barrier builtin would wait for all loads.
+template <int LEFT, bool SCALES>
+__device__ __forceinline__ void stage_barrier(bool scales) {
+  if (SCALES && scales) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT + 1) : "memory");
+  else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
 }
 
 // 16 bytes per lane from memory straight to LDS, lane i at dst + 16 i.
@@ -428,7 +426,7 @@ struct Loader {
   __device__ __forceinline__ void load_q(char *smem, int stage, int kt) const {
     kt += kt0;
     const int v = kt < last || inq ? voffq : INT32_MAX - 15;
-    char *sq = smem + 2 * C::SEGP + stage * C::SEGQ + wave * 1024;
+    char *sq = smem + C::NST * C::SEGP + stage * C::SEGQ + wave * 1024;
     const int64_t rows = p.m - m0 < C::TM ? p.m - m0 : (int64_t)C::TM;
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(gq), 0, (int)(rows * p.k), kBufWord3);
@@ -513,7 +511,7 @@ __global__ __launch_bounds__(256) void k_gemm_mx_join(GemmMx p, const float *par
 }
 
 template <class C, bool NN, bool SHORT>
-__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_gemm_mx8(GemmMx p, int64_t tiles_m,
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C::WPS))) void k_gemm_mx8(GemmMx p, int64_t tiles_m,
                                                                                              int64_t tiles_n, int steps, float *parts) {
   __shared__ __align__(1024) char smem[C::LDS];
   int64_t tm, tn;
@@ -523,15 +521,15 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
   const Loader<C, NN> ld(p, n0, m0, kt0, min(steps, (int)((p.k + kRowB - 1) / kRowB) - kt0));
   const int lane = ld.lane, wave = ld.wave, wn = wave / C::WM, wm = wave % C::WM;
   const int r = lane & 15, g = lane >> 4;
-  uint32_t *ring = reinterpret_cast<uint32_t *>(smem + 2 * C::STAGE);
+  uint32_t *ring = reinterpret_cast<uint32_t *>(smem + C::NST * C::STAGE);
   constexpr int FP = C::FP, FQ = C::FQ, HP = FP / 2, HQ = FQ / 2;
 
   // fragment addresses: row 16 i + r of the wave's panel, chunks g and 4 + g
   const int cof = (g ^ swz(r)) * 16;
-  const int rowp = (wn * (C::TN / C::WN) + r) * kRowB + cof, rowq = 2 * C::SEGP + (wm * (C::TM / C::WM) + r) * kRowB + cof;
+  const int rowp = (wn * (C::TN / C::WN) + r) * kRowB + cof, rowq = C::NST * C::SEGP + (wm * (C::TM / C::WM) + r) * kRowB + cof;
   // NN: fragment i's 16 columns are one chunk of each k row; a transposing read hands
   // a lane one column's 8 k (rows kb .. kb + 7), read 16 bytes a row by lane pairs
-  const int trp = (16 * g + (r >> 1)) * C::TN + ((r >> 1) << 4) + 8 * (r & 1) + wn * (C::TN / C::WN);
+  const int trp = (16 * g + (r >> 1)) * C::TN + (((r >> 1) << 4) ^ (wn * (C::TN / C::WN))) + 8 * (r & 1);
 
   f32x4_t acc[FP][FQ];
 #pragma unroll
@@ -594,12 +592,16 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
   };
 
   const int nk = ld.nk;
+  constexpr int NST = C::NST, NV = C::NIP + C::NIQ;   // loads of one stage, per wave
   u32x4_t sw = ld.template scales<SHORT>(0);
   ld.load_p(smem, 0, 0);
   ld.load_q(smem, 0, 0);
   put_scales(sw, 0);
-  ld.load_p(smem, 1, nk > 1 ? 1 : 0);
-  ld.load_q(smem, 1, nk > 1 ? 1 : 0);
+#pragma unroll
+  for (int st = 1; st < C::NST; ++st) {
+    ld.load_p(smem, st, min(st, nk - 1));
+    ld.load_q(smem, st, min(st, nk - 1));
+  }
   if (!SHORT) sw = ld.template scales<false>(1);
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(0) : "memory");
   __syncthreads();
@@ -638,26 +640,25 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
   // step's first.
   auto step = [&](int kt, int q, int phase, i32x8_t(&QX)[HQ], i32x8_t(&QY)[HQ], const int (&s)[FP / 4], int t,
                   int (&sn)[FP / 4], int &tn_) __attribute__((always_inline)) {
-    const int stage = phase & 1;
+    const int stage = phase % NST, next = (phase + 1) % NST;
 #pragma unroll
     for (int j = 0; j < HQ; ++j) QY[j] = ldq(stage, HQ + j);
     mma(0, QX, 0, s, t, 2 * HQ, 0, false, none);
     mma(0, QY, HQ, s, t, 0, 0, true, [&](int i) __attribute__((always_inline)) { return ldp(stage, HP + i); });
-    // every wave has read this step's stage, and the next one has landed (phase 3: but for
-    // the scales' load of the step before, 4 loads where their words lie apart)
-    if (!SHORT && phase == 3) stage_barrier<1>();
-    else stage_barrier<0>();
+    // every wave has read this step's stage, and the next one has landed: younger are the
+    // later stages' loads and, but in phase 2, the scales' (one load, or four)
+    stage_barrier<(NST - 2) * NV, !SHORT>(phase != 2 && (NST == 4 || phase == 3));
     // near the end the reload repeats the last step into a stage nobody reads again
-    ld.load_p(smem, stage, kt + 2 < nk ? kt + 2 : nk - 1);
+    ld.load_p(smem, stage, min(kt + NST, nk - 1));
     if (!SHORT && phase == 2) put_scales(sw, q + 1);
 #pragma unroll
     for (int i = 0; i < FP / 4; ++i) sn[i] = lds_scale(kt + 1, gp + i);
     tn_ = lds_scale(kt + 1, gq);
     mma(HP, QY, HQ, s, t, FP / 4 + 1, C::NIP, false, none);
-    ld.load_q(smem, stage, kt + 2 < nk ? kt + 2 : nk - 1);
+    ld.load_q(smem, stage, min(kt + NST, nk - 1));
 #pragma unroll
-    for (int j = 0; j < HQ; ++j) QY[j] = ldq(stage ^ 1, j);
-    mma(HP, QX, 0, s, t, 2 * HQ, C::NIQ, true, [&](int i) __attribute__((always_inline)) { return ldp(stage ^ 1, i); });
+    for (int j = 0; j < HQ; ++j) QY[j] = ldq(next, j);
+    mma(HP, QX, 0, s, t, 2 * HQ, C::NIQ, true, [&](int i) __attribute__((always_inline)) { return ldp(next, i); });
     // last of the step's loads, so the next barrier's wait can leave it in flight
     if (!SHORT && phase == 2) {
       pin();
@@ -716,7 +717,7 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
 // chunk per lane (64 k): its m-side fragments stay converted while the n side's pass by,
 // one converted (8 conversions) beside the previous one's 2 x FQ matrix instructions.
 template <class C, bool NN, bool SHORT>
-__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_gemm_mx16(GemmMx p, int64_t tiles_m,
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C::WPS))) void k_gemm_mx16(GemmMx p, int64_t tiles_m,
                                                                                               int64_t tiles_n, int steps, float *parts) {
   __shared__ __align__(1024) char smem[C::LDS];
   int64_t tm, tn;
@@ -726,11 +727,11 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
   const Loader<C, NN> ld(p, n0, m0, kt0, min(steps, (int)((p.k + kRowB - 1) / kRowB) - kt0));
   const int lane = ld.lane, wave = ld.wave, wn = wave / C::WM, wm = wave % C::WM;
   const int r = lane & 15, g = lane >> 4;
-  uint32_t *ring = reinterpret_cast<uint32_t *>(smem + 2 * C::STAGE);
+  uint32_t *ring = reinterpret_cast<uint32_t *>(smem + C::NST * C::STAGE);
   constexpr int FP = C::FP, FQ = C::FQ;
   const int cof = (g ^ swz(r)) * 16;
-  const int rowp = (wn * (C::TN / C::WN) + r) * kRowB + cof, rowq = 2 * C::SEGP + (wm * (C::TM / C::WM) + r) * kRowB + cof;
-  const int trp = (16 * g + (r >> 1)) * C::TN + ((r >> 1) << 4) + 8 * (r & 1) + wn * (C::TN / C::WN);
+  const int rowp = (wn * (C::TN / C::WN) + r) * kRowB + cof, rowq = C::NST * C::SEGP + (wm * (C::TM / C::WM) + r) * kRowB + cof;
+  const int trp = (16 * g + (r >> 1)) * C::TN + (((r >> 1) << 4) ^ (wn * (C::TN / C::WN))) + 8 * (r & 1);
 
   f32x4_t acc[FP][FQ];
 #pragma unroll
@@ -780,12 +781,16 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
   };
 
   const int nk = ld.nk;
+  constexpr int NST = C::NST, NV = C::NIP + C::NIQ;   // loads of one stage, per wave
   u32x4_t sw = ld.template scales<SHORT>(0);
   ld.load_p(smem, 0, 0);
   ld.load_q(smem, 0, 0);
   put_scales(sw, 0);
-  ld.load_p(smem, 1, nk > 1 ? 1 : 0);
-  ld.load_q(smem, 1, nk > 1 ? 1 : 0);
+#pragma unroll
+  for (int st = 1; st < C::NST; ++st) {
+    ld.load_p(smem, st, min(st, nk - 1));
+    ld.load_q(smem, st, min(st, nk - 1));
+  }
   if (!SHORT) sw = ld.template scales<false>(1);
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
@@ -807,14 +812,14 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
   // Half a step.  Two fragments ahead are read, one ahead is converted; with the last
   // two of the second half, which read the next stage, comes the step's barrier.
   auto half = [&](int kt, int q, int phase, int h) __attribute__((always_inline)) {
-    const int stage = phase & 1, ns = h ? stage ^ 1 : stage, nh = h ^ 1, nkt = kt + h;
+    const int stage = phase % NST, ns = h ? (phase + 1) % NST : stage, nh = h ^ 1, nkt = kt + h;
     auto one = [&](int i) __attribute__((always_inline)) {
       // fragment i + 1's conversion, then its slot takes fragment i + 3
       if (i == FP - 2) {
         if (h) {
-          if (!SHORT && phase == 3) stage_barrier<1>();
-          else stage_barrier<0>();                    // this stage is read, the next has landed
-          ld.load_p(smem, stage, kt + 2 < nk ? kt + 2 : nk - 1);
+          // this stage is read, the next has landed
+          stage_barrier<(NST - 2) * NV, !SHORT>(phase != 2 && (NST == 4 || phase == 3));
+          ld.load_p(smem, stage, min(kt + NST, nk - 1));
           if (!SHORT && phase == 2) put_scales(sw, q + 1);
         }
 #pragma unroll
@@ -823,7 +828,7 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
 #pragma unroll
         for (int j = 0; j < FQ; ++j) Q[j] = ldq(ns, nh, j);
       }
-      if (i == FP - 1 && h) ld.load_q(smem, stage, kt + 2 < nk ? kt + 2 : nk - 1);
+      if (i == FP - 1 && h) ld.load_q(smem, stage, min(kt + NST, nk - 1));
       P[i & 1] = i + 2 < FP ? ldp(stage, h, i + 2) : ldp(ns, nh, i + 2 - FP);
       if (i + 1 < FP) convert(P[(i + 1) & 1], sp[h][(i + 1) >> 2], (i + 1) & 3, pc[(i + 1) & 1]);
       else convert(P[0], sp[nh][0], 0, pc[0]);
@@ -888,8 +893,8 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) v
       store_f32(p, out, m0 + wm * (C::TM / C::WM) + 16 * j + r, n0 + wn * (C::TN / C::WN) + 16 * i + 4 * g, acc[i][j], vec);
 }
 
-using T256 = Tile<256, 256, 2, 4>;
-using T128 = Tile<128, 128, 2, 2>;
+using T256 = Tile<256, 256, 2, 4, 2>;
+using T128 = Tile<128, 128, 2, 2, 2>;
 
 template <class C, bool NN>
 hipError_t gemm_tiled(const GemmMx &g, int splits, int steps, float *parts, hipStream_t s) {
@@ -910,10 +915,10 @@ hipError_t gemm_tiled(const GemmMx &g, int splits, int steps, float *parts, hipS
   return hipGetLastError();
 }
 
-template <bool NN, bool BF16, int W, int NF, int MT, int UN, int ROT = 0>
+template <bool NN, bool BF16, int W, int NF, int MT, int UN>
 hipError_t gemm_rows(const GemmMx &g, hipStream_t s) {
   const dim3 grid((unsigned)((g.n + 16 * NF - 1) / (16 * NF)), (unsigned)((g.m + 16 * MT - 1) / (16 * MT)));
-  hipLaunchKernelGGL((k_gemm_mx_rows<NN, BF16, W, NF, MT, UN, ROT>), grid, dim3(64 * W), 0, s, g);
+  hipLaunchKernelGGL((k_gemm_mx_rows<NN, BF16, W, NF, MT, UN>), grid, dim3(64 * W), 0, s, g);
   return hipGetLastError();
 }
 
@@ -923,22 +928,56 @@ struct Shape {
   int tile, splits, steps;
 };
 
-Shape shape_of(int64_t m, int64_t n, int64_t k, bool nn) {
-  if (k < 128 || n < 128 || (m <= 64 && !nn && !getenv("MX_TILE"))) return {0, 1, 0};
+// The candidate with the least modelled time, in microseconds on an idle MI355X.  The
+// constants are fitted to 150 shapes (m 1 .. 4096, n and k 128 .. 28672, both output
+// types) timed under every candidate; the choice averages 1.2% over the best one's time
+// and was 19% over at worst, where always taking the 256-tiles costs 2x on average.
+//   few rows:  8 waves' steps in turn, or the operands' bytes, whichever is longer;
+//   128-tiles: two workgroups a CU, a step of both 0.96 us, of one alone 0.62;
+//   256-tiles: one workgroup a CU, 1.26 us a step (2.14 float32, its matrix rate is half);
+//   a K split: the join's launch, and its partial sums' bytes.
+Shape shape_of(int64_t m, int64_t n, int64_t k, bool nn, bool bf16) {
   const int nk = (int)((k + kRowB - 1) / kRowB);
-  if (const char *e = getenv("MX_TILE")) { int t = 256, sp = 1; sscanf(e, "%d,%d", &t, &sp); if (!t) return {0, 1, 0}; int st = ((nk + sp - 1) / sp + 3) / 4 * 4; return {t, (nk + st - 1) / st, st}; }
-  return {256, 1, nk};
+  Shape best{0, 1, 0};
+  double least = 1e30;
+  auto consider = [&](const Shape &s, double us) {
+    if (us < least) least = us, best = s;
+  };
+  const bool tiles = k >= kRowB && (!nn || n >= 128);   // scale words: 4 blocks along k (NN: and n)
+  if (!tiles || (!nn && m <= 256)) {
+    const int rows = m <= 16 ? 16 : m <= 32 ? 32 : 64;
+    const double step = rows == 16 ? 0.5 : rows == 32 ? 1.1 : 2.7, rate = rows == 16 ? 5.8e6 : rows == 32 ? 3.1e6 : 2.3e6;
+    const double us = std::max(step * ((nk + 7) / 8), (double)n * k * ((m + rows - 1) / rows) / rate);
+    consider({0, 1, 0}, 4.9 + us * (bf16 ? 1.0 : 1.2));
+  }
+  if (!tiles) return best;
+  static const int kSplits[] = {1, 2, 3, 4, 6, 8, 16};
+  for (int want : kSplits) {
+    const int steps = std::min(((nk + want - 1) / want + 3) / 4 * 4, nk), splits = (nk + steps - 1) / steps;
+    if (splits != want) continue;
+    const double join = splits > 1 ? 2.5 + (double)splits * m * n * 4 / 2.3e6 : 0.0;
+    const int64_t t128 = (m + 127) / 128 * ((n + 127) / 128) * splits, t256 = (m + 255) / 256 * ((n + 255) / 256) * splits;
+    const double one = bf16 ? 0.62 : 0.98, two = bf16 ? 0.96 : 1.23;
+    const int64_t pairs = t128 / 512, rest = t128 % 512;
+    double us = 2.1 + pairs * (1.5 + steps * two) + join;
+    if (rest) us += 1.5 + steps * (rest <= 256 ? one : one + (two - one) * (rest - 256) / 256);
+    consider({128, splits, steps}, us);
+    consider({256, splits, steps}, 3.4 + (t256 + 255) / 256 * (2.0 + steps * (bf16 ? 1.26 : 2.14)) + join);
+  }
+  return best;
 }
 
 }  // namespace
 
+// What either output type may need.
 int64_t gemm_mx_workspace(int64_t m, int64_t n, int64_t k, bool nn) {
-  const Shape sh = shape_of(m, n, k, nn);
-  return sh.splits > 1 ? sh.splits * m * ((n + 3) / 4 * 4) * (int64_t)sizeof(float) : 0;
+  int splits = 1;
+  for (const bool bf16 : {false, true}) splits = std::max(splits, shape_of(m, n, k, nn, bf16).splits);
+  return splits > 1 ? splits * m * ((n + 3) / 4 * 4) * (int64_t)sizeof(float) : 0;
 }
 
 hipError_t launch_gemm_mx(const GemmMx &g, void *ws, hipStream_t s) {
-  const Shape sh = shape_of(g.m, g.n, g.k, g.nn);
+  const Shape sh = shape_of(g.m, g.n, g.k, g.nn, g.bf16);
   float *parts = static_cast<float *>(ws);
   if (sh.tile == 256)
     return g.nn ? gemm_tiled<T256, true>(g, sh.splits, sh.steps, parts, s)
@@ -947,16 +986,6 @@ hipError_t launch_gemm_mx(const GemmMx &g, void *ws, hipStream_t s) {
     return g.nn ? gemm_tiled<T128, true>(g, sh.splits, sh.steps, parts, s)
                 : gemm_tiled<T128, false>(g, sh.splits, sh.steps, parts, s);
   if (g.nn) return g.bf16 ? gemm_rows<true, true, 4, 1, 1, 1>(g, s) : gemm_rows<true, false, 4, 1, 1, 1>(g, s);
-  if (const char *e = getenv("MX_ROWS")) { int c = atoi(e);
-    if (c == 1) return gemm_rows<false, true, 8, 1, 1, 2>(g, s);
-    if (c == 2) return gemm_rows<false, true, 8, 1, 1, 1>(g, s);
-    if (c == 3) return gemm_rows<false, true, 4, 1, 1, 2>(g, s);
-    if (c == 4) return gemm_rows<false, true, 16, 1, 1, 1>(g, s);
-    if (c == 5) return gemm_rows<false, true, 8, 1, 1, 1, 1>(g, s);
-    if (c == 6) return gemm_rows<false, true, 8, 1, 1, 2, 1>(g, s);
-    if (c == 7) return gemm_rows<false, true, 8, 2, 1, 1>(g, s);
-    if (c == 8) return gemm_rows<false, true, 8, 1, 1, 3>(g, s);
-  }
   if (g.m <= 16) return g.bf16 ? gemm_rows<false, true, 8, 1, 1, 1>(g, s) : gemm_rows<false, false, 8, 1, 1, 1>(g, s);
   if (g.m <= 32) return g.bf16 ? gemm_rows<false, true, 8, 1, 2, 1>(g, s) : gemm_rows<false, false, 8, 1, 2, 1>(g, s);
   return g.bf16 ? gemm_rows<false, true, 8, 2, 4, 1>(g, s) : gemm_rows<false, false, 8, 2, 4, 1>(g, s);
