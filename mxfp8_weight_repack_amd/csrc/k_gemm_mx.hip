@@ -296,14 +296,23 @@ __device__ __forceinline__ f32x4_t mx_mma_pq(int ip, int iq, const i32x8_t &p, c
 
 // Workgroup id -> output tile.  Workgroup i runs on XCD i % 8, each with its own L2:
 // each XCD gets one contiguous eighth of an order that walks the tiles in strips of
-// 8 along m, so the 32 workgroups an XCD runs at once share 8 x 4 operand panels.
+// 4 along m, so the 32 workgroups an XCD runs at once share 4 + 8 operand panels
+// (8192 x 28672 x 8192: 1.43-1.44 ms; strips of 8 1.47, of 16 1.49-1.50).
 __device__ __forceinline__ void tile_of(int64_t id, int64_t tiles_m, int64_t tiles_n, int64_t &tm, int64_t &tn) {
   const int64_t total = tiles_m * tiles_n, q = total >> 3, rem = total & 7, x = id & 7;
   const int64_t pos = x * q + min(x, rem) + (id >> 3);
-  const int64_t strip = pos / (8 * tiles_n), in = pos - strip * 8 * tiles_n;
-  const int64_t h = min<int64_t>(8, tiles_m - strip * 8);
+  const int64_t strip = pos / (4 * tiles_n), in = pos - strip * 4 * tiles_n;
+  const int64_t h = min<int64_t>(4, tiles_m - strip * 4);
   tn = in / h;
-  tm = strip * 8 + in - tn * h;
+  tm = strip * 4 + in - tn * h;
+}
+
+// The same for the n side of NN, whose stage rows are k, TN bytes each.  A transposing read
+// takes 16 bytes of 8 consecutive k rows for each 16 lanes, two such groups, 16 rows apart,
+// in one LDS pass: their 16 chunks must be all different over two 128-byte halves.
+template <int TN>
+__device__ __forceinline__ int swz_k(int k) {
+  return TN == 256 ? (k & 7) | (k >> 1 & 8) : (k >> 1 & 3) | (k >> 2 & 4);
 }
 
 // All of a workgroup's LDS accesses are done, and its loads but the newest LEFT, one more
@@ -346,9 +355,8 @@ struct Loader {
     inq = chunk * 16 < kt;
     gq = p.a + m0 * p.k;
     if (NN) {
-      // stage rows are k, 256-byte rows of TN columns; chunk c of row k at c ^ (k & 7)
       constexpr int CPR = C::TN / 16, RPI = 64 / CPR;
-      const int kr = RPI * wave + lane / CPR, c = (lane % CPR) ^ (kr & 7);
+      const int kr = RPI * wave + lane / CPR, c = (lane % CPR) ^ swz_k<C::TN>(kr);
       voffp = n0 + c * 16 < p.n ? kr * (int)p.n + c * 16 : INT32_MAX - 15;
       inp = true;                                     // k rows past K are past the resource
       gp = p.b + n0;
@@ -529,7 +537,7 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
   const int rowp = (wn * (C::TN / C::WN) + r) * kRowB + cof, rowq = C::NST * C::SEGP + (wm * (C::TM / C::WM) + r) * kRowB + cof;
   // NN: fragment i's 16 columns are one chunk of each k row; a transposing read hands
   // a lane one column's 8 k (rows kb .. kb + 7), read 16 bytes a row by lane pairs
-  const int trp = (16 * g + (r >> 1)) * C::TN + (((r >> 1) << 4) ^ (wn * (C::TN / C::WN))) + 8 * (r & 1);
+  const int trp = (16 * g + (r >> 1)) * C::TN + ((swz_k<C::TN>(16 * g + (r >> 1)) << 4) ^ (wn * (C::TN / C::WN))) + 8 * (r & 1);
 
   f32x4_t acc[FP][FQ];
 #pragma unroll
@@ -731,7 +739,7 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
   constexpr int FP = C::FP, FQ = C::FQ;
   const int cof = (g ^ swz(r)) * 16;
   const int rowp = (wn * (C::TN / C::WN) + r) * kRowB + cof, rowq = C::NST * C::SEGP + (wm * (C::TM / C::WM) + r) * kRowB + cof;
-  const int trp = (16 * g + (r >> 1)) * C::TN + (((r >> 1) << 4) ^ (wn * (C::TN / C::WN))) + 8 * (r & 1);
+  const int trp = (16 * g + (r >> 1)) * C::TN + ((swz_k<C::TN>(16 * g + (r >> 1)) << 4) ^ (wn * (C::TN / C::WN))) + 8 * (r & 1);
 
   f32x4_t acc[FP][FQ];
 #pragma unroll
