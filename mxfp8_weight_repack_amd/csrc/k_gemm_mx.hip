@@ -25,6 +25,8 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cstdlib>
+#include <cstdio>
 
 #include "internal.h"
 
@@ -244,19 +246,24 @@ __global__ __launch_bounds__(64 * W) void k_gemm_mx_rows(GemmMx p) {
 constexpr int kBufWord3 = 0x00020000;                // raw gfx9-family buffer resource
 constexpr int kRowB = 128;                           // bytes (= k) of a stage row
 
-template <int TN_, int TM_, int WN_, int WM_, int NST_>
+// KG groups of WN x WM waves make the same tile over KG parts of its K and add their sums
+// in LDS: where there are too few tiles to give every CU two workgroups, a second group
+// hides what one cannot.
+template <int TN_, int TM_, int WN_, int WM_, int KG_>
 struct Tile {
-  static constexpr int TN = TN_, TM = TM_, WN = WN_, WM = WM_, NW = WN * WM, NT = 64 * NW, NST = NST_;
+  static constexpr int TN = TN_, TM = TM_, WN = WN_, WM = WM_, NW = WN * WM, NT = 64 * NW, KG = KG_, NST = 2;
   static constexpr int FP = TN / WN / 16, FQ = TM / WM / 16;     // 16-row fragments of a wave: n side, m side
   static constexpr int SEGP = TN * kRowB, SEGQ = TM * kRowB, STAGE = SEGP + SEGQ;
   static constexpr int NIP = SEGP / 1024 / NW, NIQ = SEGQ / 1024 / NW;   // buffer loads per wave and stage
   static constexpr int GRPS = (TN + TM) / 64;                   // 64-row scale groups, n side first
   static constexpr int RING = 2 * 4 * GRPS * 64 * 4;            // scale words: 2 x 4 steps
   static constexpr int EPI = TM * (TN + 8) * 2;                 // bfloat16 output tile
-  static constexpr int LDS = NST * STAGE + RING > EPI ? NST * STAGE + RING : EPI;
-  static constexpr int WPS = NT * (163840 / LDS) / 256;         // waves per SIMD
+  static constexpr int GROUP = NST * STAGE + RING;             // LDS of one wave group
+  static constexpr int LDS = KG * GROUP > EPI ? KG * GROUP : EPI;
+  static constexpr int WPS = NT * KG * (163840 / LDS) / 256;    // waves per SIMD
   static_assert(FP % 4 == 0 && FQ == 4 && NT == TN + TM, "a thread per scale row, 64-row groups");
-  static_assert((NST == 2 || NST == 4) && (NST - 1) * SEGP + SEGP / WN <= 65536, "stages are LDS read offsets");
+  static_assert((NST - 1) * SEGP + SEGP / WN <= 65536, "stages are LDS read offsets");
+  static_assert(KG == 1 || (KG == 2 && FP * FQ * 16 * NT <= GROUP), "the other group's sums fit its LDS");
 };
 
 // Chunk swizzle of a stage row: 8 consecutive rows, one LDS pass, hit 8 different chunks.
@@ -268,6 +275,13 @@ __device__ __forceinline__ uint32_t lane_transpose(uint32_t x, int lane) {
   x = __builtin_amdgcn_perm(a[1], a[0], lane < 32 ? 0x05040100u : 0x07060302u);
   auto b = __builtin_amdgcn_permlane16_swap(x, x, false, false);      // [0]: even rows of 16 twice, [1]: odd
   return __builtin_amdgcn_perm(b[1], b[0], lane & 16 ? 0x07030501u : 0x06020400u);
+}
+
+// The lane's number anew, for where keeping it would cost a register over the loop.
+__device__ __forceinline__ int lane_again() {
+  int all = -1;
+  asm volatile("" : "+s"(all));
+  return __builtin_amdgcn_mbcnt_hi(all, __builtin_amdgcn_mbcnt_lo(all, 0));
 }
 
 // One 8-bit matrix instruction; ip, iq: byte selects of the scale words (constants once unrolled).
@@ -315,17 +329,33 @@ __device__ __forceinline__ int swz_k(int k) {
   return TN == 256 ? (k & 7) | (k >> 1 & 8) : (k >> 1 & 3) | (k >> 2 & 4);
 }
 
-// All of a workgroup's LDS accesses are done, and its loads but the newest LEFT, one more
-// if `scales` (a constant once unrolled).  The barrier builtin would wait for all loads.
-template <int LEFT, bool SCALES>
-__device__ __forceinline__ void stage_barrier(bool scales) {
-  if (SCALES && scales) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT + 1) : "memory");
-  else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
+// All of a workgroup's LDS accesses and loads are done, but the newest load if `newest`
+// (a constant once unrolled).  The barrier builtin would wait for that one as well.
+template <bool SCALES>
+__device__ __forceinline__ void stage_barrier(bool newest) {
+  if (SCALES && newest) asm volatile("s_waitcnt vmcnt(1) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// 16 bytes per lane from memory straight to LDS, lane i at dst + 16 i.
-__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, char *dst, int voff, int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 16, voff, soff, 0, 0);
+// 16 bytes per lane from `bytes` of memory at base straight to LDS, lane i at dst + 16 i;
+// zeros past the end.  The caller waits
+// for it.  PLAIN: the compiler takes a transposing read as one that any load to LDS in
+// flight may write under, and puts a wait for all of them before it (NN 8192^3: 401
+// against 468 us without); as plain instructions the loads are none of its concern.  (M0 is
+// the compiler's own to set before each of its uses; none is left in such a kernel.)
+template <bool PLAIN>
+__device__ __forceinline__ void dma16(const uint8_t *base, int64_t bytes, char *dst, int voff, int soff) {
+  if (PLAIN) {
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    const u32x4_t w = {(uint32_t)b, (uint32_t)(b >> 32) & 0xFFFFu, (uint32_t)bytes, (uint32_t)kBufWord3};
+    const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)dst;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff), "s"(w),
+                 "s"(soff));
+  } else {
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), 0, (int)bytes, kBufWord3);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 16, voff, soff, 0, 0);
+  }
 }
 
 // The operand stages' addressing, shared by both matrix forms.
@@ -347,7 +377,7 @@ struct Loader {
       : p(p_), n0(n0_), m0(m0_), kt0(kt0_), nk(nk_) {
     const int t = threadIdx.x;
     lane = t & 63;
-    wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    wave = __builtin_amdgcn_readfirstlane(t >> 6) % C::NW;
     last = (int)((p.k + kRowB - 1) / kRowB) - 1;
     const int kt = (int)(p.k - (int64_t)last * kRowB);        // k of the last step (a multiple of 32)
     const int row = 8 * wave + (lane >> 3), chunk = (lane & 7) ^ swz(row);
@@ -413,33 +443,28 @@ struct Loader {
   // them for as long as all waves' loads take to issue.
   __device__ __forceinline__ void load_p(char *smem, int stage, int kt) const {
     kt += kt0;
-    const int v = kt < last || inp ? voffp : INT32_MAX - 15;
+    const int v = kt < last || (inp && (C::KG == 1 || kt == last)) ? voffp : INT32_MAX - 15;
     char *sp = smem + stage * C::SEGP + wave * 1024;
     const int64_t k0 = (int64_t)kt * kRowB;
     if (NN) {
       constexpr int RPI = 64 / (C::TN / 16);
-      const int64_t left = (p.k - k0 < kRowB ? p.k - k0 : (int64_t)kRowB) * p.n - n0;
-      const __amdgpu_buffer_rsrc_t r =
-          __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(gp + k0 * p.n), 0, (int)left, kBufWord3);
+      int64_t left = (p.k - k0 < kRowB ? p.k - k0 : (int64_t)kRowB) * p.n - n0;
+      if (C::KG > 1) left = max(left, (int64_t)0);
 #pragma unroll
-      for (int i = 0; i < C::NIP; ++i) dma16(r, sp + i * C::NW * 1024, v, i * RPI * C::NW * (int)p.n);
+      for (int i = 0; i < C::NIP; ++i) dma16<NN>(gp + k0 * p.n, left, sp + i * C::NW * 1024, v, i * RPI * C::NW * (int)p.n);
     } else {
       const int64_t rows = p.n - n0 < C::TN ? p.n - n0 : (int64_t)C::TN;
-      const __amdgpu_buffer_rsrc_t r =
-          __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(gp), 0, (int)(rows * p.k), kBufWord3);
 #pragma unroll
-      for (int i = 0; i < C::NIP; ++i) dma16(r, sp + i * C::NW * 1024, v, i * 8 * C::NW * (int)p.k + (int)k0);
+      for (int i = 0; i < C::NIP; ++i) dma16<NN>(gp, rows * p.k, sp + i * C::NW * 1024, v, i * 8 * C::NW * (int)p.k + (int)k0);
     }
   }
   __device__ __forceinline__ void load_q(char *smem, int stage, int kt) const {
     kt += kt0;
-    const int v = kt < last || inq ? voffq : INT32_MAX - 15;
+    const int v = kt < last || (inq && (C::KG == 1 || kt == last)) ? voffq : INT32_MAX - 15;
     char *sq = smem + C::NST * C::SEGP + stage * C::SEGQ + wave * 1024;
     const int64_t rows = p.m - m0 < C::TM ? p.m - m0 : (int64_t)C::TM;
-    const __amdgpu_buffer_rsrc_t r =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(gq), 0, (int)(rows * p.k), kBufWord3);
 #pragma unroll
-    for (int i = 0; i < C::NIQ; ++i) dma16(r, sq + i * C::NW * 1024, v, i * 8 * C::NW * (int)p.k + kt * kRowB);
+    for (int i = 0; i < C::NIQ; ++i) dma16<NN>(gq, rows * p.k, sq + i * C::NW * 1024, v, i * 8 * C::NW * (int)p.k + kt * kRowB);
   }
 
   // The bytes of this wave's 64 scale rows for steps 4 q .. 4 q + 3 as they lie in memory,
@@ -465,7 +490,7 @@ struct Loader {
   // Step 4 q + j's word for the matrix instruction: lane 16 g + r gets block g's bytes of
   // the rows r, 16 + r, 32 + r, 48 + r.
   template <bool SHORT>
-  __device__ __forceinline__ void scale_words(const u32x4_t &raw, int q, uint32_t (&out)[4]) const {
+  __device__ __forceinline__ void scale_words(const u32x4_t &raw, int q, int lane, uint32_t (&out)[4]) const {
     u32x4_t w = raw;
     // what was read from before its place moves down (no branches here: see pin below);
     // zeros come in beside codes that are all zero
@@ -487,6 +512,25 @@ struct Loader {
   }
 };
 
+
+// The second wave group's sums through LDS to the first, which goes on alone.
+template <class C>
+__device__ __forceinline__ bool join_groups(char *all, int grp, f32x4_t (&acc)[C::FP][C::FQ]) {
+  f32x4_t *q = reinterpret_cast<f32x4_t *>(all + C::GROUP) + threadIdx.x % C::NT;
+  if (grp == 1) {
+#pragma unroll
+    for (int i = 0; i < C::FP; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FQ; ++j) q[(i * C::FQ + j) * C::NT] = acc[i][j];
+  }
+  __syncthreads();
+  if (grp == 1) return false;
+#pragma unroll
+  for (int i = 0; i < C::FP; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FQ; ++j) acc[i][j] += q[(i * C::FQ + j) * C::NT];
+  return true;
+}
 
 // One K split's sums of a tile, dense M x N4 float32 per split (N4: N to a multiple of 4).
 template <class C>
@@ -519,14 +563,18 @@ __global__ __launch_bounds__(256) void k_gemm_mx_join(GemmMx p, const float *par
 }
 
 template <class C, bool NN, bool SHORT>
-__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C::WPS))) void k_gemm_mx8(GemmMx p, int64_t tiles_m,
+__global__ __launch_bounds__(C::NT * C::KG) __attribute__((amdgpu_waves_per_eu(C::WPS, C::WPS))) void k_gemm_mx8(GemmMx p, int64_t tiles_m,
                                                                                              int64_t tiles_n, int steps, float *parts) {
-  __shared__ __align__(1024) char smem[C::LDS];
+  __shared__ __align__(1024) char all[C::LDS];
   int64_t tm, tn;
   tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
   const int64_t n0 = tn * C::TN, m0 = tm * C::TM;
-  const int kt0 = (int)blockIdx.y * steps;
-  const Loader<C, NN> ld(p, n0, m0, kt0, min(steps, (int)((p.k + kRowB - 1) / kRowB) - kt0));
+  // `steps`: of one wave group.  Groups past the last step run as many, on zeros: the
+  // barriers are the whole workgroup's.
+  const int grp = C::KG > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / C::NT) : 0;
+  char *smem = all + grp * C::GROUP;
+  const int kt0 = (int)blockIdx.y * C::KG * steps;
+  const Loader<C, NN> ld(p, n0, m0, kt0 + grp * steps, min(steps, (int)((p.k + kRowB - 1) / kRowB) - kt0));
   const int lane = ld.lane, wave = ld.wave, wn = wave / C::WM, wm = wave % C::WM;
   const int r = lane & 15, g = lane >> 4;
   uint32_t *ring = reinterpret_cast<uint32_t *>(smem + C::NST * C::STAGE);
@@ -585,12 +633,13 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
   i32x8_t P[HP], Q0[HQ], Q1[HQ];
   int sp[2][FP / 4], sq[2];
   auto put_scales = [&](const u32x4_t &raw, int q) __attribute__((always_inline)) {
+    const int lane = lane_again();
     uint32_t w[4];
-    ld.template scale_words<SHORT>(raw, q, w);
+    ld.template scale_words<SHORT>(raw, q, lane, w);
 #pragma unroll
     for (int j = 0; j < 4; ++j) ring[((4 * (q & 1) + j) * C::GRPS + wave) * 64 + lane] = w[j];
   };
-  // Control flow keeps nothing from moving matrix instructions to where their sums are
+  // Control flow lets the compiler move matrix instructions to where their sums are
   // next used, past a barrier: this pins them.
   auto pin = [&]() __attribute__((always_inline)) {
 #pragma unroll
@@ -600,7 +649,7 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
   };
 
   const int nk = ld.nk;
-  constexpr int NST = C::NST, NV = C::NIP + C::NIQ;   // loads of one stage, per wave
+  constexpr int NST = C::NST;
   u32x4_t sw = ld.template scales<SHORT>(0);
   ld.load_p(smem, 0, 0);
   ld.load_q(smem, 0, 0);
@@ -649,16 +698,17 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
   auto step = [&](int kt, int q, int phase, i32x8_t(&QX)[HQ], i32x8_t(&QY)[HQ], const int (&s)[FP / 4], int t,
                   int (&sn)[FP / 4], int &tn_) __attribute__((always_inline)) {
     const int stage = phase % NST, next = (phase + 1) % NST;
+    // here, where the fewest fragments are held
+    if (!SHORT && phase == 3) put_scales(sw, q + 1);
 #pragma unroll
     for (int j = 0; j < HQ; ++j) QY[j] = ldq(stage, HQ + j);
     mma(0, QX, 0, s, t, 2 * HQ, 0, false, none);
     mma(0, QY, HQ, s, t, 0, 0, true, [&](int i) __attribute__((always_inline)) { return ldp(stage, HP + i); });
-    // every wave has read this step's stage, and the next one has landed: younger are the
-    // later stages' loads and, but in phase 2, the scales' (one load, or four)
-    stage_barrier<(NST - 2) * NV, !SHORT>(phase != 2 && (NST == 4 || phase == 3));
+    // every wave has read this step's stage, and the next one has landed: younger is only,
+    // in phase 0, the scales' load (or the last of its four)
+    stage_barrier<!SHORT>(phase == 0);
     // near the end the reload repeats the last step into a stage nobody reads again
     ld.load_p(smem, stage, min(kt + NST, nk - 1));
-    if (!SHORT && phase == 2) put_scales(sw, q + 1);
 #pragma unroll
     for (int i = 0; i < FP / 4; ++i) sn[i] = lds_scale(kt + 1, gp + i);
     tn_ = lds_scale(kt + 1, gq);
@@ -668,7 +718,7 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
     for (int j = 0; j < HQ; ++j) QY[j] = ldq(next, j);
     mma(HP, QX, 0, s, t, 2 * HQ, C::NIQ, true, [&](int i) __attribute__((always_inline)) { return ldp(next, i); });
     // last of the step's loads, so the next barrier's wait can leave it in flight
-    if (!SHORT && phase == 2) {
+    if (!SHORT && phase == 3) {
       pin();
       sw = ld.template scales<false>(q + 2);
     }
@@ -686,8 +736,13 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // the trailing reloads
   __syncthreads();
 
+  if (C::KG > 1 && !join_groups<C>(all, grp, acc)) return;
+  // the lane again, so that nothing of it is kept in registers over the loop
+  int t_end = threadIdx.x;
+  asm volatile("" : "+v"(t_end));
+  const int r_end = t_end & 15, g_end = t_end >> 4 & 3;
   if (parts) {
-    store_part<C>(p, parts, n0, m0, wn, wm, lane, acc);
+    store_part<C>(p, parts, n0, m0, wn, wm, t_end & 63, acc);
     return;
   }
   // bfloat16 tile through LDS (rows m), then whole rows of 16-byte stores
@@ -698,13 +753,13 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
 #pragma unroll
     for (int j = 0; j < FQ; ++j) {
       const f32x4_t &v = acc[i][j];
-      uint2 *d = reinterpret_cast<uint2 *>(lt + (wm * (C::TM / C::WM) + 16 * j + r) * LP + wn * (C::TN / C::WN) + 16 * i + 4 * g);
+      uint2 *d = reinterpret_cast<uint2 *>(lt + (wm * (C::TM / C::WM) + 16 * j + r_end) * LP + wn * (C::TN / C::WN) + 16 * i + 4 * g_end);
       *d = make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
     }
   __syncthreads();
   uint16_t *out = static_cast<uint16_t *>(p.out);
   constexpr int CH = C::TN / 8;
-  for (int id = threadIdx.x; id < C::TM * CH; id += C::NT) {
+  for (int id = t_end; id < C::TM * CH; id += C::NT) {
     const int row = id / CH, c = (id - row * CH) * 8;
     const int64_t m = m0 + row, n = n0 + c;
     if (m >= p.m || n >= p.n) continue;
@@ -725,14 +780,18 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
 // chunk per lane (64 k): its m-side fragments stay converted while the n side's pass by,
 // one converted (8 conversions) beside the previous one's 2 x FQ matrix instructions.
 template <class C, bool NN, bool SHORT>
-__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C::WPS))) void k_gemm_mx16(GemmMx p, int64_t tiles_m,
+__global__ __launch_bounds__(C::NT * C::KG) __attribute__((amdgpu_waves_per_eu(C::WPS, C::WPS))) void k_gemm_mx16(GemmMx p, int64_t tiles_m,
                                                                                               int64_t tiles_n, int steps, float *parts) {
-  __shared__ __align__(1024) char smem[C::LDS];
+  __shared__ __align__(1024) char all[C::LDS];
   int64_t tm, tn;
   tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
   const int64_t n0 = tn * C::TN, m0 = tm * C::TM;
-  const int kt0 = (int)blockIdx.y * steps;
-  const Loader<C, NN> ld(p, n0, m0, kt0, min(steps, (int)((p.k + kRowB - 1) / kRowB) - kt0));
+  // `steps`: of one wave group.  Groups past the last step run as many, on zeros: the
+  // barriers are the whole workgroup's.
+  const int grp = C::KG > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / C::NT) : 0;
+  char *smem = all + grp * C::GROUP;
+  const int kt0 = (int)blockIdx.y * C::KG * steps;
+  const Loader<C, NN> ld(p, n0, m0, kt0 + grp * steps, min(steps, (int)((p.k + kRowB - 1) / kRowB) - kt0));
   const int lane = ld.lane, wave = ld.wave, wn = wave / C::WM, wm = wave % C::WM;
   const int r = lane & 15, g = lane >> 4;
   uint32_t *ring = reinterpret_cast<uint32_t *>(smem + C::NST * C::STAGE);
@@ -774,12 +833,13 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
   };
   const int gp = wn * (FP / 4), gq = C::TN / 64 + wm;
   auto put_scales = [&](const u32x4_t &raw, int q) __attribute__((always_inline)) {
+    const int lane = lane_again();
     uint32_t w[4];
-    ld.template scale_words<SHORT>(raw, q, w);
+    ld.template scale_words<SHORT>(raw, q, lane, w);
 #pragma unroll
     for (int j = 0; j < 4; ++j) ring[((4 * (q & 1) + j) * C::GRPS + wave) * 64 + lane] = w[j];
   };
-  // Control flow keeps nothing from moving matrix instructions to where their sums are
+  // Control flow lets the compiler move matrix instructions to where their sums are
   // next used, past a barrier: this pins them.
   auto pin = [&]() __attribute__((always_inline)) {
 #pragma unroll
@@ -789,7 +849,7 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
   };
 
   const int nk = ld.nk;
-  constexpr int NST = C::NST, NV = C::NIP + C::NIQ;   // loads of one stage, per wave
+  constexpr int NST = C::NST;
   u32x4_t sw = ld.template scales<SHORT>(0);
   ld.load_p(smem, 0, 0);
   ld.load_q(smem, 0, 0);
@@ -826,9 +886,8 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
       if (i == FP - 2) {
         if (h) {
           // this stage is read, the next has landed
-          stage_barrier<(NST - 2) * NV, !SHORT>(phase != 2 && (NST == 4 || phase == 3));
+          stage_barrier<!SHORT>(phase == 0);
           ld.load_p(smem, stage, min(kt + NST, nk - 1));
-          if (!SHORT && phase == 2) put_scales(sw, q + 1);
         }
 #pragma unroll
         for (int k = 0; k < FP / 4; ++k) sp[nh][k] = lds_scale(nkt, nh, gp + k);
@@ -866,9 +925,10 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
       }
       __builtin_amdgcn_sched_barrier(0);
     };
+    if (!SHORT && phase == 3 && !h) put_scales(sw, q + 1);
 #pragma unroll
     for (int i = 0; i < FP; ++i) one(i);
-    if (!SHORT && phase == 2 && h) {
+    if (!SHORT && phase == 3 && h) {
       pin();
       sw = ld.template scales<false>(q + 2);
     }
@@ -888,8 +948,13 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
     if (kt + 4 >= nk) break;
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // the trailing reloads
+  if (C::KG > 1 && !join_groups<C>(all, grp, acc)) return;
+  // the lane again, so that nothing of it is kept in registers over the loop
+  int t_end = threadIdx.x;
+  asm volatile("" : "+v"(t_end));
+  const int r_end = t_end & 15, g_end = t_end >> 4 & 3;
   if (parts) {
-    store_part<C>(p, parts, n0, m0, wn, wm, lane, acc);
+    store_part<C>(p, parts, n0, m0, wn, wm, t_end & 63, acc);
     return;
   }
   float *out = static_cast<float *>(p.out);
@@ -898,16 +963,18 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
   for (int j = 0; j < FQ; ++j)
 #pragma unroll
     for (int i = 0; i < FP; ++i)
-      store_f32(p, out, m0 + wm * (C::TM / C::WM) + 16 * j + r, n0 + wn * (C::TN / C::WN) + 16 * i + 4 * g, acc[i][j], vec);
+      store_f32(p, out, m0 + wm * (C::TM / C::WM) + 16 * j + r_end, n0 + wn * (C::TN / C::WN) + 16 * i + 4 * g_end,
+                acc[i][j], vec);
 }
 
-using T256 = Tile<256, 256, 2, 4, 2>;
-using T128 = Tile<128, 128, 2, 2, 2>;
+using T256 = Tile<256, 256, 2, 4, 1>;
+using T128 = Tile<128, 128, 2, 2, 1>;
+using T128K = Tile<128, 128, 2, 2, 2>;
 
 template <class C, bool NN>
 hipError_t gemm_tiled(const GemmMx &g, int splits, int steps, float *parts, hipStream_t s) {
   const int64_t tm = (g.m + C::TM - 1) / C::TM, tn = (g.n + C::TN - 1) / C::TN;
-  const dim3 grid((unsigned)(tm * tn), (unsigned)splits), block(C::NT);
+  const dim3 grid((unsigned)(tm * tn), (unsigned)splits), block(C::NT * C::KG);
   if (splits == 1) parts = nullptr;
   const bool sh = g.k <= 4 * kRowB;
   if (g.bf16 && sh) hipLaunchKernelGGL((k_gemm_mx8<C, NN, true>), grid, block, 0, s, g, tm, tn, steps, parts);
@@ -946,6 +1013,7 @@ struct Shape {
 //   a K split: the join's launch, and its partial sums' bytes.
 Shape shape_of(int64_t m, int64_t n, int64_t k, bool nn, bool bf16) {
   const int nk = (int)((k + kRowB - 1) / kRowB);
+  if (const char *e = getenv("MX_TILE")) { int t = 256, sp = 1; sscanf(e, "%d,%d", &t, &sp); if (t && k >= 128 && (n >= 128 || !nn)) { int gr = t == 129 ? 2 : 1; int st = ((nk + sp * gr - 1) / (sp * gr) + 3) / 4 * 4; return {t, (nk + st * gr - 1) / (st * gr), st}; } }
   Shape best{0, 1, 0};
   double least = 1e30;
   auto consider = [&](const Shape &s, double us) {
@@ -990,6 +1058,9 @@ hipError_t launch_gemm_mx(const GemmMx &g, void *ws, hipStream_t s) {
   if (sh.tile == 256)
     return g.nn ? gemm_tiled<T256, true>(g, sh.splits, sh.steps, parts, s)
                 : gemm_tiled<T256, false>(g, sh.splits, sh.steps, parts, s);
+  if (sh.tile == 129)
+    return g.nn ? gemm_tiled<T128K, true>(g, sh.splits, sh.steps, parts, s)
+                : gemm_tiled<T128K, false>(g, sh.splits, sh.steps, parts, s);
   if (sh.tile == 128)
     return g.nn ? gemm_tiled<T128, true>(g, sh.splits, sh.steps, parts, s)
                 : gemm_tiled<T128, false>(g, sh.splits, sh.steps, parts, s);
