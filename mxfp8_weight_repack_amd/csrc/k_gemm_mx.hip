@@ -25,8 +25,6 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <cstdlib>
-#include <cstdio>
 
 #include "internal.h"
 
@@ -997,24 +995,25 @@ hipError_t gemm_rows(const GemmMx &g, hipStream_t s) {
   return hipGetLastError();
 }
 
-// How a product runs: few-row kernel (tile 0), or tiles of 256 or 128 with K in `splits`
-// runs of `steps` 128-k steps (a multiple of 4: scale words come 4 steps at a time).
+// How a product runs: few-row kernel (tile 0), or tiles of 256 or 128 by `groups` wave
+// groups, with K in `splits` parts, each of `groups` runs of `steps` 128-k steps (a
+// multiple of 4: scale words come 4 steps at a time).
 struct Shape {
-  int tile, splits, steps;
+  int tile, groups, splits, steps;
 };
 
 // The candidate with the least modelled time, in microseconds on an idle MI355X.  The
-// constants are fitted to 150 shapes (m 1 .. 4096, n and k 128 .. 28672, both output
-// types) timed under every candidate; the choice averages 1.2% over the best one's time
-// and was 19% over at worst, where always taking the 256-tiles costs 2x on average.
-//   few rows:  8 waves' steps in turn, or the operands' bytes, whichever is longer;
-//   128-tiles: two workgroups a CU, a step of both 0.96 us, of one alone 0.62;
-//   256-tiles: one workgroup a CU, 1.26 us a step (2.14 float32, its matrix rate is half);
+// constants are fitted to 300 timed choices from m 1 .. 4096, n and k 128 .. 28672, both
+// operand forms and output types; what it picks takes 1.5% more than the best candidate
+// on average and 27% more at worst.  Always 128-tiles: 19% and 4x.
+//   few rows:  the operands' bytes as the kernel gets them, or its waves' steps in turn;
+//   128-tiles: two workgroups a CU, 0.95 us for a step of both, 0.61 for one alone;
+//   128-tiles by two wave groups: one workgroup a CU, 1.1 us for a step of both;
+//   256-tiles: one workgroup a CU, 1.21 us a step (1.87 float32, its matrix rate is half);
 //   a K split: the join's launch, and its partial sums' bytes.
 Shape shape_of(int64_t m, int64_t n, int64_t k, bool nn, bool bf16) {
   const int nk = (int)((k + kRowB - 1) / kRowB);
-  if (const char *e = getenv("MX_TILE")) { int t = 256, sp = 1; sscanf(e, "%d,%d", &t, &sp); if (t && k >= 128 && (n >= 128 || !nn)) { int gr = t == 129 ? 2 : 1; int st = ((nk + sp * gr - 1) / (sp * gr) + 3) / 4 * 4; return {t, (nk + st * gr - 1) / (st * gr), st}; } }
-  Shape best{0, 1, 0};
+  Shape best{0, 1, 1, 0};
   double least = 1e30;
   auto consider = [&](const Shape &s, double us) {
     if (us < least) least = us, best = s;
@@ -1022,24 +1021,30 @@ Shape shape_of(int64_t m, int64_t n, int64_t k, bool nn, bool bf16) {
   const bool tiles = k >= kRowB && (!nn || n >= 128);   // scale words: 4 blocks along k (NN: and n)
   if (!tiles || (!nn && m <= 256)) {
     const int rows = m <= 16 ? 16 : m <= 32 ? 32 : 64;
-    const double step = rows == 16 ? 0.5 : rows == 32 ? 1.1 : 2.7, rate = rows == 16 ? 5.8e6 : rows == 32 ? 3.1e6 : 2.3e6;
-    const double us = std::max(step * ((nk + 7) / 8), (double)n * k * ((m + rows - 1) / rows) / rate);
-    consider({0, 1, 0}, 4.9 + us * (bf16 ? 1.0 : 1.2));
+    const double rate = rows == 16 ? 5.8e6 : rows == 32 ? 3.4e6 : 5.0e6;
+    const double us = std::max(rows == 64 ? 1.34 * ((nk + 7) / 8) : 0.0, (double)n * k * ((m + rows - 1) / rows) / rate);
+    consider({0, 1, 1, 0}, 6.7 + us * (bf16 ? 1.0 : 1.2));
   }
   if (!tiles) return best;
-  static const int kSplits[] = {1, 2, 3, 4, 6, 8, 16};
-  for (int want : kSplits) {
-    const int steps = std::min(((nk + want - 1) / want + 3) / 4 * 4, nk), splits = (nk + steps - 1) / steps;
-    if (splits != want) continue;
-    const double join = splits > 1 ? 2.5 + (double)splits * m * n * 4 / 2.3e6 : 0.0;
-    const int64_t t128 = (m + 127) / 128 * ((n + 127) / 128) * splits, t256 = (m + 255) / 256 * ((n + 255) / 256) * splits;
-    const double one = bf16 ? 0.62 : 0.98, two = bf16 ? 0.96 : 1.23;
-    const int64_t pairs = t128 / 512, rest = t128 % 512;
-    double us = 2.1 + pairs * (1.5 + steps * two) + join;
-    if (rest) us += 1.5 + steps * (rest <= 256 ? one : one + (two - one) * (rest - 256) / 256);
-    consider({128, splits, steps}, us);
-    consider({256, splits, steps}, 3.4 + (t256 + 255) / 256 * (2.0 + steps * (bf16 ? 1.26 : 2.14)) + join);
-  }
+  const int64_t t128 = (m + 127) / 128 * ((n + 127) / 128), t256 = (m + 255) / 256 * ((n + 255) / 256);
+  for (int groups : {1, 2})
+    for (int want : {1, 2, 3, 4, 6, 8, 16}) {
+      const int parts = groups * want, steps = ((nk + parts - 1) / parts + 3) / 4 * 4;
+      const int splits = (nk + groups * steps - 1) / (groups * steps);
+      if (splits != want || (groups == 2 && nk <= steps)) continue;
+      const double join = splits > 1 ? 3.0 + (double)splits * m * n * 4 / 2.66e6 : 0.0;
+      if (groups == 2) {
+        consider({128, 2, splits, steps}, 2.8 + (t128 * splits + 255) / 256 * (1.2 + steps * (bf16 ? 1.1 : 1.94)) + join);
+        continue;
+      }
+      const int run = std::min(steps, nk);
+      const double one = bf16 ? 0.61 : 0.9, two = bf16 ? 0.95 : 1.13;
+      const int64_t pairs = t128 * splits / 512, rest = t128 * splits % 512;
+      double us = 3.2 + pairs * (1.4 + run * two) + join;
+      if (rest) us += 1.4 + run * (rest <= 256 ? one : one + (two - one) * (rest - 256) / 256);
+      consider({128, 1, splits, steps}, us);
+      consider({256, 1, splits, steps}, 4.5 + (t256 * splits + 255) / 256 * (2.3 + run * (bf16 ? 1.21 : 1.87)) + join);
+    }
   return best;
 }
 
@@ -1058,7 +1063,7 @@ hipError_t launch_gemm_mx(const GemmMx &g, void *ws, hipStream_t s) {
   if (sh.tile == 256)
     return g.nn ? gemm_tiled<T256, true>(g, sh.splits, sh.steps, parts, s)
                 : gemm_tiled<T256, false>(g, sh.splits, sh.steps, parts, s);
-  if (sh.tile == 129)
+  if (sh.groups == 2)
     return g.nn ? gemm_tiled<T128K, true>(g, sh.splits, sh.steps, parts, s)
                 : gemm_tiled<T128K, false>(g, sh.splits, sh.steps, parts, s);
   if (sh.tile == 128)
