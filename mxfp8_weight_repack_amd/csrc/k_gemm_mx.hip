@@ -957,12 +957,32 @@ __global__ __launch_bounds__(C::NT * C::KG) __attribute__((amdgpu_waves_per_eu(C
   }
   float *out = static_cast<float *>(p.out);
   const bool vec = p.ld % 4 == 0;
+  const int64_t mw = m0 + wm * (C::TM / C::WM) + r_end, nw = n0 + wn * (C::TN / C::WN) + 4 * g_end;
+  if (vec && n0 + C::TN <= p.n) {
+    // 16-byte words all inside: one row block's addend words in flight together (rows past
+    // the end read the last one)
+#pragma unroll
+    for (int j = 0; j < FQ; ++j) {
+      const int64_t m = mw + 16 * j, e = m * p.ld + nw;
+      if (p.addend) {
+        const f32x4_t *ad = reinterpret_cast<const f32x4_t *>(p.addend + min(m, p.m - 1) * p.ld + nw);
+        f32x4_t v[FP];
+#pragma unroll
+        for (int i = 0; i < FP; ++i) v[i] = __builtin_nontemporal_load(ad + 4 * i);
+#pragma unroll
+        for (int i = 0; i < FP; ++i) acc[i][j] += v[i];
+      }
+      if (m < p.m) {
+#pragma unroll
+        for (int i = 0; i < FP; ++i) *reinterpret_cast<f32x4_t *>(out + e + 16 * i) = acc[i][j];
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < FQ; ++j)
 #pragma unroll
-    for (int i = 0; i < FP; ++i)
-      store_f32(p, out, m0 + wm * (C::TM / C::WM) + 16 * j + r_end, n0 + wn * (C::TN / C::WN) + 16 * i + 4 * g_end,
-                acc[i][j], vec);
+    for (int i = 0; i < FP; ++i) store_f32(p, out, mw + 16 * j, nw + 16 * i, acc[i][j], vec);
 }
 
 using T256 = Tile<256, 256, 2, 4, 1>;
