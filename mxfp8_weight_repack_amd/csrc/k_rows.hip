@@ -37,18 +37,19 @@ __global__ __launch_bounds__(256) void k_quant_rows(const void *src, int64_t run
 
 constexpr int kQtRows = 128, kQtCols = 128;          // tile of one workgroup
 
-// A 128 x 128 tile goes through LDS as float32.  Reading it: a row's 128 elements
-// are 16 lanes' 8 each (full 256- or 512-byte lines).  Along columns a lane then
-// takes one column's 32 rows, so a block is one lane's and needs no exchange; 4
-// consecutive lanes take the 4 row groups of a column, i.e. 128 consecutive bytes
-// of codes_t.  LDS columns are rotated by the row group (element (r, c) sits at
-// column c ^ 16 * (r / 32)), so the 4 groups x 16 columns a wave reads at one step
-// fall on all 64 banks.  Rows past the end count as zeros.
+// A 128 x 128 tile goes through LDS in src's own type.  Reading it: a row's 128 elements
+// are 16 lanes' 8 each (full 256- or 512-byte lines).  Along columns a lane then takes two
+// neighbouring columns' 32 rows, one LDS read a row, so a block is one lane's and needs no
+// exchange; 4 consecutive lanes take the 4 row groups of a column pair, i.e. 128
+// consecutive bytes of codes_t.  LDS columns are rotated by the row group (element (r, c)
+// sits at column c ^ S * (r / 32), S = 32 of bfloat16 or 16 of float32), so the 4 groups
+// that a wave reads at one step fall on different banks.  Rows past the end count as zeros.
 template <bool BF16, bool ROWS>
 __global__ __launch_bounds__(256) void k_quant_tiles(const void *src, int64_t rows, int64_t cols, int64_t ld,
                                                      uint8_t *codes, uint8_t *scales, uint8_t *codes_t,
                                                      uint8_t *scales_t, int64_t tiles_c) {
-  __shared__ float sm[kQtRows * kQtCols];
+  constexpr int ES = BF16 ? 2 : 4, ROT = BF16 ? 32 : 16;
+  __shared__ __align__(16) char sm[kQtRows * kQtCols * ES];
   const int t = threadIdx.x;
   const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
   const int64_t r0 = tr * kQtRows, c0 = tc * kQtCols;
@@ -64,9 +65,10 @@ __global__ __launch_bounds__(256) void k_quant_tiles(const void *src, int64_t ro
 #pragma unroll
   for (int p = 0; p < kQtRows / 16; ++p) {
     const int rr = lr + 16 * p;
-    float v[8];
-    unpack8<BF16>(raw[p], v);
+    *reinterpret_cast<Raw8<BF16> *>(sm + (rr * kQtCols + (lc ^ ((rr >> 5) * ROT))) * ES) = raw[p];
     if (ROWS) {
+      float v[8];
+      unpack8<BF16>(raw[p], v);
       const uint32_t sb = mx_scale_byte(mx_amax4(v));
       if (in_c && r0 + rr < rows) {
         const int64_t e = (r0 + rr) * cols + c0 + lc;
@@ -74,36 +76,42 @@ __global__ __launch_bounds__(256) void k_quant_tiles(const void *src, int64_t ro
         if ((t & 3) == 0) scales[e >> 5] = (uint8_t)sb;
       }
     }
-    float4 *d = reinterpret_cast<float4 *>(sm + rr * kQtCols + (lc ^ ((rr >> 5) << 4)));
-    d[0] = make_float4(v[0], v[1], v[2], v[3]);
-    d[1] = make_float4(v[4], v[5], v[6], v[7]);
   }
   __syncthreads();
   const int64_t rp = (rows + 31) / 32 * 32;
-  const int grp = t & 3;
+  const int grp = t & 3, c = (t >> 2) * 2;
+  const int64_t r = r0 + 32 * grp;
+  if (c0 + c >= cols || r >= rp) return;
+  const char *q = sm + (32 * grp * kQtCols + (c ^ (grp * ROT))) * ES;
+  float v[2][32];
+  uint32_t a[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    if (BF16) {
+      const uint32_t w = *reinterpret_cast<const uint32_t *>(q + j * kQtCols * ES);
+      v[0][j] = __uint_as_float(w << 16);
+      v[1][j] = __uint_as_float(w & 0xFFFF0000u);
+    } else {
+      const float2 w = *reinterpret_cast<const float2 *>(q + j * kQtCols * ES);
+      v[0][j] = w.x;
+      v[1][j] = w.y;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) a[h] = max(a[h], __float_as_uint(v[h][j]) & 0x7FFFFFFFu);
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int c = (t >> 2) + 64 * h;
-    const int64_t r = r0 + 32 * grp;
-    float v[32];
-    uint32_t a = 0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      v[j] = sm[(32 * grp + j) * kQtCols + (c ^ (grp << 4))];
-      a = max(a, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-    }
-    if (c0 + c >= cols || r >= rp) continue;
-    const uint32_t sb = mx_scale_byte(a);
+    const uint32_t sb = mx_scale_byte(a[h]);
     u32x4r_t w[2];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      w[j >> 2][j & 3] = mx_encode4(make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]), sb);
+      w[j >> 2][j & 3] = mx_encode4(make_float4(v[h][4 * j], v[h][4 * j + 1], v[h][4 * j + 2], v[h][4 * j + 3]), sb);
     if (sb == 0xFFu && r + 32 > rows) {               // the missing rows' codes stay 0 in a NaN block too
 #pragma unroll
       for (int j = 0; j < 32; ++j)
         if (r + j >= rows) w[j >> 4][(j >> 2) & 3] &= ~(0xFFu << (8 * (j & 3)));
     }
-    const int64_t e = (c0 + c) * rp + r;
+    const int64_t e = (c0 + c + h) * rp + r;
     u32x4r_t *o = reinterpret_cast<u32x4r_t *>(codes_t + e);
     o[0] = w[0];
     o[1] = w[1];
