@@ -281,12 +281,34 @@ __global__ __launch_bounds__(C::kThreads) void k_rmsnorm_grad(sshdp_rmsnorm_grad
       if (live && run < runs) store8<BF16>(a.dx, row * a.cols + run * 8, pack8<BF16>(dx));
     }
   }
-  // one partial row per row slot of the workgroup
+  // one partial row per workgroup: its waves' rows are added in wave order
+  if (C::kRows > 1) {
+    __shared__ float4 part[C::kRows > 1 ? C::kRows - 1 : 1][C::kNch][2][64];
+#pragma unroll
+    for (int c = 0; c < C::kNch; ++c)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (sub) part[sub - 1][c][h][lane] = make_float4(dw[c][4 * h], dw[c][4 * h + 1], dw[c][4 * h + 2], dw[c][4 * h + 3]);
+    __syncthreads();
+    if (sub) return;
+#pragma unroll
+    for (int c = 0; c < C::kNch; ++c)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < C::kRows - 1; ++k) {
+          const float4 v = part[k][c][h][lane];
+          dw[c][4 * h] += v.x;
+          dw[c][4 * h + 1] += v.y;
+          dw[c][4 * h + 2] += v.z;
+          dw[c][4 * h + 3] += v.w;
+        }
+  }
 #pragma unroll
   for (int c = 0; c < C::kNch; ++c) {
     const int run = run0 + c * C::kWpr * 64;
     if (run < runs) {
-      float4 *p = reinterpret_cast<float4 *>(partials + ((int64_t)blockIdx.x * C::kRows + sub) * a.cols + run * 8);
+      float4 *p = reinterpret_cast<float4 *>(partials + (int64_t)blockIdx.x * a.cols + run * 8);
       p[0] = make_float4(dw[c][0], dw[c][1], dw[c][2], dw[c][3]);
       p[1] = make_float4(dw[c][4], dw[c][5], dw[c][6], dw[c][7]);
     }
@@ -334,7 +356,10 @@ void with_rows(int64_t cols, F f) {
 }
 
 constexpr int64_t kNormGroups = 2048;                  // workgroups of the forward at most
-constexpr int64_t kGradRows = 1024;                    // partial rows of the weight gradient at most
+// Workgroups of the backward, each leaving a partial row of the weight gradient, at most:
+// two per CU keep HBM busy, and each more is a row written and read back (8191 x 8192
+// bfloat16: 103 us; 256 108, 1024 110).
+constexpr int64_t kGradGroups = 512;
 
 template <class C>
 int64_t norm_groups(int64_t rows, int64_t most) {
@@ -354,7 +379,7 @@ hipError_t rmsnorm(const sshdp_rmsnorm &a, hipStream_t s) {
 
 template <class C>
 hipError_t rmsnorm_grad(const sshdp_rmsnorm_grad &a, float *partials, hipStream_t s) {
-  const dim3 grid((unsigned)norm_groups<C>(a.rows, kGradRows / C::kRows)), block(C::kThreads);
+  const dim3 grid((unsigned)norm_groups<C>(a.rows, kGradGroups)), block(C::kThreads);
   const bool b = a.dtype == SSHDP_DTYPE_BF16, wb = a.weight_dtype == SSHDP_DTYPE_BF16;
   if (b && wb) hipLaunchKernelGGL((k_rmsnorm_grad<true, true, C>), grid, block, 0, s, a, partials);
   else if (b) hipLaunchKernelGGL((k_rmsnorm_grad<true, false, C>), grid, block, 0, s, a, partials);
@@ -399,7 +424,7 @@ int64_t rmsnorm_partials(int64_t rows, int64_t cols) {
   int64_t n = 0;
   with_rows(cols, [&](auto c) {
     using C = decltype(c);
-    n = norm_groups<C>(rows, kGradRows / C::kRows) * C::kRows;
+    n = norm_groups<C>(rows, kGradGroups);
   });
   return n;
 }
