@@ -91,14 +91,14 @@ __device__ __forceinline__ void store_bf16(const GemmMx &p, int64_t m, int64_t n
 // not take: bound by reading B once.  A workgroup's W waves share 16 * NF columns n and
 // split K among them, one 128-k step in W each, so together they read runs of W * 128
 // bytes of B's rows; codes go straight from memory to the matrix instructions, UN steps'
-// loads in flight per wave.  MT * 16 rows of m at a time (grid.y); rows past the end
-// repeat the last one.  The waves' sums meet in LDS and are added in wave order.
+// loads in flight per wave.  MT * 16 rows of m at a time; rows past the end repeat the
+// last one.  The waves' sums meet in LDS and are added in wave order.
 template <bool NN, bool BF16, int W, int NF, int MT, int UN>
-__global__ __launch_bounds__(64 * W) void k_gemm_mx_rows(GemmMx p) {
+__global__ __launch_bounds__(64 * W) void k_gemm_mx_rows(GemmMx p, int64_t tiles_n) {
   __shared__ __align__(16) f32x4_t part[W][NF * MT][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int64_t nb = (int64_t)blockIdx.x * 16 * NF, mb = (int64_t)blockIdx.y * 16 * MT;
+  const int64_t nb = blockIdx.x % tiles_n * 16 * NF, mb = blockIdx.x / tiles_n * 16 * MT;
   const int KB = (int)(p.k >> 5), nk = (int)((p.k + 127) / 128);
   const uint8_t *pb[NF], *pa[MT], *sb[NF], *sa[MT];
   int tb, ta;                                        // scale bytes: block kb of the row at (kb / 4) * t + kb % 4
@@ -1010,8 +1010,8 @@ hipError_t gemm_tiled(const GemmMx &g, int splits, int steps, float *parts, hipS
 
 template <bool NN, bool BF16, int W, int NF, int MT, int UN>
 hipError_t gemm_rows(const GemmMx &g, hipStream_t s) {
-  const dim3 grid((unsigned)((g.n + 16 * NF - 1) / (16 * NF)), (unsigned)((g.m + 16 * MT - 1) / (16 * MT)));
-  hipLaunchKernelGGL((k_gemm_mx_rows<NN, BF16, W, NF, MT, UN>), grid, dim3(64 * W), 0, s, g);
+  const int64_t tn = (g.n + 16 * NF - 1) / (16 * NF), tm = (g.m + 16 * MT - 1) / (16 * MT);
+  hipLaunchKernelGGL((k_gemm_mx_rows<NN, BF16, W, NF, MT, UN>), dim3((unsigned)(tm * tn)), dim3(64 * W), 0, s, g, tn);
   return hipGetLastError();
 }
 

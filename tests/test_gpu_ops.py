@@ -444,3 +444,248 @@ def test_gemm_empty_sizes():
     add = rng.standard_normal((5, 5)).astype(np.float32)
     assert np.all(_gemm(k0, k0, 5, 5, "bf16", pad=3) == 0)
     assert np.array_equal(_gemm(k0, k0, 5, 5, "fp32", addend=add, in_place=True), add)
+
+
+# What the shape choice may pick: few rows (split over waves), 128-tiles by one wave group
+# or two, 256-tiles, each with up to 4 steps or more of 128 k, K splits where tiles are few.
+PICKS = [("nt", 1, 64, 544), ("nt", 33, 64, 544), ("nt", 257, 64, 544), ("nt", 1, 64, 128), ("nt", 33, 64, 8224),
+         ("nt", 257, 64, 2080), ("nt", 3000, 160, 2048), ("nt", 2050, 4128, 544), ("nt", 3001, 4127, 544),
+         ("nt", 8001, 3101, 128), ("nt", 2050, 6017, 224), ("nt", 130, 8224, 1056), ("nn", 1, 64, 544),
+         ("nn", 1, 160, 544), ("nn", 1, 160, 128), ("nn", 3, 160, 1056), ("nn", 5, 160, 2080), ("nn", 3000, 160, 2048),
+         ("nn", 2050, 4128, 544), ("nn", 3001, 4128, 544), ("nn", 8001, 3104, 128), ("nn", 2050, 6016, 224)]
+
+
+@pytest.mark.parametrize("op,m,n,k", PICKS)
+def test_gemm_every_shape_exact(op, m, n, k):
+    """Whole-number operands, both output types, scales at an odd address: exact sums
+    (bfloat16: rounded once; its products differ by less than 2^14, so none is cut off)."""
+    say(f"gemm shapes {op} {m}x{n}x{k}")
+    rng = np.random.default_rng(m + 3 * n + k)
+    nn = op == "nn"
+    ac, as_, a = _operand(rng, m, k, "rowmajor", True)
+    bc, bs, b = _operand(rng, k if nn else n, n if nn else k, "block32x32" if nn else "rowmajor", True)
+    ad, bd = torch.from_numpy(a).cuda(), torch.from_numpy(b).cuda()
+    ref = (ad @ (bd if nn else bd.t())).float()
+    A = sh.mx_matrix(dev(ac), dev(np.concatenate([[0], as_]).astype(np.uint8))[1:], m, k)
+    B = sh.mx_matrix(dev(bc), dev(np.concatenate([[0, 0, 0], bs]).astype(np.uint8))[3:], bc.shape[0], bc.shape[1],
+                     "block32x32" if nn else "rowmajor")
+    nb = sh.gemm_mxfp8_workspace(A, B, op=op)
+    ws = work(nb)
+    add = torch.randint(-50, 50, (m, n), device="cuda").float()
+    for dtype, td in (("fp32", torch.float32), ("bf16", torch.bfloat16)):
+        out = buf(m, n, dtype=td, fill=3.0)
+        sh.gemm_mxfp8(A, B, out, dtype, op=op, workspace=ws, workspace_bytes=nb, stream=stream())
+        assert torch.equal(out, ref.to(td)), dtype
+    out = add.clone()
+    sh.gemm_mxfp8(A, B, out, "fp32", op=op, addend=out, workspace=ws, workspace_bytes=nb, stream=stream())
+    assert torch.equal(out, ref + add)
+
+
+@pytest.mark.parametrize("n,k", [(64, 640), (2080, 1152), (160, 4224)])
+@pytest.mark.parametrize("layout", ["tile32x4", "block32x32"])
+def test_gemm_long_rows_in_every_layout(n, k, layout):
+    """The weight's layouts where rows take several quads of steps, the last one short."""
+    say(f"gemm long rows {layout} {n}x{k}")
+    rng = np.random.default_rng(n + k)
+    for m in (1, 40, 384):
+        ac, as_, a = _operand(rng, m, k, "rowmajor", True)
+        bc, bs, b = _operand(rng, n, k, layout, True)
+        assert np.array_equal(_gemm((ac, as_), (bc, bs), m, n, "fp32", layouts=("rowmajor", layout)), a @ b.T)
+
+
+# ----------------------------------------------------------------- together, and shared
+
+class Layer:
+    """Norm, up and down projection of a small block on a plan: weights in 32 x 32 blocks,
+    two microbatches of a ragged token count, then clip and update."""
+    M, D, F = 77, 128, 256
+
+    def __init__(self, seed=0):
+        D, F = self.D, self.F
+        q = dict(parent=-1, is_unit=True, optimizer="muon", quantize=True)
+        nodes = [dict(q, offset=0, rows=F, cols=D, row_stride=D), dict(q, offset=F * D, rows=D, cols=F, row_stride=F),
+                 dict(parent=-1, offset=2 * F * D, rows=1, cols=D, row_stride=D, is_unit=True, optimizer="adamw",
+                      quantize=None)]
+        self.n = 2 * F * D + D
+        self.plan = sh.Plan(nodes, self.n, layout="block32x32")
+        st = self.plan.stats()
+        rng = np.random.default_rng(seed)
+        w = rng.standard_normal(self.n).astype(np.float32) * 0.05
+        w[2 * F * D:] = 1 + 0.1 * rng.standard_normal(D)
+        self.w, self.g, self.gc = dev(w), torch.zeros(self.n, device="cuda"), torch.zeros(self.n, device="cuda")
+        self.m, self.v = torch.zeros(self.n, device="cuda"), torch.zeros(self.n, device="cuda")
+        self.codes, self.scales = buf(self.n, fill=0), buf(st["scale_bytes"], fill=0)
+        self.x = [dev(rng.standard_normal((self.M, D)).astype(np.float32), "bf16") for _ in range(2)]
+        self.res = [dev(rng.standard_normal((self.M, D)).astype(np.float32), "bf16") for _ in range(2)]
+        self.dy = [dev(rng.standard_normal((self.M, D)).astype(np.float32) * 0.01, "bf16") for _ in range(2)]
+        self.ws_bytes = max(st["workspace_bytes"], sh.grad_workspace(self.plan), 1 << 20)
+        self.ws, self.stats = buf(self.ws_bytes), buf(2, dtype=torch.float32, fill=0)
+        self.W1, self.W2 = (self.plan.mx_matrix(i, self.codes, self.scales) for i in (0, 1))
+        sh.requant_mxfp8(self.plan, self.w, self.codes, self.scales, stream())
+        M, P = self.M, (self.M + 31) // 32 * 32
+        b16 = dict(dtype=torch.bfloat16)
+        self.t = {"h": buf(M, D, **b16), "y": buf(M, D, **b16), "rstd": buf(M, dtype=torch.float32), "a": buf(M, F, **b16),
+                  "out": buf(M, D, dtype=torch.float32), "da": buf(M, F, **b16), "dn": buf(M, D, **b16), "dx": buf(M, D, **b16)}
+        for name, r, c in (("yq", M, D), ("aq", M, F), ("dyq", M, D), ("daq", M, F)):
+            self.t[name], self.t[name + "_s"] = buf(r, c), buf(r, c // 32)
+        for name, r in (("yt", D), ("at", F), ("dyt", D), ("dat", F)):
+            self.t[name], self.t[name + "_s"] = buf(r, P), buf(r, P // 32)
+
+    def mat(self, name):
+        return sh.mx_matrix(self.t[name], self.t[name + "_s"], *self.t[name].shape)
+
+    def gemm(self, a, b, out, dtype, op="nt", addend=None):
+        assert sh.gemm_mxfp8_workspace(a, b, op=op) <= self.ws_bytes
+        sh.gemm_mxfp8(a, b, out, dtype, op=op, addend=addend, workspace=self.ws, workspace_bytes=self.ws_bytes,
+                      stream=stream())
+
+    def quant(self, src, rows, cols, name=None, name_t=None):
+        q = [self.t[n] if n else None for n in (name, name and name + "_s", name_t, name_t and name_t + "_s")]
+        sh.quant_mxfp8(src, "bf16", rows, cols, *q, stream=stream())
+
+    def microbatch(self, i):
+        t, M, D, F, s = self.t, self.M, self.D, self.F, stream()
+        gamma = self.w[2 * F * D:]
+        sh.rmsnorm_mxfp8(self.x[i], gamma, M, D, residual=self.res[i], h=t["h"], y=t["y"], codes=t["yq"],
+                         scales=t["yq_s"], rstd=t["rstd"], stream=s)
+        self.gemm(self.mat("yq"), self.W1, t["a"], "bf16")
+        self.quant(t["a"], M, F, "aq", "at")
+        self.gemm(self.mat("aq"), self.W2, t["out"], "fp32")
+        self.quant(self.dy[i], M, D, "dyq", "dyt")
+        self.gemm(self.mat("dyq"), self.W2, t["da"], "bf16", "nn")
+        g1, g2, g3 = self.g[:F * D], self.g[F * D:2 * F * D], self.g[2 * F * D:]
+        self.gemm(self.mat("dyt"), self.mat("at"), g2, "fp32", addend=g2 if i else None)
+        self.quant(t["da"], M, F, "daq", "dat")
+        self.quant(t["y"], M, D, None, "yt")
+        self.gemm(self.mat("daq"), self.W1, t["dn"], "bf16", "nn")
+        self.gemm(self.mat("dat"), self.mat("yt"), g1, "fp32", addend=g1 if i else None)
+        sh.rmsnorm_backward(t["dn"], t["h"], gamma, t["rstd"], t["dx"], g3, M, D, dh=self.dy[i], first=i == 0,
+                            workspace=self.ws, workspace_bytes=self.ws_bytes, stream=s)
+
+    def step(self):
+        for i in range(2):
+            self.microbatch(i)
+        sh.grad_clip_norm(self.plan, self.g, self.gc, 0.5, self.stats, self.ws, self.ws_bytes, stream())
+        sh.update_step(self.plan, sh.buffers(self.w, self.gc, self.m, self.v, self.codes, self.scales), sh.muon_hp(),
+                       sh.adamw_hp(), 1, self.ws, self.ws_bytes, stream())
+
+    def state(self):
+        torch.cuda.synchronize()
+        return {k: getattr(self, k).clone() for k in ("w", "g", "gc", "m", "v", "codes", "scales", "stats")} | \
+            {k: v.clone() for k, v in self.t.items()}
+
+
+def test_a_layer_forwards_backwards_and_updates():
+    """Every operator's result inside the run, each against its reference on the run's own inputs."""
+    say("layer")
+    L = Layer()
+    t, M, D, F = L.t, L.M, L.D, L.F
+    w0 = host(L.w).copy()
+    wq = [R.decode(host(L.codes)[i * F * D:(i + 1) * F * D].reshape(s), host(L.scales)[i * F * D // 1024:], "block32x32")
+          for i, s in ((0, (F, D)), (1, (D, F)))]
+    grads = np.zeros(L.n)
+    bounds = np.zeros(L.n)
+    for i in range(2):
+        L.microbatch(i)
+        T = {k: host(v) for k, v in t.items()}
+        dec = lambda n: R.decode(T[n], T[n + "_s"], "rowmajor")   # noqa: E731
+        h, rstd, y = R.rmsnorm(host(L.x[i]), host(L.res[i]), w0[2 * F * D:], 1e-6, "bf16")
+        assert np.array_equal(T["h"], h) and np.array_equal(T["yq"], R.quant_rows(y)[0])
+        for got, (a, b), dtype in ((T["a"], (dec("yq"), wq[0]), "bf16"), (T["out"], (dec("aq"), wq[1]), "fp32"),
+                                   (T["da"], (dec("dyq"), wq[1].T), "bf16"), (T["dn"], (dec("daq"), wq[0].T), "bf16")):
+            ref, bound = R.product(a, b, None, dtype)
+            assert np.all(np.abs(got - ref) <= bound)
+        assert np.array_equal(T["at"], R.quant_cols(T["a"])[0]) and np.array_equal(T["dat_s"], R.quant_cols(T["da"])[1])
+        for off, (a, b) in ((0, ("dat", "yt")), (F * D, ("dyt", "at"))):
+            ref, bound = R.product(dec(a), dec(b), None, "fp32")
+            grads[off:off + F * D] += ref.reshape(-1)
+            bounds[off:off + F * D] += bound.reshape(-1)
+        dx, bdx, dw, bdw = R.rmsnorm_grad(T["dn"], T["h"], w0[2 * F * D:], T["rstd"], host(L.dy[i]), "bf16")
+        assert np.all(np.abs(T["dx"] - dx) <= bdx)
+        grads[2 * F * D:] += dw
+        bounds[2 * F * D:] += bdw
+    # the second microbatch's addition rounds once more
+    g = host(L.g)
+    assert np.all(np.abs(g - grads) <= bounds + 2 * R.U * np.abs(grads))
+    M2 = Layer()
+    M2.step()
+    assert torch.equal(M2.g, L.g)                      # the same run again, to the bit
+    norm = np.sqrt(np.sum(g.astype(np.float64) ** 2))
+    assert norm > 0.5 and abs(host(M2.stats)[0] - norm) <= 1.01 * R.U * norm
+    assert np.all(np.abs(host(M2.gc) - g * (0.5 / norm)) <= 2.02 * R.U * np.abs(g))
+    # the update's codes are G of its new weights, and the next forward reads them
+    assert not np.array_equal(host(M2.w), w0)
+    for i, s in ((0, (F, D)), (1, (D, F))):
+        c, _ = R.quant_weight(host(M2.w)[i * F * D:(i + 1) * F * D].reshape(s), "block32x32")
+        assert np.array_equal(host(M2.codes)[i * F * D:(i + 1) * F * D].reshape(s), c)
+
+
+def test_a_step_captured_in_a_hip_graph():
+    """Forward, backward, clip and update captured once and replayed three times on new
+    inputs, with eager work between, each replay against an eager step from the same state."""
+    say("layer graph")
+    G, E = Layer(1), Layer(1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        G.step()                                       # warm up outside the capture
+    torch.cuda.current_stream().wait_stream(side)
+    E.step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        G.step()
+    for rep in range(3):
+        rng = np.random.default_rng(10 + rep)
+        for L in (G, E):
+            r = np.random.default_rng(10 + rep)
+            for k in range(2):
+                L.x[k].copy_(dev(r.standard_normal((L.M, L.D)).astype(np.float32), "bf16"))
+                L.dy[k].copy_(dev(r.standard_normal((L.M, L.D)).astype(np.float32) * 0.01, "bf16"))
+        graph.replay()
+        E.step()
+        torch.cuda.synchronize()
+        a, b = G.state(), E.state()
+        for k in a:
+            assert torch.equal(a[k], b[k]) or (a[k].is_floating_point() and torch.equal(a[k].nan_to_num(), b[k].nan_to_num())), (rep, k)
+        del rng
+
+
+def test_two_streams_at_once():
+    """Two layers' steps on two streams, issued in turn, give what each gives alone."""
+    say("two streams")
+    alone = []
+    for seed in (2, 3):
+        L = Layer(seed)
+        L.step()
+        alone.append(L.state())
+    layers, streams = [Layer(2), Layer(3)], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for L, s in zip(layers, streams):
+        with torch.cuda.stream(s):
+            L.step()
+    torch.cuda.synchronize()
+    for L, a in zip(layers, alone):
+        b = L.state()
+        assert all(torch.equal(a[k], b[k]) for k in a)
+
+
+def test_foreign_pointers_are_refused():
+    """Host memory that the runtime does not know is an argument error, not a GPU fault."""
+    h = torch.zeros(64, 64)
+    d = torch.zeros(64, 64, device="cuda")
+    u = torch.zeros(64 * 64, dtype=torch.uint8, device="cuda")
+    p = h.data_ptr() + (-h.data_ptr() % 16)
+    node = unit(0, 1, 64)
+    plan = sh.Plan([node], 64)
+    m = sh.mx_matrix(u, u, 32, 64)
+    for call in (lambda: sh.quant_mxfp8(p, "fp32", 4, 64, u, u, stream=stream()),
+                 lambda: sh.rmsnorm_mxfp8(d, p, 4, 64, dtype="fp32", y=d, stream=stream()),
+                 lambda: sh.gemm_mxfp8(m, m, p, "fp32", stream=stream()),
+                 lambda: sh.gemm_mxfp8(sh.mx_matrix(u, p, 32, 64), m, d, "fp32", stream=stream()),
+                 lambda: sh.grad_clip_norm(plan, d, d, 1.0, d, p, 1 << 20, stream()),
+                 lambda: sh.grad_clip_norm(plan, p, d, 1.0, d, u, 4096, stream())):
+        with pytest.raises(sh.SshdpError) as e:
+            call()
+        assert e.value.name == "ARG"
+    torch.cuda.synchronize()
