@@ -398,7 +398,7 @@ enum { SSHDP_DTYPE_FP32 = 0, SSHDP_DTYPE_BF16 = 1 };
  * tokens for the weight gradient.
  * Errors: ARG (null src, half a pair or no pair, bad dtype, rows or cols < 0),
  * SCHEMA (cols not a multiple of 32, ld < cols, ld rows not 16-byte multiples,
- * an edge over 2^30), ALIGN (src, codes, codes_t, scales_t; scales: any); HIP. */
+ * an edge over 2^30), ALIGN (src, codes, codes_t; scales: any); HIP. */
 int sshdp_quant_mxfp8(const void *src, int32_t dtype, int64_t rows, int64_t cols, int64_t ld, uint8_t *codes,
                       uint8_t *scales, uint8_t *codes_t, uint8_t *scales_t, void *stream);
 
@@ -410,14 +410,16 @@ int sshdp_quant_mxfp8(const void *src, int32_t dtype, int64_t rows, int64_t cols
  * float32 but for products within 2^-29 of a rounding border, and its codes
  * follow the oracle's bit for bit.  Outputs are dense (rows x cols; scales
  * ROWMAJOR rows x cols/32), each NULL if not wanted, codes and scales together:
- * `h` (only with residual; may be x or residual), `y` in `dtype`, and `rstd`,
- * one float per row (what the backward needs).  x and residual have rows ld_x
- * and ld_residual elements apart; `weight` has cols elements of weight_dtype.
+ * `h` (only with residual; may be x or residual where that one is dense), `y` in
+ * `dtype`, and `rstd`, one float per row (what the backward needs).  x and
+ * residual have rows ld_x and ld_residual elements apart; `weight` has cols
+ * elements of weight_dtype.
  * A NaN makes its whole row's y NaN; an infinity makes rstd 0, y NaN where it
  * stands and 0 elsewhere; G gives blocks holding NaN scale 0xFF and codes 0x7F.
  * Errors: ARG (null x or weight, no output, half a pair, h without residual,
  * bad dtype, eps < 0 or NaN, rows or cols < 0), SCHEMA (cols not a multiple of
- * 32 or over 32768, ld < cols, rows not 16-byte multiples), ALIGN; HIP. */
+ * 32 or over 32768, ld < cols, rows not 16-byte multiples, h in place of rows
+ * with gaps), ALIGN; HIP. */
 typedef struct {
   const void *x, *residual, *weight;
   void *h, *y;
@@ -475,8 +477,9 @@ int sshdp_plan_mx_matrix(const sshdp_plan *plan, int32_t node, const uint8_t *co
  * even).  Float32 output is a float32 sum of exact products.  For bfloat16 output
  * the matrix cores multiply the codes themselves, twice as fast: each 8
  * consecutive k's products are cut off at 2^-14 of their largest before they are
- * added (about 1.4e-5 of the result, against bfloat16's own 2^-8).  `addend` (float32 output only, NULL for none) has out's shape and ld
- * and is added to the sums; it may be `out`: gradients of microbatches.
+ * added (about 1.4e-5 of the result, against bfloat16's own 2^-8).  `addend`
+ * (float32 output only, NULL for none) has out's shape and ld and is added to
+ * the sums; it may be `out`: gradients of microbatches.
  * Any M and N, K a multiple of 32; K == 0 gives the addend, or zeros.  NaN
  * blocks (scale 0xFF) give NaN.  `workspace`: sshdp_gemm_mxfp8_workspace bytes
  * (0: none needed), 16-byte aligned.  The result does not depend on timing.

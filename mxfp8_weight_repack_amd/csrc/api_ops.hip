@@ -163,6 +163,10 @@ int sshdp_rmsnorm_mxfp8(const sshdp_rmsnorm *a, void *stream) {
   if (a->rows == 0 || a->cols == 0) return SSHDP_OK;
   if (!a->x || !a->weight || !a->codes != !a->scales || (a->h && !a->residual)) return SSHDP_ERR_ARG;
   if (!a->h && !a->y && !a->codes && !a->rstd) return SSHDP_ERR_ARG;
+  // h is dense: written over rows with gaps it would run into rows not read yet
+  if (a->h && a->rows > 1 &&
+      ((a->h == a->x && a->ld_x != a->cols) || (a->h == a->residual && a->ld_residual != a->cols)))
+    return SSHDP_ERR_SCHEMA;
   if (!aligned16(a->x) || !aligned16(a->residual) || !aligned16(a->weight) || !aligned16(a->h) || !aligned16(a->y) ||
       !aligned16(a->codes) || !aligned16(a->rstd))
     return SSHDP_ERR_ALIGN;

@@ -67,6 +67,12 @@ def test_rmsnorm_refusals():
     sh.rmsnorm_mxfp8(None, None, 0, 64)
 
 
+def test_rmsnorm_in_place_needs_dense_rows():
+    """h is dense: over x or a residual with gaps it would overwrite rows not read yet."""
+    for kw in (dict(h=P, ld_x=64), dict(h=P + 4096, residual=P + 4096, ld_residual=40)):
+        refused("SCHEMA", lambda: sh.rmsnorm_mxfp8(P, P, 4, 32, **dict(dict(residual=P + 8192), **kw)))
+
+
 def test_rmsnorm_backward_refusals():
     nb = sh.rmsnorm_backward_workspace(4, 64)
     assert nb >= 64 * 4 and nb % 16 == 0
