@@ -94,11 +94,12 @@ __device__ __forceinline__ void store_bf16(const GemmMx &p, int64_t m, int64_t n
 // loads in flight per wave.  MT * 16 rows of m at a time; rows past the end repeat the
 // last one.  The waves' sums meet in LDS and are added in wave order.
 template <bool NN, bool BF16, int W, int NF, int MT, int UN>
-__global__ __launch_bounds__(64 * W) void k_gemm_mx_rows(GemmMx p, int64_t tiles_n) {
+__global__ __launch_bounds__(64 * W) void k_gemm_mx_rows(GemmMx p, int64_t tiles_n, int64_t first) {
   __shared__ __align__(16) f32x4_t part[W][NF * MT][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int64_t nb = blockIdx.x % tiles_n * 16 * NF, mb = blockIdx.x / tiles_n * 16 * MT;
+  const int64_t id = first + blockIdx.x;
+  const int64_t nb = id % tiles_n * 16 * NF, mb = id / tiles_n * 16 * MT;
   const int KB = (int)(p.k >> 5), nk = (int)((p.k + 127) / 128);
   const uint8_t *pb[NF], *pa[MT], *sb[NF], *sa[MT];
   int tb, ta;                                        // scale bytes: block kb of the row at (kb / 4) * t + kb % 4
@@ -1011,8 +1012,14 @@ hipError_t gemm_tiled(const GemmMx &g, int splits, int steps, float *parts, hipS
 template <bool NN, bool BF16, int W, int NF, int MT, int UN>
 hipError_t gemm_rows(const GemmMx &g, hipStream_t s) {
   const int64_t tn = (g.n + 16 * NF - 1) / (16 * NF), tm = (g.m + 16 * MT - 1) / (16 * MT);
-  hipLaunchKernelGGL((k_gemm_mx_rows<NN, BF16, W, NF, MT, UN>), dim3((unsigned)(tm * tn)), dim3(64 * W), 0, s, g, tn);
-  return hipGetLastError();
+  const int64_t most = 1 << 22;                        // a launch has under 2^32 threads: outputs past that take several
+  for (int64_t first = 0; first < tm * tn; first += most) {
+    const dim3 grid((unsigned)std::min(tm * tn - first, most));
+    hipLaunchKernelGGL((k_gemm_mx_rows<NN, BF16, W, NF, MT, UN>), grid, dim3(64 * W), 0, s, g, tn, first);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // How a product runs: few-row kernel (tile 0), or tiles of 256 or 128 by `groups` wave
@@ -1025,7 +1032,8 @@ struct Shape {
 // The candidate with the least modelled time, in microseconds on an idle MI355X.  The
 // constants are fitted to 300 timed choices from m 1 .. 4096, n and k 128 .. 28672, both
 // operand forms and output types; what it picks takes 1.5% more than the best candidate
-// on average and 27% more at worst.  Always 128-tiles: 19% and 4x.
+// on average and 27% more at worst.  Always unsplit 128-tiles: 42% and 5.2x; always
+// 256-tiles: 97% on average.
 //   few rows:  the operands' bytes as the kernel gets them, or its waves' steps in turn;
 //   128-tiles: two workgroups a CU, 0.95 us for a step of both, 0.61 for one alone;
 //   128-tiles by two wave groups: one workgroup a CU, 1.1 us for a step of both;

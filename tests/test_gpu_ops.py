@@ -689,3 +689,118 @@ def test_foreign_pointers_are_refused():
             call()
         assert e.value.name == "ARG"
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ past 32-bit offsets
+
+def _codes(rows, cols, seed=0):
+    """Codes of 1, 2 and 4 and scales of 1 and 2, made on the GPU: exact sums."""
+    torch.manual_seed(seed)
+    c = torch.randint(0, 3, (rows, cols), dtype=torch.uint8, device="cuda").mul_(8).add_(0x38)
+    return c, torch.randint(127, 129, (rows, cols // 32), dtype=torch.uint8, device="cuda")
+
+
+def _mm(a, b, m, n, dtype="fp32", op="nt"):
+    out = torch.full((m, n), 3.0, dtype=torch.float32 if dtype == "fp32" else torch.bfloat16, device="cuda")
+    nb = sh.gemm_mxfp8_workspace(a, b, op=op)
+    sh.gemm_mxfp8(a, b, out, dtype, op=op, workspace=work(nb), workspace_bytes=nb, stream=stream())
+    return out
+
+
+def test_rows_past_32_bit_offsets():
+    """The last rows of matrices of more than 2^32 elements are what they are alone."""
+    rows, cols, cut = 140001, 32768, 139872             # cut: a multiple of 32
+    n = rows - cut
+    say("quant past 2^32")
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_()
+    c, s = buf(rows, cols), buf(rows, cols // 32)
+    ct, st = buf(cols, (rows + 31) // 32 * 32), buf(cols, (rows + 31) // 32)
+    sh.quant_mxfp8(x, "bf16", rows, cols, c, s, ct, st, stream=stream())
+    c1, s1, ct1, st1 = buf(n, cols), buf(n, cols // 32), buf(cols, (n + 31) // 32 * 32), buf(cols, (n + 31) // 32)
+    sh.quant_mxfp8(x[cut:], "bf16", n, cols, c1, s1, ct1, st1, stream=stream())
+    assert torch.equal(c[cut:], c1) and torch.equal(s[cut:], s1)
+    assert torch.equal(ct[:, cut:], ct1) and torch.equal(st[:, cut // 32:], st1)
+    c.fill_(0xA5)
+    sh.quant_mxfp8(x, "bf16", rows, cols, c, s, stream=stream())
+    assert torch.equal(c[cut:], c1)
+    del ct, st
+    say("rmsnorm past 2^32")
+    w = torch.ones(cols, device="cuda")
+    h, rs = torch.empty_like(x), torch.empty(rows, device="cuda")
+    sh.rmsnorm_mxfp8(x, w, rows, cols, residual=x, h=h, codes=c, scales=s, rstd=rs, stream=stream())
+    h1, rs1 = torch.empty_like(x[cut:]), torch.empty(n, device="cuda")
+    sh.rmsnorm_mxfp8(x[cut:], w, n, cols, residual=x[cut:], h=h1, codes=c1, scales=s1, rstd=rs1, stream=stream())
+    assert torch.equal(h[cut:], h1) and torch.equal(rs[cut:], rs1)
+    assert torch.equal(c[cut:], c1) and torch.equal(s[cut:], s1)
+    say("rmsnorm backward past 2^32")
+    x[:-1] = 0                                          # dy: the last row alone, so its weight gradient is exact
+    dw, dw1 = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+    nb = sh.rmsnorm_backward_workspace(rows, cols)
+    dx = torch.empty_like(x)
+    sh.rmsnorm_backward(x, h, w, rs, dx, dw, rows, cols, workspace=work(nb), workspace_bytes=nb, stream=stream())
+    dx1 = torch.empty_like(x[cut:])
+    sh.rmsnorm_backward(x[cut:], h1, w, rs1, dx1, dw1, n, cols, workspace=work(nb), workspace_bytes=nb, stream=stream())
+    assert torch.equal(dx[cut:], dx1) and torch.equal(dw, dw1) and bool((dw != 0).any())
+
+
+def test_products_past_32_bit_offsets():
+    rows, k, cut = 140001, 32768, 139700
+    n = rows - cut
+    c, s = _codes(rows, k)
+    big, tail = sh.mx_matrix(c, s, rows, k), sh.mx_matrix(c[cut:], s[cut:], n, k)
+    for m in (5, 100, 300):                             # few rows, and tiles
+        say(f"operand past 2^32, m {m}")
+        a = sh.mx_matrix(*_codes(m, k, 1), m, k)
+        for dtype in ("fp32", "bf16"):
+            assert torch.equal(_mm(a, big, m, rows, dtype)[:, cut:], _mm(a, tail, m, n, dtype))
+            assert torch.equal(_mm(big, a, rows, m, dtype)[cut:], _mm(tail, a, n, m, dtype))
+    del c, s, big, tail
+    say("nn operand past 2^32")
+    rows, cut = 140032, 139712
+    n = rows - cut
+    c = _codes(k, rows)[0]
+    s = torch.randint(127, 129, (k // 32, rows // 32), dtype=torch.uint8, device="cuda")
+    big = sh.mx_matrix(c, s, k, rows, "block32x32")
+    tail = sh.mx_matrix(c[:, cut:].t().contiguous(), s[:, cut // 32:].t().contiguous(), n, k, "block32x32")
+    a = sh.mx_matrix(*_codes(300, k, 1), 300, k)
+    for dtype in ("fp32", "bf16"):
+        assert torch.equal(_mm(a, big, 300, rows, dtype, "nn")[:, cut:], _mm(a, tail, 300, n, dtype))
+    del c, s, big, tail
+    say("output past 2^32")
+    m, n, k, cut = 70001, 65536, 256, 69800
+    c, s = _codes(m, k)
+    b = sh.mx_matrix(*_codes(n, k, 1), n, k)
+    for dtype in ("fp32", "bf16"):
+        assert torch.equal(_mm(sh.mx_matrix(c, s, m, k), b, m, n, dtype)[cut:],
+                           _mm(sh.mx_matrix(c[cut:], s[cut:], m - cut, k), b, m - cut, n, dtype))
+
+
+def test_narrow_outputs_of_very_many_rows():
+    """More workgroups than one launch may have threads for."""
+    say("2^27 + 5 rows")
+    m, n, k = (1 << 27) + 5, 32, 32
+    c, s = _codes(m, k)
+    for op in ("nt", "nn"):
+        b = sh.mx_matrix(_codes(32, 32, 1)[0], torch.full((32,), 127, dtype=torch.uint8, device="cuda"), 32, 32,
+                         "rowmajor" if op == "nt" else "block32x32")
+        out = _mm(sh.mx_matrix(c, s, m, k), b, m, n, "bf16", op)
+        for at in [i << 22 for i in range(0, 32)] + [m - 40]:
+            lo, hi = max(at - 40, 0), min(at + 40, m)
+            assert torch.equal(out[lo:hi], _mm(sh.mx_matrix(c[lo:hi], s[lo:hi], hi - lo, k), b, hi - lo, n, "bf16", op))
+
+
+def test_clip_past_32_bit_offsets():
+    say("clip past 2^32")
+    n, at = (1 << 32) + 3_000_000, (1 << 32) - 1_000_003
+    plan = sh.Plan([unit(1, 1, 1000), unit(at, 1, 3_000_001)], n)
+    g = torch.full((n,), float("nan"), device="cuda")
+    for lo, ln in ((1, 1000), (at, 3_000_001)):
+        g[lo:lo + ln].normal_()
+    own = torch.cat([g[1:1001], g[at:at + 3_000_001]])
+    out, stats, nb = torch.full_like(g, 7.0), buf(2, dtype=torch.float32, fill=0), sh.grad_workspace(plan)
+    sh.grad_clip_norm(plan, g, out, 0.5, stats, work(nb), nb, stream())
+    norm = float(own.double().norm())
+    st = host(stats)
+    assert abs(st[0] - norm) <= 2 * R.U * norm and abs(st[1] - 0.5 / norm) <= 4 * R.U * st[1]
+    assert torch.equal(torch.cat([out[1:1001], out[at:at + 3_000_001]]), own * float(st[1]))
+    assert bool((out[1001:at] == 7.0).all()) and bool((out[at + 3_000_001:] == 7.0).all())
