@@ -129,7 +129,20 @@ struct RowCfg {
   static constexpr int kWpr = WPR, kNch = NCH;
   static constexpr int kThreads = WPR > 4 ? 64 * WPR : 256;
   static constexpr int kRows = kThreads / 64 / WPR;    // rows a workgroup works on at once
+  // 16 waves leave a lane 128 registers: with more than 16 values of a row in them, the
+  // weights and dh are read anew for each row, from the caches, and the weight gradient's
+  // sums are held in LDS (4096 x 32768 bfloat16: 230 us, gradient 280; all of it in
+  // registers, and spilled, 299 and 552)
+  static constexpr bool kLean = WPR * NCH > 32;
 };
+
+// Run `run`'s 8 weights, 0 past the end.
+template <bool WBF16>
+__device__ __forceinline__ void weights(const void *weight, int run, int runs, float (&w)[8]) {
+  Raw8<WBF16> r{};
+  if (run < runs) r = load8<WBF16>(weight, run * 8);
+  unpack8<WBF16>(r, w);
+}
 
 // Sum over a row's lanes: a butterfly in the wave, then the waves in order.
 template <int WPR>
@@ -155,12 +168,9 @@ __global__ __launch_bounds__(C::kThreads) void k_rmsnorm(sshdp_rmsnorm a) {
   const int sub = wave / C::kWpr, run0 = (wave % C::kWpr) * 64 + lane;
   const int runs = (int)(a.cols >> 3);
   float w[C::kNch][8];
+  if (!C::kLean) {
 #pragma unroll
-  for (int c = 0; c < C::kNch; ++c) {
-    const int run = run0 + c * C::kWpr * 64;
-    Raw8<WBF16> r{};
-    if (run < runs) r = load8<WBF16>(a.weight, run * 8);
-    unpack8<WBF16>(r, w[c]);
+    for (int c = 0; c < C::kNch; ++c) weights<WBF16>(a.weight, run0 + c * C::kWpr * 64, runs, w[c]);
   }
   // the loop bound is the same for all waves of a workgroup (barriers inside)
   for (int64_t g = blockIdx.x; g * C::kRows < a.rows; g += gridDim.x) {
@@ -195,6 +205,10 @@ __global__ __launch_bounds__(C::kThreads) void k_rmsnorm(sshdp_rmsnorm a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) s = fma((double)h[c][j], (double)h[c][j], s);
     }
+    if (C::kLean) {
+#pragma unroll
+      for (int c = 0; c < C::kNch; ++c) weights<WBF16>(a.weight, run0 + c * C::kWpr * 64, runs, w[c]);
+    }
     s = row_sum<C::kWpr>(s, sm);
     const double rstd = 1.0 / sqrt(s / (double)a.cols + (double)a.eps);
     if (a.rstd && live && run0 == 0) a.rstd[row] = (float)rstd;
@@ -219,11 +233,26 @@ __global__ __launch_bounds__(C::kThreads) void k_rmsnorm(sshdp_rmsnorm a) {
 
 // --------------------------------------------------------------------- its gradient
 
+// A lane's own 8 sums of chunk c in LDS.
+__device__ __forceinline__ void get_dw(const float4 *sums, int c, float (&v)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float4 x = sums[(2 * c + h) * blockDim.x + threadIdx.x];
+    v[4 * h] = x.x, v[4 * h + 1] = x.y, v[4 * h + 2] = x.z, v[4 * h + 3] = x.w;
+  }
+}
+__device__ __forceinline__ void put_dw(float4 *sums, int c, const float (&v)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    sums[(2 * c + h) * blockDim.x + threadIdx.x] = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+}
+
 // Workgroups keep their columns' weight-gradient sums in registers over all their
 // rows and leave one partial row each; k_dweight adds the partial rows.
 template <bool BF16, bool WBF16, class C>
 __global__ __launch_bounds__(C::kThreads) void k_rmsnorm_grad(sshdp_rmsnorm_grad a, float *partials) {
   __shared__ double sm[C::kThreads / 64];
+  __shared__ float4 sums[C::kLean ? C::kNch * 2 * C::kThreads : 1];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int sub = wave / C::kWpr, run0 = (wave % C::kWpr) * 64 + lane;
   const int runs = (int)(a.cols >> 3);
@@ -231,11 +260,10 @@ __global__ __launch_bounds__(C::kThreads) void k_rmsnorm_grad(sshdp_rmsnorm_grad
 #pragma unroll
   for (int c = 0; c < C::kNch; ++c) {
     const int run = run0 + c * C::kWpr * 64;
-    Raw8<WBF16> r{};
-    if (run < runs) r = load8<WBF16>(a.weight, run * 8);
-    unpack8<WBF16>(r, w[c]);
+    if (!C::kLean) weights<WBF16>(a.weight, run, runs, w[c]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[c][j] = 0.f;
+    if (C::kLean) put_dw(sums, c, dw[c]);
   }
   for (int64_t g = blockIdx.x; g * C::kRows < a.rows; g += gridDim.x) {
     const int64_t row = g * C::kRows + sub;
@@ -251,7 +279,7 @@ __global__ __launch_bounds__(C::kThreads) void k_rmsnorm_grad(sshdp_rmsnorm_grad
         const int64_t e = row * a.cols + run * 8;
         ry[c] = load8<BF16>(a.dy, e);
         rh[c] = load8<BF16>(a.h, e);
-        if (a.dh) rd[c] = load8<BF16>(a.dh, e);
+        if (!C::kLean && a.dh) rd[c] = load8<BF16>(a.dh, e);
       }
     }
     const float rstd = live ? a.rstd[row] : 0.f;
@@ -261,18 +289,27 @@ __global__ __launch_bounds__(C::kThreads) void k_rmsnorm_grad(sshdp_rmsnorm_grad
       float dy[8], h[8];
       unpack8<BF16>(ry[c], dy);
       unpack8<BF16>(rh[c], h);
+      if (C::kLean) {
+        weights<WBF16>(a.weight, run0 + c * C::kWpr * 64, runs, w[c]);
+        get_dw(sums, c, dw[c]);
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float xhat = h[j] * rstd;
         s = fmaf(w[c][j] * dy[j], xhat, s);
         dw[c][j] = fmaf(dy[j], xhat, dw[c][j]);
       }
+      if (C::kLean) put_dw(sums, c, dw[c]);
     }
     const float mean = (float)(row_sum<C::kWpr>((double)s, sm) / (double)a.cols);
 #pragma unroll
     for (int c = 0; c < C::kNch; ++c) {
       const int run = run0 + c * C::kWpr * 64;
       float dy[8], h[8], dx[8];
+      if (C::kLean) {
+        weights<WBF16>(a.weight, run, runs, w[c]);
+        if (a.dh && live && run < runs) rd[c] = load8<BF16>(a.dh, row * a.cols + run * 8);
+      }
       unpack8<BF16>(ry[c], dy);
       unpack8<BF16>(rh[c], h);
       unpack8<BF16>(rd[c], dx);                          // zeros without dh
@@ -307,6 +344,7 @@ __global__ __launch_bounds__(C::kThreads) void k_rmsnorm_grad(sshdp_rmsnorm_grad
 #pragma unroll
   for (int c = 0; c < C::kNch; ++c) {
     const int run = run0 + c * C::kWpr * 64;
+    if (C::kLean) get_dw(sums, c, dw[c]);
     if (run < runs) {
       float4 *p = reinterpret_cast<float4 *>(partials + (int64_t)blockIdx.x * a.cols + run * 8);
       p[0] = make_float4(dw[c][0], dw[c][1], dw[c][2], dw[c][3]);
@@ -340,6 +378,7 @@ using R1x4 = RowCfg<1, 4>;
 using R4x2 = RowCfg<4, 2>;
 using R4x4 = RowCfg<4, 4>;
 using R16x2 = RowCfg<16, 2>;
+using R16x3 = RowCfg<16, 3>;
 using R16x4 = RowCfg<16, 4>;
 
 // Calls f with the row layout for `cols`: the fewest waves per row whose
@@ -352,6 +391,7 @@ void with_rows(int64_t cols, F f) {
   else if (cols <= 4096) f(R4x2{});
   else if (cols <= 8192) f(R4x4{});
   else if (cols <= 16384) f(R16x2{});
+  else if (cols <= 24576) f(R16x3{});
   else f(R16x4{});
 }
 
