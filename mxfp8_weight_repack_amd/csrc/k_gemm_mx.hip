@@ -38,6 +38,8 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
+constexpr int kBufWord3 = 0x00020000;                // raw gfx9-family buffer resource
+
 __device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
 }
@@ -228,6 +230,101 @@ __global__ __launch_bounds__(64 * W) void k_gemm_mx_rows(GemmMx p, int64_t tiles
   }
 }
 
+// bfloat16 output of up to 16 rows, K <= 512 * W: a wave keeps its 4 steps of A in registers
+// and walks groups of 16 columns, each 16 codes' slot loaded anew for the next group right
+// after its matrix instruction, so B streams without a pause and A is read once a workgroup
+// (16 rows of A per 16 of B are as many cache lines again).  The waves' sums of a group are
+// added in wave order by one wave, in turn, while the others go on.  Bound by reading B:
+// 1 x 28672 x 8192 43.0 us (5.5 TB/s), 16 rows 47.6; split 128-tiles 54.5 and 58.6, the
+// kernel above 54 to 67 and 77; smaller ones gain as much (1 x 2048 x 8192 8.5 against 10.5).
+template <int W>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4, 4))) void k_gemm_mx_few(GemmMx p, int groups) {
+  constexpr int S = 4;
+  typedef uint32_t u32x4u_t __attribute__((ext_vector_type(4), aligned(1)));   // scales lie at any address
+  typedef uint32_t u32u_t __attribute__((aligned(1)));
+  __shared__ __align__(16) f32x4_t part[2][W][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int KB = (int)(p.k >> 5), kb0 = 4 * S * wave;       // the wave's blocks: kb0 .. kb0 + 15
+  const bool full = kb0 + 4 * S <= KB;
+  // word j: a row's blocks kb0 + 4 j .. + 3, zeros past the end
+  auto scales = [&](const uint8_t *s, int layout, int64_t row) __attribute__((always_inline)) {
+    const bool tile = layout == SSHDP_SCALE_TILE32X4;
+    s += tile ? (row >> 5) * (KB >> 2) * 128 + (row & 31) * 4 : (layout == SSHDP_SCALE_ROWMAJOR ? row : row >> 5) * KB;
+    u32x4_t w = {0, 0, 0, 0};
+    if (full && !tile) {
+      w = *reinterpret_cast<const u32x4u_t *>(s + kb0);
+    } else if (full) {
+#pragma unroll
+      for (int j = 0; j < S; ++j) w[j] = *reinterpret_cast<const u32u_t *>(s + ((kb0 >> 2) + j) * 128);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4 * S; ++j) {
+        const int kb = kb0 + j;
+        if (kb < KB) w[j >> 2] |= (uint32_t)s[tile ? (kb >> 2) * 128 + (kb & 3) : kb] << (8 * (kb & 3));
+      }
+    }
+    return w;
+  };
+  // The lane's chunk c (16 bytes) is inside K if 64 c < left; chunks past K and rows past N
+  // are sent out of the resource's range, and read as zeros.
+  const int k0 = kb0 * 32 + 16 * g, left = (int)p.k - k0, voff = r * (int)p.k + k0;
+  auto resource = [&](int grp) __attribute__((always_inline)) {
+    const int64_t rows = grp < groups ? min<int64_t>(p.n - grp * 16ll, 16) : 0;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p.b + (rows ? grp * 16ll * p.k : 0)), 0,
+                                             (int)(rows * p.k), kBufWord3);
+  };
+  auto load = [&](__amdgpu_buffer_rsrc_t rs, int c) __attribute__((always_inline)) {
+    return __builtin_bit_cast(u32x4_t,
+                              __builtin_amdgcn_raw_buffer_load_b128(rs, 64 * c < left ? voff + 64 * c : INT32_MAX - 15, 0, 0));
+  };
+  auto b_scales = [&](int grp) __attribute__((always_inline)) { return scales(p.bs, p.lb, min(grp * 16ll + r, p.n - 1)); };
+  const bool vec = p.ld % 4 == 0;
+  int grp = blockIdx.x;
+  u32x4_t a[2 * S], b[2 * S];
+  const __amdgpu_buffer_rsrc_t first = resource(grp);
+#pragma unroll
+  for (int c = 0; c < 2 * S; ++c) b[c] = load(first, c);
+  u32x4_t wb = b_scales(grp);
+  const int64_t m = min((int64_t)r, p.m - 1);               // rows past the end repeat the last one
+#pragma unroll
+  for (int c = 0; c < 2 * S; ++c) {
+    a[c] = u32x4_t{0, 0, 0, 0};
+    if (64 * c < left) a[c] = *reinterpret_cast<const u32x4_t *>(p.a + m * p.k + k0 + 64 * c);
+  }
+  const u32x4_t wa = scales(p.as, p.la, m);
+  for (int it = 0; grp < groups; ++it) {
+    const int next = grp + gridDim.x;
+    const __amdgpu_buffer_rsrc_t rs = resource(next);
+    u32x4_t wn = wb;
+    if (next < groups) wn = b_scales(next);
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+      i32x8_t x, y;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = (int)b[2 * s + (j >> 2)][j & 3], y[j] = (int)a[2 * s + (j >> 2)][j & 3];
+      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, 0, 0, 0, (int)(wb[s] >> (8 * g)), 0,
+                                                             (int)(wa[s] >> (8 * g)));
+      b[2 * s] = load(rs, 2 * s);
+      b[2 * s + 1] = load(rs, 2 * s + 1);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    part[it & 1][wave][lane] = acc;
+    // one barrier a group: a wave that adds up one half passes the next before the half is
+    // written again (the barrier builtin would also wait for the loads in flight)
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (wave == it % W) {
+      f32x4_t v = part[it & 1][0][lane];
+#pragma unroll
+      for (int w = 1; w < W; ++w) v += part[it & 1][w][lane];
+      store_bf16(p, r, grp * 16ll + 4 * g, v, vec);
+    }
+    wb = wn;
+    grp = next;
+  }
+}
+
 // ------------------------------------------------------------------ tiled products
 //
 // A workgroup makes a TN x TM block of the output (n x m), its waves WN x WM of them
@@ -242,7 +339,6 @@ __global__ __launch_bounds__(64 * W) void k_gemm_mx_rows(GemmMx p, int64_t tiles
 // 16 g + r holds block g's byte of the rows r, 16 + r, 32 + r, 48 + r of its 64-row
 // group, picked by the instruction's byte select.
 
-constexpr int kBufWord3 = 0x00020000;                // raw gfx9-family buffer resource
 constexpr int kRowB = 128;                           // bytes (= k) of a stage row
 
 // KG groups of WN x WM waves make the same tile over KG parts of its K and add their sums
@@ -554,8 +650,16 @@ __global__ __launch_bounds__(256) void k_gemm_mx_join(GemmMx p, const float *par
   for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < words; i += (int64_t)gridDim.x * 256) {
     const int64_t m = i / (n4 >> 2), n = (i - m * (n4 >> 2)) * 4;
     const f32x4_t *q = reinterpret_cast<const f32x4_t *>(parts) + i;
-    f32x4_t v = q[0];
-    for (int s = 1; s < splits; ++s) v += q[s * words];
+    f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+    for (int s0 = 0; s0 < splits; s0 += 8) {           // 8 splits' loads in flight
+      f32x4_t r[8];
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if (s0 + s < splits) r[s] = q[(s0 + s) * words];
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if (s0 + s < splits) v = s0 + s ? v + r[s] : r[s];
+    }
     if (BF16) store_bf16(p, m, n, v, vec);
     else store_f32(p, static_cast<float *>(p.out), m, n, v, vec);
   }
@@ -1009,6 +1113,14 @@ hipError_t gemm_tiled(const GemmMx &g, int splits, int steps, float *parts, hipS
   return hipGetLastError();
 }
 
+template <int W>
+hipError_t gemm_few(const GemmMx &g, hipStream_t s) {
+  const int groups = (int)((g.n + 15) / 16);
+  // 16 waves a CU, each with 8 KB of B in flight; more groups than that are walked
+  hipLaunchKernelGGL((k_gemm_mx_few<W>), dim3((unsigned)std::min(groups, 256 * 16 / W)), dim3(64 * W), 0, s, g, groups);
+  return hipGetLastError();
+}
+
 template <bool NN, bool BF16, int W, int NF, int MT, int UN>
 hipError_t gemm_rows(const GemmMx &g, hipStream_t s) {
   const int64_t tn = (g.n + 16 * NF - 1) / (16 * NF), tm = (g.m + 16 * MT - 1) / (16 * MT);
@@ -1022,7 +1134,7 @@ hipError_t gemm_rows(const GemmMx &g, hipStream_t s) {
   return hipSuccess;
 }
 
-// How a product runs: few-row kernel (tile 0), or tiles of 256 or 128 by `groups` wave
+// How a product runs: few-row kernel (tile 0; 16: A in registers), or tiles of 256 or 128 by `groups` wave
 // groups, with K in `splits` parts, each of `groups` runs of `steps` 128-k steps (a
 // multiple of 4: scale words come 4 steps at a time).
 struct Shape {
@@ -1040,6 +1152,8 @@ struct Shape {
 //   256-tiles: one workgroup a CU, 1.21 us a step (1.87 float32, its matrix rate is half);
 //   a K split: the join's launch, and its partial sums' bytes.
 Shape shape_of(int64_t m, int64_t n, int64_t k, bool nn, bool bf16) {
+  // ahead in every one of 35 sizes timed (n 512 .. 28672, k 544 .. 8192), by up to 45%
+  if (!nn && bf16 && m <= 16 && k <= 8192) return {16, 1, 1, 0};
   const int nk = (int)((k + kRowB - 1) / kRowB);
   Shape best{0, 1, 1, 0};
   double least = 1e30;
@@ -1088,6 +1202,7 @@ int64_t gemm_mx_workspace(int64_t m, int64_t n, int64_t k, bool nn) {
 hipError_t launch_gemm_mx(const GemmMx &g, void *ws, hipStream_t s) {
   const Shape sh = shape_of(g.m, g.n, g.k, g.nn, g.bf16);
   float *parts = static_cast<float *>(ws);
+  if (sh.tile == 16) return g.k <= 2048 ? gemm_few<4>(g, s) : g.k <= 4096 ? gemm_few<8>(g, s) : gemm_few<16>(g, s);
   if (sh.tile == 256)
     return g.nn ? gemm_tiled<T256, true>(g, sh.splits, sh.steps, parts, s)
                 : gemm_tiled<T256, false>(g, sh.splits, sh.steps, parts, s);

@@ -481,6 +481,59 @@ def test_gemm_every_shape_exact(op, m, n, k):
     assert torch.equal(out, ref + add)
 
 
+# Up to 16 rows in bfloat16: 4, 8 or 16 waves by K, its end inside a wave's part, more groups of
+# 16 columns than run at once, the last one short.
+FEW = [(1, 1, 32), (16, 17, 2048), (5, 16421, 2016), (2, 300, 2080), (16, 8225, 4096), (7, 8200, 3552), (1, 100, 4128),
+       (16, 4130, 8192), (3, 9001, 8160), (13, 4097, 7680), (1, 4112, 6176)]
+
+
+@pytest.mark.parametrize("m,n,k", FEW)
+def test_gemm_few_rows_exact(m, n, k):
+    """Whole-number operands, scales at an odd address: the exact sums rounded once (no product is cut off)."""
+    say(f"gemm few rows {m}x{n}x{k}")
+    rng = np.random.default_rng(m + 3 * n + k)
+    ac, as_, a = _operand(rng, m, k, "rowmajor", True)
+    bc, bs, b = _operand(rng, n, k, "rowmajor", True)
+    A = sh.mx_matrix(dev(ac), dev(np.concatenate([[0], as_]).astype(np.uint8))[1:], m, k)
+    B = sh.mx_matrix(dev(bc), dev(np.concatenate([[0, 0, 0], bs]).astype(np.uint8))[3:], n, k)
+    for ld in (n, n + 3, (n + 7) // 4 * 4):
+        out = buf(m + 1, ld, dtype=torch.bfloat16, fill=3.0)
+        nb = sh.gemm_mxfp8_workspace(A, B)
+        sh.gemm_mxfp8(A, B, out, "bf16", ld_out=ld, workspace=work(nb), workspace_bytes=nb, stream=stream())
+        assert np.array_equal(host(out)[:m, :n], R.as_dtype((a @ b.T).astype(np.float32), "bf16"))
+        assert bool((out[m] == 3.0).all()) and bool((out[:, n:] == 3.0).all())
+
+
+@pytest.mark.parametrize("layout", ["tile32x4", "block32x32"])
+@pytest.mark.parametrize("n,k", [(64, 640), (4128, 1920), (5024, 3968), (4160, 8064), (4320, 5376)])
+def test_gemm_few_rows_in_every_layout(n, k, layout):
+    say(f"gemm few rows {layout} {n}x{k}")
+    rng = np.random.default_rng(n + k)
+    for m in (1, 9):
+        ac, as_, a = _operand(rng, m, k, "rowmajor", True)
+        bc, bs, b = _operand(rng, n, k, layout, True)
+        assert np.array_equal(_gemm((ac, as_), (bc, bs), m, n, "bf16", layouts=("rowmajor", layout)),
+                              R.as_dtype((a @ b.T).astype(np.float32), "bf16"))
+
+
+@pytest.mark.parametrize("n,k", [(48, 384), (4400, 4064), (4200, 8000)])
+def test_gemm_few_rows_nan_blocks_stay_in_their_row(n, k):
+    """NaN scales at a row's ends, next to rows and K ends that are read around."""
+    say(f"gemm few rows NaN {n}x{k}")
+    rng = np.random.default_rng(n + k)
+    m = 6
+    ac, as_, a = _operand(rng, m, k, "rowmajor", True)
+    bc, bs, b = _operand(rng, n, k, "rowmajor", True)
+    clean = _gemm((ac, as_), (bc, bs), m, n, "bf16")
+    assert np.array_equal(clean, R.as_dtype((a @ b.T).astype(np.float32), "bf16"))
+    sa, sb = as_.reshape(m, k // 32).copy(), bs.reshape(n, k // 32).copy()
+    sa[2, 0], sa[4, -1], sb[16, 0], sb[n - 2, -1], sb[31, k // 64] = 255, 255, 255, 255, 255
+    got = _gemm((ac, sa), (bc, sb), m, n, "bf16")
+    bad = np.zeros((m, n), bool)
+    bad[[2, 4], :], bad[:, [16, n - 2, 31]] = True, True
+    assert np.all(np.isnan(got[bad])) and np.array_equal(got[~bad], clean[~bad])
+
+
 @pytest.mark.parametrize("n,k", [(64, 640), (2080, 1152), (160, 4224)])
 @pytest.mark.parametrize("layout", ["tile32x4", "block32x32"])
 def test_gemm_long_rows_in_every_layout(n, k, layout):
