@@ -464,7 +464,9 @@ struct Loader {
   bool inp, inq;                                     // whether the lane's chunk lies inside the last step
   const uint8_t *gp, *gq;
   const uint8_t *sbase;                              // scales: the wave's 64-row group ...
-  int soff, xstep, xlane, xmax, xmul, tshift;        // ... and the lane's address in it
+  int soff, xstep, xlane, xmax, xmul, xend, tshift;  // ... and the lane's address in it
+  int narrow;                                        // blocks of a row too short for a 4-byte word, else 0
+  static constexpr bool kEnd = NN && C::TN < 256;    // 256-tiles take no NN with N < 128 (and have no register to spare)
   bool xwords;                                       // a step's words lie apart: 4-byte loads
   uint32_t psel;
 
@@ -491,8 +493,8 @@ struct Loader {
       gp = p.b + n0 * p.k;
     }
     // Scales: wave = 64-row group, n side first.  A lane reads one row's 4 bytes of a step
-    // at sbase + soff + min(step * xstep + xlane, xmax) * xmul.  Rows past the end repeat
-    // the last one: their codes are zeros and their results unused.
+    // at sbase + soff + min(min(step * xstep + xlane, xmax) * xmul, xend).  Rows past the end
+    // repeat the last one: their codes are zeros and their results unused.
     const bool ps = wave < C::TN / 64;
     const int layout = ps ? p.lb : p.la, KB = (int)(p.k >> 5);
     const int64_t r0 = ps ? n0 + 64 * wave : m0 + 64 * (wave - C::TN / 64);
@@ -502,19 +504,23 @@ struct Loader {
     sbase = ps ? p.bs : p.as;
     xmul = 1;
     xlane = 0;
+    xend = INT32_MAX;
+    narrow = 0;
     tshift = 0;
     psel = 0;
     xwords = true;
     if (NN && ps) {
       // the group's 64 columns are two blocks: lane 16 g + r reads 4 neighbouring columns'
-      // blocks in block row 4 step + g and keeps its two
-      const int NB = (int)(p.n >> 5), nb = min((int)(n0 >> 5) + 2 * wave, NB - 1), first = min(nb, NB - 4);
+      // blocks in block row 4 step + g and keeps its two.  Under 4 blocks a row, that word
+      // may run into the next row, and from the last one is read from before its place.
+      const int NB = (int)(p.n >> 5), nb = min((int)(n0 >> 5) + 2 * wave, NB - 1), first = max(min(nb, NB - 4), 0);
       sbase += first;
       soff = 0;
       xstep = 4;
       xlane = lane >> 4;
       xmax = KB - 1;
       xmul = NB;
+      xend = KB * NB - 4 - first;
       psel = (uint32_t)(nb - first) * 0x0101u + (uint32_t)min(nb - first + 1, 3) * 0x01010000u;
     } else if (layout == SSHDP_SCALE_TILE32X4) {
       sbase += (rb >> 5) * (KB >> 2) * 128;
@@ -526,7 +532,8 @@ struct Loader {
       sbase += (rb >> sh) * KB;
       soff = (rr >> sh) * KB;
       xstep = 4;
-      xmax = KB - 4;
+      xmax = max(KB - 4, 0);
+      narrow = KB < 4 ? KB : 0;
       tshift = 8;
       xwords = false;
     }
@@ -569,12 +576,15 @@ struct Loader {
   template <bool SHORT>
   __device__ __forceinline__ u32x4_t scales(int q) const {
     u32x4_t w;
-    if (SHORT || xwords) {
+    if (SHORT && narrow) {
+      w = u32x4_t{0, 0, 0, 0};
+      for (int i = 0; i < narrow; ++i) w[0] |= (uint32_t)sbase[soff + i] << (8 * i);
+    } else if (SHORT || xwords) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int x = (kt0 + 4 * q + j) * xstep + xlane;
         uint32_t v;
-        __builtin_memcpy(&v, sbase + (uint32_t)(soff + min(x, xmax) * xmul), 4);   // any alignment
+        __builtin_memcpy(&v, sbase + (uint32_t)(soff + (kEnd ? min(min(x, xmax) * xmul, xend) : min(x, xmax) * xmul)), 4);   // any alignment
         w[j] = v;
       }
     } else {
@@ -589,7 +599,10 @@ struct Loader {
     u32x4_t w = raw;
     // what was read from before its place moves down (no branches here: see pin below);
     // zeros come in beside codes that are all zero
-    if (SHORT) {
+    if (kEnd && wave < C::TN / 64) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] >>= 8 * max(min((kt0 + 4 * q + j) * xstep + xlane, xmax) * xmul - xend, 0);
+    } else if (SHORT) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) w[j] >>= min(max((kt0 + 4 * q + j) * xstep - xmax, 0) * tshift, 24);
     } else {
@@ -1160,7 +1173,7 @@ Shape shape_of(int64_t m, int64_t n, int64_t k, bool nn, bool bf16) {
   auto consider = [&](const Shape &s, double us) {
     if (us < least) least = us, best = s;
   };
-  const bool tiles = k >= kRowB && (!nn || n >= 128);   // scale words: 4 blocks along k (NN: and n)
+  const bool tiles = nn ? (k >> 5) * (n >> 5) >= 4 : k > 0;   // NN reads scales 4 at a time
   if (!tiles || (!nn && m <= 256)) {
     const int rows = m <= 16 ? 16 : m <= 32 ? 32 : 64;
     const double rate = rows == 16 ? 5.8e6 : rows == 32 ? 3.4e6 : 5.0e6;
@@ -1185,6 +1198,7 @@ Shape shape_of(int64_t m, int64_t n, int64_t k, bool nn, bool bf16) {
       double us = 3.2 + pairs * (1.4 + run * two) + join;
       if (rest) us += 1.4 + run * (rest <= 256 ? one : one + (two - one) * (rest - 256) / 256);
       consider({128, 1, splits, steps}, us);
+      if (nn && n < 128) continue;
       consider({256, 1, splits, steps}, 4.5 + (t256 * splits + 255) / 256 * (2.3 + run * (bf16 ? 1.21 : 1.87)) + join);
     }
   return best;

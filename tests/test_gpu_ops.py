@@ -534,6 +534,45 @@ def test_gemm_few_rows_nan_blocks_stay_in_their_row(n, k):
     assert np.all(np.isnan(got[bad])) and np.array_equal(got[~bad], clean[~bad])
 
 
+# Rows of fewer scale bytes than a word: K under 128, and of an NN operand N under 128.
+THIN = [("nt", 300, 520, 32, "rowmajor"), ("nt", 1030, 300, 96, "rowmajor"), ("nt", 257, 260, 64, "rowmajor"),
+        ("nt", 3000, 2050, 32, "rowmajor"), ("nt", 300, 544, 96, "block32x32"), ("nt", 513, 1024, 32, "block32x32"),
+        ("nn", 300, 32, 128, None), ("nn", 129, 64, 1056, None), ("nn", 2229, 96, 4480, None), ("nn", 40, 96, 64, None),
+        ("nn", 5, 96, 2080, None), ("nn", 700, 160, 32, None), ("nn", 1, 320, 96, None), ("nn", 2500, 2048, 64, None),
+        ("nn", 3, 64, 64, None), ("nn", 300, 64, 32, None)]
+
+
+@pytest.mark.parametrize("op,m,n,k,layout", THIN)
+def test_gemm_thin_operands(op, m, n, k, layout):
+    """Exact sums, and NaN scales that spoil their own block's row or columns alone."""
+    say(f"gemm thin {op} {m}x{n}x{k} {layout}")
+    rng = np.random.default_rng(m + 3 * n + k)
+    nn = op == "nn"
+    lay = "block32x32" if nn else layout
+    ac, as_, a = _operand(rng, m, k, "rowmajor", True)
+    bc, bs, b = _operand(rng, k if nn else n, n if nn else k, lay, True)
+    ref = (a @ (b if nn else b.T)).astype(np.float32)
+    sa, sb = as_.reshape(m, k // 32).copy(), bs.copy()
+    sa[m // 2, 0], sa[m - 1, -1] = 255, 255
+    sb[sb.size // 2], sb[-1] = 255, 255
+    bad = np.zeros((m, n), bool)
+    bad[[m // 2, m - 1], :] = True
+    for i in (sb.size // 2, sb.size - 1):
+        if nn:
+            bad[:, i % (n // 32) * 32:i % (n // 32) * 32 + 32] = True
+        elif lay == "block32x32":
+            bad[:, i // (k // 32) * 32:i // (k // 32) * 32 + 32] = True
+        else:
+            bad[:, i // (k // 32)] = True
+    lays = ("rowmajor", lay)
+    for out in ("fp32", "bf16"):
+        assert np.array_equal(_gemm((ac, as_), (bc, bs), m, n, out, op, layouts=lays, pad=3), R.as_dtype(ref, out)), out
+        got = _gemm((ac, sa), (bc, sb), m, n, out, op, layouts=lays)
+        assert np.all(np.isnan(got[bad])) and np.array_equal(got[~bad], R.as_dtype(ref, out)[~bad]), out
+    add = rng.integers(-50, 50, (m, n)).astype(np.float32)
+    assert np.array_equal(_gemm((ac, as_), (bc, bs), m, n, "fp32", op, addend=add, layouts=lays, in_place=True), ref + add)
+
+
 @pytest.mark.parametrize("n,k", [(64, 640), (2080, 1152), (160, 4224)])
 @pytest.mark.parametrize("layout", ["tile32x4", "block32x32"])
 def test_gemm_long_rows_in_every_layout(n, k, layout):

@@ -131,6 +131,20 @@ def test_gemm_refusals():
     sh.gemm_mxfp8(mat(0, 64, codes=None, scales=None), b, None)           # no rows: nothing to do
 
 
+def test_gemm_workspace_of_every_small_size():
+    """Down to empty operands: none divides by nothing, and each answer holds a whole number of partial outputs."""
+    for m in (0, 1, 16, 17, 300, 5000):
+        for n in (0, 1, 32, 96, 128, 8192):
+            for k in (0, 32, 96, 128, 544, 4096):
+                for op in ("nt", "nn"):
+                    if op == "nn" and n % 32:
+                        continue
+                    a = sh.mx_matrix(P, P, m, k)
+                    b = sh.mx_matrix(P, P, *((k, n, "block32x32") if op == "nn" else (n, k)))
+                    size = sh.gemm_mxfp8_workspace(a, b, op=op)
+                    assert size >= 0 and size % max(4 * m * ((n + 3) // 4 * 4), 1) == 0
+
+
 def test_grad_refusals_on_a_host_only_plan():
     node = dict(parent=-1, offset=0, rows=1, cols=64, row_stride=64, is_unit=True, optimizer="adamw", quantize=None)
     p = sh.Plan([node], 64, host_only=True)
