@@ -247,11 +247,45 @@ __device__ __forceinline__ void put_dw(float4 *sums, int c, const float (&v)[8])
     sums[(2 * c + h) * blockDim.x + threadIdx.x] = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
 }
 
+// dweight of 32 columns from c0 on: 64 threads' rows of 8 columns each, then the threads in
+// order.
+template <bool BF16>
+__device__ __forceinline__ void column_grads(const sshdp_rmsnorm_grad &a, int c0) {
+  __shared__ float sums[64][33];
+  const int t = threadIdx.x, c = (t & 3) * 8, sl = t >> 2;
+  float s[8] = {};
+  for (int64_t row = sl; row < a.rows; row += 64) {
+    const int64_t e = row * a.cols + c0 + c;
+    float dy[8], h[8];
+    unpack8<BF16>(load8<BF16>(a.dy, e), dy);
+    unpack8<BF16>(load8<BF16>(a.h, e), h);
+    const float rstd = a.rstd[row];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] = fmaf(dy[j], h[j] * rstd, s[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sums[sl][c + j] = s[j];
+  __syncthreads();
+  if (t >= 32) return;
+  float v = a.first ? 0.f : a.dweight[c0 + t], d = 0.f;
+#pragma unroll
+  for (int k = 0; k < 64; ++k) d += sums[k][t];
+  a.dweight[c0 + t] = v + d;
+}
+
 // Workgroups keep their columns' weight-gradient sums in registers over all their
 // rows and leave one partial row each; k_dweight adds the partial rows.
-template <bool BF16, bool WBF16, class C>
-__global__ __launch_bounds__(C::kThreads) void k_rmsnorm_grad(sshdp_rmsnorm_grad a, float *partials) {
+//
+// ONCE, for few rows: no partial rows and no second launch.  Workgroups from `row_groups` on
+// take 32 columns each and add their weight gradient over all rows, read a second time (the
+// rows' statistics are not needed for it: rstd is given).
+template <bool BF16, bool WBF16, class C, bool ONCE>
+__global__ __launch_bounds__(C::kThreads) void k_rmsnorm_grad(sshdp_rmsnorm_grad a, float *partials, int row_groups) {
   __shared__ double sm[C::kThreads / 64];
+  if (ONCE && blockIdx.x >= (unsigned)row_groups) {
+    column_grads<BF16>(a, (int)(blockIdx.x - row_groups) * 32);
+    return;
+  }
   __shared__ float4 sums[C::kLean ? C::kNch * 2 * C::kThreads : 1];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int sub = wave / C::kWpr, run0 = (wave % C::kWpr) * 64 + lane;
@@ -265,7 +299,7 @@ __global__ __launch_bounds__(C::kThreads) void k_rmsnorm_grad(sshdp_rmsnorm_grad
     for (int j = 0; j < 8; ++j) dw[c][j] = 0.f;
     if (C::kLean) put_dw(sums, c, dw[c]);
   }
-  for (int64_t g = blockIdx.x; g * C::kRows < a.rows; g += gridDim.x) {
+  for (int64_t g = blockIdx.x; g * C::kRows < a.rows; g += row_groups) {
     const int64_t row = g * C::kRows + sub;
     const bool live = row < a.rows;
     Raw8<BF16> ry[C::kNch], rh[C::kNch], rd[C::kNch];
@@ -318,6 +352,7 @@ __global__ __launch_bounds__(C::kThreads) void k_rmsnorm_grad(sshdp_rmsnorm_grad
       if (live && run < runs) store8<BF16>(a.dx, row * a.cols + run * 8, pack8<BF16>(dx));
     }
   }
+  if (ONCE) return;
   // one partial row per workgroup: its waves' rows are added in wave order
   if (C::kRows > 1) {
     __shared__ float4 part[C::kRows > 1 ? C::kRows - 1 : 1][C::kNch][2][64];
@@ -400,6 +435,7 @@ constexpr int64_t kNormGroups = 2048;                  // workgroups of the forw
 // two per CU keep HBM busy, and each more is a row written and read back (8191 x 8192
 // bfloat16: 103 us; 256 108, 1024 110).
 constexpr int64_t kGradGroups = 512;
+constexpr int64_t kOnceRows = 1024;
 
 template <class C>
 int64_t norm_groups(int64_t rows, int64_t most) {
@@ -417,14 +453,24 @@ hipError_t rmsnorm(const sshdp_rmsnorm &a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Up to 1024 rows a second reading costs less than a second launch (bfloat16, 33 x 2048: 4.9
+// us a call against 7.5, 512 x 8192 9.6 against 18.9, 1024 x 8192 18.1 against 19.3; 2048 x
+// 8192 33.8 against 25.8).
+// Not over dy itself: it is read by other workgroups while dx is written.
 template <class C>
+bool norm_grad_once(const sshdp_rmsnorm_grad &a) {
+  return C::kThreads == 256 && a.rows <= kOnceRows && a.dx != a.dy;
+}
+
+template <class C, bool ONCE>
 hipError_t rmsnorm_grad(const sshdp_rmsnorm_grad &a, float *partials, hipStream_t s) {
-  const dim3 grid((unsigned)norm_groups<C>(a.rows, kGradGroups)), block(C::kThreads);
+  const int groups = (int)norm_groups<C>(a.rows, kGradGroups);
+  const dim3 grid((unsigned)(groups + (ONCE ? a.cols / 32 : 0))), block(C::kThreads);
   const bool b = a.dtype == SSHDP_DTYPE_BF16, wb = a.weight_dtype == SSHDP_DTYPE_BF16;
-  if (b && wb) hipLaunchKernelGGL((k_rmsnorm_grad<true, true, C>), grid, block, 0, s, a, partials);
-  else if (b) hipLaunchKernelGGL((k_rmsnorm_grad<true, false, C>), grid, block, 0, s, a, partials);
-  else if (wb) hipLaunchKernelGGL((k_rmsnorm_grad<false, true, C>), grid, block, 0, s, a, partials);
-  else hipLaunchKernelGGL((k_rmsnorm_grad<false, false, C>), grid, block, 0, s, a, partials);
+  if (b && wb) hipLaunchKernelGGL((k_rmsnorm_grad<true, true, C, ONCE>), grid, block, 0, s, a, partials, groups);
+  else if (b) hipLaunchKernelGGL((k_rmsnorm_grad<true, false, C, ONCE>), grid, block, 0, s, a, partials, groups);
+  else if (wb) hipLaunchKernelGGL((k_rmsnorm_grad<false, true, C, ONCE>), grid, block, 0, s, a, partials, groups);
+  else hipLaunchKernelGGL((k_rmsnorm_grad<false, false, C, ONCE>), grid, block, 0, s, a, partials, groups);
   return hipGetLastError();
 }
 
@@ -471,8 +517,17 @@ int64_t rmsnorm_partials(int64_t rows, int64_t cols) {
 
 hipError_t launch_rmsnorm_backward(const sshdp_rmsnorm_grad &a, float *partials, hipStream_t s) {
   hipError_t e = hipSuccess;
-  if (a.rows) with_rows(a.cols, [&](auto c) { e = rmsnorm_grad<decltype(c)>(a, partials, s); });
-  if (e != hipSuccess) return e;
+  bool once = false;
+  if (a.rows)
+    with_rows(a.cols, [&](auto c) {
+      using C = decltype(c);
+      once = norm_grad_once<C>(a);
+      if constexpr (C::kThreads == 256) {
+        if (once) e = rmsnorm_grad<C, true>(a, nullptr, s);
+      }
+      if (!once) e = rmsnorm_grad<C, false>(a, partials, s);
+    });
+  if (e != hipSuccess || once) return e;
   hipLaunchKernelGGL(k_dweight, dim3((unsigned)(a.cols / 32)), dim3(1024), 0, s, partials,
                      a.rows ? rmsnorm_partials(a.rows, a.cols) : 0, a.cols, a.first, a.dweight);
   return hipGetLastError();

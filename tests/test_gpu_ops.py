@@ -289,6 +289,49 @@ def test_rmsnorm_backward_against_float64(rows, cols, dtype, wdtype):
         assert np.all(np.abs(got[:cols] - dw) <= bdw) and got[cols] == 9.0
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(64, 2048), (65, 96), (1000, 544), (1024, 8192), (1025, 8192), (1024, 32), (300, 16416)])
+def test_rmsnorm_backward_of_few_rows_and_more(rows, cols, dtype):
+    """On both sides of where one launch does it all; twice into the same weight gradient, reproducibly."""
+    say(f"rmsnorm backward rows {rows}x{cols} {dtype}")
+    rng = np.random.default_rng(rows + 5 * cols)
+    dy, h, dh = (_matrix(rng, rows, cols, dtype, special=False) for _ in range(3))
+    w = (1 + 0.2 * rng.standard_normal(cols)).astype(np.float32)
+    rstd = R.rmsnorm(h, None, w, 1e-6, dtype)[1].astype(np.float32)
+    dx, bdx, dw, bdw = R.rmsnorm_grad(dy, h, w, rstd, dh, dtype)
+    nb, td = sh.rmsnorm_backward_workspace(rows, cols), torch.bfloat16 if dtype == "bf16" else torch.float32
+    runs = []
+    for _ in range(2):
+        dxd, dwd = buf(rows, cols, dtype=td, fill=3.0), buf(cols, dtype=torch.float32, fill=3.0)
+        for first in (True, False):
+            sh.rmsnorm_backward(dev(dy, dtype), dev(h, dtype), dev(w), dev(rstd), dxd, dwd, rows, cols, dtype=dtype,
+                                dh=dev(dh, dtype), first=first, workspace=work(nb), workspace_bytes=nb, stream=stream())
+        assert np.all(np.abs(host(dxd) - dx) <= bdx)
+        assert np.all(np.abs(host(dwd) - 2 * dw) <= 2 * bdw + R.U * np.abs(2 * dw))
+        runs.append((dxd, dwd))
+    assert torch.equal(runs[0][0], runs[1][0]) and torch.equal(runs[0][1], runs[1][1])
+
+
+@pytest.mark.parametrize("over", ["dy", "dh"])
+@pytest.mark.parametrize("rows,cols", [(33, 2048), (700, 8192), (1024, 512), (1500, 1056)])
+def test_rmsnorm_backward_over_its_inputs(rows, cols, over):
+    """dx may be dy or dh, at any number of rows."""
+    say(f"rmsnorm backward over {over} {rows}x{cols}")
+    rng = np.random.default_rng(rows + cols)
+    dy, h, dh = (_matrix(rng, rows, cols, "bf16", special=False) for _ in range(3))
+    w = (1 + 0.2 * rng.standard_normal(cols)).astype(np.float32)
+    rstd = R.rmsnorm(h, None, w, 1e-6, "bf16")[1].astype(np.float32)
+    dx, bdx, dw, bdw = R.rmsnorm_grad(dy, h, w, rstd, dh, "bf16")
+    nb = sh.rmsnorm_backward_workspace(rows, cols)
+    args = [dev(h, "bf16"), dev(w), dev(rstd)]
+    for _ in range(5):
+        dyd, dhd, dwd = dev(dy, "bf16"), dev(dh, "bf16"), buf(cols, dtype=torch.float32, fill=3.0)
+        out = dyd if over == "dy" else dhd
+        sh.rmsnorm_backward(dyd, *args, out, dwd, rows, cols, dh=dhd, workspace=work(nb), workspace_bytes=nb,
+                            stream=stream())
+        assert np.all(np.abs(host(out) - dx) <= bdx) and np.all(np.abs(host(dwd) - dw) <= bdw)
+
+
 def test_rmsnorm_backward_in_place_and_empty():
     rng = np.random.default_rng(8)
     rows, cols = 20, 96
