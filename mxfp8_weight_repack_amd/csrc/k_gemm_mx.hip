@@ -93,13 +93,16 @@ __device__ __forceinline__ void store_bf16(const GemmMx &p, int64_t m, int64_t n
 
 // ------------------------------------------------------------------- few-row products
 
-// out of p.m rows for a few m (one token to a small batch), and whatever the tiles below do
-// not take: bound by reading B once.  A workgroup's W waves share 16 * NF columns n and
-// split K among them, one 128-k step in W each, so together they read runs of W * 128
-// bytes of B's rows; codes go straight from memory to the matrix instructions, UN steps'
-// loads in flight per wave.  MT * 16 rows of m at a time; rows past the end repeat the
-// last one.  The waves' sums meet in LDS and are added in wave order.
-template <bool NN, bool BF16, int W, int NF, int MT, int UN>
+// out of p.m rows for a few m, and NN operands of fewer scale blocks than a word: bound by
+// reading B once, and by the L1's rate of lines (16 rows of codes are 16 lines a load, and
+// A's and the scales' are as many again).  A workgroup's W waves share 16 * NF columns n and
+// split K among them, one 128-k step in W each, so together they read runs of W * 128 bytes
+// of B's rows; codes go straight from memory to the matrix instructions, one step's loads in
+// flight while another's are multiplied (two to four in flight were slower: fewer waves).
+// MT * 16 rows of m at a time; rows past the end repeat the last one.  The waves' sums meet
+// in LDS and are added in wave order.  32 x 2048 x 2048: 6.1 us; 1 x 2048 x 8192 with float32
+// output 13.6 us.
+template <bool NN, bool BF16, int W, int NF, int MT>
 __global__ __launch_bounds__(64 * W) void k_gemm_mx_rows(GemmMx p, int64_t tiles_n, int64_t first) {
   __shared__ __align__(16) f32x4_t part[W][NF * MT][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -197,21 +200,16 @@ __global__ __launch_bounds__(64 * W) void k_gemm_mx_rows(GemmMx p, int64_t tiles
         }
       }
   };
-  Step st[2][UN];
-#pragma unroll
-  for (int u = 0; u < UN; ++u) fetch(st[0][u], wave + u * W);
+  Step st[2];
+  fetch(st[0], wave);
   for (int k0 = wave;;) {
-#pragma unroll
-    for (int u = 0; u < UN; ++u) fetch(st[1][u], k0 + UN * W + u * W);
-#pragma unroll
-    for (int u = 0; u < UN; ++u) multiply(st[0][u]);
-    k0 += UN * W;
+    fetch(st[1], k0 + W);
+    multiply(st[0]);
+    k0 += W;
     if (k0 >= nk) break;
-#pragma unroll
-    for (int u = 0; u < UN; ++u) fetch(st[0][u], k0 + UN * W + u * W);
-#pragma unroll
-    for (int u = 0; u < UN; ++u) multiply(st[1][u]);
-    k0 += UN * W;
+    fetch(st[0], k0 + W);
+    multiply(st[1]);
+    k0 += W;
     if (k0 >= nk) break;
   }
 #pragma unroll
@@ -340,12 +338,17 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4, 4))) 
 // apart turns each step's 4 bytes into the word the matrix instruction wants: lane
 // 16 g + r holds block g's byte of the rows r, 16 + r, 32 + r, 48 + r of its 64-row
 // group, picked by the instruction's byte select.
+//
+// 8192 x 28672 x 8192, bfloat16: 1.43-1.66 ms, 2.3-2.7 PFLOP/s (the clock falls with the data's
+// activity), matrix cores busy 71% of the time.  The rest is operand latency beyond the L2
+// (with every load a hit: 1.32 ms) and the scales (without any: 1.38 ms).
 
 constexpr int kRowB = 128;                           // bytes (= k) of a stage row
 
 // KG groups of WN x WM waves make the same tile over KG parts of its K and add their sums
 // in LDS: where there are too few tiles to give every CU two workgroups, a second group
-// hides what one cannot.
+// hides what one cannot (1999 x 2048 x 8192 NN: 43.9 us, one group 50.3; 26 us at the large
+// product's rate -- 64 steps one after another, each waiting for its stage's loads).
 template <int TN_, int TM_, int WN_, int WM_, int KG_>
 struct Tile {
   static constexpr int TN = TN_, TM = TM_, WN = WN_, WM = WM_, NW = WN * WM, NT = 64 * NW, KG = KG_, NST = 2;
@@ -657,7 +660,8 @@ __device__ __forceinline__ void store_part(const GemmMx &p, float *parts, int64_
     }
 }
 
-// The splits' sums added in split order, 4 consecutive n per thread.
+// The splits' sums added in split order, 4 consecutive n per thread (1 x 8192 x 28672, six
+// splits: 50.8 us with the tiles, their loads one after another 52.1).
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_gemm_mx_join(GemmMx p, const float *parts, int splits) {
   const int64_t n4 = (p.n + 3) & ~(int64_t)3, words = p.m * (n4 >> 2);
@@ -896,6 +900,9 @@ __global__ __launch_bounds__(C::NT * C::KG) __attribute__((amdgpu_waves_per_eu(C
 // bfloat16 on their way from LDS to the matrix instructions.  A half step is one 16-byte
 // chunk per lane (64 k): its m-side fragments stay converted while the n side's pass by,
 // one converted (8 conversions) beside the previous one's 2 x FQ matrix instructions.
+// 8192 x 2048 x 4096 with an addend: 117-121 us, 1.2 PFLOP/s of a bfloat16 rate of 1.38 that a
+// large library product reaches here; 67 MB of addend in and as much out are 28 us of it,
+// which one workgroup a CU hides only in part.
 template <class C, bool NN, bool SHORT>
 __global__ __launch_bounds__(C::NT * C::KG) __attribute__((amdgpu_waves_per_eu(C::WPS, C::WPS))) void k_gemm_mx16(GemmMx p, int64_t tiles_m,
                                                                                               int64_t tiles_n, int steps, float *parts) {
@@ -1134,13 +1141,13 @@ hipError_t gemm_few(const GemmMx &g, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool NN, bool BF16, int W, int NF, int MT, int UN>
+template <bool NN, bool BF16, int W, int NF, int MT>
 hipError_t gemm_rows(const GemmMx &g, hipStream_t s) {
   const int64_t tn = (g.n + 16 * NF - 1) / (16 * NF), tm = (g.m + 16 * MT - 1) / (16 * MT);
   const int64_t most = 1 << 22;                        // a launch has under 2^32 threads: outputs past that take several
   for (int64_t first = 0; first < tm * tn; first += most) {
     const dim3 grid((unsigned)std::min(tm * tn - first, most));
-    hipLaunchKernelGGL((k_gemm_mx_rows<NN, BF16, W, NF, MT, UN>), grid, dim3(64 * W), 0, s, g, tn, first);
+    hipLaunchKernelGGL((k_gemm_mx_rows<NN, BF16, W, NF, MT>), grid, dim3(64 * W), 0, s, g, tn, first);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -1226,10 +1233,10 @@ hipError_t launch_gemm_mx(const GemmMx &g, void *ws, hipStream_t s) {
   if (sh.tile == 128)
     return g.nn ? gemm_tiled<T128, true>(g, sh.splits, sh.steps, parts, s)
                 : gemm_tiled<T128, false>(g, sh.splits, sh.steps, parts, s);
-  if (g.nn) return g.bf16 ? gemm_rows<true, true, 4, 1, 1, 1>(g, s) : gemm_rows<true, false, 4, 1, 1, 1>(g, s);
-  if (g.m <= 16) return g.bf16 ? gemm_rows<false, true, 8, 1, 1, 1>(g, s) : gemm_rows<false, false, 8, 1, 1, 1>(g, s);
-  if (g.m <= 32) return g.bf16 ? gemm_rows<false, true, 8, 1, 2, 1>(g, s) : gemm_rows<false, false, 8, 1, 2, 1>(g, s);
-  return g.bf16 ? gemm_rows<false, true, 8, 2, 4, 1>(g, s) : gemm_rows<false, false, 8, 2, 4, 1>(g, s);
+  if (g.nn) return g.bf16 ? gemm_rows<true, true, 4, 1, 1>(g, s) : gemm_rows<true, false, 4, 1, 1>(g, s);
+  if (g.m <= 16) return g.bf16 ? gemm_rows<false, true, 8, 1, 1>(g, s) : gemm_rows<false, false, 8, 1, 1>(g, s);
+  if (g.m <= 32) return g.bf16 ? gemm_rows<false, true, 8, 1, 2>(g, s) : gemm_rows<false, false, 8, 1, 2>(g, s);
+  return g.bf16 ? gemm_rows<false, true, 8, 2, 4>(g, s) : gemm_rows<false, false, 8, 2, 4>(g, s);
 }
 
 }  // namespace sshdp
