@@ -231,41 +231,54 @@ __global__ __launch_bounds__(64 * W) void k_gemm_mx_rows(GemmMx p, int64_t tiles
   }
 }
 
-// bfloat16 output of up to 16 rows, K <= 512 * W: a wave keeps its 4 steps of A in registers
-// and walks groups of 16 columns, each 16 codes' slot loaded anew for the next group right
-// after its matrix instruction, so B streams without a pause and A is read once a workgroup
-// (16 rows of A per 16 of B are as many cache lines again).  The waves' sums of a group are
-// added in wave order by one wave, in turn, while the others go on.  Bound by reading B:
-// 1 x 28672 x 8192 43.0 us (5.5 TB/s), 16 rows 47.6; split 128-tiles 54.5 and 58.6, the
-// kernel above 54 to 67 and 77; smaller ones gain as much (1 x 2048 x 8192 8.5 against 10.5).
-template <int W>
-__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4, 4))) void k_gemm_mx_few(GemmMx p, int groups) {
-  constexpr int S = 4;
+// Up to 16 rows, K <= 1024 * W: a wave keeps its 8 steps of A in registers and walks groups
+// of 16 columns, each 16 codes' slot loaded anew for the next group right after its matrix
+// instructions, so B streams without a pause and A is read once a workgroup (16 rows of A per
+// 16 of B are as many cache lines again).  The waves' sums of a group are added in wave order
+// by one wave, in turn, while the others go on.  Bound by reading B: 1 x 28672 x 8192 42.4 us
+// (5.5 TB/s), 16 rows 46.9, float32 output 42.2; split 128-tiles 54.5, 58.6 and 60.6, the
+// kernel above 54 to 67; smaller ones gain as much (1 x 2048 x 8192 8.1 against 10.5).  Twice
+// the waves with 4 steps each: up to 15% slower (16 x 12288 x 4096: 17.5 against 15.3).
+constexpr int kFewSteps = 8;
+
+template <bool BF16, int W>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_gemm_mx_few(GemmMx p, int groups) {
+  constexpr int S = kFewSteps;
   typedef uint32_t u32x4u_t __attribute__((ext_vector_type(4), aligned(1)));   // scales lie at any address
   typedef uint32_t u32u_t __attribute__((aligned(1)));
+  struct Words {
+    uint32_t w[S];
+  };
   __shared__ __align__(16) f32x4_t part[2][W][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int KB = (int)(p.k >> 5), kb0 = 4 * S * wave;       // the wave's blocks: kb0 .. kb0 + 15
+  const int KB = (int)(p.k >> 5), kb0 = 4 * S * wave;       // the wave's blocks: 4 S from kb0 on
   const bool full = kb0 + 4 * S <= KB;
   // word j: a row's blocks kb0 + 4 j .. + 3, zeros past the end
   auto scales = [&](const uint8_t *s, int layout, int64_t row) __attribute__((always_inline)) {
     const bool tile = layout == SSHDP_SCALE_TILE32X4;
     s += tile ? (row >> 5) * (KB >> 2) * 128 + (row & 31) * 4 : (layout == SSHDP_SCALE_ROWMAJOR ? row : row >> 5) * KB;
-    u32x4_t w = {0, 0, 0, 0};
+    Words v{};
     if (full && !tile) {
-      w = *reinterpret_cast<const u32x4u_t *>(s + kb0);
+#pragma unroll
+      for (int j = 0; j < S; j += 4) {
+        const u32x4_t x = *reinterpret_cast<const u32x4u_t *>(s + kb0 + 4 * j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v.w[j + i] = x[i];
+      }
     } else if (full) {
 #pragma unroll
-      for (int j = 0; j < S; ++j) w[j] = *reinterpret_cast<const u32u_t *>(s + ((kb0 >> 2) + j) * 128);
+      for (int j = 0; j < S; ++j) v.w[j] = *reinterpret_cast<const u32u_t *>(s + ((kb0 >> 2) + j) * 128);
     } else {
 #pragma unroll
-      for (int j = 0; j < 4 * S; ++j) {
-        const int kb = kb0 + j;
-        if (kb < KB) w[j >> 2] |= (uint32_t)s[tile ? (kb >> 2) * 128 + (kb & 3) : kb] << (8 * (kb & 3));
+      for (int j = 0; j < S; ++j) {
+        const int kb = kb0 + 4 * j, n = min(KB - kb, 4);
+        const uint8_t *q = s + (tile ? (kb >> 2) * 128 : kb);
+        if (n == 4) v.w[j] = *reinterpret_cast<const u32u_t *>(q);
+        else for (int i = 0; i < n; ++i) v.w[j] |= (uint32_t)q[i] << (8 * i);
       }
     }
-    return w;
+    return v;
   };
   // The lane's chunk c (16 bytes) is inside K if 64 c < left; chunks past K and rows past N
   // are sent out of the resource's range, and read as zeros.
@@ -285,27 +298,36 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4, 4))) 
   const __amdgpu_buffer_rsrc_t first = resource(grp);
 #pragma unroll
   for (int c = 0; c < 2 * S; ++c) b[c] = load(first, c);
-  u32x4_t wb = b_scales(grp);
+  Words wb = b_scales(grp);
   const int64_t m = min((int64_t)r, p.m - 1);               // rows past the end repeat the last one
 #pragma unroll
   for (int c = 0; c < 2 * S; ++c) {
     a[c] = u32x4_t{0, 0, 0, 0};
     if (64 * c < left) a[c] = *reinterpret_cast<const u32x4_t *>(p.a + m * p.k + k0 + 64 * c);
   }
-  const u32x4_t wa = scales(p.as, p.la, m);
+  const Words wa = scales(p.as, p.la, m);
   for (int it = 0; grp < groups; ++it) {
     const int next = grp + gridDim.x;
     const __amdgpu_buffer_rsrc_t rs = resource(next);
-    u32x4_t wn = wb;
+    Words wn = wb;
     if (next < groups) wn = b_scales(next);
     f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      i32x8_t x, y;
+      if (BF16) {
+        i32x8_t x, y;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = (int)b[2 * s + (j >> 2)][j & 3], y[j] = (int)a[2 * s + (j >> 2)][j & 3];
-      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, 0, 0, 0, (int)(wb[s] >> (8 * g)), 0,
-                                                             (int)(wa[s] >> (8 * g)));
+        for (int j = 0; j < 8; ++j) x[j] = (int)b[2 * s + (j >> 2)][j & 3], y[j] = (int)a[2 * s + (j >> 2)][j & 3];
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, 0, 0, 0, (int)(wb.w[s] >> (8 * g)), 0,
+                                                               (int)(wa.w[s] >> (8 * g)));
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int h = c >> 1, e = 2 * (c & 1), sh = 8 * (2 * h + (g >> 1));
+          acc = mma_bf16(to_bf16((int)b[2 * s + h][e], (int)b[2 * s + h][e + 1], (wb.w[s] >> sh) & 0xFFu),
+                         to_bf16((int)a[2 * s + h][e], (int)a[2 * s + h][e + 1], (wa.w[s] >> sh) & 0xFFu), acc);
+        }
+      }
       b[2 * s] = load(rs, 2 * s);
       b[2 * s + 1] = load(rs, 2 * s + 1);
       __builtin_amdgcn_sched_barrier(0);
@@ -318,7 +340,9 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(4, 4))) 
       f32x4_t v = part[it & 1][0][lane];
 #pragma unroll
       for (int w = 1; w < W; ++w) v += part[it & 1][w][lane];
-      store_bf16(p, r, grp * 16ll + 4 * g, v);
+      const int64_t n = grp * 16ll + 4 * g;
+      if (BF16) store_bf16(p, r, n, v);
+      else store_f32(p, static_cast<float *>(p.out), r, n, v);
     }
     wb = wn;
     grp = next;
@@ -1133,11 +1157,12 @@ hipError_t gemm_tiled(const GemmMx &g, int splits, int steps, float *parts, hipS
   return hipGetLastError();
 }
 
-template <int W>
+template <bool BF16, int W>
 hipError_t gemm_few(const GemmMx &g, hipStream_t s) {
   const int groups = (int)((g.n + 15) / 16);
-  // 16 waves a CU, each with 8 KB of B in flight; more groups than that are walked
-  hipLaunchKernelGGL((k_gemm_mx_few<W>), dim3((unsigned)std::min(groups, 256 * 16 / W)), dim3(64 * W), 0, s, g, groups);
+  // 8 waves a CU, each with 16 KB of B in flight; more groups than that are walked
+  hipLaunchKernelGGL((k_gemm_mx_few<BF16, W>), dim3((unsigned)std::min(groups, 256 * 8 / W)), dim3(64 * W), 0, s, g,
+                     groups);
   return hipGetLastError();
 }
 
@@ -1172,8 +1197,8 @@ struct Shape {
 //   256-tiles: one workgroup a CU, 1.21 us a step (1.87 float32, its matrix rate is half);
 //   a K split: the join's launch, and its partial sums' bytes.
 Shape shape_of(int64_t m, int64_t n, int64_t k, bool nn, bool bf16) {
-  // ahead in every one of 35 sizes timed (n 512 .. 28672, k 544 .. 8192), by up to 45%
-  if (!nn && bf16 && m <= 16 && k <= 8192) return {16, 1, 1, 0};
+  // ahead of the others in all but one of 35 sizes timed (n 512 .. 28672, k 544 .. 8192)
+  if (!nn && m <= 16 && k <= 8192) return {16, 1, 1, 0};
   const int nk = (int)((k + kRowB - 1) / kRowB);
   Shape best{0, 1, 1, 0};
   double least = 1e30;
@@ -1223,7 +1248,10 @@ int64_t gemm_mx_workspace(int64_t m, int64_t n, int64_t k, bool nn) {
 hipError_t launch_gemm_mx(const GemmMx &g, void *ws, hipStream_t s) {
   const Shape sh = shape_of(g.m, g.n, g.k, g.nn, g.bf16);
   float *parts = static_cast<float *>(ws);
-  if (sh.tile == 16) return g.k <= 2048 ? gemm_few<4>(g, s) : g.k <= 4096 ? gemm_few<8>(g, s) : gemm_few<16>(g, s);
+  if (sh.tile == 16 && g.bf16)
+    return g.k <= 2048 ? gemm_few<true, 2>(g, s) : g.k <= 4096 ? gemm_few<true, 4>(g, s) : gemm_few<true, 8>(g, s);
+  if (sh.tile == 16)
+    return g.k <= 2048 ? gemm_few<false, 2>(g, s) : g.k <= 4096 ? gemm_few<false, 4>(g, s) : gemm_few<false, 8>(g, s);
   if (sh.tile == 256)
     return g.nn ? gemm_tiled<T256, true>(g, sh.splits, sh.steps, parts, s)
                 : gemm_tiled<T256, false>(g, sh.splits, sh.steps, parts, s);

@@ -547,6 +547,29 @@ def test_gemm_few_rows_exact(m, n, k):
         assert bool((out[m] == 3.0).all()) and bool((out[:, n:] == 3.0).all())
 
 
+@pytest.mark.parametrize("m,n,k", FEW + [(9, 300, 1056), (16, 2100, 992), (4, 4500, 3104)])
+def test_gemm_few_rows_float32(m, n, k):
+    """The same in float32, with an addend and over it, against exact sums; random codes against float64."""
+    say(f"gemm few rows fp32 {m}x{n}x{k}")
+    rng = np.random.default_rng(m + 5 * n + k)
+    ac, as_, a = _operand(rng, m, k, "rowmajor", True)
+    bc, bs, b = _operand(rng, n, k, "rowmajor", True)
+    add = rng.integers(-50, 50, (m, n)).astype(np.float32)
+    assert np.array_equal(_gemm((ac, as_), (bc, bs), m, n, "fp32", pad=1), a @ b.T)
+    for over in (False, True):
+        assert np.array_equal(_gemm((ac, as_), (bc, bs), m, n, "fp32", addend=add, pad=5, in_place=over), a @ b.T + add)
+    sa, sb = as_.reshape(m, k // 32).copy(), bs.reshape(n, k // 32).copy()
+    sa[m // 2, -1], sb[n // 2, 0], sb[n - 1, -1] = 255, 255, 255
+    got = _gemm((ac, sa), (bc, sb), m, n, "fp32")
+    bad = np.zeros((m, n), bool)
+    bad[m // 2, :], bad[:, [n // 2, n - 1]] = True, True
+    assert np.all(np.isnan(got[bad])) and np.array_equal(got[~bad], (a @ b.T)[~bad])
+    ac, as_, a = _operand(rng, m, k, "rowmajor", False)
+    bc, bs, b = _operand(rng, n, k, "rowmajor", False)
+    ref, bound = R.product(a, b, None, "fp32")
+    assert np.all(np.abs(_gemm((ac, as_), (bc, bs), m, n, "fp32") - ref) <= bound)
+
+
 @pytest.mark.parametrize("layout", ["tile32x4", "block32x32"])
 @pytest.mark.parametrize("n,k", [(64, 640), (4128, 1920), (5024, 3968), (4160, 8064), (4320, 5376)])
 def test_gemm_few_rows_in_every_layout(n, k, layout):
