@@ -650,7 +650,9 @@ struct Loader {
 };
 
 
-// The second wave group's sums through LDS to the first, which goes on alone.
+// The second wave group's sums through LDS to the first, which goes on alone.  The caller
+// lets every wave's loads to LDS land and passes a barrier first: the sums take the place of
+// stages that other waves' last loads still write and their last fragments are read from.
 template <class C>
 __device__ __forceinline__ bool join_groups(char *all, int grp, f32x4_t (&acc)[C::FP][C::FQ]) {
   f32x4_t *q = reinterpret_cast<f32x4_t *>(all + C::GROUP) + threadIdx.x % C::NT;
@@ -1096,7 +1098,10 @@ __global__ __launch_bounds__(C::NT * C::KG) __attribute__((amdgpu_waves_per_eu(C
     if (kt + 4 >= nk) break;
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // the trailing reloads
-  if (C::KG > 1 && !join_groups<C>(all, grp, acc)) return;
+  if (C::KG > 1) {
+    __syncthreads();
+    if (!join_groups<C>(all, grp, acc)) return;
+  }
   // the lane again, so that nothing of it is kept in registers over the loop
   int t_end = threadIdx.x;
   asm volatile("" : "+v"(t_end));

@@ -1,0 +1,97 @@
+"""MXFP8 products in every way the library may run one, against exact sums on the
+GPU: codes of small whole numbers under scales 1 and 2, so every partial sum is a
+whole number below 2^24 and float32 output must equal the float64 product (bfloat16:
+that, rounded once; a group of 8 products spans less than 2^14, so none is cut off)."""
+
+import pytest
+
+import mxfp8_weight_repack_amd as sh
+from gpu_util import say
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    sh.lib()
+
+
+CODES = [0x00, 0x38, 0x40, 0x44, 0xB8, 0xC0, 0x48]     # 0 1 2 3 -1 -2 4
+VALUES = [0.0, 1.0, 2.0, 3.0, -1.0, -2.0, 4.0]
+
+
+class Operand:
+    """A random rows x cols operand in `layout`: codes, blocks (scale bytes as a matrix), values."""
+
+    def __init__(self, rows, cols, layout, seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        pick = torch.randint(0, len(CODES), (rows, cols), generator=g, device="cuda")
+        br = 32 if layout == "block32x32" else 1
+        self.rows, self.cols, self.layout, self.br = rows, cols, layout, br
+        self.codes = torch.tensor(CODES, dtype=torch.uint8, device="cuda")[pick]
+        self.blocks = torch.randint(127, 129, (rows // br, cols // 32), generator=g, device="cuda", dtype=torch.uint8)
+        scale = torch.exp2((self.blocks.double() - 127)).repeat_interleave(br, 0).repeat_interleave(32, 1)
+        self.values = torch.tensor(VALUES, dtype=torch.float64, device="cuda")[pick] * scale
+
+    def matrix(self):
+        s = self.blocks
+        if self.layout == "tile32x4":                  # 32 rows x 4 blocks: one word a row, rows in order
+            s = s.view(self.rows // 32, 32, self.cols // 128, 4).permute(0, 2, 1, 3)
+        odd = torch.empty(s.numel() + 1, dtype=torch.uint8, device="cuda")[1:]     # scales lie at any address
+        return sh.mx_matrix(self.codes, odd.copy_(s.reshape(-1)), self.rows, self.cols, self.layout)
+
+
+def product(a, b, op, dtype, pad=0, addend=None):
+    """The product in a frame that must stay as it was; twice, with the same bits."""
+    m, n = a.rows, b.cols if op == "nn" else b.rows
+    A, B = a.matrix(), b.matrix()
+    nb = sh.gemm_mxfp8_workspace(A, B, op=op)
+    td = torch.bfloat16 if dtype == "bf16" else torch.float32
+    runs = []
+    for _ in range(2):
+        out = torch.full((m + 1, n + pad), 3.0, dtype=td, device="cuda")
+        if addend is not None:
+            out[:m, :n] = addend
+        ws = torch.full((max(nb, 16),), 0xFF, dtype=torch.uint8, device="cuda")
+        sh.gemm_mxfp8(A, B, out, dtype, op=op, addend=None if addend is None else out, ld_out=n + pad, workspace=ws,
+                      workspace_bytes=nb, stream=torch.cuda.current_stream().cuda_stream)
+        assert bool((out[m] == 3.0).all()) and bool((out[:, n:] == 3.0).all())
+        runs.append(out[:m, :n])
+    bits = torch.int16 if dtype == "bf16" else torch.int32
+    assert torch.equal(runs[0].contiguous().view(bits), runs[1].contiguous().view(bits))
+    return runs[0]
+
+
+def check(op, m, n, k, dtype, la="rowmajor", lb="rowmajor"):
+    """Plain, over an addend (float32), and with NaN blocks, which spoil their own rows and columns alone."""
+    lb = "block32x32" if op == "nn" else lb
+    a = Operand(m, k, la, m + 3 * n + k)
+    b = Operand(*((k, n) if op == "nn" else (n, k)), lb, m + 3 * n + k + 1)
+    td = torch.bfloat16 if dtype == "bf16" else torch.float32
+    ref = a.values @ (b.values if op == "nn" else b.values.t())
+    assert torch.equal(product(a, b, op, dtype, pad=3), ref.to(td))
+    if dtype == "fp32":
+        add = torch.randint(-50, 50, (m, n), device="cuda").float()
+        assert torch.equal(product(a, b, op, dtype, pad=1, addend=add), (ref + add).float())
+    a.blocks[a.blocks.shape[0] // 2, -1] = 255
+    b.blocks[-1, 0] = 255
+    bad = torch.zeros(m, n, dtype=torch.bool, device="cuda")
+    r = a.blocks.shape[0] // 2 * a.br
+    bad[r:r + a.br] = True
+    if op == "nn":
+        bad[:, :32] = True
+    else:
+        bad[:, n - b.br:] = True
+    got = product(a, b, op, dtype)
+    assert bool(got[bad].isnan().all()) and torch.equal(got[~bad], ref.to(td)[~bad])
+
+
+@pytest.mark.parametrize("op,m,n,k", [("nt", 5896, 32, 960), ("nn", 78, 2432, 928), ("nt", 35, 40, 5824),
+                                      ("nn", 5, 160, 2080)])
+def test_float32_by_two_wave_groups(op, m, n, k):
+    """One product over two runs of K at once, their sums joined in LDS; the last two with K split besides."""
+    say(f"gemm two groups {op} {m}x{n}x{k}")
+    check(op, m, n, k, "fp32")
