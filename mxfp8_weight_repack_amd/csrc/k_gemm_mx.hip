@@ -465,8 +465,8 @@ __device__ __forceinline__ void stage_barrier(bool newest) {
 // zeros past the end.  The caller waits
 // for it.  PLAIN: the compiler takes a transposing read as one that any load to LDS in
 // flight may write under, and puts a wait for all of them before it (NN 8192^3: 401
-// against 468 us without); as plain instructions the loads are none of its concern.  (M0 is
-// the compiler's own to set before each of its uses; none is left in such a kernel.)
+// against 468 us without); as plain instructions the loads are none of its concern, and M0,
+// which they take their LDS address from, is named as overwritten.
 template <bool PLAIN>
 __device__ __forceinline__ void dma16(const uint8_t *base, int64_t bytes, char *dst, int voff, int soff) {
   if (PLAIN) {
@@ -474,7 +474,8 @@ __device__ __forceinline__ void dma16(const uint8_t *base, int64_t bytes, char *
     const u32x4_t w = {(uint32_t)b, (uint32_t)(b >> 32) & 0xFFFFu, (uint32_t)bytes, (uint32_t)kBufWord3};
     const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)dst;
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff), "s"(w),
-                 "s"(soff));
+                 "s"(soff)
+                 : "m0");
   } else {
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), 0, (int)bytes, kBufWord3);
