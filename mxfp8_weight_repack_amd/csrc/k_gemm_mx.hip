@@ -25,6 +25,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 
@@ -1149,11 +1150,18 @@ hipError_t gemm_tiled(const GemmMx &g, int splits, int steps, float *parts, hipS
   const int64_t tm = (g.m + C::TM - 1) / C::TM, tn = (g.n + C::TN - 1) / C::TN;
   const dim3 grid((unsigned)(tm * tn), (unsigned)splits), block(C::NT * C::KG);
   if (splits == 1) parts = nullptr;
-  const bool sh = g.k <= 4 * kRowB;
-  if (g.bf16 && sh) hipLaunchKernelGGL((k_gemm_mx8<C, NN, true>), grid, block, 0, s, g, tm, tn, steps, parts);
-  else if (g.bf16) hipLaunchKernelGGL((k_gemm_mx8<C, NN, false>), grid, block, 0, s, g, tm, tn, steps, parts);
-  else if (sh) hipLaunchKernelGGL((k_gemm_mx16<C, NN, true>), grid, block, 0, s, g, tm, tn, steps, parts);
-  else hipLaunchKernelGGL((k_gemm_mx16<C, NN, false>), grid, block, 0, s, g, tm, tn, steps, parts);
+  auto launch = [&](auto sh) {
+    constexpr bool SHORT = decltype(sh)::value;
+    if (g.bf16) hipLaunchKernelGGL((k_gemm_mx8<C, NN, SHORT>), grid, block, 0, s, g, tm, tn, steps, parts);
+    else hipLaunchKernelGGL((k_gemm_mx16<C, NN, SHORT>), grid, block, 0, s, g, tm, tn, steps, parts);
+  };
+  // two wave groups take matrices of more than 4 steps only
+  if constexpr (C::KG == 1) {
+    if (g.k <= 4 * kRowB) launch(std::true_type{});
+    else launch(std::false_type{});
+  } else {
+    launch(std::false_type{});
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
   const int64_t words = g.m * ((g.n + 3) / 4);
