@@ -456,8 +456,13 @@ int sshdp_rmsnorm_backward(const sshdp_rmsnorm_grad *args, void *workspace, size
 
 /* A matrix in MXFP8: dense row-major codes and scales in one of the
  * SSHDP_SCALE_* layouts (the region formulas with o = 0, from `scales` on).
- * sshdp_plan_mx_matrix describes an MXFP8 region of a plan inside the codes and
- * scales roots, so a product reads the runtime weight where G left it. */
+ * sshdp_plan_mx_matrix describes a node of a plan inside the codes and scales
+ * roots, so a product reads the runtime weight where G left it: an MXFP8 region,
+ * or a view of whole rows of one (an expert of a bank, a head of a packed
+ * projection), whatever node carries `quantize`.  In the layouts that group 32
+ * rows the view starts at a multiple of 32 of the region's rows and has a
+ * multiple of 32.  Errors: ARG (null pointer, no such node), SCHEMA (any other
+ * node). */
 typedef struct {
   const uint8_t *codes, *scales;
   int64_t rows, cols;

@@ -277,7 +277,8 @@ class Plan:
         return a.value, g.value
 
     def mx_matrix(self, i, codes, scales):
-        """Node i's MXFP8 region inside the codes and scales roots, as an operand of gemm_mxfp8."""
+        """Node i, an MXFP8 region or a view of whole rows of one, inside the codes and scales roots, as an operand
+        of gemm_mxfp8."""
         m = MxMatrix()
         _check(lib().sshdp_plan_mx_matrix(self.handle, i, _ptr(codes), _ptr(scales), ctypes.byref(m)),
                "sshdp_plan_mx_matrix")

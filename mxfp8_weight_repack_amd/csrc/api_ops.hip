@@ -72,6 +72,20 @@ int check_matrix(const sshdp_mx_matrix *m) {
   return SSHDP_OK;
 }
 
+// The MXFP8 region that a node at element o is, or whole rows of; NULL if none.  A region's
+// codes and scales then hold the node's from o on in every layout, as its first row and row
+// count are multiples of 32 where 32 rows share a word run or a scale.
+const QRegion *region_of(const sshdp_plan &p, const sshdp_node &nd, int64_t o) {
+  if (nd.rows > 1 && nd.row_stride != nd.cols) return nullptr;
+  for (const QRegion &q : p.qregions) {
+    const int64_t at = o - q.abs;
+    if (nd.cols != q.cols || at < 0 || at % q.cols || at / q.cols + nd.rows > q.rows) continue;
+    if (p.opts.scale_layout != SSHDP_SCALE_ROWMAJOR && (at / q.cols % 32 || nd.rows % 32)) return nullptr;
+    return &q;
+  }
+  return nullptr;
+}
+
 int check_gemm(const sshdp_mx_matrix *a, const sshdp_mx_matrix *b, int32_t op) {
   int st = check_matrix(a);
   if (st != SSHDP_OK) return st;
@@ -203,8 +217,9 @@ int sshdp_plan_mx_matrix(const sshdp_plan *p, int32_t node, const uint8_t *codes
                          sshdp_mx_matrix *out) {
   if (!p || !out || !codes || !scales || node < 0 || node >= (int32_t)p->nodes.size()) return SSHDP_ERR_ARG;
   const sshdp_node &nd = p->nodes[node];
-  if (nd.quantize != SSHDP_G_MXFP8) return SSHDP_ERR_SCHEMA;
   const int64_t o = p->node_abs[node];
+  const QRegion *region = region_of(*p, nd, o);
+  if (!region) return SSHDP_ERR_SCHEMA;
   out->codes = codes + o;
   out->scales = scales + o / (p->opts.scale_layout == SSHDP_SCALE_BLOCK32X32 ? 1024 : 32);
   out->rows = nd.rows;

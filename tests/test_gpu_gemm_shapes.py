@@ -95,3 +95,34 @@ def test_float32_by_two_wave_groups(op, m, n, k):
     """One product over two runs of K at once, their sums joined in LDS; the last two with K split besides."""
     say(f"gemm two groups {op} {m}x{n}x{k}")
     check(op, m, n, k, "fp32")
+
+
+@pytest.mark.parametrize("layout", ["rowmajor", "tile32x4", "block32x32"])
+def test_an_expert_of_a_bank(layout):
+    """Products read an expert's rows where G left the bank's, as from the expert quantised by itself."""
+    say(f"gemm expert {layout}")
+    d = dict(is_unit=False, quantize=None, cols=256, row_stride=256)
+    bank = dict(d, parent=-1, offset=1024, rows=288, quantize=True)
+    experts = [(0, 96), (96, 64), (160, 128)]
+    nodes = [bank] + [dict(d, parent=0, offset=r * 256, rows=n) for r, n in experts]
+    numel = 1024 + 288 * 256
+    plan = sh.Plan(nodes, numel, layout=layout)
+    s = torch.cuda.current_stream().cuda_stream
+    g = torch.Generator(device="cuda").manual_seed(5)
+    w = torch.randn(numel, generator=g, device="cuda")
+    codes = torch.zeros(numel, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(plan.stats()["scale_bytes"], dtype=torch.uint8, device="cuda")
+    sh.requant_mxfp8(plan, w, codes, scales, s)
+    x = Operand(50, 256, "rowmajor", 6).matrix()
+    for i, (r, n) in enumerate(experts, 1):
+        own = sh.Plan([dict(bank, offset=0, rows=n)], n * 256, layout=layout)
+        oc = torch.zeros(n * 256, dtype=torch.uint8, device="cuda")
+        os_ = torch.zeros(own.stats()["scale_bytes"], dtype=torch.uint8, device="cuda")
+        ow = w[1024 + r * 256:1024 + (r + n) * 256].clone()
+        sh.requant_mxfp8(own, ow, oc, os_, s)
+        outs = []
+        for m in (plan.mx_matrix(i, codes, scales), own.mx_matrix(0, oc, os_)):
+            assert sh.gemm_mxfp8_workspace(x, m) == 0
+            outs.append(torch.full((50, n), 3.0, device="cuda"))
+            sh.gemm_mxfp8(x, m, outs[-1], "fp32", stream=s)
+        assert torch.equal(*outs) and bool(outs[0].abs().sum() > 0)

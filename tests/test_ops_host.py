@@ -15,6 +15,7 @@ import mxfp8_weight_repack_amd as sh
 from mxfp8_weight_repack_amd._lib import LAYOUT, node_array
 import ops_ref as R
 import workloads
+from oracle.mxfp8 import scale_index
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 P = 1 << 20                                            # an aligned address that no refused call follows
@@ -167,6 +168,44 @@ def test_plan_regions_as_operands(layout):
     refused("SCHEMA", lambda: p.mx_matrix(2, P, P))    # no MXFP8 region
     refused("ARG", lambda: p.mx_matrix(3, P, P))
     refused("ARG", lambda: p.mx_matrix(0, None, P))
+
+
+@pytest.mark.parametrize("layout", ["rowmajor", "tile32x4", "block32x32"])
+def test_views_of_a_region_as_operands(layout):
+    """Whole rows of a region (an expert of a bank, a head of a packed projection) are operands of their own:
+    codes from their first element on, and the very scales that the region's formula gives those rows."""
+    view = lambda offset, rows, cols=256, stride=256, parent=1: dict(   # noqa: E731
+        parent=parent, offset=offset, rows=rows, cols=cols, row_stride=stride, is_unit=False, quantize=None)
+    base, rows, cols = 4096, 160, 256
+    nodes = [dict(parent=-1, offset=0, rows=1, cols=4096, row_stride=4096, is_unit=True, optimizer="adamw"),
+             dict(parent=-1, offset=base, rows=rows, cols=cols, row_stride=cols, is_unit=False, quantize=True),
+             view(0, 64), view(64 * 256, 96), view(160, 1, 96, 96, 0), view(32 * 256, 64, 128), view(128, 2, 256),
+             view(32 * 256, 16, 256, 512), view(0, 160), view(33 * 256, 1), view(32 * 256, 32, 256, 256, 1)]
+    nodes.append(dict(nodes[10], parent=3, offset=32 * 256))           # a view of a view: rows 96 .. 127
+    p = sh.Plan(nodes, base + rows * cols, layout=layout, host_only=True)
+    index = scale_index(layout, base, rows, cols)
+    br = 32 if layout == "block32x32" else 1
+    good = {2: (0, 64), 3: (64, 96), 8: (0, 160), 10: (32, 32), 11: (96, 32)}
+    if layout == "rowmajor":
+        good[9] = (33, 1)
+    for i, (first, n) in good.items():
+        m = p.mx_matrix(i, P, 2 * P)
+        assert (m.codes, m.rows, m.cols, m.layout) == (P + base + first * cols, n, cols, LAYOUT[layout])
+        assert np.array_equal(m.scales - 2 * P + scale_index(layout, 0, n, cols), index[first // br:(first + n) // br])
+    for i in set(range(12)) - set(good) - {1}:         # outside, part of the columns, across rows, with gaps
+        refused("SCHEMA", lambda: p.mx_matrix(i, P, P))
+
+
+def test_every_expert_of_a_bank_is_an_operand():
+    """The expert bank's node carries `quantize`; its experts are views inside it."""
+    wl = workloads.config(3)
+    p = sh.Plan(wl.nodes, wl.root_numel, layout=wl.scale_layout, host_only=True)
+    bank = [i for i, n in enumerate(wl.nodes) if n["quantize"]]
+    experts = [i for i, n in enumerate(wl.nodes) if n["parent"] in bank and not n["quantize"]]
+    assert len(experts) >= 64
+    for i in experts:
+        m, o = p.mx_matrix(i, P, 2 * P), p.node(i)[0]
+        assert (m.codes, m.scales, m.rows, m.cols) == (P + o, 2 * P + o // 32, wl.nodes[i]["rows"], wl.nodes[i]["cols"])
 
 
 def test_gradient_chunks_cover_every_unit_element_once(tmp_path):
