@@ -437,8 +437,8 @@ int sshdp_rmsnorm_mxfp8(const sshdp_rmsnorm *args, void *stream);
  *   dweight = sum over rows of dy * xhat, added to what is there unless `first`.
  * dx is the gradient of x and of the residual alike; `dh` (optional) is the
  * gradient reaching h past the norm.  dy, h, dh, dx are dense rows x cols of
- * `dtype`; dweight is float32 (a norm unit's place in the gradient root).  dx
- * may be dy or dh.  Sums are held in float32 and added in a fixed order.
+ * `dtype`; dweight is float32 (a norm unit's place in the gradient root, at any
+ * element of it: 4-byte aligned).  dx may be dy or dh.  Sums are held in float32 and added in a fixed order.
  * `workspace`: sshdp_rmsnorm_backward_workspace bytes, 16-byte aligned.
  * rows == 0: dweight is set to 0 if `first`, else left.
  * Errors: ARG (null pointer but dh, bad dtype), SCHEMA (as above), ALIGN,

@@ -205,7 +205,7 @@ int sshdp_rmsnorm_backward(const sshdp_rmsnorm_grad *a, void *ws, size_t ws_byte
   if (!a->dweight) return SSHDP_ERR_ARG;
   if (a->rows && (!a->dy || !a->h || !a->weight || !a->rstd || !a->dx)) return SSHDP_ERR_ARG;
   if (!aligned16(a->dy) || !aligned16(a->h) || !aligned16(a->dh) || !aligned16(a->weight) || !aligned16(a->rstd) ||
-      !aligned16(a->dx) || !aligned16(a->dweight))
+      !aligned16(a->dx) || reinterpret_cast<uintptr_t>(a->dweight) % sizeof(float))
     return SSHDP_ERR_ALIGN;
   st = check_ws(ws, ws_bytes, need);
   if (st == SSHDP_OK) st = check_device(a->dy, a->h, a->dh, a->weight, a->rstd, a->dx, a->dweight);

@@ -1,0 +1,66 @@
+"""The residual RMS norm and its gradient beside a plan's own norm units: weight and
+weight gradient at any element of the roots, and how the weight gradient's sums are
+joined, against float64 references."""
+
+import numpy as np
+import pytest
+
+import mxfp8_weight_repack_amd as sh
+import ops_ref as R
+from gpu_util import say
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    sh.lib()
+
+
+def stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def dev(a, dtype="fp32"):
+    return torch.from_numpy(np.ascontiguousarray(a, np.float32)).cuda().to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+
+
+def host(t):
+    torch.cuda.synchronize()
+    return t.float().cpu().numpy()
+
+
+def matrix(rng, rows, cols, dtype):
+    return R.as_dtype((rng.standard_normal((rows, cols)) * np.exp(rng.standard_normal((rows, 1)))).astype(np.float32), dtype)
+
+
+def backward(dy, h, w, rstd, dw, rows, cols, first=True, dtype="fp32", weight_dtype="fp32"):
+    dx = torch.full((rows + 1, cols), 3.0, dtype=dy.dtype, device="cuda")
+    nb = sh.rmsnorm_backward_workspace(rows, cols)
+    ws = torch.full((max(nb, 16),), 0xFF, dtype=torch.uint8, device="cuda")
+    sh.rmsnorm_backward(dy, h, w, rstd, dx, dw, rows, cols, dtype=dtype, weight_dtype=weight_dtype, first=first,
+                        workspace=ws, workspace_bytes=nb, stream=stream())
+    assert bool((dx[rows] == 3.0).all())
+    return dx[:rows]
+
+
+@pytest.mark.parametrize("at", [1, 2, 3, 6])
+@pytest.mark.parametrize("rows,cols", [(1, 32), (40, 2048), (1100, 96), (70, 16416)])
+def test_weight_gradient_at_any_element(rows, cols, at):
+    """The unit's place and nothing around it, by one launch or two, set and added to."""
+    say(f"dweight at {at} {rows}x{cols}")
+    rng = np.random.default_rng(rows + cols + at)
+    dy, h = matrix(rng, rows, cols, "fp32"), matrix(rng, rows, cols, "fp32")
+    w = (1 + 0.2 * rng.standard_normal(cols)).astype(np.float32)
+    rstd = R.rmsnorm(h, None, w, 1e-6, "fp32")[1].astype(np.float32)
+    _, _, dw, bdw = R.rmsnorm_grad(dy, h, w, rstd, None, "fp32")
+    g = torch.full((cols + 9,), 7.0, device="cuda")
+    args = [dev(v) for v in (dy, h, w, rstd)]
+    backward(*args, g[at:], rows, cols)
+    backward(*args, g[at:], rows, cols, first=False)
+    got = host(g)
+    assert np.all(np.abs(got[at:at + cols] - 2 * dw) <= 2 * bdw + R.U * np.abs(2 * dw))
+    assert np.all(got[:at] == 7.0) and np.all(got[at + cols:] == 7.0)

@@ -96,6 +96,14 @@ def test_rmsnorm_backward_refusals():
     sh.rmsnorm_backward(None, None, None, None, None, None, 0, 64, first=False)
 
 
+def test_rmsnorm_weight_gradient_at_any_element():
+    """A norm unit may start at any element of the gradient root: past the alignment check, the missing workspace
+    is what is left to refuse."""
+    for at in (4, 8, 12, 20):
+        refused("WORKSPACE", lambda: sh.rmsnorm_backward(P, P, P, P, P, P + at, 4, 64))
+    refused("ALIGN", lambda: sh.rmsnorm_backward(P, P, P, P, P, P + 2, 4, 64))
+
+
 def test_gemm_refusals():
     mat = lambda r, c, layout="rowmajor", codes=P, scales=P: sh.mx_matrix(codes, scales, r, c, layout)   # noqa: E731
 
