@@ -413,7 +413,8 @@ int sshdp_quant_mxfp8(const void *src, int32_t dtype, int64_t rows, int64_t cols
  * `h` (only with residual; may be x or residual where that one is dense), `y` in
  * `dtype`, and `rstd`, one float per row (what the backward needs).  x and
  * residual have rows ld_x and ld_residual elements apart; `weight` has cols
- * elements of weight_dtype.
+ * elements of weight_dtype and may start at any of them (a norm unit's place in
+ * the main-weight or bfloat16 root).
  * A NaN makes its whole row's y NaN; an infinity makes rstd 0, y NaN where it
  * stands and 0 elsewhere; G gives blocks holding NaN scale 0xFF and codes 0x7F.
  * Errors: ARG (null x or weight, no output, half a pair, h without residual,

@@ -47,6 +47,9 @@ bool dtype_ok(int32_t d) { return d == SSHDP_DTYPE_FP32 || d == SSHDP_DTYPE_BF16
 
 int64_t dtype_size(int32_t d) { return d == SSHDP_DTYPE_BF16 ? 2 : 4; }
 
+// A norm's weight, or its gradient: at any element of its array.
+bool aligned_element(const void *p, int32_t d) { return reinterpret_cast<uintptr_t>(p) % dtype_size(d) == 0; }
+
 int check_ws(const void *ws, size_t bytes, int64_t need) {
   if (need == 0) return SSHDP_OK;
   if (!ws || bytes < (size_t)need) return SSHDP_ERR_WORKSPACE;
@@ -181,8 +184,8 @@ int sshdp_rmsnorm_mxfp8(const sshdp_rmsnorm *a, void *stream) {
   if (a->h && a->rows > 1 &&
       ((a->h == a->x && a->ld_x != a->cols) || (a->h == a->residual && a->ld_residual != a->cols)))
     return SSHDP_ERR_SCHEMA;
-  if (!aligned16(a->x) || !aligned16(a->residual) || !aligned16(a->weight) || !aligned16(a->h) || !aligned16(a->y) ||
-      !aligned16(a->codes) || !aligned16(a->rstd))
+  if (!aligned16(a->x) || !aligned16(a->residual) || !aligned_element(a->weight, a->weight_dtype) || !aligned16(a->h) ||
+      !aligned16(a->y) || !aligned16(a->codes) || !aligned16(a->rstd))
     return SSHDP_ERR_ALIGN;
   const int st = check_device(a->x, a->residual, a->weight, a->h, a->y, a->codes, a->scales, a->rstd);
   if (st != SSHDP_OK) return st;
@@ -204,8 +207,8 @@ int sshdp_rmsnorm_backward(const sshdp_rmsnorm_grad *a, void *ws, size_t ws_byte
   if (a->cols == 0 || (a->rows == 0 && !a->first)) return SSHDP_OK;
   if (!a->dweight) return SSHDP_ERR_ARG;
   if (a->rows && (!a->dy || !a->h || !a->weight || !a->rstd || !a->dx)) return SSHDP_ERR_ARG;
-  if (!aligned16(a->dy) || !aligned16(a->h) || !aligned16(a->dh) || !aligned16(a->weight) || !aligned16(a->rstd) ||
-      !aligned16(a->dx) || reinterpret_cast<uintptr_t>(a->dweight) % sizeof(float))
+  if (!aligned16(a->dy) || !aligned16(a->h) || !aligned16(a->dh) || !aligned_element(a->weight, a->weight_dtype) ||
+      !aligned16(a->rstd) || !aligned16(a->dx) || !aligned_element(a->dweight, SSHDP_DTYPE_FP32))
     return SSHDP_ERR_ALIGN;
   st = check_ws(ws, ws_bytes, need);
   if (st == SSHDP_OK) st = check_device(a->dy, a->h, a->dh, a->weight, a->rstd, a->dx, a->dweight);

@@ -139,11 +139,22 @@ struct RowCfg {
   static constexpr bool kLean = WPR * NCH > 32;
 };
 
-// Run `run`'s 8 weights, 0 past the end.
+// Run `run`'s 8 weights, 0 past the end.  They lie at any element (a norm unit's place in a
+// root), so the words have an element's alignment.
 template <bool WBF16>
 __device__ __forceinline__ void weights(const void *weight, int run, int runs, float (&w)[8]) {
+  typedef uint32_t u32x4h_t __attribute__((ext_vector_type(4), aligned(2)));
+  typedef uint32_t u32x4w_t __attribute__((ext_vector_type(4), aligned(4)));
   Raw8<WBF16> r{};
-  if (run < runs) r = load8<WBF16>(weight, run * 8);
+  if (run < runs) {
+    if constexpr (WBF16) {
+      r.w = *reinterpret_cast<const u32x4h_t *>(static_cast<const uint16_t *>(weight) + run * 8);
+    } else {
+      const u32x4w_t *q = reinterpret_cast<const u32x4w_t *>(static_cast<const float *>(weight) + run * 8);
+      r.w[0] = q[0];
+      r.w[1] = q[1];
+    }
+  }
   unpack8<WBF16>(r, w);
 }
 

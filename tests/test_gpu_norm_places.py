@@ -64,3 +64,29 @@ def test_weight_gradient_at_any_element(rows, cols, at):
     got = host(g)
     assert np.all(np.abs(got[at:at + cols] - 2 * dw) <= 2 * bdw + R.U * np.abs(2 * dw))
     assert np.all(got[:at] == 7.0) and np.all(got[at + cols:] == 7.0)
+
+
+@pytest.mark.parametrize("wdtype,at", [("fp32", 1), ("fp32", 2), ("bf16", 1), ("bf16", 3), ("bf16", 6)])
+@pytest.mark.parametrize("rows,cols", [(1, 8192), (33, 544), (1100, 96), (3, 20512)])
+def test_weight_at_any_element(rows, cols, wdtype, at):
+    """Codes, scales and gradient of a weight inside a root that is NaN around it: bit for bit those of an aligned copy."""
+    say(f"norm weight at {at} {wdtype} {rows}x{cols}")
+    rng = np.random.default_rng(rows + cols + at)
+    x, dy = matrix(rng, rows, cols, "bf16"), matrix(rng, rows, cols, "bf16")
+    w = R.as_dtype(1 + 0.2 * rng.standard_normal(cols), wdtype)
+    root = dev(np.concatenate([np.full(at, np.nan), w, np.full(9, np.nan)]), wdtype)
+    _, rstd, y = R.rmsnorm(x, None, w, 1e-6, "bf16")
+    qc, qs = R.quant_rows(y)
+    xd, dyd, runs = dev(x, "bf16"), dev(dy, "bf16"), []
+    for weight in (root[at:], dev(w, wdtype)):
+        c = torch.full((rows, cols), 0xA5, dtype=torch.uint8, device="cuda")
+        s = torch.full((rows, cols // 32), 0xA5, dtype=torch.uint8, device="cuda")
+        rs = torch.zeros(rows, device="cuda")
+        sh.rmsnorm_mxfp8(xd, weight, rows, cols, weight_dtype=wdtype, codes=c, scales=s, rstd=rs, stream=stream())
+        assert np.array_equal(host(c), qc) and np.array_equal(host(s), qs)
+        assert np.all(np.abs(host(rs) - rstd) <= 1.01 * R.U * rstd)
+        dw = torch.full((cols,), 3.0, device="cuda")
+        runs.append((backward(dyd, xd, weight, rs, dw, rows, cols, dtype="bf16", weight_dtype=wdtype), dw))
+    dx, bdx, dw, bdw = R.rmsnorm_grad(dy, x, w, host(rs), None, "bf16")
+    assert np.all(np.abs(host(runs[0][0]) - dx) <= bdx) and np.all(np.abs(host(runs[0][1]) - dw) <= bdw)
+    assert torch.equal(runs[0][0], runs[1][0]) and torch.equal(runs[0][1], runs[1][1])

@@ -104,6 +104,15 @@ def test_rmsnorm_weight_gradient_at_any_element():
     refused("ALIGN", lambda: sh.rmsnorm_backward(P, P, P, P, P, P + 2, 4, 64))
 
 
+def test_rmsnorm_weight_at_any_element():
+    """The weight may start at any element of its root; what is refused then is what comes after its alignment."""
+    for dtype, at in (("fp32", 4), ("fp32", 12), ("bf16", 2), ("bf16", 10)):
+        refused("WORKSPACE", lambda: sh.rmsnorm_backward(P, P, P + at, P, P, P, 4, 64, weight_dtype=dtype))
+        refused("ALIGN", lambda: sh.rmsnorm_backward(P, P, P + at - 1, P, P, P, 4, 64, weight_dtype=dtype))
+        refused("ALIGN", lambda: sh.rmsnorm_mxfp8(P, P + at - 1, 4, 64, weight_dtype=dtype, y=P))
+    refused("ALIGN", lambda: sh.rmsnorm_mxfp8(P, P + 2, 4, 64, weight_dtype="fp32", y=P))
+
+
 def test_gemm_refusals():
     mat = lambda r, c, layout="rowmajor", codes=P, scales=P: sh.mx_matrix(codes, scales, r, c, layout)   # noqa: E731
 
