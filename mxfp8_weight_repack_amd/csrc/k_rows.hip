@@ -265,8 +265,18 @@ __device__ __forceinline__ void put_dw(float4 *sums, int c, const float (&v)[8])
     sums[(2 * c + h) * blockDim.x + threadIdx.x] = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
 }
 
+// The sum of N values in pairs: log2(N) roundings to a value, where a chain takes up to N.
+template <int N>
+__device__ __forceinline__ float pair_sum(float (&v)[N]) {
+#pragma unroll
+  for (int n = N / 2; n > 0; n >>= 1)
+#pragma unroll
+    for (int k = 0; k < n; ++k) v[k] += v[k + n];
+  return v[0];
+}
+
 // dweight of 32 columns from c0 on: 64 threads' rows of 8 columns each, then the threads in
-// order.
+// pairs.
 template <bool BF16>
 __device__ __forceinline__ void column_grads(const sshdp_rmsnorm_grad &a, int c0) {
   __shared__ float sums[64][33];
@@ -285,10 +295,11 @@ __device__ __forceinline__ void column_grads(const sshdp_rmsnorm_grad &a, int c0
   for (int j = 0; j < 8; ++j) sums[sl][c + j] = s[j];
   __syncthreads();
   if (t >= 32) return;
-  float v = a.first ? 0.f : a.dweight[c0 + t], d = 0.f;
+  const float v = a.first ? 0.f : a.dweight[c0 + t];
+  float d[64];
 #pragma unroll
-  for (int k = 0; k < 64; ++k) d += sums[k][t];
-  a.dweight[c0 + t] = v + d;
+  for (int k = 0; k < 64; ++k) d[k] = sums[k][t];
+  a.dweight[c0 + t] = v + pair_sum(d);
 }
 
 // Workgroups keep their columns' weight-gradient sums in registers over all their
@@ -408,7 +419,7 @@ __global__ __launch_bounds__(C::kThreads) void k_rmsnorm_grad(sshdp_rmsnorm_grad
 }
 
 // dweight = (first ? 0 : dweight) + sum of the partial rows: 32 columns per
-// workgroup, 32 row slices added in slice order.
+// workgroup, 32 row slices added in pairs.
 __global__ __launch_bounds__(1024) void k_dweight(const float *partials, int64_t n, int64_t cols, int first,
                                                   float *dweight) {
   __shared__ float sm[32][33];
@@ -419,10 +430,11 @@ __global__ __launch_bounds__(1024) void k_dweight(const float *partials, int64_t
   sm[sl][c] = s;
   __syncthreads();
   if (sl == 0) {
-    float v = first ? 0.f : dweight[col];
-    s = 0.f;
-    for (int k = 0; k < 32; ++k) s += sm[k][c];
-    dweight[col] = v + s;
+    const float v = first ? 0.f : dweight[col];
+    float d[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) d[k] = sm[k][c];
+    dweight[col] = v + pair_sum(d);
   }
 }
 

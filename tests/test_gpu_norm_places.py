@@ -90,3 +90,21 @@ def test_weight_at_any_element(rows, cols, wdtype, at):
     dx, bdx, dw, bdw = R.rmsnorm_grad(dy, x, w, host(rs), None, "bf16")
     assert np.all(np.abs(host(runs[0][0]) - dx) <= bdx) and np.all(np.abs(host(runs[0][1]) - dw) <= bdw)
     assert torch.equal(runs[0][0], runs[1][0]) and torch.equal(runs[0][1], runs[1][1])
+
+
+@pytest.mark.parametrize("rows,picked", [(64, range(1, 64)), (1100, range(4, 128, 4))])
+def test_weight_gradient_sums_in_pairs(rows, picked):
+    """One large term and many of half its last place, each alone in its slice of the rows: a chain of additions
+    loses all of them (63 and 31 half steps of the sum).  Adding zeros is exact, and adding the slices in pairs
+    rounds a value once a level (6 and 5 levels) before the store, whose sum with nothing is exact."""
+    say(f"dweight in pairs {rows}")
+    cols = 64
+    h = np.ones((rows, cols), np.float32)
+    dy = np.zeros((rows, cols), np.float32)
+    dy[0] = 1.0
+    dy[list(picked)] = R.U
+    dw = torch.full((cols,), 3.0, device="cuda")
+    backward(dev(dy), dev(h), dev(np.ones(cols)), dev(np.ones(rows)), dw, rows, cols)
+    exact = 1.0 + len(picked) * R.U
+    levels = 6 if rows == 64 else 5
+    assert np.all(np.abs(host(dw).astype(np.float64) - exact) <= levels * R.U * exact)
