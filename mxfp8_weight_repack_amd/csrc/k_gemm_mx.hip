@@ -27,6 +27,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "gemm_shape.h"
 #include "internal.h"
 
 namespace sshdp {
@@ -368,7 +369,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
 // activity), matrix cores busy 71% of the time.  The rest is operand latency beyond the L2
 // (with every load a hit: 1.32 ms) and the scales (without any: 1.38 ms).
 
-constexpr int kRowB = 128;                           // bytes (= k) of a stage row
+constexpr int kRowB = kGemmStep;                     // bytes (= k) of a stage row
 
 // KG groups of WN x WM waves make the same tile over KG parts of its K and add their sums
 // in LDS: where there are too few tiles to give every CU two workgroups, a second group
@@ -1157,7 +1158,7 @@ hipError_t gemm_tiled(const GemmMx &g, int splits, int steps, float *parts, hipS
   };
   // two wave groups take matrices of more than 4 steps only
   if constexpr (C::KG == 1) {
-    if (g.k <= 4 * kRowB) launch(std::true_type{});
+    if (gemm_short(g.k)) launch(std::true_type{});
     else launch(std::false_type{});
   } else {
     launch(std::false_type{});
@@ -1193,79 +1194,23 @@ hipError_t gemm_rows(const GemmMx &g, hipStream_t s) {
   return hipSuccess;
 }
 
-// How a product runs: few-row kernel (tile 0; 16: A in registers), or tiles of 256 or 128 by `groups` wave
-// groups, with K in `splits` parts, each of `groups` runs of `steps` 128-k steps (a
-// multiple of 4: scale words come 4 steps at a time).
-struct Shape {
-  int tile, groups, splits, steps;
-};
-
-// The candidate with the least modelled time, in microseconds on an idle MI355X.  The
-// constants are fitted to 300 timed choices from m 1 .. 4096, n and k 128 .. 28672, both
-// operand forms and output types; what it picks takes 1.5% more than the best candidate
-// on average and 27% more at worst.  Always unsplit 128-tiles: 42% and 5.2x; always
-// 256-tiles: 97% on average.
-//   few rows:  the operands' bytes as the kernel gets them, or its waves' steps in turn;
-//   128-tiles: two workgroups a CU, 0.95 us for a step of both, 0.61 for one alone;
-//   128-tiles by two wave groups: one workgroup a CU, 1.1 us for a step of both;
-//   256-tiles: one workgroup a CU, 1.21 us a step (1.87 float32, its matrix rate is half);
-//   a K split: the join's launch, and its partial sums' bytes.
-Shape shape_of(int64_t m, int64_t n, int64_t k, bool nn, bool bf16) {
-  // ahead of the others in all but one of 35 sizes timed (n 512 .. 28672, k 544 .. 8192)
-  if (!nn && m <= 16 && k <= 8192) return {16, 1, 1, 0};
-  const int nk = (int)((k + kRowB - 1) / kRowB);
-  Shape best{0, 1, 1, 0};
-  double least = 1e30;
-  auto consider = [&](const Shape &s, double us) {
-    if (us < least) least = us, best = s;
-  };
-  const bool tiles = nn ? (k >> 5) * (n >> 5) >= 4 : k > 0;   // NN reads scales 4 at a time
-  if (!tiles || (!nn && m <= 256)) {
-    const int rows = m <= 16 ? 16 : m <= 32 ? 32 : 64;
-    const double rate = rows == 16 ? 5.8e6 : rows == 32 ? 3.4e6 : 5.0e6;
-    const double us = std::max(rows == 64 ? 1.34 * ((nk + 7) / 8) : 0.0, (double)n * k * ((m + rows - 1) / rows) / rate);
-    consider({0, 1, 1, 0}, 6.7 + us * (bf16 ? 1.0 : 1.2));
-  }
-  if (!tiles) return best;
-  const int64_t t128 = (m + 127) / 128 * ((n + 127) / 128), t256 = (m + 255) / 256 * ((n + 255) / 256);
-  for (int groups : {1, 2})
-    for (int want : {1, 2, 3, 4, 6, 8, 16}) {
-      const int parts = groups * want, steps = ((nk + parts - 1) / parts + 3) / 4 * 4;
-      const int splits = (nk + groups * steps - 1) / (groups * steps);
-      if (splits != want || (groups == 2 && nk <= steps)) continue;
-      const double join = splits > 1 ? 3.0 + (double)splits * m * n * 4 / 2.66e6 : 0.0;
-      if (groups == 2) {
-        consider({128, 2, splits, steps}, 2.8 + (t128 * splits + 255) / 256 * (1.2 + steps * (bf16 ? 1.1 : 1.94)) + join);
-        continue;
-      }
-      const int run = std::min(steps, nk);
-      const double one = bf16 ? 0.61 : 0.9, two = bf16 ? 0.95 : 1.13;
-      const int64_t pairs = t128 * splits / 512, rest = t128 * splits % 512;
-      double us = 3.2 + pairs * (1.4 + run * two) + join;
-      if (rest) us += 1.4 + run * (rest <= 256 ? one : one + (two - one) * (rest - 256) / 256);
-      consider({128, 1, splits, steps}, us);
-      if (nn && n < 128) continue;
-      consider({256, 1, splits, steps}, 4.5 + (t256 * splits + 255) / 256 * (2.3 + run * (bf16 ? 1.21 : 1.87)) + join);
-    }
-  return best;
-}
-
 }  // namespace
 
 // What either output type may need.
 int64_t gemm_mx_workspace(int64_t m, int64_t n, int64_t k, bool nn) {
   int splits = 1;
-  for (const bool bf16 : {false, true}) splits = std::max(splits, shape_of(m, n, k, nn, bf16).splits);
+  for (const bool bf16 : {false, true}) splits = std::max(splits, gemm_shape_of(m, n, k, nn, bf16).splits);
   return splits > 1 ? splits * m * ((n + 3) / 4 * 4) * (int64_t)sizeof(float) : 0;
 }
 
 hipError_t launch_gemm_mx(const GemmMx &g, void *ws, hipStream_t s) {
-  const Shape sh = shape_of(g.m, g.n, g.k, g.nn, g.bf16);
+  const GemmShape sh = gemm_shape_of(g.m, g.n, g.k, g.nn, g.bf16);
   float *parts = static_cast<float *>(ws);
-  if (sh.tile == 16 && g.bf16)
-    return g.k <= 2048 ? gemm_few<true, 2>(g, s) : g.k <= 4096 ? gemm_few<true, 4>(g, s) : gemm_few<true, 8>(g, s);
-  if (sh.tile == 16)
-    return g.k <= 2048 ? gemm_few<false, 2>(g, s) : g.k <= 4096 ? gemm_few<false, 4>(g, s) : gemm_few<false, 8>(g, s);
+  if (sh.tile == 16) {
+    const int waves = gemm_few_waves(g.k);
+    if (g.bf16) return waves == 2 ? gemm_few<true, 2>(g, s) : waves == 4 ? gemm_few<true, 4>(g, s) : gemm_few<true, 8>(g, s);
+    return waves == 2 ? gemm_few<false, 2>(g, s) : waves == 4 ? gemm_few<false, 4>(g, s) : gemm_few<false, 8>(g, s);
+  }
   if (sh.tile == 256)
     return g.nn ? gemm_tiled<T256, true>(g, sh.splits, sh.steps, parts, s)
                 : gemm_tiled<T256, false>(g, sh.splits, sh.steps, parts, s);
@@ -1276,8 +1221,9 @@ hipError_t launch_gemm_mx(const GemmMx &g, void *ws, hipStream_t s) {
     return g.nn ? gemm_tiled<T128, true>(g, sh.splits, sh.steps, parts, s)
                 : gemm_tiled<T128, false>(g, sh.splits, sh.steps, parts, s);
   if (g.nn) return g.bf16 ? gemm_rows<true, true, 4, 1, 1>(g, s) : gemm_rows<true, false, 4, 1, 1>(g, s);
-  if (g.m <= 16) return g.bf16 ? gemm_rows<false, true, 8, 1, 1>(g, s) : gemm_rows<false, false, 8, 1, 1>(g, s);
-  if (g.m <= 32) return g.bf16 ? gemm_rows<false, true, 8, 1, 2>(g, s) : gemm_rows<false, false, 8, 1, 2>(g, s);
+  const int rows = gemm_rows_block(g.m);
+  if (rows == 16) return g.bf16 ? gemm_rows<false, true, 8, 1, 1>(g, s) : gemm_rows<false, false, 8, 1, 1>(g, s);
+  if (rows == 32) return g.bf16 ? gemm_rows<false, true, 8, 1, 2>(g, s) : gemm_rows<false, false, 8, 1, 2>(g, s);
   return g.bf16 ? gemm_rows<false, true, 8, 2, 4>(g, s) : gemm_rows<false, false, 8, 2, 4>(g, s);
 }
 

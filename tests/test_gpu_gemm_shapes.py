@@ -6,6 +6,7 @@ that, rounded once; a group of 8 products spans less than 2^14, so none is cut o
 import pytest
 
 import mxfp8_weight_repack_amd as sh
+from gemm_sizes import INSTANCES
 from gpu_util import say
 
 torch = pytest.importorskip("torch")
@@ -126,3 +127,19 @@ def test_an_expert_of_a_bank(layout):
             outs.append(torch.full((50, n), 3.0, device="cuda"))
             sh.gemm_mxfp8(x, m, outs[-1], "fp32", stream=s)
         assert torch.equal(*outs) and bool(outs[0].abs().sum() > 0)
+
+
+@pytest.mark.parametrize("name", sorted(INSTANCES))
+def test_every_instance(name):
+    """Each compiled kernel at a ragged size, and in every scale layout that the operands may have."""
+    odd, whole = INSTANCES[name]
+    op, dtype = "nn" if " nn" in name else "nt", "bf16" if "bf16" in name else "fp32"
+    say(f"gemm instance {name}: {odd}")
+    check(op, *odd, dtype)
+    if whole:
+        m = whole[0]
+        for la, lb in (("rowmajor", "tile32x4"), ("rowmajor", "block32x32"), ("tile32x4", "block32x32"),
+                       ("block32x32", "tile32x4")):
+            if la == "rowmajor" or m % 32 == 0:
+                say(f"gemm instance {name}: {whole} {la} {lb}")
+                check(op, *whole, dtype, la, lb)
