@@ -136,10 +136,32 @@ def test_every_instance(name):
     op, dtype = "nn" if " nn" in name else "nt", "bf16" if "bf16" in name else "fp32"
     say(f"gemm instance {name}: {odd}")
     check(op, *odd, dtype)
-    if whole:
-        m = whole[0]
-        for la, lb in (("rowmajor", "tile32x4"), ("rowmajor", "block32x32"), ("tile32x4", "block32x32"),
-                       ("block32x32", "tile32x4")):
-            if la == "rowmajor" or m % 32 == 0:
-                say(f"gemm instance {name}: {whole} {la} {lb}")
-                check(op, *whole, dtype, la, lb)
+    m, n, k = whole
+    allowed = lambda layout, rows: layout == "rowmajor" or rows % 32 == 0 and (layout != "tile32x4" or k % 128 == 0)   # noqa: E731
+    pairs = [(la, "block32x32") for la in ("tile32x4", "block32x32")] if op == "nn" else \
+        [("rowmajor", "tile32x4"), ("rowmajor", "block32x32"), ("tile32x4", "block32x32"), ("block32x32", "tile32x4")]
+    ran = 0
+    for la, lb in pairs:
+        if allowed(la, m) and (op == "nn" or allowed(lb, n)):
+            say(f"gemm instance {name}: {whole} {la} {lb}")
+            check(op, *whole, dtype, la, lb)
+            ran += 1
+    assert ran >= (1 if name.startswith("rows nn") else 2)
+
+
+@pytest.mark.parametrize("name", sorted(INSTANCES))
+def test_scales_at_both_ends(name):
+    """One operand's values near 2^125, the other's near 2^-117, and the other way round: results 2^6 times the plain
+    ones, to the bit."""
+    op, dtype = "nn" if " nn" in name else "nt", "bf16" if "bf16" in name else "fp32"
+    m, n, k = INSTANCES[name][0]
+    say(f"gemm extreme scales {name}")
+    a = Operand(m, k, "rowmajor", m + n)
+    b = Operand(*((k, n) if op == "nn" else (n, k)), "block32x32" if op == "nn" else "rowmajor", m + k)
+    ref = (a.values @ (b.values if op == "nn" else b.values.t()) * 64).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    for up in (123, -117):
+        a.blocks.add_(up)
+        b.blocks.add_(6 - up)
+        assert torch.equal(product(a, b, op, dtype), ref)
+        a.blocks.sub_(up)
+        b.blocks.sub_(6 - up)
