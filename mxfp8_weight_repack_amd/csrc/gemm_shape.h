@@ -19,25 +19,29 @@ inline int gemm_few_waves(int64_t k) { return k <= 2048 ? 2 : k <= 4096 ? 4 : 8;
 // Rows of m that the few-row kernel takes at a time.
 inline int gemm_rows_block(int64_t m) { return m <= 16 ? 16 : m <= 32 ? 32 : 64; }
 
-// How a product runs: few-row kernel (tile 0; 16: A in registers), or tiles of 256 or 128 by `groups` wave
-// groups, with K in `splits` parts, each of `groups` runs of `steps` 128-k steps (a
-// multiple of 4: scale words come 4 steps at a time).
+// How a product runs: the kernel of up to 16 rows with A in registers (tile 16), the few-row
+// kernel (tile 0), or tiles of 256 or 128 by `groups` wave groups, with K in `splits` parts,
+// each of `groups` runs of `steps` 128-k steps (a multiple of 4: scale words come 4 steps at a
+// time).
 struct GemmShape {
   int tile, groups, splits, steps;
 };
 
 // The candidate with the least modelled time, in microseconds on an idle MI355X.  The
-// constants are fitted to 300 timed choices from m 1 .. 4096, n and k 128 .. 28672, both
-// operand forms and output types; what it picks takes 1.5% more than the best candidate
-// on average and 27% more at worst.  Always unsplit 128-tiles: 42% and 5.2x; always
-// 256-tiles: 97% on average.
+// constants were fitted to 300 timed choices from m 1 .. 4096, n and k 128 .. 28672, both
+// operand forms and output types.  Of 220 others timed with operands from HBM (110 sizes of
+// those ranges) what it picks takes 5.0% more than the best candidate on average; at worst
+// 1.34 times up to 16 rows, 1.83 from 17 to 256 (the few-row kernel in float32) and 1.22
+// above.  Always unsplit 128-tiles: 52% and 5.5 times; always unsplit 256-tiles: 175%.
 //   few rows:  the operands' bytes as the kernel gets them, or its waves' steps in turn;
 //   128-tiles: two workgroups a CU, 0.95 us for a step of both, 0.61 for one alone;
 //   128-tiles by two wave groups: one workgroup a CU, 1.1 us for a step of both;
 //   256-tiles: one workgroup a CU, 1.21 us a step (1.87 float32, its matrix rate is half);
 //   a K split: the join's launch, and its partial sums' bytes.
 inline GemmShape gemm_shape_of(int64_t m, int64_t n, int64_t k, bool nn, bool bf16) {
-  // ahead of the others in all but one of 35 sizes timed (n 512 .. 28672, k 544 .. 8192)
+  // from 84 MB of B on ahead of the others (1 x 10240 x 8192: 20.0 us against 22.4, float32 27.7;
+  // 16 x 23606 x 7744: 41.1 against 50.9), around 20 MB level with them; under 10 MB, where a
+  // call takes 5 to 7 us, up to 1.8 us behind the few-row kernel or unsplit tiles
   if (!nn && m <= 16 && k <= 8192) return {16, 1, 1, 0};
   const int nk = (int)((k + kGemmStep - 1) / kGemmStep);
   GemmShape best{0, 1, 1, 0};

@@ -7,9 +7,11 @@
 //
 // bfloat16 output: v_mfma_scale_f32_16x16x128_f8f6f4 (16 x 16 outputs, 128 k, i.e.
 // 4 blocks) takes codes and exponent bytes as they lie in memory.  It adds each 8
-// consecutive k's products in fixed point, cut off at 2^-14 of their largest
-// (measured: about 1.4e-5 of the result, rms), and those sums in float32: far
-// below bfloat16's half step of 2^-9 to 2^-8, but not a float32 sum.  So float32
+// consecutive k's products in fixed point, cut off at 2^-14 of the binade of their largest,
+// and those sums in float32: a group is off by less than 7 * 2^-14 of its largest product
+// (measured about 1.4e-5 rms of a result of random operands, against bfloat16's half step of
+// 2^-9 to 2^-8).  That is relative to the products: where they cancel it may pass the
+// rounding of the small result, and it is no float32 sum.  So float32
 // output converts the codes, scale included and exactly, to bfloat16
 // (v_cvt_scalef32_pk_bf16_fp8: 4 significant bits, and bfloat16 has float32's
 // exponents) and uses v_mfma_f32_16x16x32_bf16, whose sums are float32's (measured
@@ -102,8 +104,8 @@ __device__ __forceinline__ void store_bf16(const GemmMx &p, int64_t m, int64_t n
 // of B's rows; codes go straight from memory to the matrix instructions, one step's loads in
 // flight while another's are multiplied (two to four in flight were slower: fewer waves).
 // MT * 16 rows of m at a time; rows past the end repeat the last one.  The waves' sums meet
-// in LDS and are added in wave order.  32 x 2048 x 2048: 6.1 us; 1 x 2048 x 8192 with float32
-// output 13.6 us.
+// in LDS and are added in wave order.  bfloat16 and float32 output, operands from HBM: 32 x
+// 2048 x 2048 6.8 and 8.4 us, 24 x 2048 x 4864 10.1 and 12.5.
 template <bool NN, bool BF16, int W, int NF, int MT>
 __global__ __launch_bounds__(64 * W) void k_gemm_mx_rows(GemmMx p, int64_t tiles_n, int64_t first) {
   __shared__ __align__(16) f32x4_t part[W][NF * MT][64];
@@ -239,7 +241,7 @@ __global__ __launch_bounds__(64 * W) void k_gemm_mx_rows(GemmMx p, int64_t tiles
 // 16 of B are as many cache lines again).  The waves' sums of a group are added in wave order
 // by one wave, in turn, while the others go on.  Bound by reading B: 1 x 28672 x 8192 42.4 us
 // (5.5 TB/s), 16 rows 46.9, float32 output 42.2; split 128-tiles 54.5, 58.6 and 60.6, the
-// kernel above 54 to 67; smaller ones gain as much (1 x 2048 x 8192 8.1 against 10.5).  Twice
+// kernel above 54 to 67; 1 x 2048 x 8192 8.3 against 10.5; a B of under 10 MB gains nothing.  Twice
 // the waves with 4 steps each: up to 15% slower (16 x 12288 x 4096: 17.5 against 15.3).
 constexpr int kFewSteps = 8;
 
@@ -366,15 +368,17 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
 // group, picked by the instruction's byte select.
 //
 // 8192 x 28672 x 8192, bfloat16: 1.43-1.66 ms, 2.3-2.7 PFLOP/s (the clock falls with the data's
-// activity), matrix cores busy 71% of the time.  The rest is operand latency beyond the L2
+// activity), matrix cores busy 68 to 71% of the time.  The rest is operand latency beyond the L2
 // (with every load a hit: 1.32 ms) and the scales (without any: 1.38 ms).
 
 constexpr int kRowB = kGemmStep;                     // bytes (= k) of a stage row
 
 // KG groups of WN x WM waves make the same tile over KG parts of its K and add their sums
-// in LDS: where there are too few tiles to give every CU two workgroups, a second group
-// hides what one cannot (1999 x 2048 x 8192 NN: 43.9 us, one group 50.3; 26 us at the large
-// product's rate -- 64 steps one after another, each waiting for its stage's loads).
+// in LDS: where there are too few tiles to give every CU two workgroups, a second group takes
+// the place of the second workgroup (1999 x 2048 x 8192 NN, operands in the last-level cache:
+// 43.9 us, one group 50.3; 26 us at the large product's rate).  Both groups pass the one
+// barrier of a step, so they wait for their loads at the same time: matrix cores are 28%
+// busy, LDS 17%, and with operands from HBM the same product takes 54 us.
 template <int TN_, int TM_, int WN_, int WM_, int KG_>
 struct Tile {
   static constexpr int TN = TN_, TM = TM_, WN = WN_, WM = WM_, NW = WN * WM, NT = 64 * NW, KG = KG_, NST = 2;
@@ -689,8 +693,8 @@ __device__ __forceinline__ void store_part(const GemmMx &p, float *parts, int64_
     }
 }
 
-// The splits' sums added in split order, 4 consecutive n per thread (1 x 8192 x 28672, six
-// splits: 50.8 us with the tiles, their loads one after another 52.1).
+// The splits' sums added in split order, 4 consecutive n per thread (1 x 8192 x 28672, eight
+// splits: 51.5 us with the tiles, operands from HBM).
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_gemm_mx_join(GemmMx p, const float *parts, int splits) {
   const int64_t n4 = (p.n + 3) & ~(int64_t)3, words = p.m * (n4 >> 2);

@@ -489,8 +489,8 @@ def test_gemm_empty_sizes():
     assert np.array_equal(_gemm(k0, k0, 5, 5, "fp32", addend=add, in_place=True), add)
 
 
-# What the shape choice may pick: few rows (split over waves), 128-tiles by one wave group
-# or two, 256-tiles, each with up to 4 steps or more of 128 k, K splits where tiles are few.
+# Of what the shape choice may pick (all of it: gemm_sizes.py): few rows, 128-tiles by one wave
+# group or two, 256-tiles, each with up to 4 steps or more of 128 k, K splits where tiles are few.
 PICKS = [("nt", 1, 64, 544), ("nt", 33, 64, 544), ("nt", 257, 64, 544), ("nt", 1, 64, 128), ("nt", 33, 64, 8224),
          ("nt", 257, 64, 2080), ("nt", 3000, 160, 2048), ("nt", 2050, 4128, 544), ("nt", 3001, 4127, 544),
          ("nt", 8001, 3101, 128), ("nt", 2050, 6017, 224), ("nt", 130, 8224, 1056), ("nn", 1, 64, 544),
@@ -524,7 +524,7 @@ def test_gemm_every_shape_exact(op, m, n, k):
     assert torch.equal(out, ref + add)
 
 
-# Up to 16 rows in bfloat16: 4, 8 or 16 waves by K, its end inside a wave's part, more groups of
+# Up to 16 rows: 2, 4 or 8 waves by K, its end inside a wave's part, more groups of
 # 16 columns than run at once, the last one short.
 FEW = [(1, 1, 32), (16, 17, 2048), (5, 16421, 2016), (2, 300, 2080), (16, 8225, 4096), (7, 8200, 3552), (1, 100, 4128),
        (16, 4130, 8192), (3, 9001, 8160), (13, 4097, 7680), (1, 4112, 6176)]
