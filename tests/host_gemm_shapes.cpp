@@ -1,5 +1,5 @@
-// host_gemm_shapes.cpp -- which of the compiled MXFP8 product kernels a size runs, on the
-// host.  Reads lines "nn m n k bf16" and prints each one's instance; or, called with a
+// host_gemm_shapes.cpp -- which of the compiled MXFP8 product kernels a size runs, with K
+// whole or split, on the host.  Reads lines "nn m n k bf16" and prints each one's instance; or, called with a
 // count, prints every instance that as many drawn sizes reach, with its smallest size (least
 // m n k; of rows and columns in 32s and k in 128s if a second argument is given).
 #include <stdio.h>

@@ -131,7 +131,7 @@ def test_an_expert_of_a_bank(layout):
 
 @pytest.mark.parametrize("name", sorted(INSTANCES))
 def test_every_instance(name):
-    """Each compiled kernel at a ragged size, and in every scale layout that the operands may have."""
+    """Each compiled kernel, K whole and split, at a ragged size, and in every scale layout that the operands may have."""
     odd, whole = INSTANCES[name]
     op, dtype = "nn" if " nn" in name else "nt", "bf16" if "bf16" in name else "fp32"
     say(f"gemm instance {name}: {odd}")
