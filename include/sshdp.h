@@ -506,6 +506,104 @@ int sshdp_gemm_mxfp8_workspace(const sshdp_mx_matrix *a, const sshdp_mx_matrix *
 int sshdp_gemm_mxfp8(const sshdp_mx_matrix *a, const sshdp_mx_matrix *b, int32_t op, const float *addend, void *out,
                      int32_t out_dtype, int64_t ld_out, void *workspace, size_t workspace_bytes, void *stream);
 
+/* A mixture-of-experts layer on the expert banks: tokens are sorted by expert,
+ * each expert's tokens pass through its own weights as consecutive rows, and the
+ * results go back to their tokens.
+ *
+ * sshdp_moe_sort orders the tokens x top_k slots of `ids` (slot s = t * top_k + j:
+ * token t's choice j; int32, or int64 if ids_dtype is SSHDP_INDEX_I64) by expert,
+ * equal experts by slot.  An id outside [0, experts) drops its slot: a padding
+ * token, or an expert of another GPU.  Each expert's rows start at a multiple of
+ * `align` (a power of two up to 256):
+ *   offsets  experts + 1: expert e has the rows offsets[e] .. offsets[e + 1] - 1,
+ *            its slots first, then under `align` rows of padding;
+ *   place    tokens x top_k: each slot's row, -1 if dropped;
+ *   source   rows: each row's slot, -1 for padding and behind the last expert.
+ * `rows` is the buffers' size, at least sshdp_moe_rows of the same sizes (the most
+ * that any ids take; with align >= 32 a multiple of 128).  An expert may be chosen
+ * twice by one token.  align 32 and over keeps the blocks of 32 rows that the
+ * weight gradient's operands have inside one expert.  `workspace`:
+ * sshdp_moe_sort_workspace bytes, 16-byte aligned.
+ * Errors: ARG (null pointer, tokens < 0, top_k < 1, experts < 1, align no power of
+ * two, bad dtype), SCHEMA (experts over 1024, top_k over 64, over 2^24 slots, align
+ * over 256, rows too few or over 2^30), ALIGN (offsets, place, source; ids: its own
+ * type's), WORKSPACE; HIP. */
+enum { SSHDP_INDEX_I32 = 0, SSHDP_INDEX_I64 = 1 };
+int sshdp_moe_rows(int64_t tokens, int32_t top_k, int32_t experts, int32_t align, int64_t *rows);
+int sshdp_moe_sort_workspace(int64_t tokens, int32_t top_k, int32_t experts, int64_t *bytes);
+int sshdp_moe_sort(const void *ids, int32_t ids_dtype, int64_t tokens, int32_t top_k, int32_t experts, int32_t align,
+                   int32_t *offsets, int32_t *place, int32_t *source, int64_t rows, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/* An MXFP8 output: codes and scales along rows, codes_t and scales_t along columns
+ * (the transpose), as sshdp_quant_mxfp8 lays them out; NULL: not wanted. */
+typedef struct {
+  uint8_t *codes, *scales, *codes_t, *scales_t;
+} sshdp_mx_out;
+
+/* Tokens to the experts' rows: row p of the result is
+ *   v[p] = weights[s] * x[s / top_k],  s = source[p]   (weights NULL: 1),
+ * and zeros where source has -1 (or no slot of these tokens).  `y` receives v in
+ * `dtype`, `out` G(v) of v rounded to float32: along the rows, along the columns
+ * (pitch `rows`, a multiple of 32; its blocks are of 32 sorted rows), or both.
+ * Rows from offsets[experts] on are left as they were (columns: blocks that start
+ * there).  x has rows ld_x elements apart.  The gradient of x is sshdp_moe_combine
+ * of the rows' gradients, with the same weights.
+ * Errors: ARG (null x, source or offsets, no output, half a pair, bad dtype, a
+ * negative size, top_k or experts < 1), SCHEMA (cols not a multiple of 32, rows not
+ * one with codes_t, ld_x < cols or its rows not 16-byte multiples, an edge over
+ * 2^30, experts over 1024, top_k over 64, over 2^24 slots), ALIGN (all but the
+ * scales; weights, source and offsets 4); HIP. */
+typedef struct {
+  const void *x;
+  const float *weights;
+  const int32_t *source, *offsets;
+  void *y;
+  sshdp_mx_out out;
+  int64_t tokens, rows, cols, ld_x;
+  int32_t top_k, experts, dtype, pad_;
+} sshdp_moe_gather;
+int sshdp_moe_gather_mxfp8(const sshdp_moe_gather *args, void *stream);
+
+/* The experts' rows back to their tokens:
+ *   out[t] = residual[t] + sum over j of weights[t][j] * y[place[t][j]],
+ * added up in float32 in the order of j, the residual last, rounded to `dtype`
+ * once; dropped slots (a place outside [0, rows)) add nothing.  weights NULL: 1;
+ * residual NULL: 0.  y is rows x cols, out and residual tokens x cols, all dense;
+ * out may be residual.
+ * Errors: ARG (null y, place or out, bad dtype, a negative size, top_k < 1), SCHEMA
+ * (cols not a multiple of 32, an edge over 2^30, top_k over 64, over 2^24 slots),
+ * ALIGN (as above); HIP. */
+typedef struct {
+  const void *y;
+  const int32_t *place;
+  const float *weights;
+  const void *residual;
+  void *out;
+  int64_t tokens, rows, cols;
+  int32_t top_k, dtype;
+} sshdp_moe_combine_args;
+int sshdp_moe_combine(const sshdp_moe_combine_args *args, void *stream);
+
+/* Its gradient.  dy[p] = weights[s] * dout[s / top_k], s = source[p], as
+ * sshdp_moe_gather_mxfp8 writes it (`dy` in `dtype`, `out` in MXFP8), and
+ *   dweights[t][j] = sum over columns of dout[t] * y[place[t][j]]
+ * in float32, 0 for dropped slots.  Either may be left out: dy and out NULL (source
+ * and offsets are then not read), or dweights NULL (y and place are then not read).
+ * The residual's gradient is dout itself.  Errors: as for the two calls above, ARG
+ * also for no output at all. */
+typedef struct {
+  const void *dout, *y;
+  const float *weights;
+  const int32_t *place, *source, *offsets;
+  void *dy;
+  sshdp_mx_out out;
+  float *dweights;
+  int64_t tokens, rows, cols, ld_dout;
+  int32_t top_k, experts, dtype, pad_;
+} sshdp_moe_combine_grad;
+int sshdp_moe_combine_backward(const sshdp_moe_combine_grad *args, void *stream);
+
 /* Diagnostics.  The batched NT contraction used by Newton-Schulz, exposed to
  * test it alone: for b < batch, O[b] = bf16(alpha * P[b] Q[b]^T + beta * D[b])
  * with P[b] M x K, Q[b] N x K, O[b] M x N (bf16, row-major, dense, batch strides

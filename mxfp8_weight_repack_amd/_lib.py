@@ -110,6 +110,35 @@ class MxMatrix(ctypes.Structure):
                 ("cols", ctypes.c_int64), ("layout", ctypes.c_int32), ("pad_", ctypes.c_int32)]
 
 
+class MxOut(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("codes_t", ctypes.c_void_p),
+                ("scales_t", ctypes.c_void_p)]
+
+
+class MoeGather(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("source", ctypes.c_void_p),
+                ("offsets", ctypes.c_void_p), ("y", ctypes.c_void_p), ("out", MxOut), ("tokens", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld_x", ctypes.c_int64),
+                ("top_k", ctypes.c_int32), ("experts", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("pad_", ctypes.c_int32)]
+
+
+class MoeCombine(ctypes.Structure):
+    _fields_ = [("y", ctypes.c_void_p), ("place", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("out", ctypes.c_void_p), ("tokens", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("top_k", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class MoeCombineGrad(ctypes.Structure):
+    _fields_ = [("dout", ctypes.c_void_p), ("y", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+                ("place", ctypes.c_void_p), ("source", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+                ("dy", ctypes.c_void_p), ("out", MxOut), ("dweights", ctypes.c_void_p), ("tokens", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld_dout", ctypes.c_int64),
+                ("top_k", ctypes.c_int32), ("experts", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("pad_", ctypes.c_int32)]
+
+
 # every symbol include/sshdp.h declares, with its argument and return types
 _P = ctypes.c_void_p
 SIGNATURES = {
@@ -154,6 +183,15 @@ SIGNATURES = {
                                     ctypes.POINTER(ctypes.c_int64)], ctypes.c_int),
     "sshdp_gemm_mxfp8": ([ctypes.POINTER(MxMatrix), ctypes.POINTER(MxMatrix), ctypes.c_int32, _P, _P, ctypes.c_int32,
                           ctypes.c_int64, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "sshdp_moe_rows": ([ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                        ctypes.POINTER(ctypes.c_int64)], ctypes.c_int),
+    "sshdp_moe_sort_workspace": ([ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(ctypes.c_int64)],
+                                 ctypes.c_int),
+    "sshdp_moe_sort": ([_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P, _P,
+                        ctypes.c_int64, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "sshdp_moe_gather_mxfp8": ([ctypes.POINTER(MoeGather), _P], ctypes.c_int),
+    "sshdp_moe_combine": ([ctypes.POINTER(MoeCombine), _P], ctypes.c_int),
+    "sshdp_moe_combine_backward": ([ctypes.POINTER(MoeCombineGrad), _P], ctypes.c_int),
     "sshdp_ns_executed": ([_P, _P, ctypes.c_size_t, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_double),
                            _P], ctypes.c_int),
     "sshdp_profile_enable": ([_P, ctypes.c_int32], ctypes.c_int),
@@ -447,6 +485,63 @@ def gemm_mxfp8(a, b, out, out_dtype="bf16", op="nt", addend=None, ld_out=None, w
     _check(lib().sshdp_gemm_mxfp8(ctypes.byref(a), ctypes.byref(b), GEMM_OP.get(op, -1), _ptr(addend), _ptr(out),
                                   DTYPE.get(out_dtype, -1), ld_out, _ptr(workspace), int(workspace_bytes),
                                   _stream(stream)), "sshdp_gemm_mxfp8")
+
+
+INDEX = {"int32": 0, "int64": 1}    # SSHDP_INDEX_*
+
+
+def mx_pair(codes=None, scales=None, codes_t=None, scales_t=None):
+    """An MXFP8 output along rows (codes, scales) and/or along columns (codes_t, scales_t)."""
+    o = MxOut(_ptr(codes), _ptr(scales), _ptr(codes_t), _ptr(scales_t))
+    o._keep = (codes, scales, codes_t, scales_t)
+    return o
+
+
+def moe_rows(tokens, top_k, experts, align=1):
+    """Rows that the sorted buffers of tokens x top_k slots need, each expert's first one at a multiple of align."""
+    n = ctypes.c_int64()
+    _check(lib().sshdp_moe_rows(tokens, top_k, experts, align, ctypes.byref(n)), "sshdp_moe_rows")
+    return n.value
+
+
+def moe_sort_workspace(tokens, top_k, experts):
+    n = ctypes.c_int64()
+    _check(lib().sshdp_moe_sort_workspace(tokens, top_k, experts, ctypes.byref(n)), "sshdp_moe_sort_workspace")
+    return n.value
+
+
+def moe_sort(ids, tokens, top_k, experts, offsets, place, source, rows, align=1, ids_dtype="int32", workspace=None,
+             workspace_bytes=0, stream=None):
+    """Slots sorted by expert: offsets (experts + 1), place (of each slot) and source (of each row), all int32."""
+    _check(lib().sshdp_moe_sort(_ptr(ids), INDEX.get(ids_dtype, -1), tokens, top_k, experts, align, _ptr(offsets),
+                                _ptr(place), _ptr(source), rows, _ptr(workspace), int(workspace_bytes),
+                                _stream(stream)), "sshdp_moe_sort")
+
+
+def moe_gather_mxfp8(x, source, offsets, tokens, top_k, experts, rows, cols, dtype="bf16", weights=None, y=None,
+                     codes=None, scales=None, codes_t=None, scales_t=None, ld_x=None, stream=None):
+    """Tokens to the experts' rows (y, in x's type) and/or their MXFP8 along rows and columns."""
+    a = MoeGather(_ptr(x), _ptr(weights), _ptr(source), _ptr(offsets), _ptr(y),
+                  MxOut(_ptr(codes), _ptr(scales), _ptr(codes_t), _ptr(scales_t)), tokens, rows, cols,
+                  cols if ld_x is None else ld_x, top_k, experts, DTYPE.get(dtype, -1), 0)
+    _check(lib().sshdp_moe_gather_mxfp8(ctypes.byref(a), _stream(stream)), "sshdp_moe_gather_mxfp8")
+
+
+def moe_combine(y, place, out, tokens, top_k, rows, cols, dtype="bf16", weights=None, residual=None, stream=None):
+    """out[t] = residual[t] + sum over j of weights[t][j] * y[place[t][j]]."""
+    a = MoeCombine(_ptr(y), _ptr(place), _ptr(weights), _ptr(residual), _ptr(out), tokens, rows, cols, top_k,
+                   DTYPE.get(dtype, -1))
+    _check(lib().sshdp_moe_combine(ctypes.byref(a), _stream(stream)), "sshdp_moe_combine")
+
+
+def moe_combine_backward(dout, y, weights, place, source, offsets, tokens, top_k, experts, rows, cols, dtype="bf16",
+                         dy=None, codes=None, scales=None, codes_t=None, scales_t=None, dweights=None, ld_dout=None,
+                         stream=None):
+    """The gradient of y, as dy and/or MXFP8 along rows and columns, and of the weights."""
+    a = MoeCombineGrad(_ptr(dout), _ptr(y), _ptr(weights), _ptr(place), _ptr(source), _ptr(offsets), _ptr(dy),
+                       MxOut(_ptr(codes), _ptr(scales), _ptr(codes_t), _ptr(scales_t)), _ptr(dweights), tokens, rows,
+                       cols, cols if ld_dout is None else ld_dout, top_k, experts, DTYPE.get(dtype, -1), 0)
+    _check(lib().sshdp_moe_combine_backward(ctypes.byref(a), _stream(stream)), "sshdp_moe_combine_backward")
 
 
 def _ref(x):

@@ -1,0 +1,422 @@
+// k_moe.hip -- tokens to the experts' rows and back: the slots' order by expert, rows
+// gathered into that order with G behind, the weighted sum back to the tokens, and the
+// weights' gradient.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "moe.h"
+#include "mx_rows.h"
+
+namespace sshdp {
+namespace {
+
+// --------------------------------------------------------------------- slots by expert
+
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+constexpr int kSortOnce = 4096;                      // slots that one workgroup sorts alone
+constexpr int kSortMostChunks = 256;
+
+// Slots a workgroup takes: all of up to 4096, else the fewest of a power of two from 1024 on
+// that leave at most 256 workgroups, each of which reads every other's counts.
+int64_t sort_chunk(int64_t slots) {
+  if (slots <= kSortOnce) return kSortOnce;
+  int64_t c = kSortThreads;
+  while ((slots + c - 1) / c > kSortMostChunks) c *= 2;
+  return c;
+}
+
+// The slot's expert, `experts` where it has none or lies past the end.
+template <class I>
+__device__ __forceinline__ int expert_of(const I *ids, int64_t slot, int64_t slots, int experts) {
+  if (slot >= slots) return experts;
+  const I id = ids[slot];
+  return id >= 0 && id < (I)experts ? (int)id : experts;
+}
+
+template <class I>
+__global__ __launch_bounds__(kSortThreads) void k_moe_count(const I *ids, int64_t slots, int experts, int64_t chunk,
+                                                            int32_t *counts) {
+  __shared__ int n[kMoeMaxExperts + 1];
+  const int t = threadIdx.x;
+  for (int e = t; e <= experts; e += kSortThreads) n[e] = 0;
+  __syncthreads();
+  const int64_t first = blockIdx.x * chunk;
+  for (int64_t i = t; i < chunk; i += kSortThreads) {
+    const int e = expert_of(ids, first + i, slots, experts);
+    if (e < experts) atomicAdd(&n[e], 1);             // whole numbers: any order gives the same
+  }
+  __syncthreads();
+  for (int e = t; e < experts; e += kSortThreads) counts[(int64_t)blockIdx.x * experts + e] = n[e];
+}
+
+// The lanes whose key is the caller's; every lane of the wave must call it.
+__device__ __forceinline__ uint64_t same_key(int key, int bits) {
+  uint64_t m = ~0ull;
+  for (int b = 0; b < bits; ++b) {
+    const bool one = key >> b & 1;
+    const uint64_t v = __ballot(one);
+    m &= one ? v : ~v;
+  }
+  return m;
+}
+
+// A workgroup places its chunk's slots: a wave takes consecutive ones, counts its slots of
+// each expert 64 at a time (a lane's rank among the 64 is the number of lower lanes with its
+// expert), the waves' counts become first rows, and the same passes over the slots hand the
+// rows out.  Slots of one expert so keep their order, with no atomics.
+template <class I>
+__global__ __launch_bounds__(kSortThreads) void k_moe_place(const I *ids, int64_t slots, int experts, int align,
+                                                            int64_t rows, int64_t chunk, const int32_t *counts,
+                                                            int32_t *offsets, int32_t *place, int32_t *source) {
+  __shared__ int next[kSortWaves][kMoeMaxExperts];    // counts, then each wave's next row of each expert
+  __shared__ int total[kMoeMaxExperts], before[kMoeMaxExperts], first_row[kMoeMaxExperts + 1], sums[kSortWaves];
+  const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
+  const int bits = 32 - __builtin_clz(experts);       // of the keys 0 .. experts
+  for (int e = lane; e < experts; e += 64) next[wave][e] = 0;
+  for (int e = t; e < experts; e += kSortThreads) total[e] = before[e] = 0;
+  __syncthreads();
+  const int64_t per = chunk / kSortWaves, s0 = blockIdx.x * chunk + wave * per;
+  const uint64_t lower = (1ull << lane) - 1;
+  for (int64_t i = 0; i < per; i += 64) {
+    if (s0 + i >= slots) break;
+    const int e = expert_of(ids, s0 + i + lane, slots, experts);
+    const uint64_t m = same_key(e, bits);
+    if (e < experts && !(m & lower)) next[wave][e] += __popcll(m);
+  }
+  if (counts) {
+    // all chunks' counts, and those of the chunks before this one
+    const int pitch = experts <= 64 ? 64 : experts <= 256 ? 256 : 1024;
+    const int e = t % pitch, parts = kSortThreads / pitch;
+    if (e < experts) {
+      int all = 0, mine = 0;
+      for (int c = t / pitch; c < (int)gridDim.x; c += parts) {
+        const int v = counts[(int64_t)c * experts + e];
+        all += v;
+        if (c < (int)blockIdx.x) mine += v;
+      }
+      atomicAdd(&total[e], all);
+      atomicAdd(&before[e], mine);
+    }
+  }
+  __syncthreads();
+  // experts' first rows: an exclusive sum of their rows, one expert a thread
+  int n = 0;
+  if (t < experts) {
+    if (counts) {
+      n = total[t];
+    } else {
+      for (int w = 0; w < kSortWaves; ++w) n += next[w][t];
+      total[t] = n;
+    }
+  }
+  const int size = (n + align - 1) / align * align;
+  int x = size;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 63) sums[wave] = x;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) x += sums[w];
+  if (t < experts) {
+    first_row[t] = x - size;
+    if (t == experts - 1) first_row[experts] = x;
+    int at = x - size + before[t];
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int c = next[w][t];
+      next[w][t] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  for (int64_t i = 0; i < per; i += 64) {
+    const int64_t s = s0 + i + lane;
+    if (s0 + i >= slots) break;
+    const int e = expert_of(ids, s, slots, experts);
+    const uint64_t m = same_key(e, bits);
+    int at = -1;
+    if (e < experts) {
+      at = next[wave][e] + __popcll(m & lower);
+      source[at] = (int)s;
+    }
+    // the lanes of one expert have read its next row before their first one moves it
+    if (e < experts && !(m & lower)) next[wave][e] = at + __popcll(m);
+    if (s < slots) place[s] = at;
+  }
+  if (blockIdx.x == 0)
+    for (int e = t; e <= experts; e += kSortThreads) offsets[e] = first_row[e];
+  // padding behind each expert's slots, and what is behind the last expert
+  const int lanes = (int)gridDim.x * kSortThreads, id = blockIdx.x * kSortThreads + t;
+  if (align > 1)
+    for (int e = blockIdx.x * kSortWaves + wave; e < experts; e += (int)gridDim.x * kSortWaves)
+      for (int r = first_row[e] + total[e] + lane; r < first_row[e + 1]; r += 64) source[r] = -1;
+  for (int64_t r = first_row[experts] + (int64_t)id; r < rows; r += lanes) source[r] = -1;
+}
+
+// ---------------------------------------------------------------------- rows gathered
+
+// The token and weight of a sorted row; false for padding.
+__device__ __forceinline__ bool row_of(const sshdp_moe_gather &a, int64_t p, int64_t &token, float &w) {
+  const int slot = a.source[p];
+  token = 0;
+  w = 0.f;
+  if (slot < 0 || slot >= a.tokens * a.top_k) return false;
+  token = slot / a.top_k;
+  w = a.weights ? a.weights[slot] : 1.f;
+  return true;
+}
+
+// Rows in use, whatever the offsets hold.
+__device__ __forceinline__ int64_t rows_in_use(const sshdp_moe_gather &a) {
+  return min((int64_t)max(a.offsets[a.experts], 0), a.rows);
+}
+
+// Along the rows: 8 elements a lane, 4 lanes a block, as k_quant_rows.
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_moe_rows(sshdp_moe_gather a, int runs_per_row) {
+  const int64_t runs = rows_in_use(a) * runs_per_row;  // a multiple of 4: a block's lanes leave together
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < runs; i += (int64_t)gridDim.x * 256) {
+    const int64_t p = i / runs_per_row;
+    int64_t token;
+    float w, v[8];
+    Raw8<BF16> raw{};
+    if (row_of(a, p, token, w)) raw = load8<BF16>(a.x, token * a.ld_x + (i - p * runs_per_row) * 8);
+    unpack8<BF16>(raw, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= w;
+    if (a.y) store8<BF16>(a.y, i * 8, pack8<BF16>(v));
+    if (a.out.codes) {
+      const uint32_t sb = mx_scale_byte(mx_amax4(v));
+      *reinterpret_cast<u32x2_t *>(a.out.codes + i * 8) = mx_encode8(v, sb);
+      if ((i & 3) == 0) a.out.scales[i >> 2] = (uint8_t)sb;
+    }
+  }
+}
+
+constexpr int kMtRows = 128, kMtCols = 128;          // tile of one workgroup
+
+// Both ways, or along the columns: the tile of k_quant_tiles (LDS columns rotated by the row
+// group, a lane two columns' 32 rows), its rows fetched by `source`, the weights beside them.
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_moe_tiles(sshdp_moe_gather a, int tiles_c) {
+  constexpr int ES = BF16 ? 2 : 4, ROT = BF16 ? 32 : 16;
+  __shared__ __align__(16) char sm[kMtRows * kMtCols * ES];
+  __shared__ float sw[kMtRows];
+  const int t = threadIdx.x;
+  const int64_t tr = blockIdx.x / tiles_c, r0 = tr * kMtRows, c0 = (blockIdx.x - tr * tiles_c) * (int64_t)kMtCols;
+  const int64_t used = rows_in_use(a);
+  if (r0 >= used) return;
+  const int lc = (t & 15) * 8, lr = t >> 4;
+  const bool in_c = c0 + lc < a.cols;
+  Raw8<BF16> raw[kMtRows / 16];
+  float w[kMtRows / 16];
+#pragma unroll
+  for (int p = 0; p < kMtRows / 16; ++p) {
+    const int64_t r = r0 + lr + 16 * p;
+    int64_t token;
+    raw[p] = Raw8<BF16>{};
+    w[p] = 0.f;
+    if (r < used && row_of(a, r, token, w[p]) && in_c) raw[p] = load8<BF16>(a.x, token * a.ld_x + c0 + lc);
+  }
+#pragma unroll
+  for (int p = 0; p < kMtRows / 16; ++p) {
+    const int rr = lr + 16 * p;
+    *reinterpret_cast<Raw8<BF16> *>(sm + (rr * kMtCols + (lc ^ ((rr >> 5) * ROT))) * ES) = raw[p];
+    if (lc == 0) sw[rr] = w[p];
+    float v[8];
+    unpack8<BF16>(raw[p], v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= w[p];
+    const uint32_t sb = mx_scale_byte(mx_amax4(v));
+    if (in_c && r0 + rr < used) {
+      const int64_t e = (r0 + rr) * a.cols + c0 + lc;
+      if (a.y) store8<BF16>(a.y, e, pack8<BF16>(v));
+      if (a.out.codes) {
+        *reinterpret_cast<u32x2_t *>(a.out.codes + e) = mx_encode8(v, sb);
+        if ((t & 3) == 0) a.out.scales[e >> 5] = (uint8_t)sb;
+      }
+    }
+  }
+  __syncthreads();
+  const int grp = t & 3, c = (t >> 2) * 2;
+  const int64_t r = r0 + 32 * grp;
+  if (c0 + c >= a.cols || r >= used) return;
+  const char *q = sm + (32 * grp * kMtCols + (c ^ (grp * ROT))) * ES;
+  float v[2][32];
+  uint32_t m[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const float wj = sw[32 * grp + j];
+    if (BF16) {
+      const uint32_t x = *reinterpret_cast<const uint32_t *>(q + j * kMtCols * ES);
+      v[0][j] = __uint_as_float(x << 16) * wj;
+      v[1][j] = __uint_as_float(x & 0xFFFF0000u) * wj;
+    } else {
+      const float2 x = *reinterpret_cast<const float2 *>(q + j * kMtCols * ES);
+      v[0][j] = x.x * wj;
+      v[1][j] = x.y * wj;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) m[h] = max(m[h], __float_as_uint(v[h][j]) & 0x7FFFFFFFu);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t sb = mx_scale_byte(m[h]);
+    u32x4r_t o[2];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      o[j >> 2][j & 3] = mx_encode4(make_float4(v[h][4 * j], v[h][4 * j + 1], v[h][4 * j + 2], v[h][4 * j + 3]), sb);
+    const int64_t e = (c0 + c + h) * a.rows + r;
+    u32x4r_t *d = reinterpret_cast<u32x4r_t *>(a.out.codes_t + e);
+    d[0] = o[0];
+    d[1] = o[1];
+    a.out.scales_t[e >> 5] = (uint8_t)sb;
+  }
+}
+
+// --------------------------------------------------------------------- back to the tokens
+
+constexpr int kCombineAt = 8;                        // choices whose rows are in flight together
+
+// 8 elements of a token a lane: its choices' rows are read together and added in order.
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_moe_combine(sshdp_moe_combine_args a, int runs_per_row) {
+  const int64_t runs = a.tokens * runs_per_row;
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < runs; i += (int64_t)gridDim.x * 256) {
+    const int64_t t = i / runs_per_row, c = (i - t * runs_per_row) * 8;
+    float acc[8] = {};
+    for (int j0 = 0; j0 < a.top_k; j0 += kCombineAt) {
+      Raw8<BF16> raw[kCombineAt];
+      float w[kCombineAt];
+      bool have[kCombineAt];
+#pragma unroll
+      for (int j = 0; j < kCombineAt; ++j) {
+        have[j] = false;
+        if (j0 + j < a.top_k) {
+          const int64_t s = t * a.top_k + j0 + j;
+          const int p = a.place[s];
+          have[j] = p >= 0 && p < a.rows;
+          if (have[j]) {
+            w[j] = a.weights ? a.weights[s] : 1.f;
+            raw[j] = load8<BF16>(a.y, p * a.cols + c);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kCombineAt; ++j)
+        if (have[j]) {
+          float v[8];
+          unpack8<BF16>(raw[j], v);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) acc[k] = fmaf(w[j], v[k], acc[k]);
+        }
+    }
+    if (a.residual) {
+      float v[8];
+      unpack8<BF16>(load8<BF16>(a.residual, i * 8), v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] += v[k];
+    }
+    store8<BF16>(a.out, i * 8, pack8<BF16>(acc));
+  }
+}
+
+// The weights' gradient: a wave per token, 512 columns at a time.
+template <bool BF16>
+__global__ __launch_bounds__(256) void k_moe_dweights(sshdp_moe_combine_grad a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = blockIdx.x * (int64_t)4 + (threadIdx.x >> 6);
+  if (t >= a.tokens) return;
+  for (int j0 = 0; j0 < a.top_k; j0 += kCombineAt) {
+    int p[kCombineAt];
+    float sum[kCombineAt] = {};
+#pragma unroll
+    for (int j = 0; j < kCombineAt; ++j) {
+      p[j] = j0 + j < a.top_k ? a.place[t * a.top_k + j0 + j] : -1;
+      if (p[j] >= a.rows) p[j] = -1;
+    }
+    for (int64_t c = lane * 8; c < a.cols; c += 512) {
+      float d[8];
+      unpack8<BF16>(load8<BF16>(a.dout, t * a.ld_dout + c), d);
+#pragma unroll
+      for (int j = 0; j < kCombineAt; ++j)
+        if (p[j] >= 0) {
+          float v[8];
+          unpack8<BF16>(load8<BF16>(a.y, p[j] * a.cols + c), v);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sum[j] = fmaf(d[k], v[k], sum[j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kCombineAt; ++j) {
+      if (j0 + j >= a.top_k) break;
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) sum[j] += __shfl_xor(sum[j], d);
+      if (lane == 0) a.dweights[t * a.top_k + j0 + j] = sum[j];
+    }
+  }
+}
+
+template <class I>
+hipError_t moe_sort(const MoeSort &a, int32_t *counts, hipStream_t s) {
+  const int64_t chunk = sort_chunk(a.slots);
+  const unsigned chunks = (unsigned)std::max<int64_t>(1, (a.slots + chunk - 1) / chunk);
+  const I *ids = static_cast<const I *>(a.ids);
+  if (chunks > 1) {
+    hipLaunchKernelGGL((k_moe_count<I>), dim3(chunks), dim3(kSortThreads), 0, s, ids, a.slots, a.experts, chunk, counts);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((k_moe_place<I>), dim3(chunks), dim3(kSortThreads), 0, s, ids, a.slots, a.experts, a.align, a.rows,
+                     chunk, chunks > 1 ? counts : nullptr, a.offsets, a.place, a.source);
+  return hipGetLastError();
+}
+
+dim3 run_grid(int64_t runs) { return dim3((unsigned)std::min<int64_t>((runs + 255) / 256, 1 << 20)); }
+
+}  // namespace
+
+int64_t moe_sort_counts(int64_t slots, int experts) {
+  const int64_t chunk = sort_chunk(slots), chunks = (slots + chunk - 1) / chunk;
+  return chunks > 1 ? chunks * experts : 0;
+}
+
+hipError_t launch_moe_sort(const MoeSort &a, int32_t *counts, hipStream_t s) {
+  return a.i64 ? moe_sort<int64_t>(a, counts, s) : moe_sort<int32_t>(a, counts, s);
+}
+
+hipError_t launch_moe_gather(const sshdp_moe_gather &a, hipStream_t s) {
+  const bool bf16 = a.dtype == SSHDP_DTYPE_BF16;
+  const dim3 block(256);
+  if (a.out.codes_t) {
+    const int64_t tc = (a.cols + kMtCols - 1) / kMtCols, tr = (a.rows + kMtRows - 1) / kMtRows;
+    const dim3 grid((unsigned)(tr * tc));
+    if (bf16) hipLaunchKernelGGL((k_moe_tiles<true>), grid, block, 0, s, a, (int)tc);
+    else hipLaunchKernelGGL((k_moe_tiles<false>), grid, block, 0, s, a, (int)tc);
+  } else {
+    const int runs = (int)(a.cols / 8);
+    if (bf16) hipLaunchKernelGGL((k_moe_rows<true>), run_grid(a.rows * runs), block, 0, s, a, runs);
+    else hipLaunchKernelGGL((k_moe_rows<false>), run_grid(a.rows * runs), block, 0, s, a, runs);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_combine(const sshdp_moe_combine_args &a, hipStream_t s) {
+  const int runs = (int)(a.cols / 8);
+  if (a.dtype == SSHDP_DTYPE_BF16)
+    hipLaunchKernelGGL((k_moe_combine<true>), run_grid(a.tokens * runs), dim3(256), 0, s, a, runs);
+  else
+    hipLaunchKernelGGL((k_moe_combine<false>), run_grid(a.tokens * runs), dim3(256), 0, s, a, runs);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_dweights(const sshdp_moe_combine_grad &a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.tokens + 3) / 4));
+  if (a.dtype == SSHDP_DTYPE_BF16) hipLaunchKernelGGL((k_moe_dweights<true>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_moe_dweights<false>), grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace sshdp

@@ -1,0 +1,27 @@
+// moe.h -- launchers of the expert layer's operators (k_moe.hip).
+#pragma once
+#include "internal.h"
+
+namespace sshdp {
+
+constexpr int kMoeMaxExperts = 1024;
+constexpr int kMoeMaxTopK = 64;
+constexpr int64_t kMoeMaxSlots = 1 << 24;
+
+// Slots sorted by expert.  counts: moe_sort_counts(slots, experts) ints of workspace.
+struct MoeSort {
+  const void *ids;
+  int64_t slots, rows;
+  int32_t experts, align;
+  int32_t *offsets, *place, *source;
+  bool i64;
+};
+int64_t moe_sort_counts(int64_t slots, int experts);
+hipError_t launch_moe_sort(const MoeSort &a, int32_t *counts, hipStream_t s);
+
+// Rows gathered, weighted and quantised: sshdp_moe_gather's fields.
+hipError_t launch_moe_gather(const sshdp_moe_gather &a, hipStream_t s);
+hipError_t launch_moe_combine(const sshdp_moe_combine_args &a, hipStream_t s);
+hipError_t launch_moe_dweights(const sshdp_moe_combine_grad &a, hipStream_t s);
+
+}  // namespace sshdp

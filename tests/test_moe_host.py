@@ -1,0 +1,162 @@
+"""The expert layer's operators on the host (no GPU): their refusals (every argument error comes before anything
+touches the device), the sizes they ask for, and their gradients' formulas against differences."""
+
+import itertools
+
+import numpy as np
+import pytest
+
+import mxfp8_weight_repack_amd as sh
+import moe_ref as M
+
+P = 1 << 20                                            # an aligned address that no refused call follows
+
+
+def refused(name, call, *a, **k):
+    with pytest.raises(sh.SshdpError) as e:
+        call(*a, **k)
+    assert e.value.name == name, (e.value.name, name)
+
+
+@pytest.mark.parametrize("align", [1, 2, 16, 32, 64, 256])
+def test_rows_hold_the_worst_ids(align):
+    """Every way to spread the slots over the experts fits, and some way needs each expert's whole padding."""
+    for t, k, e in [(0, 1, 3), (1, 1, 1), (3, 2, 2), (5, 1, 4), (2, 2, 64)]:
+        n = sh.moe_rows(t, k, e, align)
+        assert n == M.rows_for(t, k, e, align)
+        worst = 0
+        for ids in itertools.product(range(min(e, 4)), repeat=t * k):
+            worst = max(worst, int(M.sort(ids, e, align, n)[0][-1]))
+        spread = M.sort([i % e for i in range(t * k)], e, align, n)[0][-1]
+        assert max(worst, spread) <= n
+        assert align < 32 or n % 128 == 0
+
+
+def test_rows_and_workspace_refusals():
+    for f in (lambda *a: sh.moe_rows(*a, 1), sh.moe_sort_workspace):
+        refused("ARG", f, -1, 1, 1)
+        refused("ARG", f, 1, 0, 1)
+        refused("ARG", f, 1, 1, 0)
+        refused("SCHEMA", f, 1, 65, 1)
+        refused("SCHEMA", f, 1, 1, 1025)
+        refused("SCHEMA", f, (1 << 24) // 3 + 1, 3, 8)
+    refused("ARG", sh.moe_rows, 1, 1, 1, 0)
+    refused("ARG", sh.moe_rows, 1, 1, 1, 48)
+    refused("SCHEMA", sh.moe_rows, 1, 1, 1, 512)
+    assert sh.moe_sort_workspace(1, 6, 64) == 0
+    assert sh.moe_sort_workspace(16381, 6, 64) % 4 == 0 < sh.moe_sort_workspace(16381, 6, 64)
+
+
+def test_sort_refusals():
+    def q(ids=P, tokens=9, top_k=2, experts=4, offsets=P, place=P, source=P, rows=18, **k):
+        return lambda: sh.moe_sort(ids, tokens, top_k, experts, offsets, place, source, rows, **k)
+    refused("ARG", q(ids_dtype="int8"))
+    for k in ("ids", "offsets", "place", "source"):
+        refused("ARG", q(**{k: None}))
+        refused("ALIGN", q(**{k: P + 2}))
+    refused("ALIGN", q(ids=P + 4, ids_dtype="int64"))
+    refused("ARG", q(align=3))
+    refused("SCHEMA", q(rows=17))
+    refused("SCHEMA", q(rows=18, align=2))
+    refused("SCHEMA", q(rows=(1 << 30) + 1))
+    refused("SCHEMA", q(experts=1025))
+    n = sh.moe_sort_workspace(4096, 2, 4)
+    refused("WORKSPACE", q(tokens=4096, rows=8192))
+    refused("WORKSPACE", q(tokens=4096, rows=8192, workspace=P, workspace_bytes=n - 1))
+    refused("ALIGN", q(tokens=4096, rows=8192, workspace=P + 4, workspace_bytes=n))
+
+
+def test_gather_refusals():
+    def q(x=P, source=P, offsets=P, tokens=4, top_k=2, experts=4, rows=32, cols=64, **k):
+        return lambda: sh.moe_gather_mxfp8(x, source, offsets, tokens, top_k, experts, rows, cols,
+                                           **{**dict(codes=P, scales=P), **k})
+    refused("ARG", q(dtype="fp16"))
+    refused("ARG", q(rows=-1))
+    refused("ARG", q(cols=-32))
+    refused("ARG", q(codes=None, scales=None))         # no output
+    refused("ARG", q(scales=None))
+    refused("ARG", q(codes_t=P))
+    for k in ("x", "source", "offsets"):
+        refused("ARG", q(**{k: None}))
+    refused("SCHEMA", q(cols=48))
+    refused("SCHEMA", q(ld_x=32))
+    refused("SCHEMA", q(ld_x=68))
+    refused("SCHEMA", q(rows=33, codes_t=P, scales_t=P))
+    refused("SCHEMA", q(rows=(1 << 30) + 32))
+    refused("SCHEMA", q(top_k=65))
+    refused("SCHEMA", q(experts=1025))
+    refused("ALIGN", q(x=P + 8))
+    refused("ALIGN", q(y=P + 8))
+    refused("ALIGN", q(codes=P + 8))
+    refused("ALIGN", q(codes_t=P + 8, scales_t=P))
+    for k in ("source", "offsets", "weights"):
+        refused("ALIGN", q(**{k: P + 2}))
+    q(rows=0)()                                        # nothing to do
+    q(cols=0)()
+
+
+def test_combine_refusals():
+    def q(y=P, place=P, out=P, tokens=4, top_k=2, rows=8, cols=64, **k):
+        return lambda: sh.moe_combine(y, place, out, tokens, top_k, rows, cols, **k)
+    refused("ARG", q(dtype="x"))
+    refused("ARG", q(rows=-1))
+    refused("ARG", q(tokens=-1))
+    refused("ARG", q(top_k=0))
+    for k in ("y", "place", "out"):
+        refused("ARG", q(**{k: None}))
+    refused("SCHEMA", q(cols=40))
+    refused("SCHEMA", q(top_k=65))
+    refused("SCHEMA", q(rows=(1 << 30) + 1))
+    for k in ("y", "out", "residual"):
+        refused("ALIGN", q(**{k: P + 8}))
+    for k in ("place", "weights"):
+        refused("ALIGN", q(**{k: P + 2}))
+    q(tokens=0, y=None, place=None, out=None)()
+    q(cols=0, y=None, place=None, out=None)()
+
+
+def test_combine_backward_refusals():
+    def q(dout=P, y=P, weights=P, place=P, source=P, offsets=P, tokens=4, top_k=2, experts=4, rows=32, cols=64, **k):
+        return lambda: sh.moe_combine_backward(dout, y, weights, place, source, offsets, tokens, top_k, experts, rows,
+                                               cols, **{**dict(codes=P, scales=P, dweights=P), **k})
+    none = dict(codes=None, scales=None)
+    refused("ARG", q(dtype="x"))
+    refused("ARG", q(**none, dweights=None))           # no output
+    refused("ARG", q(scales=None))
+    for k in ("dout", "source", "offsets"):
+        refused("ARG", q(**{k: None}))
+    for k in ("dout", "y", "place"):
+        refused("ARG", q(**none, **{k: None}))
+    refused("SCHEMA", q(cols=40))
+    refused("SCHEMA", q(ld_dout=32))
+    refused("SCHEMA", q(rows=33, codes_t=P, scales_t=P))
+    for k in ("dout", "dy", "codes"):
+        refused("ALIGN", q(**{k: P + 8}))
+    for k in ("y", "place", "dweights"):
+        refused("ALIGN", q(**none, **{k: P + 2}))
+    q(rows=0, tokens=0, dout=None, y=None, place=None)()
+
+
+def test_combine_gradient_formulas_against_differences():
+    """The loss sum(dout * combine(y, weights)) moves with y and weights as their gradients say."""
+    rng = np.random.default_rng(3)
+    tokens, top_k, experts, cols = 7, 3, 5, 32
+    ids = rng.integers(-1, experts, (tokens, top_k))
+    rows = M.rows_for(tokens, top_k, experts, 2)
+    offsets, place, source = M.sort(ids, experts, 2, rows)
+    y, w = rng.standard_normal((rows, cols)), rng.random((tokens, top_k))
+    dout = rng.standard_normal((tokens, cols)).astype(np.float32)
+    w = w.astype(np.float32)
+    loss = lambda y_, w_: float(np.sum(dout * M.combine(y_, place, w_, None, top_k, "fp32")[0]))   # noqa: E731
+    dy = M.gather(dout, w, source, offsets, top_k)
+    dw, _ = M.dweights(dout, y, place, top_k)
+    vy, vw, h = rng.standard_normal(y.shape), rng.standard_normal(w.shape), 2.0 ** -10
+    # the loss is linear in each: differences are exact but for float64's (and dy's float32) rounding
+    got = (loss(y + h * vy, w) - loss(y - h * vy, w)) / (2 * h)
+    assert abs(got - np.sum(dy * vy)) <= 1e-5 * np.sum(np.abs(dy * vy))
+    got = (loss(y, w + h * vw) - loss(y, w - h * vw)) / (2 * h)
+    assert abs(got - np.sum(dw * vw)) <= 1e-9 * np.sum(np.abs(dw * vw))
+    # x's gradient through the gather is the combine of the rows' gradients
+    x, g = rng.standard_normal((tokens, cols)).astype(np.float32), rng.standard_normal((rows, cols))
+    lx = np.sum(M.gather(x, w, source, offsets, top_k).astype(np.float64) * g)
+    assert abs(lx - np.sum(x * M.combine(g, place, w, None, top_k, "fp32")[0])) <= 1e-5 * np.sum(np.abs(x)) * 4
