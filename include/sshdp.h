@@ -604,6 +604,51 @@ typedef struct {
 } sshdp_moe_combine_grad;
 int sshdp_moe_combine_backward(const sshdp_moe_combine_grad *args, void *stream);
 
+/* MXFP8 products grouped by expert: the rows of A that sshdp_moe_sort gave expert e
+ * (offsets[e] .. offsets[e + 1] - 1) with that expert's own matrix of the bank B,
+ * whose rows are the experts' one after the other (groups equal parts: a bank
+ * region of a plan, by sshdp_plan_mx_matrix).  Padding rows are rows like others.
+ *   SSHDP_GEMM_NT: out[p][n] = sum_k A[p][k] B_e[n][k] (+ addend[p][n]);
+ *   SSHDP_GEMM_NN: out[p][n] = sum_k A[p][k] B_e[k][n] (+ addend[p][n]),  B in
+ *     BLOCK32X32: the input gradient, from the forward product's own codes;
+ *   SSHDP_GEMM_TN: out_e[m][n] = sum over e's rows p of A[m][p] B[n][p] (+ addend):
+ *     the weight gradients, groups x A.rows rows of float32.  A and B are the
+ *     transposed operands of the two sides (codes_t, scales_t), the sorted rows
+ *     along their columns; offsets must be multiples of 32.  An expert without rows
+ *     gets its addend, or zeros.
+ * Types and arithmetic are those of sshdp_gemm_mxfp8.  A's scales (TN: both) are
+ * ROWMAJOR, B's in any layout.  `addend` (NULL for none) has out's type, shape and
+ * ld, and may be out; for bfloat16 it is added in float32 ahead of the rounding.
+ * `offsets`, groups + 1 device integers, may be NULL with one group, which then
+ * has all rows.  Rows outside every expert's (behind the last one) are neither
+ * read nor written; offsets that run backwards or past the rows make the call
+ * write a part of out, never memory outside it.  No workspace.
+ * Errors: ARG (null pointer, bad op, layout or dtype, groups < 1, no offsets for
+ * several groups, TN with bfloat16), SCHEMA (the operands' K differ or are 0 or
+ * over 2^22; B.rows not groups equal parts, of multiples of 32 in layouts that
+ * group 32 rows; A's layout; NN without BLOCK32X32, of experts of under 4 blocks or
+ * with B.cols over 2^23; TN with columns not a multiple of 128; ld_out < N; groups
+ * over 1024; more than 2^22 tiles of 128 x 128), ALIGN (codes, addend, out;
+ * offsets 4); HIP. */
+enum { SSHDP_GEMM_TN = 2 };
+int sshdp_gemm_mxfp8_grouped(const sshdp_mx_matrix *a, const sshdp_mx_matrix *b, int32_t op, const int32_t *offsets,
+                             int32_t groups, const void *addend, void *out, int32_t out_dtype, int64_t ld_out,
+                             void *stream);
+
+/* The gated pair of products of an expert's (or, with one group, a dense) MLP, the
+ * activation and G in one pass:
+ *   gate = A Bg_e^T,  up = A Bu_e^T,  h = silu(gate) * up,
+ *   silu(x) = x / (1 + exp(-x)),  codes, scales = G(h) along the rows (ROWMAJOR).
+ * The products are sshdp_gemm_mxfp8's of bfloat16 output; h is computed in float32
+ * (within 2^-20 of itself) from the sums, before they are rounded.  `gate` and `up`
+ * (both or neither) receive the products in bfloat16, what the backward pass
+ * needs; codes and scales may be left out then.  All outputs are dense, A.rows x N,
+ * N = gate_w.rows / groups a multiple of 32; gate_w and up_w have the same shape
+ * and layout.  The rest is as in sshdp_gemm_mxfp8_grouped with SSHDP_GEMM_NT. */
+int sshdp_gemm_mxfp8_swiglu(const sshdp_mx_matrix *a, const sshdp_mx_matrix *gate_w, const sshdp_mx_matrix *up_w,
+                            const int32_t *offsets, int32_t groups, uint8_t *codes, uint8_t *scales, void *gate,
+                            void *up, void *stream);
+
 /* Diagnostics.  The batched NT contraction used by Newton-Schulz, exposed to
  * test it alone: for b < batch, O[b] = bf16(alpha * P[b] Q[b]^T + beta * D[b])
  * with P[b] M x K, Q[b] N x K, O[b] M x N (bf16, row-major, dense, batch strides

@@ -192,6 +192,10 @@ SIGNATURES = {
     "sshdp_moe_gather_mxfp8": ([ctypes.POINTER(MoeGather), _P], ctypes.c_int),
     "sshdp_moe_combine": ([ctypes.POINTER(MoeCombine), _P], ctypes.c_int),
     "sshdp_moe_combine_backward": ([ctypes.POINTER(MoeCombineGrad), _P], ctypes.c_int),
+    "sshdp_gemm_mxfp8_grouped": ([ctypes.POINTER(MxMatrix), ctypes.POINTER(MxMatrix), ctypes.c_int32, _P,
+                                  ctypes.c_int32, _P, _P, ctypes.c_int32, ctypes.c_int64, _P], ctypes.c_int),
+    "sshdp_gemm_mxfp8_swiglu": ([ctypes.POINTER(MxMatrix), ctypes.POINTER(MxMatrix), ctypes.POINTER(MxMatrix), _P,
+                                 ctypes.c_int32, _P, _P, _P, _P, _P], ctypes.c_int),
     "sshdp_ns_executed": ([_P, _P, ctypes.c_size_t, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_double),
                            _P], ctypes.c_int),
     "sshdp_profile_enable": ([_P, ctypes.c_int32], ctypes.c_int),
@@ -409,6 +413,7 @@ def rs_accumulate(inputs, in_dtype, g, n, first, stream=None):
 
 DTYPE = {"fp32": 0, "bf16": 1}      # SSHDP_DTYPE_*
 GEMM_OP = {"nt": 0, "nn": 1}
+GROUPED_OP = dict(GEMM_OP, tn=2)
 # an unknown name becomes a value the library rejects (ARG)
 
 
@@ -542,6 +547,23 @@ def moe_combine_backward(dout, y, weights, place, source, offsets, tokens, top_k
                        MxOut(_ptr(codes), _ptr(scales), _ptr(codes_t), _ptr(scales_t)), _ptr(dweights), tokens, rows,
                        cols, cols if ld_dout is None else ld_dout, top_k, experts, DTYPE.get(dtype, -1), 0)
     _check(lib().sshdp_moe_combine_backward(ctypes.byref(a), _stream(stream)), "sshdp_moe_combine_backward")
+
+
+def gemm_mxfp8_grouped(a, b, out, offsets, groups, out_dtype="bf16", op="nt", addend=None, ld_out=None, stream=None):
+    """Products of each expert's rows of A with its part of B (op "nt", "nn"), or over them (op "tn": the weight
+    gradients, from transposed operands), plus addend."""
+    if ld_out is None:
+        ld_out = b.rows // max(groups, 1) if op == "nt" else b.cols if op == "nn" else b.rows
+    _check(lib().sshdp_gemm_mxfp8_grouped(ctypes.byref(a), ctypes.byref(b), GROUPED_OP.get(op, -1), _ptr(offsets), groups,
+                                          _ptr(addend), _ptr(out), DTYPE.get(out_dtype, -1), ld_out, _stream(stream)),
+           "sshdp_gemm_mxfp8_grouped")
+
+
+def gemm_mxfp8_swiglu(a, gate_w, up_w, codes=None, scales=None, offsets=None, groups=1, gate=None, up=None, stream=None):
+    """MXFP8 of silu(A gate_w^T) * (A up_w^T) by expert, and/or the two products in bfloat16."""
+    _check(lib().sshdp_gemm_mxfp8_swiglu(ctypes.byref(a), ctypes.byref(gate_w), ctypes.byref(up_w), _ptr(offsets), groups,
+                                         _ptr(codes), _ptr(scales), _ptr(gate), _ptr(up), _stream(stream)),
+           "sshdp_gemm_mxfp8_swiglu")
 
 
 def _ref(x):

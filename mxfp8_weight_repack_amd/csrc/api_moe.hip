@@ -42,6 +42,55 @@ int check_gather_pointers(const sshdp_moe_gather &a) {
   return check_device(a.x, a.weights, a.source, a.offsets, a.y, a.out.codes, a.out.scales, a.out.codes_t, a.out.scales_t);
 }
 
+constexpr int64_t kMaxTiles = 1 << 22;
+
+// B of a product of experts' rows: groups equal parts, each a matrix by the layout's rules.
+int check_bank(const sshdp_mx_matrix &b, int32_t groups) {
+  if (b.rows % groups) return SSHDP_ERR_SCHEMA;
+  return b.layout != SSHDP_SCALE_ROWMAJOR && b.rows / groups % 32 ? SSHDP_ERR_SCHEMA : SSHDP_OK;
+}
+
+int check_groups(const int32_t *offsets, int32_t groups) {
+  if (groups < 1 || (!offsets && groups != 1)) return SSHDP_ERR_ARG;
+  return groups > kMoeMaxExperts ? SSHDP_ERR_SCHEMA : SSHDP_OK;
+}
+
+// The operands' part of a grouped product, checked.
+int make_grouped(const sshdp_mx_matrix *a, const sshdp_mx_matrix *b, GroupForm form, const int32_t *offsets,
+                 int32_t groups, GemmGrouped &g) {
+  int st = check_matrix(a);
+  if (st == SSHDP_OK) st = check_matrix(b);
+  if (st == SSHDP_OK) st = check_groups(offsets, groups);
+  if (st != SSHDP_OK) return st;
+  if (a->layout != SSHDP_SCALE_ROWMAJOR) return SSHDP_ERR_SCHEMA;
+  g.form = form;
+  g.offsets = offsets;
+  g.groups = groups;
+  g.p.a = a->codes;
+  g.p.as = a->scales;
+  g.p.b = b->codes;
+  g.p.bs = b->scales;
+  g.p.la = a->layout;
+  g.p.lb = b->layout;
+  g.p.nn = form == kRowsNN;
+  g.p.m = a->rows;
+  g.p.k = a->cols;
+  if (form == kColumns) {
+    if (b->layout != SSHDP_SCALE_ROWMAJOR || a->cols != b->cols || a->cols % 128) return SSHDP_ERR_SCHEMA;
+    g.p.n = b->rows;
+  } else {
+    st = check_bank(*b, groups);
+    if (st != SSHDP_OK) return st;
+    const int64_t rows = b->rows / groups;
+    if (a->cols != (g.p.nn ? rows : b->cols) || a->cols == 0) return SSHDP_ERR_SCHEMA;
+    if (g.p.nn && (b->layout != SSHDP_SCALE_BLOCK32X32 || b->cols > (1 << 23) || (rows >> 5) * (b->cols >> 5) < 4))
+      return SSHDP_ERR_SCHEMA;
+    g.p.n = g.p.nn ? b->cols : rows;
+  }
+  if (a->cols > (1 << 22)) return SSHDP_ERR_SCHEMA;
+  return gemm_grouped_tiles(g) > kMaxTiles ? SSHDP_ERR_SCHEMA : SSHDP_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -135,6 +184,59 @@ int sshdp_moe_combine_backward(const sshdp_moe_combine_grad *a, void *stream) {
     if (st != SSHDP_OK) return st;
   }
   return run_dots ? hip_status(launch_moe_dweights(*a, s)) : SSHDP_OK;
+}
+
+int sshdp_gemm_mxfp8_grouped(const sshdp_mx_matrix *a, const sshdp_mx_matrix *b, int32_t op, const int32_t *offsets,
+                             int32_t groups, const void *addend, void *out, int32_t out_dtype, int64_t ld_out,
+                             void *stream) {
+  if (op != SSHDP_GEMM_NT && op != SSHDP_GEMM_NN && op != SSHDP_GEMM_TN) return SSHDP_ERR_ARG;
+  const bool tn = op == SSHDP_GEMM_TN;
+  if (!dtype_ok(out_dtype) || (tn && out_dtype != SSHDP_DTYPE_FP32)) return SSHDP_ERR_ARG;
+  GemmGrouped g{};
+  int st = make_grouped(a, b, tn ? kColumns : op == SSHDP_GEMM_NN ? kRowsNN : kRowsNT, offsets, groups, g);
+  if (st != SSHDP_OK) return st;
+  if (ld_out < g.p.n || ld_out > kMaxEdge) return SSHDP_ERR_SCHEMA;
+  if (g.p.m == 0 || g.p.n == 0) return SSHDP_OK;
+  if (!out) return SSHDP_ERR_ARG;
+  if (!aligned16(a->codes) || !aligned16(b->codes) || !aligned16(addend) || !aligned16(out) || !aligned4(offsets))
+    return SSHDP_ERR_ALIGN;
+  st = check_device(a->codes, a->scales, b->codes, b->scales, offsets, addend, out);
+  if (st != SSHDP_OK) return st;
+  g.bf16 = out_dtype == SSHDP_DTYPE_BF16;
+  g.p.out = out;
+  g.p.ld = ld_out;
+  g.p.bf16 = g.bf16;
+  if (g.bf16) g.addend16 = static_cast<const uint16_t *>(addend);
+  else g.p.addend = static_cast<const float *>(addend);
+  return hip_status(launch_gemm_grouped(g, static_cast<hipStream_t>(stream)));
+}
+
+int sshdp_gemm_mxfp8_swiglu(const sshdp_mx_matrix *a, const sshdp_mx_matrix *gate_w, const sshdp_mx_matrix *up_w,
+                            const int32_t *offsets, int32_t groups, uint8_t *codes, uint8_t *scales, void *gate,
+                            void *up, void *stream) {
+  GemmGrouped g{};
+  int st = check_matrix(up_w);
+  if (st == SSHDP_OK) st = make_grouped(a, gate_w, kRowsGated, offsets, groups, g);
+  if (st != SSHDP_OK) return st;
+  if (up_w->rows != gate_w->rows || up_w->cols != gate_w->cols || up_w->layout != gate_w->layout || g.p.n % 32)
+    return SSHDP_ERR_SCHEMA;
+  if (g.p.m == 0 || g.p.n == 0) return SSHDP_OK;
+  if (!codes != !scales || !gate != !up || (!codes && !gate)) return SSHDP_ERR_ARG;
+  if (!aligned16(a->codes) || !aligned16(gate_w->codes) || !aligned16(up_w->codes) || !aligned16(codes) ||
+      !aligned16(gate) || !aligned16(up) || !aligned4(offsets))
+    return SSHDP_ERR_ALIGN;
+  st = check_device(a->codes, a->scales, gate_w->codes, gate_w->scales, up_w->codes, up_w->scales, offsets, codes,
+                    scales, gate, up);
+  if (st != SSHDP_OK) return st;
+  g.bf16 = g.p.bf16 = true;
+  g.p.ld = g.p.n;
+  g.b2 = up_w->codes;
+  g.b2s = up_w->scales;
+  g.codes = codes;
+  g.scales = scales;
+  g.gate = static_cast<uint16_t *>(gate);
+  g.up = static_cast<uint16_t *>(up);
+  return hip_status(launch_gemm_grouped(g, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -232,16 +232,28 @@ __device__ __forceinline__ void dma16(const uint8_t *base, int64_t bytes, char *
   }
 }
 
+// What a workgroup's operands are: whole matrices; a gated product, whose n side is two
+// matrices of p.n rows, taking turns every 8 * NW rows of a tile's LDS rows; or a range of K
+// of wider matrices (rows `pitch` apart, from `start` on, both multiples of 32), whose scales
+// are row-major.
+enum Form { kWhole, kGated, kRange };
+struct GemmPart : GemmMx {
+  const uint8_t *b2, *b2s;                           // kGated: the second matrix
+  int64_t pitch;                                     // kRange
+  int start;
+};
+
 // The operand stages' addressing, shared by both matrix forms.
-template <class C, bool NN>
+template <class C, bool NN, Form F = kWhole>
 struct Loader {
-  const GemmMx &p;
+  using Args = std::conditional_t<F == kWhole, GemmMx, GemmPart>;
+  const Args &p;
   int64_t n0, m0;
   int kt0, nk, last;                                 // this workgroup's steps: kt0 .. kt0 + nk - 1; the matrix's last
   int wave, lane;
   int voffp, voffq;                                  // lane byte offsets
   bool inp, inq;                                     // whether the lane's chunk lies inside the last step
-  const uint8_t *gp, *gq;
+  const uint8_t *gp, *gq, *gp2;
   const uint8_t *sbase;                              // scales: the wave's 64-row group ...
   int soff, xstep, xlane, xmax, xmul, xend, tshift;  // ... and the lane's address in it
   int narrow;                                        // blocks of a row too short for a 4-byte word, else 0
@@ -249,7 +261,18 @@ struct Loader {
   bool xwords;                                       // a step's words lie apart: 4-byte loads
   uint32_t psel;
 
-  __device__ __forceinline__ Loader(const GemmMx &p_, int64_t n0_, int64_t m0_, int kt0_, int nk_)
+  __device__ __forceinline__ int64_t pitch() const {
+    if constexpr (F == kRange) return p.pitch;
+    else return p.k;
+  }
+  // Bytes of an operand from a tile's first row on.
+  __device__ __forceinline__ int64_t span(int64_t rows) const {
+    if constexpr (F == kRange) return (rows - 1) * p.pitch + p.k;
+    else return rows * p.k;
+  }
+
+  // kGated: n0 counts the rows of each of the two matrices.
+  __device__ __forceinline__ Loader(const Args &p_, int64_t n0_, int64_t m0_, int kt0_, int nk_)
       : p(p_), n0(n0_), m0(m0_), kt0(kt0_), nk(nk_) {
     const int t = threadIdx.x;
     lane = t & 63;
@@ -257,9 +280,10 @@ struct Loader {
     last = (int)((p.k + kRowB - 1) / kRowB) - 1;
     const int kt = (int)(p.k - (int64_t)last * kRowB);        // k of the last step (a multiple of 32)
     const int row = 8 * wave + (lane >> 3), chunk = (lane & 7) ^ swz(row);
-    voffq = row * (int)p.k + chunk * 16;
+    voffq = row * (int)pitch() + chunk * 16;
     inq = chunk * 16 < kt;
-    gq = p.a + m0 * p.k;
+    gq = p.a + m0 * pitch();
+    if constexpr (F == kRange) gq += p.start;
     if (NN) {
       constexpr int CPR = C::TN / 16, RPI = 64 / CPR;
       const int kr = RPI * wave + lane / CPR, c = (lane % CPR) ^ swz_k<C::TN>(kr);
@@ -269,18 +293,31 @@ struct Loader {
     } else {
       voffp = voffq;
       inp = inq;
-      gp = p.b + n0 * p.k;
+      gp = p.b + n0 * pitch();
+      if constexpr (F == kRange) gp += p.start;
+      if constexpr (F == kGated) gp2 = p.b2 + n0 * p.k;
     }
     // Scales: wave = 64-row group, n side first.  A lane reads one row's 4 bytes of a step
     // at sbase + soff + min(min(step * xstep + xlane, xmax) * xmul, xend).  Rows past the end
     // repeat the last one: their codes are zeros and their results unused.
     const bool ps = wave < C::TN / 64;
-    const int layout = ps ? p.lb : p.la, KB = (int)(p.k >> 5);
-    const int64_t r0 = ps ? n0 + 64 * wave : m0 + 64 * (wave - C::TN / 64);
+    const int layout = ps ? p.lb : p.la, KB = (int)(pitch() >> 5);
+    int64_t r0 = ps ? n0 + 64 * wave : m0 + 64 * (wave - C::TN / 64);
+    int in = lane;
+    bool second = false;                             // kGated: the lane's row is one of the second matrix
+    if constexpr (F == kGated) {
+      constexpr int H = 8 * C::NW;                   // rows of a turn: 64, or 32 (the wave's halves)
+      if (ps) {
+        second = H == 64 ? wave & 1 : lane >> 5;
+        r0 = n0 + (H == 64 ? 64 * (wave >> 1) : 32 * wave);
+        in = lane & (H - 1);
+      }
+    }
     // the group's first row, or the last row's block of 32 where the group is past the end
     const int64_t rl = (ps ? p.n : p.m) - 1, rb = min(r0, rl & ~(int64_t)31);
-    const int rr = (int)min<int64_t>(lane, rl - rb);
+    const int rr = (int)min<int64_t>(in, rl - rb);
     sbase = ps ? p.bs : p.as;
+    if constexpr (F == kGated) sbase = second ? p.b2s : sbase;
     xmul = 1;
     xlane = 0;
     xend = INT32_MAX;
@@ -301,6 +338,15 @@ struct Loader {
       xmul = NB;
       xend = KB * NB - 4 - first;
       psel = (uint32_t)(nb - first) * 0x0101u + (uint32_t)min(nb - first + 1, 3) * 0x01010000u;
+    } else if (F == kRange) {
+      // words of the range's steps, from the row's last one where that would pass the row's end
+      if constexpr (F == kRange) {
+        sbase += rb * KB;
+        soff = rr * KB;
+        xstep = 4;
+        xlane = p.start >> 5;
+        xmax = KB - 4;
+      }
     } else if (layout == SSHDP_SCALE_TILE32X4) {
       sbase += (rb >> 5) * (KB >> 2) * 128;
       soff = (rr >> 5) * (KB >> 2) * 128 + (rr & 31) * 4;
@@ -334,9 +380,13 @@ struct Loader {
 #pragma unroll
       for (int i = 0; i < C::NIP; ++i) dma16<NN>(gp + k0 * p.n, left, sp + i * C::NW * 1024, v, i * RPI * C::NW * (int)p.n);
     } else {
-      const int64_t rows = p.n - n0 < C::TN ? p.n - n0 : (int64_t)C::TN;
+      constexpr int TN = F == kGated ? C::TN / 2 : C::TN;
+      const int64_t rows = p.n - n0 < TN ? p.n - n0 : (int64_t)TN;
 #pragma unroll
-      for (int i = 0; i < C::NIP; ++i) dma16<NN>(gp, rows * p.k, sp + i * C::NW * 1024, v, i * 8 * C::NW * (int)p.k + (int)k0);
+      for (int i = 0; i < C::NIP; ++i) {
+        const int at = F == kGated ? i >> 1 : i;
+        dma16<NN>(F == kGated && (i & 1) ? gp2 : gp, span(rows), sp + i * C::NW * 1024, v, at * 8 * C::NW * (int)pitch() + (int)k0);
+      }
     }
   }
   __device__ __forceinline__ void load_q(char *smem, int stage, int kt) const {
@@ -345,7 +395,7 @@ struct Loader {
     char *sq = smem + C::NST * C::SEGP + stage * C::SEGQ + wave * 1024;
     const int64_t rows = p.m - m0 < C::TM ? p.m - m0 : (int64_t)C::TM;
 #pragma unroll
-    for (int i = 0; i < C::NIQ; ++i) dma16<NN>(gq, rows * p.k, sq + i * C::NW * 1024, v, i * 8 * C::NW * (int)p.k + kt * kRowB);
+    for (int i = 0; i < C::NIQ; ++i) dma16<NN>(gq, span(rows), sq + i * C::NW * 1024, v, i * 8 * C::NW * (int)pitch() + kt * kRowB);
   }
 
   // The bytes of this wave's 64 scale rows for steps 4 q .. 4 q + 3 as they lie in memory,
@@ -381,6 +431,14 @@ struct Loader {
     if (kEnd && wave < C::TN / 64) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) w[j] >>= 8 * max(min((kt0 + 4 * q + j) * xstep + xlane, xmax) * xmul - xend, 0);
+    } else if (F == kRange) {
+      // and what lies past the range's end counts as zeros too: it is the next range's
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int x = (kt0 + 4 * q + j) * 4, in = (int)(p.k >> 5) - x;
+        w[j] >>= min(8 * max(x + xlane - xmax, 0), 24);
+        w[j] &= in >= 4 ? ~0u : in <= 0 ? 0u : (1u << (8 * in)) - 1;
+      }
     } else if (SHORT) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) w[j] >>= min(max((kt0 + 4 * q + j) * xstep - xmax, 0) * tshift, 24);
@@ -761,6 +819,76 @@ __device__ __forceinline__ void sums16(const L &ld, char *smem, f32x4_t (&acc)[C
     if (kt + 4 >= nk) break;
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // the trailing reloads
+}
+
+// A tile as bfloat16 through LDS (rows m), then whole rows of 16-byte stores.
+template <class C>
+__device__ __forceinline__ void store_tile_bf16(const GemmMx &p, char *smem, int64_t n0, int64_t m0, int wn, int wm, int t_end,
+                                                const f32x4_t (&acc)[C::FP][C::FQ]) {
+  constexpr int FP = C::FP, FQ = C::FQ;
+  const int r_end = t_end & 15, g_end = t_end >> 4 & 3;
+  uint16_t *lt = reinterpret_cast<uint16_t *>(smem);
+  constexpr int LP = C::TN + 8;
+#pragma unroll
+  for (int i = 0; i < FP; ++i)
+#pragma unroll
+    for (int j = 0; j < FQ; ++j) {
+      const f32x4_t &v = acc[i][j];
+      uint2 *d = reinterpret_cast<uint2 *>(lt + (wm * (C::TM / C::WM) + 16 * j + r_end) * LP + wn * (C::TN / C::WN) + 16 * i + 4 * g_end);
+      *d = make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
+    }
+  __syncthreads();
+  uint16_t *out = static_cast<uint16_t *>(p.out);
+  constexpr int CH = C::TN / 8;
+  for (int id = t_end; id < C::TM * CH; id += C::NT) {
+    const int row = id / CH, c = (id - row * CH) * 8;
+    const int64_t m = m0 + row, n = n0 + c;
+    if (m >= p.m || n >= p.n) continue;
+    const u32x4_t v = *reinterpret_cast<const u32x4_t *>(lt + row * LP + c);
+    uint16_t *o = out + m * p.ld + n;
+    if (n + 8 <= p.n) {
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x4e_t *>(o));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (n + k < p.n) o[k] = (uint16_t)(v[k >> 1] >> (16 * (k & 1)));
+    }
+  }
+}
+
+// A tile as float32, the addend joined in.
+template <class C>
+__device__ __forceinline__ void store_tile_f32(const GemmMx &p, int64_t n0, int64_t m0, int wn, int wm, int t_end,
+                                               f32x4_t (&acc)[C::FP][C::FQ]) {
+  constexpr int FP = C::FP, FQ = C::FQ;
+  const int r_end = t_end & 15, g_end = t_end >> 4 & 3;
+  float *out = static_cast<float *>(p.out);
+  const int64_t mw = m0 + wm * (C::TM / C::WM) + r_end, nw = n0 + wn * (C::TN / C::WN) + 4 * g_end;
+  if (n0 + C::TN <= p.n) {
+    // 16-byte words all inside: one row block's addend words in flight together (rows past
+    // the end read the last one)
+#pragma unroll
+    for (int j = 0; j < FQ; ++j) {
+      const int64_t m = mw + 16 * j, e = m * p.ld + nw;
+      if (p.addend) {
+        const float *ad = p.addend + min(m, p.m - 1) * p.ld + nw;
+        f32x4_t v[FP];
+#pragma unroll
+        for (int i = 0; i < FP; ++i) v[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4e_t *>(ad + 16 * i));
+#pragma unroll
+        for (int i = 0; i < FP; ++i) acc[i][j] += v[i];
+      }
+      if (m < p.m) {
+#pragma unroll
+        for (int i = 0; i < FP; ++i) *reinterpret_cast<f32x4e_t *>(out + e + 16 * i) = acc[i][j];
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < FQ; ++j)
+#pragma unroll
+    for (int i = 0; i < FP; ++i) store_f32(p, out, mw + 16 * j, nw + 16 * i, acc[i][j]);
 }
 
 using T256 = Tile<256, 256, 2, 4, 1>;

@@ -1,0 +1,348 @@
+// k_gemm_grouped.hip -- MXFP8 products grouped by expert: consecutive rows of A with each
+// expert's own B, the gated pair of them with the activation and G behind, and the weight
+// gradients over each expert's rows.
+//
+// How many rows an expert has is known on the device alone.  A launch has as many workgroups
+// as any distribution may need; each finds its expert and tile from the offsets (one load and
+// a sum over the wave's lanes for 64 experts) and those left over end at once.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "gemm_mx.h"
+#include "moe.h"
+#include "mx_rows.h"
+
+namespace sshdp {
+namespace {
+
+// Expert e's rows, inside the matrix whatever the offsets hold.
+__device__ __forceinline__ void rows_of(const int32_t *offsets, int groups, int rows, int e, int &first, int &n) {
+  first = n = 0;
+  if (e >= groups) return;
+  if (!offsets) {
+    n = rows;
+    return;
+  }
+  // both ends are brought inside before they are subtracted: the difference cannot overflow
+  first = min(max(offsets[e], 0), rows);
+  n = max(min(max(offsets[e + 1], 0), rows) - first, 0);
+}
+
+// Sum of the lanes up to this one.
+__device__ __forceinline__ int scan_lanes(int x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+struct Found {
+  int e, first, rows;                                // the expert and its rows
+  int at;                                            // which of its pieces
+};
+
+// The experts' rows in pieces of PIECE, one expert after the other; false past the last
+// piece.  Every lane of the wave must call it, with the same `at`.
+template <int PIECE>
+__device__ __forceinline__ bool find_piece(const int32_t *offsets, int groups, int rows, int at, Found &f) {
+  const int lane = threadIdx.x & 63;
+  for (int e0 = 0; e0 < groups; e0 += 64) {
+    int first, n;
+    rows_of(offsets, groups, rows, e0 + lane, first, n);
+    const int mine = (n + PIECE - 1) / PIECE, upto = scan_lanes(mine, lane);
+    const uint64_t past = __ballot(upto > at);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      f.e = e0 + l;
+      f.first = __builtin_amdgcn_readlane(first, l);
+      f.rows = __builtin_amdgcn_readlane(n, l);
+      f.at = at - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(mine, l));
+      return true;
+    }
+    at -= __builtin_amdgcn_readlane(upto, 63);
+  }
+  return false;
+}
+
+// All pieces.
+template <int PIECE>
+__device__ __forceinline__ int count_pieces(const int32_t *offsets, int groups, int rows) {
+  const int lane = threadIdx.x & 63;
+  int total = 0;
+  for (int e0 = 0; e0 < groups; e0 += 64) {
+    int first, n;
+    rows_of(offsets, groups, rows, e0 + lane, first, n);
+    total += __builtin_amdgcn_readlane(scan_lanes((n + PIECE - 1) / PIECE, lane), 63);
+  }
+  return total;
+}
+
+// A workgroup's tile: XCD i % 8 takes one contiguous eighth of an order that goes through the
+// experts, and through each one's tiles in strips of 4 along its rows, so the workgroups an
+// XCD runs at once share an expert's panels.
+template <int TM>
+__device__ __forceinline__ bool find_tile(const GemmGrouped &g, int tiles_n, Found &f, int &tn) {
+  const int total = count_pieces<TM>(g.offsets, g.groups, (int)g.p.m) * tiles_n;
+  const int id = blockIdx.x, q = total >> 3, rem = total & 7, x = id & 7;
+  if (id >= total) return false;
+  const int pos = x * q + min(x, rem) + (id >> 3);
+  // tiles_n tiles to each of an expert's row pieces, taken strip by strip
+  if (!find_piece<TM>(g.offsets, g.groups, (int)g.p.m, pos / tiles_n, f)) return false;
+  const int tiles_m = (f.rows + TM - 1) / TM, in = pos - (pos / tiles_n - f.at) * tiles_n;
+  const int strip = in / (4 * tiles_n), rest = in - strip * 4 * tiles_n, h = min(4, tiles_m - 4 * strip);
+  tn = rest / h;
+  f.at = 4 * strip + rest - tn * h;
+  return true;
+}
+
+// The expert's part of the operands.
+__device__ __forceinline__ void take_rows(GemmMx &p, const GemmMx &a, const Found &f, bool nn) {
+  p.m = f.rows;
+  p.a = a.a + f.first * a.k;
+  p.as = a.as + f.first * (a.k >> 5);
+  const int64_t block = a.lb == SSHDP_SCALE_BLOCK32X32 ? 1024 : 32;
+  p.b = a.b + f.e * (a.n * a.k);
+  p.bs = a.bs + f.e * (a.n * a.k / block);
+}
+
+// silu(gate) * up, to about 2^-21 of itself.
+__device__ __forceinline__ float swiglu(float gate, float up) {
+  return gate * __builtin_amdgcn_rcpf(1.f + __expf(-gate)) * up;
+}
+
+// A gated tile's end.  A wave holds its columns' gates in the first half of its n fragments
+// and their ups in the second, so the activation needs no exchange, and a block of 32 columns
+// is two fragments of the four lanes that share a row.
+template <class C>
+__device__ __forceinline__ void finish_gated(const GemmGrouped &g, const GemmMx &p, char *smem, int64_t n0, int64_t m0, int first,
+                                             int wn, int wm, int t, const f32x4_t (&acc)[C::FP][C::FQ]) {
+  constexpr int HP = C::FP / 2, FQ = C::FQ, HN = C::TN / 2, WN2 = HN / C::WN;   // columns of a tile, of a wave
+  const int r = t & 15, gq = t >> 4 & 3;
+  if (g.gate) {
+    // gates in the tile's first half of columns, ups in the second
+    uint16_t *lt = reinterpret_cast<uint16_t *>(smem);
+    constexpr int LP = C::TN + 8, CH = C::TN / 8;
+#pragma unroll
+    for (int i = 0; i < C::FP; ++i)
+#pragma unroll
+      for (int j = 0; j < FQ; ++j) {
+        const f32x4_t &v = acc[i][j];
+        const int c = (i < HP ? 0 : HN) + wn * WN2 + 16 * (i % HP) + 4 * gq;
+        *reinterpret_cast<uint2 *>(lt + (wm * (C::TM / C::WM) + 16 * j + r) * LP + c) =
+            make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
+      }
+    __syncthreads();
+    for (int id = t; id < C::TM * CH; id += C::NT) {
+      const int row = id / CH, c = (id - row * CH) * 8, cc = c & (HN - 1);
+      if (m0 + row >= p.m || n0 + cc >= p.n) continue;      // whole chunks: n is a multiple of 32
+      const u32x4_t v = *reinterpret_cast<const u32x4_t *>(lt + row * LP + c);
+      uint16_t *o = (c < HN ? g.gate : g.up) + (first + m0 + row) * p.n + n0 + cc;
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t *>(o));
+    }
+    __syncthreads();
+  }
+  if (!g.codes) return;
+  // codes and scales of the tile in LDS, then 16 codes and a row's scales a lane
+  constexpr int CP = HN + 16, SB = HN / 32;
+  uint8_t *lc = reinterpret_cast<uint8_t *>(smem), *ls = lc + C::TM * CP;
+#pragma unroll
+  for (int j = 0; j < FQ; ++j)
+#pragma unroll
+    for (int b = 0; b < HP / 2; ++b) {
+      float h[8];
+      uint32_t a = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        h[k] = swiglu(acc[2 * b + (k >> 2)][j][k & 3], acc[HP + 2 * b + (k >> 2)][j][k & 3]);
+        a = max(a, __float_as_uint(h[k]) & 0x7FFFFFFFu);
+      }
+      a = max(a, (uint32_t)__shfl_xor((int)a, 16));
+      a = max(a, (uint32_t)__shfl_xor((int)a, 32));
+      const uint32_t sb = mx_scale_byte(a);
+      const u32x2_t c = mx_encode8(h, sb);
+      const int row = wm * (C::TM / C::WM) + 16 * j + r, col = wn * WN2 + 32 * b;
+      *reinterpret_cast<uint32_t *>(lc + row * CP + col + 4 * gq) = c[0];
+      *reinterpret_cast<uint32_t *>(lc + row * CP + col + 16 + 4 * gq) = c[1];
+      if (gq == 0) ls[row * SB + (col >> 5)] = (uint8_t)sb;
+    }
+  __syncthreads();
+  for (int id = t; id < C::TM * (HN / 16); id += C::NT) {
+    const int row = id / (HN / 16), c = (id - row * (HN / 16)) * 16;
+    if (m0 + row >= p.m || n0 + c >= p.n) continue;
+    *reinterpret_cast<u32x4_t *>(g.codes + (first + m0 + row) * p.n + n0 + c) =
+        *reinterpret_cast<const u32x4_t *>(lc + row * CP + c);
+  }
+  for (int id = t; id < C::TM * SB; id += C::NT) {
+    const int row = id / SB, b = id - row * SB;
+    if (m0 + row < p.m && n0 + 32 * b < p.n)
+      g.scales[(first + m0 + row) * (p.n >> 5) + (n0 >> 5) + b] = ls[id];
+  }
+}
+
+// bfloat16 addend into a tile's sums, 4 columns of a row a lane; rows past the end read the
+// last one's.
+template <class C>
+__device__ __forceinline__ void add_bf16(const GemmMx &p, const uint16_t *addend, int64_t n0, int64_t m0, int wn, int wm, int t,
+                                         f32x4_t (&acc)[C::FP][C::FQ]) {
+  const int64_t mw = m0 + wm * (C::TM / C::WM) + (t & 15), nw = n0 + wn * (C::TN / C::WN) + 4 * (t >> 4 & 3);
+#pragma unroll
+  for (int j = 0; j < C::FQ; ++j) {
+    const uint16_t *row = addend + min(mw + 16 * j, p.m - 1) * p.ld;
+#pragma unroll
+    for (int i = 0; i < C::FP; ++i) {
+      const int64_t n = nw + 16 * i;
+      if (n + 4 <= p.n) {
+        const u32x2e_t w = *reinterpret_cast<const u32x2e_t *>(row + n);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][j][k] += __uint_as_float(k & 1 ? w[k >> 1] & 0xFFFF0000u : w[k >> 1] << 16);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (n + k < p.n) acc[i][j][k] += __uint_as_float((uint32_t)row[n + k] << 16);
+      }
+    }
+  }
+}
+
+template <class C, bool NN, bool SHORT, Form F>
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C::WPS))) void k_group8(GemmGrouped g, int tiles_n) {
+  __shared__ __align__(1024) char smem[C::LDS];
+  Found f;
+  int tn;
+  if (!find_tile<C::TM>(g, tiles_n, f, tn)) return;
+  GemmPart p;
+  static_cast<GemmMx &>(p) = g.p;
+  take_rows(p, g.p, f, NN);
+  if (F == kGated) {
+    p.b2 = g.b2 + (p.b - g.p.b);
+    p.b2s = g.b2s + (p.bs - g.p.bs);
+  }
+  const int64_t n0 = (int64_t)tn * (F == kGated ? C::TN / 2 : C::TN), m0 = (int64_t)f.at * C::TM;
+  const Loader<C, NN, F> ld(p, n0, m0, 0, (int)((p.k + kRowB - 1) / kRowB));
+  const int wn = ld.wave / C::WM, wm = ld.wave % C::WM;
+  f32x4_t acc[C::FP][C::FQ];
+  sums8<C, NN, SHORT>(ld, smem, acc);
+  __syncthreads();
+  int t_end = threadIdx.x;
+  asm volatile("" : "+v"(t_end));
+  if constexpr (F == kGated) {
+    finish_gated<C>(g, p, smem, n0, m0, f.first, wn, wm, t_end, acc);
+  } else {
+    const int64_t out = f.first * p.ld;
+    p.out = static_cast<uint16_t *>(p.out) + out;
+    if (g.addend16) add_bf16<C>(p, g.addend16 + out, n0, m0, wn, wm, t_end, acc);
+    store_tile_bf16<C>(p, smem, n0, m0, wn, wm, t_end, acc);
+  }
+}
+
+template <class C, bool NN, bool SHORT>
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C::WPS))) void k_group16(GemmGrouped g, int tiles_n) {
+  __shared__ __align__(1024) char smem[C::LDS];
+  Found f;
+  int tn;
+  if (!find_tile<C::TM>(g, tiles_n, f, tn)) return;
+  GemmMx p = g.p;
+  take_rows(p, g.p, f, NN);
+  const int64_t n0 = (int64_t)tn * C::TN, m0 = (int64_t)f.at * C::TM;
+  const Loader<C, NN> ld(p, n0, m0, 0, (int)((p.k + kRowB - 1) / kRowB));
+  const int wn = ld.wave / C::WM, wm = ld.wave % C::WM;
+  f32x4_t acc[C::FP][C::FQ];
+  sums16<C, NN, SHORT>(ld, smem, acc);
+  int t_end = threadIdx.x;
+  asm volatile("" : "+v"(t_end));
+  const int64_t out = f.first * p.ld;
+  p.out = static_cast<float *>(p.out) + out;
+  if (p.addend) p.addend += out;
+  store_tile_f32<C>(p, n0, m0, wn, wm, t_end, acc);
+}
+
+// Weight gradients: expert e's tile of A^T B over its rows, which both operands have along
+// their columns.  An expert without rows leaves its addend, or zeros.
+template <class C>
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C::WPS))) void k_group_columns(GemmGrouped g, int tiles_m,
+                                                                                            int tiles_n) {
+  __shared__ __align__(1024) char smem[C::LDS];
+  const int tiles = tiles_m * tiles_n, total = tiles * g.groups, q = total >> 3, rem = total & 7, x = blockIdx.x & 7;
+  const int pos = x * q + min(x, rem) + ((int)blockIdx.x >> 3), e = pos / tiles, in = pos - e * tiles;
+  const int strip = in / (4 * tiles_n), rest = in - strip * 4 * tiles_n, h = min(4, tiles_m - 4 * strip);
+  const int64_t n0 = (int64_t)(rest / h) * C::TN, m0 = (int64_t)(4 * strip + rest % h) * C::TM;
+  int first, n;
+  rows_of(g.offsets, g.groups, (int)g.p.k, e, first, n);
+  GemmPart p;
+  static_cast<GemmMx &>(p) = g.p;
+  p.pitch = g.p.k;
+  p.start = first & ~31;
+  p.k = n & ~31;
+  const int64_t out = e * p.m * p.ld;
+  p.out = static_cast<float *>(p.out) + out;
+  if (p.addend) p.addend += out;
+  f32x4_t acc[C::FP][C::FQ];
+  int wn, wm;
+  if (p.k) {
+    const Loader<C, false, kRange> ld(p, n0, m0, 0, (int)((p.k + kRowB - 1) / kRowB));
+    wn = ld.wave / C::WM;
+    wm = ld.wave % C::WM;
+    sums16<C, false, false>(ld, smem, acc);
+  } else {
+    if (p.addend == p.out) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    wn = wave / C::WM;
+    wm = wave % C::WM;
+#pragma unroll
+    for (int i = 0; i < C::FP; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FQ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+  int t_end = threadIdx.x;
+  asm volatile("" : "+v"(t_end));
+  store_tile_f32<C>(p, n0, m0, wn, wm, t_end, acc);
+}
+
+constexpr int kTile = 128;
+
+int tile_cols(const GemmGrouped &g) { return g.form == kRowsGated ? kTile / 2 : kTile; }
+
+template <class C, bool NN, Form F>
+hipError_t group_rows(const GemmGrouped &g, hipStream_t s) {
+  const int tn = (int)((g.p.n + tile_cols(g) - 1) / tile_cols(g));
+  const dim3 grid((unsigned)gemm_grouped_tiles(g)), block(C::NT);
+  auto launch = [&](auto sh) {
+    constexpr bool SHORT = decltype(sh)::value;
+    if constexpr (F == kGated) {
+      hipLaunchKernelGGL((k_group8<C, NN, SHORT, F>), grid, block, 0, s, g, tn);
+    } else {
+      if (g.bf16) hipLaunchKernelGGL((k_group8<C, NN, SHORT, F>), grid, block, 0, s, g, tn);
+      else hipLaunchKernelGGL((k_group16<C, NN, SHORT>), grid, block, 0, s, g, tn);
+    }
+  };
+  if (gemm_short(g.p.k)) launch(std::true_type{});
+  else launch(std::false_type{});
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t gemm_grouped_tiles(const GemmGrouped &g) {
+  const int64_t tn = (g.p.n + tile_cols(g) - 1) / tile_cols(g);
+  if (g.form == kColumns) return g.groups * ((g.p.m + kTile - 1) / kTile) * tn;
+  // no more experts than rows have any
+  return (g.p.m / kTile + std::min<int64_t>(g.groups, g.p.m)) * tn;
+}
+
+hipError_t launch_gemm_grouped(const GemmGrouped &g, hipStream_t s) {
+  switch (g.form) {
+    case kRowsNT: return group_rows<T128, false, kWhole>(g, s);
+    case kRowsNN: return group_rows<T128, true, kWhole>(g, s);
+    case kRowsGated: return group_rows<T128, false, kGated>(g, s);
+    default: break;
+  }
+  const int tm = (int)((g.p.m + kTile - 1) / kTile), tn = (int)((g.p.n + kTile - 1) / kTile);
+  hipLaunchKernelGGL((k_group_columns<T128>), dim3((unsigned)gemm_grouped_tiles(g)), dim3(T128::NT), 0, s, g, tm, tn);
+  return hipGetLastError();
+}
+
+}  // namespace sshdp

@@ -318,39 +318,11 @@ __global__ __launch_bounds__(C::NT * C::KG) __attribute__((amdgpu_waves_per_eu(C
   // the lane again, so that nothing of it is kept in registers over the loop
   int t_end = threadIdx.x;
   asm volatile("" : "+v"(t_end));
-  const int r_end = t_end & 15, g_end = t_end >> 4 & 3;
   if (parts) {
     store_part<C>(p, parts, n0, m0, wn, wm, t_end & 63, acc);
     return;
   }
-  // bfloat16 tile through LDS (rows m), then whole rows of 16-byte stores
-  uint16_t *lt = reinterpret_cast<uint16_t *>(smem);
-  constexpr int LP = C::TN + 8;
-#pragma unroll
-  for (int i = 0; i < FP; ++i)
-#pragma unroll
-    for (int j = 0; j < FQ; ++j) {
-      const f32x4_t &v = acc[i][j];
-      uint2 *d = reinterpret_cast<uint2 *>(lt + (wm * (C::TM / C::WM) + 16 * j + r_end) * LP + wn * (C::TN / C::WN) + 16 * i + 4 * g_end);
-      *d = make_uint2(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]));
-    }
-  __syncthreads();
-  uint16_t *out = static_cast<uint16_t *>(p.out);
-  constexpr int CH = C::TN / 8;
-  for (int id = t_end; id < C::TM * CH; id += C::NT) {
-    const int row = id / CH, c = (id - row * CH) * 8;
-    const int64_t m = m0 + row, n = n0 + c;
-    if (m >= p.m || n >= p.n) continue;
-    const u32x4_t v = *reinterpret_cast<const u32x4_t *>(lt + row * LP + c);
-    uint16_t *o = out + m * p.ld + n;
-    if (n + 8 <= p.n) {
-      __builtin_nontemporal_store(v, reinterpret_cast<u32x4e_t *>(o));
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (n + k < p.n) o[k] = (uint16_t)(v[k >> 1] >> (16 * (k & 1)));
-    }
-  }
+  store_tile_bf16<C>(p, smem, n0, m0, wn, wm, t_end, acc);
 }
 
 // Float32 output: the same tiles, stages and scale words, with operands converted to
@@ -384,38 +356,11 @@ __global__ __launch_bounds__(C::NT * C::KG) __attribute__((amdgpu_waves_per_eu(C
   // the lane again, so that nothing of it is kept in registers over the loop
   int t_end = threadIdx.x;
   asm volatile("" : "+v"(t_end));
-  const int r_end = t_end & 15, g_end = t_end >> 4 & 3;
   if (parts) {
     store_part<C>(p, parts, n0, m0, wn, wm, t_end & 63, acc);
     return;
   }
-  float *out = static_cast<float *>(p.out);
-  const int64_t mw = m0 + wm * (C::TM / C::WM) + r_end, nw = n0 + wn * (C::TN / C::WN) + 4 * g_end;
-  if (n0 + C::TN <= p.n) {
-    // 16-byte words all inside: one row block's addend words in flight together (rows past
-    // the end read the last one)
-#pragma unroll
-    for (int j = 0; j < FQ; ++j) {
-      const int64_t m = mw + 16 * j, e = m * p.ld + nw;
-      if (p.addend) {
-        const float *ad = p.addend + min(m, p.m - 1) * p.ld + nw;
-        f32x4_t v[FP];
-#pragma unroll
-        for (int i = 0; i < FP; ++i) v[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4e_t *>(ad + 16 * i));
-#pragma unroll
-        for (int i = 0; i < FP; ++i) acc[i][j] += v[i];
-      }
-      if (m < p.m) {
-#pragma unroll
-        for (int i = 0; i < FP; ++i) *reinterpret_cast<f32x4e_t *>(out + e + 16 * i) = acc[i][j];
-      }
-    }
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < FQ; ++j)
-#pragma unroll
-    for (int i = 0; i < FP; ++i) store_f32(p, out, mw + 16 * j, nw + 16 * i, acc[i][j]);
+  store_tile_f32<C>(p, n0, m0, wn, wm, t_end, acc);
 }
 
 template <class C, bool NN>

@@ -24,4 +24,21 @@ hipError_t launch_moe_gather(const sshdp_moe_gather &a, hipStream_t s);
 hipError_t launch_moe_combine(const sshdp_moe_combine_args &a, hipStream_t s);
 hipError_t launch_moe_dweights(const sshdp_moe_combine_grad &a, hipStream_t s);
 
+// Products grouped by expert (k_gemm_grouped.hip).  rows: all of A's (ROWS_*), n and k as in
+// GemmMx, those of one expert's product.
+enum GroupForm { kRowsNT, kRowsNN, kRowsGated, kColumns };
+struct GemmGrouped {
+  GroupForm form;
+  bool bf16;                          // output type
+  GemmMx p;                           // m: rows of A; kColumns: k is all rows, m and n of one expert
+  const uint8_t *b2, *b2s;            // kRowsGated
+  uint16_t *gate, *up;                // kRowsGated, or NULL
+  uint8_t *codes, *scales;            // kRowsGated, or NULL
+  const uint16_t *addend16;           // bfloat16 output
+  const int32_t *offsets;             // NULL: one group of all rows
+  int32_t groups;
+};
+int64_t gemm_grouped_tiles(const GemmGrouped &g);    // workgroups at most
+hipError_t launch_gemm_grouped(const GemmGrouped &g, hipStream_t s);
+
 }  // namespace sshdp

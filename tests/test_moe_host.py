@@ -160,3 +160,63 @@ def test_combine_gradient_formulas_against_differences():
     x, g = rng.standard_normal((tokens, cols)).astype(np.float32), rng.standard_normal((rows, cols))
     lx = np.sum(M.gather(x, w, source, offsets, top_k).astype(np.float64) * g)
     assert abs(lx - np.sum(x * M.combine(g, place, w, None, top_k, "fp32")[0])) <= 1e-5 * np.sum(np.abs(x)) * 4
+
+
+def _m(rows, cols, layout="rowmajor", codes=P):
+    return sh.mx_matrix(codes, P, rows, cols, layout)
+
+
+def test_grouped_product_refusals():
+    def q(a=None, b=None, out=P, offsets=P, groups=4, op="nt", **k):
+        a = a or _m(8, 64)
+        b = b or _m(4 * 64, 64, "block32x32")
+        return lambda: sh.gemm_mxfp8_grouped(a, b, out, offsets, groups, op=op, **{**dict(out_dtype="fp32"), **k})
+    refused("ARG", q(op="tt"))
+    refused("ARG", q(out_dtype="fp16"))
+    refused("ARG", q(out=None))
+    refused("ARG", q(offsets=None))
+    refused("ARG", q(groups=0))
+    refused("ARG", q(a=_m(8, 64, codes=None)))
+    refused("ARG", q(a=_m(8, 64, "other")))
+    refused("SCHEMA", q(groups=1025, b=_m(1025 * 32, 64)))
+    refused("SCHEMA", q(groups=3))                     # no equal parts
+    refused("SCHEMA", q(groups=8, b=_m(8 * 16, 64, "block32x32")))
+    refused("SCHEMA", q(a=_m(32, 64, "block32x32")))
+    refused("SCHEMA", q(a=_m(8, 96)))
+    refused("SCHEMA", q(a=_m(8, 0), b=_m(256, 0)))
+    refused("SCHEMA", q(a=_m(8, (1 << 22) + 32), b=_m(4, (1 << 22) + 32)))
+    refused("SCHEMA", q(ld_out=63))
+    refused("SCHEMA", q(op="nn", b=_m(256, 64)))
+    refused("SCHEMA", q(op="nn", a=_m(8, 32), b=_m(128, 96, "block32x32")))    # experts of three blocks
+    refused("SCHEMA", q(a=_m(1 << 30, 64), b=_m(4 * 4096, 64)))                # too many tiles
+    t = dict(op="tn", a=_m(40, 128), b=_m(64, 128))
+    refused("ARG", q(**{**t, "out_dtype": "bf16"}))
+    refused("SCHEMA", q(**{**t, "a": _m(40, 160), "b": _m(64, 160)}))
+    refused("SCHEMA", q(**{**t, "a": _m(40, 256)}))
+    refused("SCHEMA", q(**{**t, "b": _m(64, 128, "block32x32")}))
+    refused("ALIGN", q(out=P + 4))
+    refused("ALIGN", q(addend=P + 4))
+    refused("ALIGN", q(offsets=P + 2))
+    refused("ALIGN", q(a=_m(8, 64, codes=P + 8)))
+    q(a=_m(0, 64), out=None)()                         # nothing to do
+
+
+def test_gated_product_refusals():
+    def q(a=None, g=None, u=None, codes=P, scales=P, offsets=P, groups=4, **k):
+        g = g or _m(4 * 64, 64, "block32x32")
+        u = u or _m(4 * 64, 64, "block32x32")
+        return lambda: sh.gemm_mxfp8_swiglu(a or _m(8, 64), g, u, codes, scales, offsets=offsets, groups=groups, **k)
+    refused("ARG", q(codes=None))
+    refused("ARG", q(codes=None, scales=None))         # no output
+    refused("ARG", q(gate=P))
+    refused("ARG", q(offsets=None))
+    refused("ARG", q(u=_m(4 * 64, 64, "other")))
+    refused("SCHEMA", q(u=_m(4 * 32, 64, "block32x32")))
+    refused("SCHEMA", q(u=_m(4 * 64, 64)))
+    refused("SCHEMA", q(u=_m(4 * 64, 96, "block32x32")))
+    refused("SCHEMA", q(g=_m(4 * 40, 64), u=_m(4 * 40, 64)))
+    refused("SCHEMA", q(a=_m(8, 96)))
+    for k in ("codes", "gate", "up"):
+        refused("ALIGN", q(**{**dict(gate=P, up=P), k: P + 8}))
+    refused("ALIGN", q(u=_m(4 * 64, 64, "block32x32", codes=P + 8)))
+    q(a=_m(0, 64), codes=None, scales=None)()
