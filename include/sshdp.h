@@ -649,6 +649,31 @@ int sshdp_gemm_mxfp8_swiglu(const sshdp_mx_matrix *a, const sshdp_mx_matrix *gat
                             const int32_t *offsets, int32_t groups, uint8_t *codes, uint8_t *scales, void *gate,
                             void *up, void *stream);
 
+/* The gated activation's gradient, with G behind: from gate and up (bfloat16, as
+ * sshdp_gemm_mxfp8_swiglu leaves them) and dh, the gradient of h,
+ *   s = 1 / (1 + exp(-gate)):  dgate = dh * up * s * (1 + gate * (1 - s)),
+ *   dup = dh * gate * s,  and h = gate * s * up once more,
+ * each in float32 (dgate within 2^-20 of dh up s (1 + |gate|), the others of
+ * themselves) and then G along the rows, along the columns (pitch `rows`, a multiple
+ * of 32 rows; zeros past a block's last row in use), or both: the operands of the two
+ * input gradients, of the weight gradients, and h along the tokens for the next
+ * projection's.  dh, gate and up are dense rows x cols.  Rows from offsets[groups]
+ * on (offsets NULL: none) are neither read nor written.  Without dgate and dup, dh is
+ * not read and may be NULL: the activation alone, of products kept in bfloat16.
+ * s counts as 0 for gate under -87.
+ * Errors: ARG (null gate or up, dh missing, no output, half a pair, negative size,
+ * groups < 1 with offsets), SCHEMA (cols not a multiple of 32, rows not one with an
+ * output along columns, an edge over 2^30, groups over 1024), ALIGN (all but the
+ * scales; offsets 4); HIP. */
+typedef struct {
+  const void *dh, *gate, *up;
+  const int32_t *offsets;
+  sshdp_mx_out dgate, dup, h;
+  int64_t rows, cols;
+  int32_t groups, pad_;
+} sshdp_swiglu_grad;
+int sshdp_swiglu_backward_mxfp8(const sshdp_swiglu_grad *args, void *stream);
+
 /* Diagnostics.  The batched NT contraction used by Newton-Schulz, exposed to
  * test it alone: for b < batch, O[b] = bf16(alpha * P[b] Q[b]^T + beta * D[b])
  * with P[b] M x K, Q[b] N x K, O[b] M x N (bf16, row-major, dense, batch strides

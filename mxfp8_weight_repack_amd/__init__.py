@@ -11,6 +11,6 @@ from ._lib import (  # noqa: F401
     grad_workspace, grad_sumsq, grad_clip, grad_clip_norm, quant_mxfp8,
     rmsnorm_mxfp8, rmsnorm_backward, rmsnorm_backward_workspace, mx_matrix, gemm_mxfp8, gemm_mxfp8_workspace,
     mx_pair, moe_rows, moe_sort, moe_sort_workspace, moe_gather_mxfp8, moe_combine, moe_combine_backward,
-    gemm_mxfp8_grouped, gemm_mxfp8_swiglu,
+    gemm_mxfp8_grouped, gemm_mxfp8_swiglu, swiglu_backward_mxfp8,
     update_step, update_step_noalloc, gemm_bf16_nt, lib, PROF_CLASSES, ERROR_NAMES, NOALLOC_SCRATCH_BYTES,
 )

@@ -139,6 +139,12 @@ class MoeCombineGrad(ctypes.Structure):
                 ("pad_", ctypes.c_int32)]
 
 
+class SwigluGrad(ctypes.Structure):
+    _fields_ = [("dh", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("up", ctypes.c_void_p),
+                ("offsets", ctypes.c_void_p), ("dgate", MxOut), ("dup", MxOut), ("h", MxOut), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("groups", ctypes.c_int32), ("pad_", ctypes.c_int32)]
+
+
 # every symbol include/sshdp.h declares, with its argument and return types
 _P = ctypes.c_void_p
 SIGNATURES = {
@@ -196,6 +202,7 @@ SIGNATURES = {
                                   ctypes.c_int32, _P, _P, ctypes.c_int32, ctypes.c_int64, _P], ctypes.c_int),
     "sshdp_gemm_mxfp8_swiglu": ([ctypes.POINTER(MxMatrix), ctypes.POINTER(MxMatrix), ctypes.POINTER(MxMatrix), _P,
                                  ctypes.c_int32, _P, _P, _P, _P, _P], ctypes.c_int),
+    "sshdp_swiglu_backward_mxfp8": ([ctypes.POINTER(SwigluGrad), _P], ctypes.c_int),
     "sshdp_ns_executed": ([_P, _P, ctypes.c_size_t, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_double),
                            _P], ctypes.c_int),
     "sshdp_profile_enable": ([_P, ctypes.c_int32], ctypes.c_int),
@@ -564,6 +571,13 @@ def gemm_mxfp8_swiglu(a, gate_w, up_w, codes=None, scales=None, offsets=None, gr
     _check(lib().sshdp_gemm_mxfp8_swiglu(ctypes.byref(a), ctypes.byref(gate_w), ctypes.byref(up_w), _ptr(offsets), groups,
                                          _ptr(codes), _ptr(scales), _ptr(gate), _ptr(up), _stream(stream)),
            "sshdp_gemm_mxfp8_swiglu")
+
+
+def swiglu_backward_mxfp8(dh, gate, up, rows, cols, offsets=None, groups=1, dgate=None, dup=None, h=None, stream=None):
+    """The gradients of gate and up, and h = silu(gate) * up again, as MXFP8 (mx_pair outputs, None for none)."""
+    a = SwigluGrad(_ptr(dh), _ptr(gate), _ptr(up), _ptr(offsets), dgate or MxOut(), dup or MxOut(), h or MxOut(), rows,
+                   cols, groups, 0)
+    _check(lib().sshdp_swiglu_backward_mxfp8(ctypes.byref(a), _stream(stream)), "sshdp_swiglu_backward_mxfp8")
 
 
 def _ref(x):

@@ -239,4 +239,30 @@ int sshdp_gemm_mxfp8_swiglu(const sshdp_mx_matrix *a, const sshdp_mx_matrix *gat
   return hip_status(launch_gemm_grouped(g, static_cast<hipStream_t>(stream)));
 }
 
+int sshdp_swiglu_backward_mxfp8(const sshdp_swiglu_grad *a, void *stream) {
+  if (!a || a->rows < 0 || a->cols < 0) return SSHDP_ERR_ARG;
+  const sshdp_mx_out *outs[] = {&a->dgate, &a->dup, &a->h};
+  bool columns = false;
+  for (const sshdp_mx_out *o : outs) {
+    if (half_pair(*o)) return SSHDP_ERR_ARG;
+    columns = columns || o->codes_t;
+  }
+  if (a->offsets) {
+    const int st = check_groups(a->offsets, a->groups);
+    if (st != SSHDP_OK) return st;
+  }
+  if (a->cols % 32 || a->cols > kMaxEdge || a->rows > kMaxEdge || (columns && a->rows % 32)) return SSHDP_ERR_SCHEMA;
+  if (a->rows == 0 || a->cols == 0) return SSHDP_OK;
+  const bool grads = any(a->dgate) || any(a->dup);
+  if (!a->gate || !a->up || (grads && !a->dh) || (!grads && !any(a->h))) return SSHDP_ERR_ARG;
+  if (!aligned16(a->dh) || !aligned16(a->gate) || !aligned16(a->up) || !aligned4(a->offsets)) return SSHDP_ERR_ALIGN;
+  for (const sshdp_mx_out *o : outs)
+    if (!aligned16(o->codes) || !aligned16(o->codes_t)) return SSHDP_ERR_ALIGN;
+  int st = check_device(a->dh, a->gate, a->up, a->offsets);
+  for (const sshdp_mx_out *o : outs)
+    if (st == SSHDP_OK) st = check_device(o->codes, o->scales, o->codes_t, o->scales_t);
+  if (st != SSHDP_OK) return st;
+  return hip_status(launch_swiglu_grad(*a, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

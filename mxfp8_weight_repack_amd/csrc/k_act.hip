@@ -1,0 +1,152 @@
+// k_act.hip -- the gated activation and its gradient, with G along the rows, along the
+// columns, or both.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "act.h"
+#include "moe.h"
+#include "mx_rows.h"
+
+namespace sshdp {
+namespace {
+
+// One element's results: the gradients of gate and up, and the activation.
+struct Act {
+  float dg, du, h;
+};
+__device__ __forceinline__ Act act_grad(float dh, float g, float u) {
+  const float s = sigmoid(g), silu = g * s;
+  return {dh * u * fmaf(silu, 1.f - s, s), dh * silu, silu * u};
+}
+
+// Rows in use, whatever the offsets hold.
+__device__ __forceinline__ int64_t rows_in_use(const sshdp_swiglu_grad &a) {
+  return a.offsets ? min((int64_t)max(a.offsets[a.groups], 0), a.rows) : a.rows;
+}
+
+__device__ __forceinline__ void put_rows(const sshdp_mx_out &o, const float (&v)[8], int64_t e, bool in, int lane) {
+  if (!o.codes) return;
+  const uint32_t sb = mx_scale_byte(mx_amax4(v));
+  if (!in) return;
+  *reinterpret_cast<u32x2_t *>(o.codes + e) = mx_encode8(v, sb);
+  if ((lane & 3) == 0) o.scales[e >> 5] = (uint8_t)sb;
+}
+
+__device__ __forceinline__ void put_column(const sshdp_mx_out &o, const float (&v)[32], int64_t e) {
+  if (!o.codes_t) return;
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  const uint32_t sb = mx_scale_byte(m);
+  u32x4r_t w[2];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    w[j >> 2][j & 3] = mx_encode4(make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]), sb);
+  u32x4r_t *d = reinterpret_cast<u32x4r_t *>(o.codes_t + e);
+  d[0] = w[0];
+  d[1] = w[1];
+  o.scales_t[e >> 5] = (uint8_t)sb;
+}
+
+// Along the rows alone: 8 elements a lane.
+__global__ __launch_bounds__(256) void k_act_rows(sshdp_swiglu_grad a) {
+  const int64_t runs = rows_in_use(a) * (a.cols >> 3);   // a multiple of 4: a block's lanes leave together
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < runs; i += (int64_t)gridDim.x * 256) {
+    float d[8] = {}, g[8], u[8], dg[8], du[8], h[8];
+    if (a.dh) unpack8<true>(load8<true>(a.dh, i * 8), d);
+    unpack8<true>(load8<true>(a.gate, i * 8), g);
+    unpack8<true>(load8<true>(a.up, i * 8), u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const Act r = act_grad(d[j], g[j], u[j]);
+      dg[j] = r.dg;
+      du[j] = r.du;
+      h[j] = r.h;
+    }
+    put_rows(a.dgate, dg, i * 8, true, threadIdx.x);
+    put_rows(a.dup, du, i * 8, true, threadIdx.x);
+    put_rows(a.h, h, i * 8, true, threadIdx.x);
+  }
+}
+
+constexpr int kActRows = 128, kActCols = 64;         // tile of one workgroup
+
+// Columns too: a tile of the three inputs goes to LDS as it is; on the way a lane takes 8
+// elements of a row (4 lanes a block), afterwards a lane 32 rows of one column, from LDS, and
+// computes them again.
+__global__ __launch_bounds__(256) void k_act_tiles(sshdp_swiglu_grad a, int tiles_c) {
+  __shared__ __align__(16) uint16_t sm[3][kActRows][kActCols];
+  const int t = threadIdx.x;
+  const int64_t tr = blockIdx.x / tiles_c, r0 = tr * kActRows, c0 = (blockIdx.x - tr * tiles_c) * (int64_t)kActCols;
+  const int64_t used = rows_in_use(a);
+  if (r0 >= used) return;
+  const int lc = (t & 7) * 8, lr = t >> 3;
+  const bool in_c = c0 + lc < a.cols;
+  const void *src[3] = {a.dh, a.gate, a.up};
+  Raw8<true> raw[kActRows / 32][3];
+#pragma unroll
+  for (int p = 0; p < kActRows / 32; ++p)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int64_t r = r0 + lr + 32 * p;
+      raw[p][k] = Raw8<true>{};
+      if (in_c && r < used && src[k]) raw[p][k] = load8<true>(src[k], r * a.cols + c0 + lc);
+    }
+#pragma unroll
+  for (int p = 0; p < kActRows / 32; ++p) {
+    const int rr = lr + 32 * p;
+    float d[8], g[8], u[8], dg[8], du[8], h[8];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) *reinterpret_cast<Raw8<true> *>(&sm[k][rr][lc]) = raw[p][k];
+    unpack8<true>(raw[p][0], d);
+    unpack8<true>(raw[p][1], g);
+    unpack8<true>(raw[p][2], u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const Act r = act_grad(d[j], g[j], u[j]);
+      dg[j] = r.dg;
+      du[j] = r.du;
+      h[j] = r.h;
+    }
+    const int64_t e = (r0 + rr) * a.cols + c0 + lc;
+    const bool in = in_c && r0 + rr < used;
+    put_rows(a.dgate, dg, e, in, t);
+    put_rows(a.dup, du, e, in, t);
+    put_rows(a.h, h, e, in, t);
+  }
+  __syncthreads();
+  const int grp = t & 3, c = t >> 2;
+  const int64_t r = r0 + 32 * grp;
+  if (c0 + c >= a.cols || r >= used) return;
+  float dg[32], du[32], h[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    float v[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) v[k] = __uint_as_float((uint32_t)sm[k][32 * grp + j][c] << 16);
+    const Act x = act_grad(v[0], v[1], v[2]);
+    dg[j] = x.dg;
+    du[j] = x.du;
+    h[j] = x.h;
+  }
+  const int64_t e = (c0 + c) * a.rows + r;
+  put_column(a.dgate, dg, e);
+  put_column(a.dup, du, e);
+  put_column(a.h, h, e);
+}
+
+}  // namespace
+
+hipError_t launch_swiglu_grad(const sshdp_swiglu_grad &a, hipStream_t s) {
+  if (a.dgate.codes_t || a.dup.codes_t || a.h.codes_t) {
+    const int64_t tc = (a.cols + kActCols - 1) / kActCols, tr = (a.rows + kActRows - 1) / kActRows;
+    hipLaunchKernelGGL(k_act_tiles, dim3((unsigned)(tr * tc)), dim3(256), 0, s, a, (int)tc);
+  } else {
+    const int64_t runs = a.rows * (a.cols / 8);
+    hipLaunchKernelGGL(k_act_rows, dim3((unsigned)std::min<int64_t>((runs + 255) / 256, 1 << 20)), dim3(256), 0, s, a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace sshdp

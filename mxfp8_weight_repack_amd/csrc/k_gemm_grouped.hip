@@ -10,6 +10,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "act.h"
 #include "gemm_mx.h"
 #include "moe.h"
 #include "mx_rows.h"
@@ -107,11 +108,6 @@ __device__ __forceinline__ void take_rows(GemmMx &p, const GemmMx &a, const Foun
   const int64_t block = a.lb == SSHDP_SCALE_BLOCK32X32 ? 1024 : 32;
   p.b = a.b + f.e * (a.n * a.k);
   p.bs = a.bs + f.e * (a.n * a.k / block);
-}
-
-// silu(gate) * up, to about 2^-21 of itself.
-__device__ __forceinline__ float swiglu(float gate, float up) {
-  return gate * __builtin_amdgcn_rcpf(1.f + __expf(-gate)) * up;
 }
 
 // A gated tile's end.  A wave holds its columns' gates in the first half of its n fragments

@@ -1,4 +1,4 @@
-// moe.h -- launchers of the expert layer's operators (k_moe.hip).
+// moe.h -- launchers of the expert layer's operators.
 #pragma once
 #include "internal.h"
 
@@ -8,7 +8,7 @@ constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxTopK = 64;
 constexpr int64_t kMoeMaxSlots = 1 << 24;
 
-// Slots sorted by expert.  counts: moe_sort_counts(slots, experts) ints of workspace.
+// Slots sorted by expert (k_moe.hip).  counts: moe_sort_counts(slots, experts) ints of workspace.
 struct MoeSort {
   const void *ids;
   int64_t slots, rows;
@@ -23,6 +23,9 @@ hipError_t launch_moe_sort(const MoeSort &a, int32_t *counts, hipStream_t s);
 hipError_t launch_moe_gather(const sshdp_moe_gather &a, hipStream_t s);
 hipError_t launch_moe_combine(const sshdp_moe_combine_args &a, hipStream_t s);
 hipError_t launch_moe_dweights(const sshdp_moe_combine_grad &a, hipStream_t s);
+
+// The gated activation and its gradient (k_act.hip): sshdp_swiglu_grad's fields.
+hipError_t launch_swiglu_grad(const sshdp_swiglu_grad &a, hipStream_t s);
 
 // Products grouped by expert (k_gemm_grouped.hip).  rows: all of A's (ROWS_*), n and k as in
 // GemmMx, those of one expert's product.

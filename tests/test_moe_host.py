@@ -220,3 +220,38 @@ def test_gated_product_refusals():
         refused("ALIGN", q(**{**dict(gate=P, up=P), k: P + 8}))
     refused("ALIGN", q(u=_m(4 * 64, 64, "block32x32", codes=P + 8)))
     q(a=_m(0, 64), codes=None, scales=None)()
+
+
+def test_activation_gradient_refusals():
+    r, c = sh.mx_pair(P, P), sh.mx_pair(P, P, P, P)
+
+    def q(dh=P, gate=P, up=P, rows=32, cols=64, **k):
+        return lambda: sh.swiglu_backward_mxfp8(dh, gate, up, rows, cols, **{**dict(dgate=r, dup=r), **k})
+    refused("ARG", q(rows=-1))
+    refused("ARG", q(dgate=None, dup=None))            # no output
+    for k in ("dh", "gate", "up"):
+        refused("ARG", q(**{k: None}))
+        refused("ALIGN", q(**{k: P + 8}))
+    refused("ARG", q(h=sh.mx_pair(P)))
+    refused("ARG", q(h=sh.mx_pair(None, None, None, P)))
+    refused("ARG", q(offsets=P, groups=0))
+    refused("SCHEMA", q(offsets=P, groups=1025))
+    refused("SCHEMA", q(cols=40))
+    refused("SCHEMA", q(rows=33, dup=c))
+    refused("SCHEMA", q(rows=(1 << 30) + 32))
+    refused("ALIGN", q(offsets=P + 2))
+    refused("ALIGN", q(dup=sh.mx_pair(P + 8, P)))
+    refused("ALIGN", q(h=sh.mx_pair(None, None, P + 8, P)))
+    q(rows=0, dh=None, gate=None, up=None)()
+    q(cols=0)()
+
+
+def test_activation_gradient_formula_against_differences():
+    rng = np.random.default_rng(1)
+    g, u, d = rng.standard_normal(400) * 4, rng.standard_normal(400), rng.standard_normal(400)
+    f = lambda g_, u_: d * g_ / (1 + np.exp(-g_)) * u_   # noqa: E731
+    s, h = 1 / (1 + np.exp(-g)), 1e-5
+    dg, du = d * u * s * (1 + g * (1 - s)), d * g * s
+    # central differences of a function whose third derivative is under 1: off by h^2, and 1e-16 / h of rounding
+    assert np.all(np.abs((f(g + h, u) - f(g - h, u)) / (2 * h) - dg) <= 1e-9 * (1 + np.abs(d * u)) * (1 + np.abs(g)))
+    assert np.all(np.abs((f(g, u + h) - f(g, u - h)) / (2 * h) - du) <= 1e-9 * (1 + np.abs(d * g)) * (1 + np.abs(u)))
