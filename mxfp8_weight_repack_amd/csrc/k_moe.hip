@@ -4,9 +4,10 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "moe.h"
-#include "mx_rows.h"
+#include "mx_encode.h"
 
 namespace sshdp {
 namespace {
@@ -157,15 +158,9 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_place(const I *ids, int64_
 
 // ---------------------------------------------------------------------- rows gathered
 
-// The token and weight of a sorted row; false for padding.
-__device__ __forceinline__ bool row_of(const sshdp_moe_gather &a, int64_t p, int64_t &token, float &w) {
-  const int slot = a.source[p];
-  token = 0;
-  w = 0.f;
-  if (slot < 0 || slot >= a.tokens * a.top_k) return false;
-  token = slot / a.top_k;
-  w = a.weights ? a.weights[slot] : 1.f;
-  return true;
+// The token of slot `slot`, -1 for padding.
+__device__ __forceinline__ int token_of(const sshdp_moe_gather &a, int slot) {
+  return slot >= 0 && slot < a.tokens * a.top_k ? (int)((uint32_t)slot / (uint32_t)a.top_k) : -1;
 }
 
 // Rows in use, whatever the offsets hold.
@@ -173,106 +168,163 @@ __device__ __forceinline__ int64_t rows_in_use(const sshdp_moe_gather &a) {
   return min((int64_t)max(a.offsets[a.experts], 0), a.rows);
 }
 
-// Along the rows: 8 elements a lane, 4 lanes a block, as k_quant_rows.
-template <bool BF16>
-__global__ __launch_bounds__(256) void k_moe_rows(sshdp_moe_gather a, int runs_per_row) {
-  const int64_t runs = rows_in_use(a) * runs_per_row;  // a multiple of 4: a block's lanes leave together
-  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < runs; i += (int64_t)gridDim.x * 256) {
-    const int64_t p = i / runs_per_row;
-    int64_t token;
-    float w, v[8];
-    Raw8<BF16> raw{};
-    if (row_of(a, p, token, w)) raw = load8<BF16>(a.x, token * a.ld_x + (i - p * runs_per_row) * 8);
-    unpack8<BF16>(raw, v);
+constexpr int kMrRuns = 4;                           // runs of 8 elements a lane has in flight
+
+// Along the rows: 8 elements a lane and 4 lanes a block, 1024 consecutive runs of all rows a
+// workgroup.  A run waits for its row's source and then for the token: four of them together.
+template <bool BF16, bool WEIGHTED>
+__global__ __launch_bounds__(256) void k_moe_rows(sshdp_moe_gather a, uint32_t runs_per_row) {
+  const int64_t used = rows_in_use(a), first = blockIdx.x * (int64_t)(256 * kMrRuns), row0 = first / runs_per_row;
+  const uint32_t rem = (uint32_t)(first - row0 * runs_per_row);
+  int64_t row[kMrRuns];
+  uint32_t run[kMrRuns];
+  int slot[kMrRuns];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= w;
-    if (a.y) store8<BF16>(a.y, i * 8, pack8<BF16>(v));
-    if (a.out.codes) {
-      const uint32_t sb = mx_scale_byte(mx_amax4(v));
-      *reinterpret_cast<u32x2_t *>(a.out.codes + i * 8) = mx_encode8(v, sb);
-      if ((i & 3) == 0) a.out.scales[i >> 2] = (uint8_t)sb;
+  for (int u = 0; u < kMrRuns; ++u) {
+    const uint32_t x = rem + u * 256 + threadIdx.x, q = x / runs_per_row;
+    row[u] = row0 + q;
+    run[u] = x - q * runs_per_row;
+    slot[u] = row[u] < a.rows ? a.source[row[u]] : -1;
+  }
+  Raw8<BF16> raw[kMrRuns];
+  float w[kMrRuns];
+#pragma unroll
+  for (int u = 0; u < kMrRuns; ++u) {
+    const int token = token_of(a, slot[u]);
+    raw[u] = Raw8<BF16>{};
+    w[u] = 0.f;
+    if (token >= 0) {
+      if (WEIGHTED) w[u] = a.weights[slot[u]];
+      raw[u] = load8<BF16>(a.x, token * a.ld_x + run[u] * 8);
     }
+  }
+#pragma unroll
+  for (int u = 0; u < kMrRuns; ++u) {
+    const int64_t e = row[u] * runs_per_row + run[u];   // blocks are whole in or out: 4 runs each
+    const bool in = row[u] < used;
+    float v[8];
+    if (WEIGHTED) {
+      unpack8<BF16>(raw[u], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= w[u];
+      if (a.y && in) store8<BF16>(a.y, e * 8, pack8<BF16>(v));
+    } else if (a.y && in) {
+      store8<BF16>(a.y, e * 8, raw[u]);
+    }
+    if (!a.out.codes) continue;
+    uint32_t sb;
+    const u32x2_t c = WEIGHTED ? mx_codes4(v, sb) : mx_codes4_raw<BF16>(raw[u], sb);
+    if (!in) continue;
+    *reinterpret_cast<u32x2_t *>(a.out.codes + e * 8) = c;
+    if ((threadIdx.x & 3) == 0) a.out.scales[e >> 2] = (uint8_t)sb;
   }
 }
 
 constexpr int kMtRows = 128, kMtCols = 128;          // tile of one workgroup
+constexpr int64_t kMtLeast = 1024;                   // fewer leave CUs without work
 
-// Both ways, or along the columns: the tile of k_quant_tiles (LDS columns rotated by the row
-// group, a lane two columns' 32 rows), its rows fetched by `source`, the weights beside them.
-template <bool BF16>
-__global__ __launch_bounds__(256) void k_moe_tiles(sshdp_moe_gather a, int tiles_c) {
-  constexpr int ES = BF16 ? 2 : 4, ROT = BF16 ? 32 : 16;
+// Tiles, where there are enough of them or columns are wanted: the tile of k_quant_tiles (LDS
+// columns rotated by the row group, a lane two columns' 32 rows), its rows fetched by `source`,
+// their weights beside them.  A token is read once for each of its choices, by rows far apart:
+// XCD i % 8 takes a contiguous eighth of the tiles column by column, so that what it reads of x
+// at one time, 128 columns of all tokens, stays in its L2 (26624 x 2048 bfloat16 of 4093 tokens,
+// rows tile by tile instead: both ways 46 against 31 us).
+template <bool BF16, bool WEIGHTED>
+__global__ __launch_bounds__(256) void k_moe_tiles(sshdp_moe_gather a, uint32_t tiles_r, uint32_t tiles) {
+  constexpr int ES = BF16 ? 2 : 4, ROT = BF16 ? 32 : 16, NP = kMtRows / 16;
   __shared__ __align__(16) char sm[kMtRows * kMtCols * ES];
-  __shared__ float sw[kMtRows];
+  __shared__ float sw[WEIGHTED ? kMtRows : 1];
   const int t = threadIdx.x;
-  const int64_t tr = blockIdx.x / tiles_c, r0 = tr * kMtRows, c0 = (blockIdx.x - tr * tiles_c) * (int64_t)kMtCols;
-  const int64_t used = rows_in_use(a);
-  if (r0 >= used) return;
+  const uint32_t xcd = blockIdx.x & 7, pos = xcd * (tiles >> 3) + min(xcd, tiles & 7) + (blockIdx.x >> 3);
+  const int64_t r0 = pos % tiles_r * (int64_t)kMtRows, c0 = pos / tiles_r * (int64_t)kMtCols;
   const int lc = (t & 15) * 8, lr = t >> 4;
   const bool in_c = c0 + lc < a.cols;
-  Raw8<BF16> raw[kMtRows / 16];
-  float w[kMtRows / 16];
+  int slot[NP];
 #pragma unroll
-  for (int p = 0; p < kMtRows / 16; ++p) {
+  for (int p = 0; p < NP; ++p) {
     const int64_t r = r0 + lr + 16 * p;
-    int64_t token;
+    slot[p] = r < a.rows ? a.source[r] : -1;
+  }
+  const int64_t used = rows_in_use(a);
+  if (r0 >= used) return;
+  Raw8<BF16> raw[NP];
+  float w[NP];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int token = r0 + lr + 16 * p < used ? token_of(a, slot[p]) : -1;
     raw[p] = Raw8<BF16>{};
     w[p] = 0.f;
-    if (r < used && row_of(a, r, token, w[p]) && in_c) raw[p] = load8<BF16>(a.x, token * a.ld_x + c0 + lc);
-  }
-#pragma unroll
-  for (int p = 0; p < kMtRows / 16; ++p) {
-    const int rr = lr + 16 * p;
-    *reinterpret_cast<Raw8<BF16> *>(sm + (rr * kMtCols + (lc ^ ((rr >> 5) * ROT))) * ES) = raw[p];
-    if (lc == 0) sw[rr] = w[p];
-    float v[8];
-    unpack8<BF16>(raw[p], v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= w[p];
-    const uint32_t sb = mx_scale_byte(mx_amax4(v));
-    if (in_c && r0 + rr < used) {
-      const int64_t e = (r0 + rr) * a.cols + c0 + lc;
-      if (a.y) store8<BF16>(a.y, e, pack8<BF16>(v));
-      if (a.out.codes) {
-        *reinterpret_cast<u32x2_t *>(a.out.codes + e) = mx_encode8(v, sb);
-        if ((t & 3) == 0) a.out.scales[e >> 5] = (uint8_t)sb;
-      }
+    if (token >= 0) {
+      if (WEIGHTED) w[p] = a.weights[slot[p]];
+      if (in_c) raw[p] = load8<BF16>(a.x, token * a.ld_x + c0 + lc);
     }
   }
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int rr = lr + 16 * p;
+    if (a.out.codes_t) {
+      *reinterpret_cast<Raw8<BF16> *>(sm + (rr * kMtCols + (lc ^ ((rr >> 5) * ROT))) * ES) = raw[p];
+      if (WEIGHTED && lc == 0) sw[rr] = w[p];
+    }
+    const bool in = in_c && r0 + rr < used;
+    const int64_t e = (r0 + rr) * a.cols + c0 + lc;
+    float v[8];
+    if (WEIGHTED) {
+      unpack8<BF16>(raw[p], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= w[p];
+      if (a.y && in) store8<BF16>(a.y, e, pack8<BF16>(v));
+    } else if (a.y && in) {
+      store8<BF16>(a.y, e, raw[p]);
+    }
+    if (!a.out.codes) continue;
+    uint32_t sb;
+    const u32x2_t x = WEIGHTED ? mx_codes4(v, sb) : mx_codes4_raw<BF16>(raw[p], sb);
+    if (!in) continue;
+    __builtin_nontemporal_store(x, reinterpret_cast<u32x2_t *>(a.out.codes + e));
+    if ((t & 3) == 0) a.out.scales[e >> 5] = (uint8_t)sb;
+  }
+  if (!a.out.codes_t) return;
   __syncthreads();
   const int grp = t & 3, c = (t >> 2) * 2;
   const int64_t r = r0 + 32 * grp;
   if (c0 + c >= a.cols || r >= used) return;
   const char *q = sm + (32 * grp * kMtCols + (c ^ (grp * ROT))) * ES;
-  float v[2][32];
-  uint32_t m[2] = {0, 0};
+  MxColumn o[2];
+  if constexpr (BF16 && !WEIGHTED) {
+    uint32_t x[32];
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const float wj = sw[32 * grp + j];
-    if (BF16) {
-      const uint32_t x = *reinterpret_cast<const uint32_t *>(q + j * kMtCols * ES);
-      v[0][j] = __uint_as_float(x << 16) * wj;
-      v[1][j] = __uint_as_float(x & 0xFFFF0000u) * wj;
-    } else {
-      const float2 x = *reinterpret_cast<const float2 *>(q + j * kMtCols * ES);
-      v[0][j] = x.x * wj;
-      v[1][j] = x.y * wj;
+    for (int j = 0; j < 32; ++j) x[j] = *reinterpret_cast<const uint32_t *>(q + j * kMtCols * ES);
+    mx_columns_bf16(x, o);
+  } else {
+    float v[2][32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      if (BF16) {
+        const uint32_t x = *reinterpret_cast<const uint32_t *>(q + j * kMtCols * ES);
+        v[0][j] = __uint_as_float(x << 16);
+        v[1][j] = __uint_as_float(x & 0xFFFF0000u);
+      } else {
+        const float2 x = *reinterpret_cast<const float2 *>(q + j * kMtCols * ES);
+        v[0][j] = x.x;
+        v[1][j] = x.y;
+      }
+      if (WEIGHTED) {
+        const float wj = sw[32 * grp + j];
+        v[0][j] *= wj;
+        v[1][j] *= wj;
+      }
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) m[h] = max(m[h], __float_as_uint(v[h][j]) & 0x7FFFFFFFu);
+    o[0] = mx_column(v[0]);
+    o[1] = mx_column(v[1]);
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t sb = mx_scale_byte(m[h]);
-    u32x4r_t o[2];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      o[j >> 2][j & 3] = mx_encode4(make_float4(v[h][4 * j], v[h][4 * j + 1], v[h][4 * j + 2], v[h][4 * j + 3]), sb);
     const int64_t e = (c0 + c + h) * a.rows + r;
     u32x4r_t *d = reinterpret_cast<u32x4r_t *>(a.out.codes_t + e);
-    d[0] = o[0];
-    d[1] = o[1];
-    a.out.scales_t[e >> 5] = (uint8_t)sb;
+    __builtin_nontemporal_store(o[h].codes[0], d);
+    __builtin_nontemporal_store(o[h].codes[1], d + 1);
+    a.out.scales_t[e >> 5] = (uint8_t)o[h].scale;
   }
 }
 
@@ -323,31 +375,38 @@ __global__ __launch_bounds__(256) void k_moe_combine(sshdp_moe_combine_args a, i
   }
 }
 
-// The weights' gradient: a wave per token, 512 columns at a time.
+// The weights' gradient: a wave per token, 512 columns at a time, its choices' rows in flight
+// together.
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_moe_dweights(sshdp_moe_combine_grad a) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = blockIdx.x * (int64_t)4 + (threadIdx.x >> 6);
+  const int64_t t = blockIdx.x * (int64_t)4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (t >= a.tokens) return;
   for (int j0 = 0; j0 < a.top_k; j0 += kCombineAt) {
     int p[kCombineAt];
     float sum[kCombineAt] = {};
 #pragma unroll
     for (int j = 0; j < kCombineAt; ++j) {
-      p[j] = j0 + j < a.top_k ? a.place[t * a.top_k + j0 + j] : -1;
+      p[j] = j0 + j < a.top_k ? __builtin_amdgcn_readfirstlane(a.place[t * a.top_k + j0 + j]) : -1;
       if (p[j] >= a.rows) p[j] = -1;
     }
     for (int64_t c = lane * 8; c < a.cols; c += 512) {
+      const Raw8<BF16> rd = load8<BF16>(a.dout, t * a.ld_dout + c);
+      Raw8<BF16> ry[kCombineAt];
+#pragma unroll
+      for (int j = 0; j < kCombineAt; ++j) {
+        ry[j] = Raw8<BF16>{};
+        if (p[j] >= 0) ry[j] = load8<BF16>(a.y, p[j] * a.cols + c);
+      }
       float d[8];
-      unpack8<BF16>(load8<BF16>(a.dout, t * a.ld_dout + c), d);
+      unpack8<BF16>(rd, d);
 #pragma unroll
-      for (int j = 0; j < kCombineAt; ++j)
-        if (p[j] >= 0) {
-          float v[8];
-          unpack8<BF16>(load8<BF16>(a.y, p[j] * a.cols + c), v);
+      for (int j = 0; j < kCombineAt; ++j) {
+        float v[8];
+        unpack8<BF16>(ry[j], v);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) sum[j] = fmaf(d[k], v[k], sum[j]);
-        }
+        for (int k = 0; k < 8; ++k) sum[j] = p[j] >= 0 ? fmaf(d[k], v[k], sum[j]) : 0.f;
+      }
     }
 #pragma unroll
     for (int j = 0; j < kCombineAt; ++j) {
@@ -388,18 +447,22 @@ hipError_t launch_moe_sort(const MoeSort &a, int32_t *counts, hipStream_t s) {
 }
 
 hipError_t launch_moe_gather(const sshdp_moe_gather &a, hipStream_t s) {
+  auto run = [&](auto bf16, auto weighted) {
+    constexpr bool B = decltype(bf16)::value, W = decltype(weighted)::value;
+    const int64_t tr = (a.rows + kMtRows - 1) / kMtRows, tiles = tr * ((a.cols + kMtCols - 1) / kMtCols);
+    if (a.out.codes_t || tiles >= kMtLeast) {
+      hipLaunchKernelGGL((k_moe_tiles<B, W>), dim3((unsigned)tiles), dim3(256), 0, s, a, (uint32_t)tr, (uint32_t)tiles);
+    } else {
+      const int64_t runs = a.rows * (a.cols / 8), each = 256 * kMrRuns;
+      hipLaunchKernelGGL((k_moe_rows<B, W>), dim3((unsigned)((runs + each - 1) / each)), dim3(256), 0, s, a,
+                         (uint32_t)(a.cols / 8));
+    }
+  };
   const bool bf16 = a.dtype == SSHDP_DTYPE_BF16;
-  const dim3 block(256);
-  if (a.out.codes_t) {
-    const int64_t tc = (a.cols + kMtCols - 1) / kMtCols, tr = (a.rows + kMtRows - 1) / kMtRows;
-    const dim3 grid((unsigned)(tr * tc));
-    if (bf16) hipLaunchKernelGGL((k_moe_tiles<true>), grid, block, 0, s, a, (int)tc);
-    else hipLaunchKernelGGL((k_moe_tiles<false>), grid, block, 0, s, a, (int)tc);
-  } else {
-    const int runs = (int)(a.cols / 8);
-    if (bf16) hipLaunchKernelGGL((k_moe_rows<true>), run_grid(a.rows * runs), block, 0, s, a, runs);
-    else hipLaunchKernelGGL((k_moe_rows<false>), run_grid(a.rows * runs), block, 0, s, a, runs);
-  }
+  if (bf16 && a.weights) run(std::true_type{}, std::true_type{});
+  else if (bf16) run(std::true_type{}, std::false_type{});
+  else if (a.weights) run(std::false_type{}, std::true_type{});
+  else run(std::false_type{}, std::false_type{});
   return hipGetLastError();
 }
 

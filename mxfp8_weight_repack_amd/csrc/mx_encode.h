@@ -1,0 +1,104 @@
+// mx_encode.h -- G of values in registers by the scaled conversions of gfx950, which divide by the
+// scale on the way (one instruction for two codes; compared with ldexp and the plain conversion
+// on every bfloat16 and 2^24 float32 values under each of the 255 scales: the same codes).
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include "mx_rows.h"
+
+namespace sshdp {
+
+typedef short i16x2_t __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+
+// 4 codes of float32 values; `scale` has the block's exponent.
+__device__ __forceinline__ uint32_t mx_cvt4(float a, float b, float c, float d, float scale) {
+  i16x2_t o = {0, 0};
+  o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, a, b, scale, false);
+  o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, c, d, scale, true);
+  return __builtin_bit_cast(uint32_t, o);
+}
+
+// 4 codes of two words of bfloat16 pairs.
+__device__ __forceinline__ uint32_t mx_cvt4_bf16(uint32_t p, uint32_t q, float scale) {
+  i16x2_t o = {0, 0};
+  o = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(o, __builtin_bit_cast(bf16x2r_t, p), scale, false);
+  o = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(o, __builtin_bit_cast(bf16x2r_t, q), scale, true);
+  return __builtin_bit_cast(uint32_t, o);
+}
+
+__device__ __forceinline__ float mx_scale_float(uint32_t sb) { return __uint_as_float(sb << 23); }
+
+// Codes in a block holding NaN or infinity are all 0x7F.
+__device__ __forceinline__ uint32_t mx_or_nan(uint32_t codes, uint32_t sb) { return sb == 0xFFu ? 0x7F7F7F7Fu : codes; }
+
+// A lane's 8 codes and its block's scale byte, 4 aligned lanes a block.  Every lane of the
+// wave must call it.
+__device__ __forceinline__ u32x2_t mx_codes4(const float (&v)[8], uint32_t &sb) {
+  sb = mx_scale_byte(mx_amax4(v));
+  const float s = mx_scale_float(sb);
+  return u32x2_t{mx_or_nan(mx_cvt4(v[0], v[1], v[2], v[3], s), sb), mx_or_nan(mx_cvt4(v[4], v[5], v[6], v[7], s), sb)};
+}
+
+// The larger magnitudes of two words of bfloat16 pairs, half by half (`m` has no signs).
+__device__ __forceinline__ uint32_t mx_max_bf16(uint32_t m, uint32_t w) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, m),
+                                                                __builtin_bit_cast(u16x2_t, w & 0x7FFF7FFFu)));
+}
+
+// The same of 8 elements as loaded.
+template <bool BF16>
+__device__ __forceinline__ u32x2_t mx_codes4_raw(const Raw8<BF16> &r, uint32_t &sb) {
+  if constexpr (BF16) {
+    uint32_t m = mx_max_bf16(mx_max_bf16(mx_max_bf16(r.w[0] & 0x7FFF7FFFu, r.w[1]), r.w[2]), r.w[3]);
+    uint32_t a = max(m << 16, m & 0xFFFF0000u);
+    a = max(a, (uint32_t)__shfl_xor((int)a, 1));
+    a = max(a, (uint32_t)__shfl_xor((int)a, 2));
+    sb = mx_scale_byte(a);
+    const float s = mx_scale_float(sb);
+    return u32x2_t{mx_or_nan(mx_cvt4_bf16(r.w[0], r.w[1], s), sb), mx_or_nan(mx_cvt4_bf16(r.w[2], r.w[3], s), sb)};
+  } else {
+    float v[8];
+    unpack8<BF16>(r, v);
+    return mx_codes4(v, sb);
+  }
+}
+
+// One block's 32 codes that a lane holds alone.
+struct MxColumn {
+  u32x4r_t codes[2];
+  uint32_t scale;
+};
+
+__device__ __forceinline__ MxColumn mx_column(const float (&v)[32]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  MxColumn o;
+  o.scale = mx_scale_byte(m);
+  const float s = mx_scale_float(o.scale);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    o.codes[j >> 2][j & 3] = mx_or_nan(mx_cvt4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], s), o.scale);
+  return o;
+}
+
+// Two neighbouring columns' blocks, a word the two columns' bfloat16 of a row.
+__device__ __forceinline__ void mx_columns_bf16(const uint32_t (&x)[32], MxColumn (&o)[2]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) m = mx_max_bf16(m, x[j]);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    o[h].scale = mx_scale_byte(h ? m & 0xFFFF0000u : m << 16);
+    const float s = mx_scale_float(o[h].scale);
+    const uint32_t pick = h ? 0x07060302u : 0x05040100u;     // rows j and j + 1 of one column
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t p = __builtin_amdgcn_perm(x[4 * j + 1], x[4 * j], pick), q = __builtin_amdgcn_perm(x[4 * j + 3], x[4 * j + 2], pick);
+      o[h].codes[j >> 2][j & 3] = mx_or_nan(mx_cvt4_bf16(p, q, s), o[h].scale);
+    }
+  }
+}
+
+}  // namespace sshdp
