@@ -6,7 +6,7 @@
 
 #include "act.h"
 #include "moe.h"
-#include "mx_rows.h"
+#include "mx_encode.h"
 
 namespace sshdp {
 namespace {
@@ -27,26 +27,20 @@ __device__ __forceinline__ int64_t rows_in_use(const sshdp_swiglu_grad &a) {
 
 __device__ __forceinline__ void put_rows(const sshdp_mx_out &o, const float (&v)[8], int64_t e, bool in, int lane) {
   if (!o.codes) return;
-  const uint32_t sb = mx_scale_byte(mx_amax4(v));
+  uint32_t sb;
+  const u32x2_t c = mx_codes4(v, sb);
   if (!in) return;
-  *reinterpret_cast<u32x2_t *>(o.codes + e) = mx_encode8(v, sb);
+  *reinterpret_cast<u32x2_t *>(o.codes + e) = c;
   if ((lane & 3) == 0) o.scales[e >> 5] = (uint8_t)sb;
 }
 
 __device__ __forceinline__ void put_column(const sshdp_mx_out &o, const float (&v)[32], int64_t e) {
   if (!o.codes_t) return;
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 32; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-  const uint32_t sb = mx_scale_byte(m);
-  u32x4r_t w[2];
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    w[j >> 2][j & 3] = mx_encode4(make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]), sb);
+  const MxColumn c = mx_column(v);
   u32x4r_t *d = reinterpret_cast<u32x4r_t *>(o.codes_t + e);
-  d[0] = w[0];
-  d[1] = w[1];
-  o.scales_t[e >> 5] = (uint8_t)sb;
+  d[0] = c.codes[0];
+  d[1] = c.codes[1];
+  o.scales_t[e >> 5] = (uint8_t)c.scale;
 }
 
 // Along the rows alone: 8 elements a lane.

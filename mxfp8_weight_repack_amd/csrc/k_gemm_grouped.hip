@@ -8,12 +8,13 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cstdlib>
 #include <type_traits>
 
 #include "act.h"
 #include "gemm_mx.h"
 #include "moe.h"
-#include "mx_rows.h"
+#include "mx_encode.h"
 
 namespace sshdp {
 namespace {
@@ -31,13 +32,14 @@ __device__ __forceinline__ void rows_of(const int32_t *offsets, int groups, int 
   n = max(min(max(offsets[e + 1], 0), rows) - first, 0);
 }
 
-// Sum of the lanes up to this one.
-__device__ __forceinline__ int scan_lanes(int x, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(x, d);
-    if (lane >= d) x += y;
-  }
+// Sum of the lanes up to this one, within rows of 16 and then from row to row.
+__device__ __forceinline__ int scan_lanes(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);      // row_shr 1, 2, 4, 8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);      // row_bcast 15: rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);      // row_bcast 31: rows 2 and 3
   return x;
 }
 
@@ -54,7 +56,7 @@ __device__ __forceinline__ bool find_piece(const int32_t *offsets, int groups, i
   for (int e0 = 0; e0 < groups; e0 += 64) {
     int first, n;
     rows_of(offsets, groups, rows, e0 + lane, first, n);
-    const int mine = (n + PIECE - 1) / PIECE, upto = scan_lanes(mine, lane);
+    const int mine = (n + PIECE - 1) / PIECE, upto = scan_lanes(mine);
     const uint64_t past = __ballot(upto > at);
     if (past) {
       const int l = __builtin_ctzll(past);
@@ -77,7 +79,7 @@ __device__ __forceinline__ int count_pieces(const int32_t *offsets, int groups, 
   for (int e0 = 0; e0 < groups; e0 += 64) {
     int first, n;
     rows_of(offsets, groups, rows, e0 + lane, first, n);
-    total += __builtin_amdgcn_readlane(scan_lanes((n + PIECE - 1) / PIECE, lane), 63);
+    total += __builtin_amdgcn_readlane(scan_lanes((n + PIECE - 1) / PIECE), 63);
   }
   return total;
 }
@@ -156,10 +158,12 @@ __device__ __forceinline__ void finish_gated(const GemmGrouped &g, const GemmMx 
         h[k] = swiglu(acc[2 * b + (k >> 2)][j][k & 3], acc[HP + 2 * b + (k >> 2)][j][k & 3]);
         a = max(a, __float_as_uint(h[k]) & 0x7FFFFFFFu);
       }
-      a = max(a, (uint32_t)__shfl_xor((int)a, 16));
-      a = max(a, (uint32_t)__shfl_xor((int)a, 32));
-      const uint32_t sb = mx_scale_byte(a);
-      const u32x2_t c = mx_encode8(h, sb);
+      const auto x = __builtin_amdgcn_permlane16_swap(a, a, false, false);   // the lanes 16 apart
+      a = max(x[0], x[1]);
+      const auto y = __builtin_amdgcn_permlane32_swap(a, a, false, false);   // and 32
+      const uint32_t sb = mx_scale_byte(max(y[0], y[1]));
+      const float sf = mx_scale_float(sb);
+      const uint32_t c[2] = {mx_or_nan(mx_cvt4(h[0], h[1], h[2], h[3], sf), sb), mx_or_nan(mx_cvt4(h[4], h[5], h[6], h[7], sf), sb)};
       const int row = wm * (C::TM / C::WM) + 16 * j + r, col = wn * WN2 + 32 * b;
       *reinterpret_cast<uint32_t *>(lc + row * CP + col + 4 * gq) = c[0];
       *reinterpret_cast<uint32_t *>(lc + row * CP + col + 16 + 4 * gq) = c[1];
@@ -298,14 +302,26 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
   store_tile_f32<C>(p, n0, m0, wn, wm, t_end, acc);
 }
 
-constexpr int kTile = 128;
+// Tile edge: 
+int tile_of_rows(const GemmGrouped &g) {
+  static const int force = getenv("SSHDP_TILE") ? atoi(getenv("SSHDP_TILE")) : 0;
+  return force ? force : 128;
+}
 
-int tile_cols(const GemmGrouped &g) { return g.form == kRowsGated ? kTile / 2 : kTile; }
+int tile_cols(const GemmGrouped &g, int tile) { return g.form == kRowsGated ? tile / 2 : tile; }
+
+int64_t tiles_of(const GemmGrouped &g, int tile) {
+  const int cols = tile_cols(g, tile);
+  const int64_t tn = (g.p.n + cols - 1) / cols;
+  if (g.form == kColumns) return g.groups * ((g.p.m + tile - 1) / tile) * tn;
+  // no more experts than rows have any
+  return (g.p.m / tile + std::min<int64_t>(g.groups, g.p.m)) * tn;
+}
 
 template <class C, bool NN, Form F>
 hipError_t group_rows(const GemmGrouped &g, hipStream_t s) {
-  const int tn = (int)((g.p.n + tile_cols(g) - 1) / tile_cols(g));
-  const dim3 grid((unsigned)gemm_grouped_tiles(g)), block(C::NT);
+  const int cols = tile_cols(g, C::TM), tn = (int)((g.p.n + cols - 1) / cols);
+  const dim3 grid((unsigned)tiles_of(g, C::TM)), block(C::NT);
   auto launch = [&](auto sh) {
     constexpr bool SHORT = decltype(sh)::value;
     if constexpr (F == kGated) {
@@ -320,25 +336,25 @@ hipError_t group_rows(const GemmGrouped &g, hipStream_t s) {
   return hipGetLastError();
 }
 
-}  // namespace
-
-int64_t gemm_grouped_tiles(const GemmGrouped &g) {
-  const int64_t tn = (g.p.n + tile_cols(g) - 1) / tile_cols(g);
-  if (g.form == kColumns) return g.groups * ((g.p.m + kTile - 1) / kTile) * tn;
-  // no more experts than rows have any
-  return (g.p.m / kTile + std::min<int64_t>(g.groups, g.p.m)) * tn;
+template <class C>
+hipError_t group_columns(const GemmGrouped &g, hipStream_t s) {
+  const int tm = (int)((g.p.m + C::TM - 1) / C::TM), tn = (int)((g.p.n + C::TN - 1) / C::TN);
+  hipLaunchKernelGGL((k_group_columns<C>), dim3((unsigned)tiles_of(g, C::TM)), dim3(C::NT), 0, s, g, tm, tn);
+  return hipGetLastError();
 }
 
+}  // namespace
+
+int64_t gemm_grouped_tiles(const GemmGrouped &g) { return tiles_of(g, 128); }
+
 hipError_t launch_gemm_grouped(const GemmGrouped &g, hipStream_t s) {
+  const bool large = tile_of_rows(g) == 256;
   switch (g.form) {
-    case kRowsNT: return group_rows<T128, false, kWhole>(g, s);
-    case kRowsNN: return group_rows<T128, true, kWhole>(g, s);
-    case kRowsGated: return group_rows<T128, false, kGated>(g, s);
-    default: break;
+    case kRowsNT: return large ? group_rows<T256, false, kWhole>(g, s) : group_rows<T128, false, kWhole>(g, s);
+    case kRowsNN: return large ? group_rows<T256, true, kWhole>(g, s) : group_rows<T128, true, kWhole>(g, s);
+    case kRowsGated: return large ? group_rows<T256, false, kGated>(g, s) : group_rows<T128, false, kGated>(g, s);
+    default: return large ? group_columns<T256>(g, s) : group_columns<T128>(g, s);
   }
-  const int tm = (int)((g.p.m + kTile - 1) / kTile), tn = (int)((g.p.n + kTile - 1) / kTile);
-  hipLaunchKernelGGL((k_group_columns<T128>), dim3((unsigned)gemm_grouped_tiles(g)), dim3(T128::NT), 0, s, g, tm, tn);
-  return hipGetLastError();
 }
 
 }  // namespace sshdp

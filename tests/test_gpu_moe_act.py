@@ -10,7 +10,6 @@ from test_gpu_moe_products import check_codes, decode, stream
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-NEAR = 2.0 ** -20                                      # what the call promises of its float32 values
 TINY = 2.0 ** -118                                     # float32 ends its normal range near gates of -87
 
 
@@ -21,14 +20,22 @@ def _gpu():
     sh.lib()
 
 
+def near(g):
+    """The sigmoid's error relative to itself, and silu's and h's: the exponent x log2(e) is off by half a step of its
+    rounding and log2(e) by 2^-26.1 of itself, together 1.23 |x| 2^-24 of the exponential; then exp2 and the reciprocal
+    (a step, 2, each), the sum and two products (half a step, 1, each): 7."""
+    return (1.25 * g.abs() + 8) * 2.0 ** -24
+
+
 def formula(dh, gate, up):
-    """{name: (value, bound)} in float64."""
+    """{name: (value, bound)} in float64.  dgate's factor s + silu (1 - s) has each s off by near, 1 - s by that and a
+    rounding, in terms no larger than s (1 + |gate|); then five more roundings."""
     d, g, u = (t.double() for t in (dh, gate, up))
-    s = torch.where(g < -87, torch.zeros_like(g), torch.special.expit(g))
+    s = torch.special.expit(g)
     dg, du, h = d * u * s * (1 + g * (1 - s)), d * g * s, g * s * u
     edge = TINY * (1 + g.abs()) * (1 + d.abs()) * (1 + u.abs())
-    return {"dgate": (dg, NEAR * (d * u * s).abs() * (1 + g.abs()) + edge), "dup": (du, NEAR * du.abs() + edge),
-            "h": (h, NEAR * h.abs() + edge)}
+    return {"dgate": (dg, (2 * near(g) + 2.0 ** -22) * (d * u * s).abs() * (1 + g.abs()) + edge),
+            "dup": (du, near(g) * du.abs() + edge), "h": (h, near(g) * h.abs() + edge)}
 
 
 def call(dh, gate, up, wanted, offsets=None, groups=1):
