@@ -260,6 +260,66 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
   store_tile_f32<C>(p, n0, m0, wn, wm, t_end, acc);
 }
 
+// A tile's rows in memory's order, through LDS: 4 columns a lane, whole lines an instruction.
+// Straight from the sums' layout, 64 bytes of 16 rows an instruction, HBM gave 2.7 TB/s (64
+// gradients of 1408 x 2048 over 26624 rows: 555 us).
+template <class C>
+struct RowOrder {
+  static constexpr int LP = C::TN + 4, PER = C::NT * 4 / C::TN, N = C::TM / PER;   // rows an instruction; of them
+  static_assert(C::TM * LP * 4 <= C::LDS, "the tile fits the stages");
+  const GemmMx &p;
+  const int64_t n;
+  const int row;
+  const int64_t m0;
+
+  __device__ __forceinline__ RowOrder(const GemmMx &p_, int64_t n0, int64_t m0_, int t)
+      : p(p_), n(n0 + (t * 4) % C::TN), row(t * 4 / C::TN), m0(m0_) {}
+
+  __device__ __forceinline__ void load(const float *src, f32x4_t (&v)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int64_t m = m0 + row + i * PER;
+      v[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      if (m >= p.m || n >= p.n) continue;
+      const float *q = src + m * p.ld + n;
+      if (n + 4 <= p.n) {
+        v[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4e_t *>(q));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (n + k < p.n) v[i][k] = q[k];
+      }
+    }
+  }
+
+  // acc (in `smem` by the way) + v to the output.
+  __device__ __forceinline__ void store(char *smem, int wn, int wm, int t, const f32x4_t (&acc)[C::FP][C::FQ],
+                                        const f32x4_t (&v)[N]) const {
+    float *lt = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int j = 0; j < C::FQ; ++j)
+#pragma unroll
+      for (int i = 0; i < C::FP; ++i)
+        *reinterpret_cast<f32x4_t *>(lt + (wm * (C::TM / C::WM) + 16 * j + (t & 15)) * LP + wn * (C::TN / C::WN) + 16 * i +
+                                     4 * (t >> 4 & 3)) = acc[i][j];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int64_t m = m0 + row + i * PER;
+      if (m >= p.m || n >= p.n) continue;
+      const f32x4_t x = *reinterpret_cast<const f32x4_t *>(lt + (row + i * PER) * LP + (t * 4) % C::TN) + v[i];
+      float *o = static_cast<float *>(p.out) + m * p.ld + n;
+      if (n + 4 <= p.n) {
+        __builtin_nontemporal_store(x, reinterpret_cast<f32x4e_t *>(o));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (n + k < p.n) o[k] = x[k];
+      }
+    }
+  }
+};
+
 // Weight gradients: expert e's tile of A^T B over its rows, which both operands have along
 // their columns.  An expert without rows leaves its addend, or zeros.
 template <class C>
@@ -280,18 +340,23 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
   const int64_t out = e * p.m * p.ld;
   p.out = static_cast<float *>(p.out) + out;
   if (p.addend) p.addend += out;
+  if (!p.k && p.addend == p.out) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wn = wave / C::WM, wm = wave % C::WM;
+  // the addend is on its way while the products are made
+  const RowOrder<C> rows(p, n0, m0, threadIdx.x);
+  f32x4_t add[RowOrder<C>::N];
+  if (p.addend) {
+    rows.load(p.addend, add);
+  } else {
+#pragma unroll
+    for (int i = 0; i < RowOrder<C>::N; ++i) add[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
   f32x4_t acc[C::FP][C::FQ];
-  int wn, wm;
   if (p.k) {
     const Loader<C, false, kRange> ld(p, n0, m0, 0, (int)((p.k + kRowB - 1) / kRowB));
-    wn = ld.wave / C::WM;
-    wm = ld.wave % C::WM;
     sums16<C, false, false>(ld, smem, acc);
+    __syncthreads();
   } else {
-    if (p.addend == p.out) return;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    wn = wave / C::WM;
-    wm = wave % C::WM;
 #pragma unroll
     for (int i = 0; i < C::FP; ++i)
 #pragma unroll
@@ -299,7 +364,7 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
   }
   int t_end = threadIdx.x;
   asm volatile("" : "+v"(t_end));
-  store_tile_f32<C>(p, n0, m0, wn, wm, t_end, acc);
+  rows.store(smem, wn, wm, t_end, acc, add);
 }
 
 // Tile edge: 
@@ -353,7 +418,7 @@ hipError_t launch_gemm_grouped(const GemmGrouped &g, hipStream_t s) {
     case kRowsNT: return large ? group_rows<T256, false, kWhole>(g, s) : group_rows<T128, false, kWhole>(g, s);
     case kRowsNN: return large ? group_rows<T256, true, kWhole>(g, s) : group_rows<T128, true, kWhole>(g, s);
     case kRowsGated: return large ? group_rows<T256, false, kGated>(g, s) : group_rows<T128, false, kGated>(g, s);
-    default: return large ? group_columns<T256>(g, s) : group_columns<T128>(g, s);
+    default: return group_columns<T128>(g, s);
   }
 }
 
