@@ -662,8 +662,10 @@ __device__ __forceinline__ void sums8(const L &ld, char *smem, f32x4_t (&acc)[C:
 // matrix instructions.  A half step is one 16-byte chunk per lane (64 k): its m-side fragments
 // stay converted while the n side's pass by, one converted (8 conversions) beside the previous
 // one's 2 x FQ matrix instructions.
-template <class C, bool NN, bool SHORT, class L>
-__device__ __forceinline__ void sums16(const L &ld, char *smem, f32x4_t (&acc)[C::FP][C::FQ]) {
+// `beside` issues BESIDE other loads behind the first two stages'; the first two steps do not
+// wait for them.
+template <class C, bool NN, bool SHORT, int BESIDE = 0, class L, class B>
+__device__ __forceinline__ void sums16(const L &ld, char *smem, f32x4_t (&acc)[C::FP][C::FQ], B beside) {
   const int lane = ld.lane, wave = ld.wave, wn = wave / C::WM, wm = wave % C::WM;
   const int r = lane & 15, g = lane >> 4;
   uint32_t *ring = reinterpret_cast<uint32_t *>(smem + C::NST * C::STAGE);
@@ -731,8 +733,15 @@ __device__ __forceinline__ void sums16(const L &ld, char *smem, f32x4_t (&acc)[C
     ld.load_q(smem, st, min(st, nk - 1));
   }
   if (!SHORT) sw = ld.template scales<false>(1);
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
+  if constexpr (BESIDE > 0) {
+    __builtin_amdgcn_sched_barrier(0);
+    beside();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(BESIDE) : "memory");
+  } else {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+  }
 
   u32x4_t P[2], Q[FQ];                                // raw: the next two n-side fragments, the next half's m side
   u32x4_t pc[2][2], qc[FQ][2];                       // converted: this and the next n-side fragment, the m side
@@ -757,7 +766,8 @@ __device__ __forceinline__ void sums16(const L &ld, char *smem, f32x4_t (&acc)[C
       if (i == FP - 2) {
         if (h) {
           // this stage is read, the next has landed
-          stage_barrier<!SHORT>(phase == 0);
+          if (BESIDE > 0 && kt == 0) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");   // both stages have landed
+          else stage_barrier<!SHORT>(phase == 0);
           ld.load_p(smem, stage, min(kt + NST, nk - 1));
         }
 #pragma unroll
@@ -819,6 +829,11 @@ __device__ __forceinline__ void sums16(const L &ld, char *smem, f32x4_t (&acc)[C
     if (kt + 4 >= nk) break;
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // the trailing reloads
+}
+
+template <class C, bool NN, bool SHORT, class L>
+__device__ __forceinline__ void sums16(const L &ld, char *smem, f32x4_t (&acc)[C::FP][C::FQ]) {
+  sums16<C, NN, SHORT, 0>(ld, smem, acc, [] {});
 }
 
 // A tile as bfloat16 through LDS (rows m), then whole rows of 16-byte stores.

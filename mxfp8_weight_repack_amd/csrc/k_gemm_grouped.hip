@@ -292,9 +292,15 @@ struct RowOrder {
     }
   }
 
-  // acc (in `smem` by the way) + v to the output.
-  __device__ __forceinline__ void store(char *smem, int wn, int wm, int t, const f32x4_t (&acc)[C::FP][C::FQ],
-                                        const f32x4_t (&v)[N]) const {
+  // Of a tile that lies inside: exactly N loads.
+  __device__ __forceinline__ void load_whole(const float *src, f32x4_t (&v)[N]) const {
+    const float *q = src + (m0 + row) * p.ld + n;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4e_t *>(q + i * PER * p.ld));
+  }
+
+  // The sums to LDS, by the threads that have them; a barrier comes before store.
+  static __device__ __forceinline__ void put(char *smem, int wn, int wm, int t, const f32x4_t (&acc)[C::FP][C::FQ]) {
     float *lt = reinterpret_cast<float *>(smem);
 #pragma unroll
     for (int j = 0; j < C::FQ; ++j)
@@ -302,7 +308,11 @@ struct RowOrder {
       for (int i = 0; i < C::FP; ++i)
         *reinterpret_cast<f32x4_t *>(lt + (wm * (C::TM / C::WM) + 16 * j + (t & 15)) * LP + wn * (C::TN / C::WN) + 16 * i +
                                      4 * (t >> 4 & 3)) = acc[i][j];
-    __syncthreads();
+  }
+
+  // LDS + v to the output.
+  __device__ __forceinline__ void store(const char *smem, int t, const f32x4_t (&v)[N]) const {
+    const float *lt = reinterpret_cast<const float *>(smem);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int64_t m = m0 + row + i * PER;
@@ -320,51 +330,116 @@ struct RowOrder {
   }
 };
 
-// Weight gradients: expert e's tile of A^T B over its rows, which both operands have along
-// their columns.  An expert without rows leaves its addend, or zeros.
+// Weight gradients: tile `pos` of all experts', one expert's after the other's, each one's in
+// strips of 4 along m.
 template <class C>
-__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C::WPS))) void k_group_columns(GemmGrouped g, int tiles_m,
-                                                                                            int tiles_n) {
-  __shared__ __align__(1024) char smem[C::LDS];
-  const int tiles = tiles_m * tiles_n, total = tiles * g.groups, q = total >> 3, rem = total & 7, x = blockIdx.x & 7;
-  const int pos = x * q + min(x, rem) + ((int)blockIdx.x >> 3), e = pos / tiles, in = pos - e * tiles;
-  const int strip = in / (4 * tiles_n), rest = in - strip * 4 * tiles_n, h = min(4, tiles_m - 4 * strip);
-  const int64_t n0 = (int64_t)(rest / h) * C::TN, m0 = (int64_t)(4 * strip + rest % h) * C::TM;
-  int first, n;
-  rows_of(g.offsets, g.groups, (int)g.p.k, e, first, n);
+struct ColumnTile {
   GemmPart p;
-  static_cast<GemmMx &>(p) = g.p;
-  p.pitch = g.p.k;
-  p.start = first & ~31;
-  p.k = n & ~31;
-  const int64_t out = e * p.m * p.ld;
-  p.out = static_cast<float *>(p.out) + out;
-  if (p.addend) p.addend += out;
-  if (!p.k && p.addend == p.out) return;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wn = wave / C::WM, wm = wave % C::WM;
-  // the addend is on its way while the products are made
-  const RowOrder<C> rows(p, n0, m0, threadIdx.x);
-  f32x4_t add[RowOrder<C>::N];
-  if (p.addend) {
-    rows.load(p.addend, add);
-  } else {
-#pragma unroll
-    for (int i = 0; i < RowOrder<C>::N; ++i) add[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  int64_t n0, m0;
+
+  __device__ __forceinline__ ColumnTile(const GemmGrouped &g, int pos, int tiles_m, int tiles_n) {
+    const int tiles = tiles_m * tiles_n, e = pos / tiles, in = pos - e * tiles;
+    const int strip = in / (4 * tiles_n), rest = in - strip * 4 * tiles_n, h = min(4, tiles_m - 4 * strip);
+    n0 = (int64_t)(rest / h) * C::TN;
+    m0 = (int64_t)(4 * strip + rest % h) * C::TM;
+    int first, n;
+    rows_of(g.offsets, g.groups, (int)g.p.k, e, first, n);
+    static_cast<GemmMx &>(p) = g.p;
+    p.pitch = g.p.k;
+    p.start = first & ~31;
+    p.k = n & ~31;
+    const int64_t out = e * p.m * p.ld;
+    p.out = static_cast<float *>(p.out) + out;
+    if (p.addend) p.addend += out;
   }
-  f32x4_t acc[C::FP][C::FQ];
-  if (p.k) {
-    const Loader<C, false, kRange> ld(p, n0, m0, 0, (int)((p.k + kRowB - 1) / kRowB));
+  __device__ __forceinline__ int steps() const { return (int)((p.k + kRowB - 1) / kRowB); }
+  // an expert without rows leaves what is there
+  __device__ __forceinline__ bool nothing() const { return !p.k && p.addend == p.out; }
+};
+
+template <class C>
+__device__ __forceinline__ void column_sums(const ColumnTile<C> &t, char *smem, f32x4_t (&acc)[C::FP][C::FQ]) {
+  if (t.p.k) {
+    const Loader<C, false, kRange> ld(t.p, t.n0, t.m0, 0, t.steps());
     sums16<C, false, false>(ld, smem, acc);
-    __syncthreads();
   } else {
 #pragma unroll
     for (int i = 0; i < C::FP; ++i)
 #pragma unroll
       for (int j = 0; j < C::FQ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
+}
+
+template <class C>
+__device__ __forceinline__ void column_addend(const ColumnTile<C> &t, const RowOrder<C> &rows, f32x4_t (&add)[RowOrder<C>::N]) {
+  if (t.p.addend) {
+    rows.load(t.p.addend, add);
+  } else {
+#pragma unroll
+    for (int i = 0; i < RowOrder<C>::N; ++i) add[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+}
+
+// One tile a workgroup, for experts of many rows: the products are what takes the time.
+template <class C>
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C::WPS))) void k_group_columns(GemmGrouped g, int tiles_m,
+                                                                                            int tiles_n) {
+  __shared__ __align__(1024) char smem[C::LDS];
+  const int total = tiles_m * tiles_n * g.groups, q = total >> 3, rem = total & 7, x = blockIdx.x & 7;
+  const ColumnTile<C> tile(g, x * q + min(x, rem) + ((int)blockIdx.x >> 3), tiles_m, tiles_n);
+  if (tile.nothing()) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const RowOrder<C> rows(tile.p, tile.n0, tile.m0, threadIdx.x);
+  f32x4_t add[RowOrder<C>::N], acc[C::FP][C::FQ];
+  if (tile.p.k && tile.p.addend && tile.m0 + C::TM <= tile.p.m && tile.n0 + C::TN <= tile.p.n) {
+    const Loader<C, false, kRange> ld(tile.p, tile.n0, tile.m0, 0, tile.steps());
+    sums16<C, false, false, RowOrder<C>::N>(ld, smem, acc, [&]() __attribute__((always_inline)) { rows.load_whole(tile.p.addend, add); });
+  } else {
+    column_addend<C>(tile, rows, add);
+    column_sums<C>(tile, smem, acc);
+  }
+  __syncthreads();
   int t_end = threadIdx.x;
   asm volatile("" : "+v"(t_end));
-  rows.store(smem, wn, wm, t_end, acc, add);
+  RowOrder<C>::put(smem, wave / C::WM, wave % C::WM, t_end, acc);
+  __syncthreads();
+  rows.store(smem, t_end, add);
+}
+
+// Experts of few rows: the addend and the output are what takes the time.  A workgroup a CU
+// walks its tiles with half of its waves on the products and half on memory: while one tile's
+// products are made, the addend of that tile comes in and the one before goes out.  Both
+// halves pass the same barriers: sums16's (one, and one a step; without rows one) and one where
+// the sums are in LDS, which the second half reads before the next of them.
+template <class C>
+__global__ __launch_bounds__(2 * C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_group_columns_walk(GemmGrouped g, int tiles_m,
+                                                                                             int tiles_n) {
+  constexpr int OUT = C::TM * RowOrder<C>::LP * 4;
+  __shared__ __align__(1024) char smem[C::LDS + OUT];
+  static_assert(C::LDS + OUT <= 163840 && C::NW == 4, "one workgroup a CU");
+  const int total = tiles_m * tiles_n * g.groups, q = total >> 3, rem = total & 7, x = blockIdx.x & 7;
+  const int end = x * q + min(x, rem) + q + (x < rem), step = (int)(gridDim.x + 7 - x) >> 3;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), t = threadIdx.x & (C::NT - 1);
+  for (int pos = x * q + min(x, rem) + ((int)blockIdx.x >> 3); pos < end; pos += step) {
+    const ColumnTile<C> tile(g, pos, tiles_m, tiles_n);
+    if (tile.nothing()) continue;
+    if (wave < C::NW) {
+      f32x4_t acc[C::FP][C::FQ];
+      column_sums<C>(tile, smem, acc);
+      // the tile before has been read once the other half passes a barrier of this one
+      if (!tile.p.k) asm volatile("s_barrier" ::: "memory");
+      RowOrder<C>::put(smem + C::LDS, wave / C::WM, wave % C::WM, t, acc);
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    } else {
+      const RowOrder<C> rows(tile.p, tile.n0, tile.m0, t);
+      f32x4_t add[RowOrder<C>::N];
+      column_addend<C>(tile, rows, add);
+      const int barriers = 1 + tile.steps();
+      for (int b = 0; b < barriers; ++b) asm volatile("s_barrier" ::: "memory");
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      rows.store(smem + C::LDS, t, add);
+    }
+  }
 }
 
 // Tile edge: 
@@ -404,7 +479,15 @@ hipError_t group_rows(const GemmGrouped &g, hipStream_t s) {
 template <class C>
 hipError_t group_columns(const GemmGrouped &g, hipStream_t s) {
   const int tm = (int)((g.p.m + C::TM - 1) / C::TM), tn = (int)((g.p.n + C::TN - 1) / C::TN);
-  hipLaunchKernelGGL((k_group_columns<C>), dim3((unsigned)tiles_of(g, C::TM)), dim3(C::NT), 0, s, g, tm, tn);
+  const int64_t tiles = tiles_of(g, C::TM);
+  static const int force = getenv("SSHDP_WALK") ? atoi(getenv("SSHDP_WALK")) : 1;
+  if constexpr (C::TM == 128) {
+    if (force) {
+      hipLaunchKernelGGL((k_group_columns_walk<C>), dim3((unsigned)std::min<int64_t>(tiles, 256)), dim3(2 * C::NT), 0, s, g, tm, tn);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((k_group_columns<C>), dim3((unsigned)tiles), dim3(C::NT), 0, s, g, tm, tn);
   return hipGetLastError();
 }
 
