@@ -361,7 +361,7 @@ template <class C>
 __device__ __forceinline__ void column_sums(const ColumnTile<C> &t, char *smem, f32x4_t (&acc)[C::FP][C::FQ]) {
   if (t.p.k) {
     const Loader<C, false, kRange> ld(t.p, t.n0, t.m0, 0, t.steps());
-    sums16<C, false, false>(ld, smem, acc);
+    sums16<C, false, false, true>(ld, smem, acc);
   } else {
 #pragma unroll
     for (int i = 0; i < C::FP; ++i)
@@ -380,65 +380,65 @@ __device__ __forceinline__ void column_addend(const ColumnTile<C> &t, const RowO
   }
 }
 
-// One tile a workgroup, for experts of many rows: the products are what takes the time.
+// Where XCD x's tiles of all experts' begin, in an order of one expert's after the other's: the
+// eighths are of equal work, a tile's being its steps and as much as kTileWork more for what
+// every tile moves.  Experts' rows differ many times over; eighths of equal numbers of tiles
+// take as long as the one with the most rows (458 against 375 us).
+constexpr int kTileWork = 6;
+__device__ __forceinline__ int xcd_begin(const GemmGrouped &g, int tiles, int x) {
+  if (x == 0) return 0;
+  if (x == 8) return tiles * g.groups;
+  const int lane = threadIdx.x & 63;
+  auto work_of = [&](int e) __attribute__((always_inline)) {
+    int first, n;
+    rows_of(g.offsets, g.groups, (int)g.p.k, e, first, n);
+    return e < g.groups ? kTileWork + (n + kRowB - 1) / kRowB : 0;
+  };
+  int total = 0;
+  for (int e0 = 0; e0 < g.groups; e0 += 64) total += __builtin_amdgcn_readlane(scan_lanes(work_of(e0 + lane)), 63);
+  const int64_t target = (int64_t)total * x;          // in eighths of a unit
+  int64_t base = 0;
+  for (int e0 = 0; e0 < g.groups; e0 += 64) {
+    const int mine = work_of(e0 + lane), upto = scan_lanes(mine);
+    const uint64_t past = __ballot(8 * (base + upto) > target);
+    if (past) {
+      const int l = __builtin_ctzll(past), c = __builtin_amdgcn_readlane(mine, l);
+      const int64_t in = target - 8 * (base + __builtin_amdgcn_readlane(upto, l) - c);
+      return (e0 + l) * tiles + (int)(in * tiles / (8 * c));
+    }
+    base += __builtin_amdgcn_readlane(upto, 63);
+  }
+  return tiles * g.groups;
+}
+
+// A workgroup walks its XCD's tiles, two workgroups a CU.  The addend comes in behind the first
+// two stages' operands, while the first products are made; experts of a few hundred rows leave
+// little more time than that.
 template <class C>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C::WPS))) void k_group_columns(GemmGrouped g, int tiles_m,
                                                                                             int tiles_n) {
   __shared__ __align__(1024) char smem[C::LDS];
-  const int total = tiles_m * tiles_n * g.groups, q = total >> 3, rem = total & 7, x = blockIdx.x & 7;
-  const ColumnTile<C> tile(g, x * q + min(x, rem) + ((int)blockIdx.x >> 3), tiles_m, tiles_n);
-  if (tile.nothing()) return;
+  const int x = blockIdx.x & 7, end = xcd_begin(g, tiles_m * tiles_n, x + 1), step = (int)(gridDim.x + 7 - x) >> 3;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const RowOrder<C> rows(tile.p, tile.n0, tile.m0, threadIdx.x);
-  f32x4_t add[RowOrder<C>::N], acc[C::FP][C::FQ];
-  if (tile.p.k && tile.p.addend && tile.m0 + C::TM <= tile.p.m && tile.n0 + C::TN <= tile.p.n) {
-    const Loader<C, false, kRange> ld(tile.p, tile.n0, tile.m0, 0, tile.steps());
-    sums16<C, false, false, RowOrder<C>::N>(ld, smem, acc, [&]() __attribute__((always_inline)) { rows.load_whole(tile.p.addend, add); });
-  } else {
-    column_addend<C>(tile, rows, add);
-    column_sums<C>(tile, smem, acc);
-  }
-  __syncthreads();
-  int t_end = threadIdx.x;
-  asm volatile("" : "+v"(t_end));
-  RowOrder<C>::put(smem, wave / C::WM, wave % C::WM, t_end, acc);
-  __syncthreads();
-  rows.store(smem, t_end, add);
-}
-
-// Experts of few rows: the addend and the output are what takes the time.  A workgroup a CU
-// walks its tiles with half of its waves on the products and half on memory: while one tile's
-// products are made, the addend of that tile comes in and the one before goes out.  Both
-// halves pass the same barriers: sums16's (one, and one a step; without rows one) and one where
-// the sums are in LDS, which the second half reads before the next of them.
-template <class C>
-__global__ __launch_bounds__(2 * C::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_group_columns_walk(GemmGrouped g, int tiles_m,
-                                                                                             int tiles_n) {
-  constexpr int OUT = C::TM * RowOrder<C>::LP * 4;
-  __shared__ __align__(1024) char smem[C::LDS + OUT];
-  static_assert(C::LDS + OUT <= 163840 && C::NW == 4, "one workgroup a CU");
-  const int total = tiles_m * tiles_n * g.groups, q = total >> 3, rem = total & 7, x = blockIdx.x & 7;
-  const int end = x * q + min(x, rem) + q + (x < rem), step = (int)(gridDim.x + 7 - x) >> 3;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), t = threadIdx.x & (C::NT - 1);
-  for (int pos = x * q + min(x, rem) + ((int)blockIdx.x >> 3); pos < end; pos += step) {
+  for (int pos = xcd_begin(g, tiles_m * tiles_n, x) + ((int)blockIdx.x >> 3); pos < end; pos += step) {
     const ColumnTile<C> tile(g, pos, tiles_m, tiles_n);
     if (tile.nothing()) continue;
-    if (wave < C::NW) {
-      f32x4_t acc[C::FP][C::FQ];
-      column_sums<C>(tile, smem, acc);
-      // the tile before has been read once the other half passes a barrier of this one
-      if (!tile.p.k) asm volatile("s_barrier" ::: "memory");
-      RowOrder<C>::put(smem + C::LDS, wave / C::WM, wave % C::WM, t, acc);
-      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    const RowOrder<C> rows(tile.p, tile.n0, tile.m0, t);
+    f32x4_t add[RowOrder<C>::N], acc[C::FP][C::FQ];
+    if (tile.p.k && tile.p.addend && tile.m0 + C::TM <= tile.p.m && tile.n0 + C::TN <= tile.p.n) {
+      const Loader<C, false, kRange> ld(tile.p, tile.n0, tile.m0, 0, tile.steps());
+      sums16<C, false, false, true, RowOrder<C>::N>(ld, smem, acc, [&]() __attribute__((always_inline)) { rows.load_whole(tile.p.addend, add); });
     } else {
-      const RowOrder<C> rows(tile.p, tile.n0, tile.m0, t);
-      f32x4_t add[RowOrder<C>::N];
       column_addend<C>(tile, rows, add);
-      const int barriers = 1 + tile.steps();
-      for (int b = 0; b < barriers; ++b) asm volatile("s_barrier" ::: "memory");
-      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      rows.store(smem + C::LDS, t, add);
+      column_sums<C>(tile, smem, acc);
     }
+    __syncthreads();
+    RowOrder<C>::put(smem, wave / C::WM, wave % C::WM, t, acc);
+    __syncthreads();
+    rows.store(smem, t, add);
+    __syncthreads();                                 // read before the next tile's stages are written
   }
 }
 
@@ -479,15 +479,8 @@ hipError_t group_rows(const GemmGrouped &g, hipStream_t s) {
 template <class C>
 hipError_t group_columns(const GemmGrouped &g, hipStream_t s) {
   const int tm = (int)((g.p.m + C::TM - 1) / C::TM), tn = (int)((g.p.n + C::TN - 1) / C::TN);
-  const int64_t tiles = tiles_of(g, C::TM);
-  static const int force = getenv("SSHDP_WALK") ? atoi(getenv("SSHDP_WALK")) : 1;
-  if constexpr (C::TM == 128) {
-    if (force) {
-      hipLaunchKernelGGL((k_group_columns_walk<C>), dim3((unsigned)std::min<int64_t>(tiles, 256)), dim3(2 * C::NT), 0, s, g, tm, tn);
-      return hipGetLastError();
-    }
-  }
-  hipLaunchKernelGGL((k_group_columns<C>), dim3((unsigned)tiles), dim3(C::NT), 0, s, g, tm, tn);
+  // what the CUs hold at once: every XCD has its share whatever the number of tiles
+  hipLaunchKernelGGL((k_group_columns<C>), dim3(512), dim3(C::NT), 0, s, g, tm, tn);
   return hipGetLastError();
 }
 
