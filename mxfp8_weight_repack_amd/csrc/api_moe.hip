@@ -88,7 +88,7 @@ int make_grouped(const sshdp_mx_matrix *a, const sshdp_mx_matrix *b, GroupForm f
     g.p.n = g.p.nn ? b->cols : rows;
   }
   if (a->cols > (1 << 22)) return SSHDP_ERR_SCHEMA;
-  return gemm_grouped_tiles(g) > kMaxTiles ? SSHDP_ERR_SCHEMA : SSHDP_OK;
+  return grouped_tiles(form, groups, g.p.m, g.p.n, 128) > kMaxTiles ? SSHDP_ERR_SCHEMA : SSHDP_OK;
 }
 
 }  // namespace

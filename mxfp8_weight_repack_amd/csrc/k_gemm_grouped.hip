@@ -8,7 +8,6 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <cstdlib>
 #include <type_traits>
 
 #include "act.h"
@@ -183,28 +182,35 @@ __device__ __forceinline__ void finish_gated(const GemmGrouped &g, const GemmMx 
   }
 }
 
-// bfloat16 addend into a tile's sums, 4 columns of a row a lane; rows past the end read the
+// bfloat16 addend into a tile's sums, 4 columns of a row a lane, a row block's words in flight
+// together (more of them would not fit beside a 256-tile's sums); rows past the end read the
 // last one's.
 template <class C>
 __device__ __forceinline__ void add_bf16(const GemmMx &p, const uint16_t *addend, int64_t n0, int64_t m0, int wn, int wm, int t,
                                          f32x4_t (&acc)[C::FP][C::FQ]) {
   const int64_t mw = m0 + wm * (C::TM / C::WM) + (t & 15), nw = n0 + wn * (C::TN / C::WN) + 4 * (t >> 4 & 3);
+  const bool whole = n0 + C::TN <= p.n;
 #pragma unroll
   for (int j = 0; j < C::FQ; ++j) {
-    const uint16_t *row = addend + min(mw + 16 * j, p.m - 1) * p.ld;
+    const uint16_t *row = addend + min(mw + 16 * j, p.m - 1) * p.ld + nw;
+    u32x2e_t w[C::FP];
 #pragma unroll
     for (int i = 0; i < C::FP; ++i) {
-      const int64_t n = nw + 16 * i;
-      if (n + 4 <= p.n) {
-        const u32x2e_t w = *reinterpret_cast<const u32x2e_t *>(row + n);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[i][j][k] += __uint_as_float(k & 1 ? w[k >> 1] & 0xFFFF0000u : w[k >> 1] << 16);
+      w[i] = u32x2e_t{0, 0};
+      if (whole || nw + 16 * i + 4 <= p.n) {
+        w[i] = *reinterpret_cast<const u32x2e_t *>(row + 16 * i);
       } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (n + k < p.n) acc[i][j][k] += __uint_as_float((uint32_t)row[n + k] << 16);
+          if (nw + 16 * i + k < p.n) w[i][k >> 1] |= (uint32_t)row[16 * i + k] << (16 * (k & 1));
       }
     }
+#pragma unroll
+    for (int i = 0; i < C::FP; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[i][j][k] += __uint_as_float(k & 1 ? w[i][k >> 1] & 0xFFFF0000u : w[i][k >> 1] << 16);
+#pragma unroll
+    for (int i = 0; i < C::FP; ++i) asm volatile("" : "+v"(acc[i][j])::"memory");
   }
 }
 
@@ -383,7 +389,8 @@ __device__ __forceinline__ void column_addend(const ColumnTile<C> &t, const RowO
 // Where XCD x's tiles of all experts' begin, in an order of one expert's after the other's: the
 // eighths are of equal work, a tile's being its steps and as much as kTileWork more for what
 // every tile moves.  Experts' rows differ many times over; eighths of equal numbers of tiles
-// take as long as the one with the most rows (458 against 375 us).
+// take as long as the one with the most rows (410 to 455 against 368 to 418 us; at a unit of 2,
+// 12 and 24 for the rest 401, 401 and 413).
 constexpr int kTileWork = 6;
 __device__ __forceinline__ int xcd_begin(const GemmGrouped &g, int tiles, int x) {
   if (x == 0) return 0;
@@ -442,60 +449,209 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
   }
 }
 
-// Tile edge: 
-int tile_of_rows(const GemmGrouped &g) {
-  static const int force = getenv("SSHDP_TILE") ? atoi(getenv("SSHDP_TILE")) : 0;
-  return force ? force : 128;
-}
+// ----------------------------------------------------------------- a few rows an expert
+//
+// Bound by reading the experts' B once.  A workgroup makes 16 rows of one expert by 64 rows of
+// B (gated: 32 of each matrix): its W waves share K, a wave has 4 steps of all of them in
+// flight at once, straight from memory to registers, and its sums meet the others' in LDS.
+// The products are float32 sums whatever the output: the conversions that takes cost nothing
+// beside the reads.
+constexpr int kFewSteps = 4, kFewFrags = 4;
 
-int tile_cols(const GemmGrouped &g, int tile) { return g.form == kRowsGated ? tile / 2 : tile; }
-
-int64_t tiles_of(const GemmGrouped &g, int tile) {
-  const int cols = tile_cols(g, tile);
-  const int64_t tn = (g.p.n + cols - 1) / cols;
-  if (g.form == kColumns) return g.groups * ((g.p.m + tile - 1) / tile) * tn;
-  // no more experts than rows have any
-  return (g.p.m / tile + std::min<int64_t>(g.groups, g.p.m)) * tn;
+template <Form F, bool BF16, int W>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_group_few(GemmGrouped g, int blocks_n) {
+  constexpr int S = kFewSteps, NF = kFewFrags;
+  typedef uint32_t u32x4u_t __attribute__((ext_vector_type(4), aligned(1)));   // scales lie at any address
+  typedef uint32_t u32u_t __attribute__((aligned(1)));
+  __shared__ __align__(16) f32x4_t part[W][NF][64];
+  Found f;
+  int block;
+  if (!find_tile<16>(g, blocks_n, f, block)) return;
+  GemmPart p;
+  static_cast<GemmMx &>(p) = g.p;
+  take_rows(p, g.p, f, false);
+  if (F == kGated) {
+    p.b2 = g.b2 + (p.b - g.p.b);
+    p.b2s = g.b2s + (p.bs - g.p.bs);
+  }
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, q = lane >> 4;
+  const int KB = (int)(p.k >> 5), m0 = 16 * f.at, rows = min(16, f.rows - m0);
+  const int64_t n0 = (int64_t)block * (F == kGated ? 32 : 64);
+  // fragment i: 16 rows of B from n on
+  auto column = [&](int i) __attribute__((always_inline)) { return n0 + 16 * (F == kGated ? i & 1 : i); };
+  // Rows past the end are past their resource, chunks past K are sent there: both read as zeros.
+  auto resource = [&](const uint8_t *base, int64_t n) __attribute__((always_inline)) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), 0, (int)(n * p.k), kBufWord3);
+  };
+  const __amdgpu_buffer_rsrc_t ra = resource(p.a + m0 * p.k, rows);
+  __amdgpu_buffer_rsrc_t rb[NF];
+#pragma unroll
+  for (int i = 0; i < NF; ++i) {
+    const int64_t n = column(i), left = max(min<int64_t>(p.n - n, 16), (int64_t)0);
+    rb[i] = resource((F == kGated && i >= 2 ? p.b2 : p.b) + (left ? n * p.k : 0), left);
+  }
+  // word j: a row's blocks kb + 4 j .. + 3, zeros past the end
+  struct Words {
+    uint32_t w[S];
+  };
+  auto scales = [&](const uint8_t *s, int layout, int64_t row, int kb) __attribute__((always_inline)) {
+    const bool tile = layout == SSHDP_SCALE_TILE32X4;
+    s += tile ? (row >> 5) * (KB >> 2) * 128 + (row & 31) * 4 : (layout == SSHDP_SCALE_ROWMAJOR ? row : row >> 5) * KB;
+    Words v{};
+    if (kb + 4 * S <= KB && !tile) {
+      const u32x4_t x = *reinterpret_cast<const u32x4u_t *>(s + kb);
+#pragma unroll
+      for (int j = 0; j < S; ++j) v.w[j] = x[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        const int at = kb + 4 * j, n = min(KB - at, 4);
+        const uint8_t *b = s + (tile ? (at >> 2) * 128 : at);
+        if (n == 4) v.w[j] = *reinterpret_cast<const u32u_t *>(b);
+        else for (int i = 0; i < n; ++i) v.w[j] |= (uint32_t)b[i] << (8 * i);
+      }
+    }
+    return v;
+  };
+  f32x4_t acc[NF];
+#pragma unroll
+  for (int i = 0; i < NF; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int kb = 4 * S * wave; kb < KB; kb += 4 * S * W) {
+    const int k0 = kb * 32 + 16 * q, left = (int)p.k - k0, voff = r * (int)p.k + k0;
+    auto load = [&](__amdgpu_buffer_rsrc_t rs, int c) __attribute__((always_inline)) {
+      return __builtin_bit_cast(u32x4_t,
+                                __builtin_amdgcn_raw_buffer_load_b128(rs, 64 * c < left ? voff + 64 * c : INT32_MAX - 15, 0, 0));
+    };
+    u32x4_t a[2 * S], b[NF][2 * S];
+    Words wa, wb[NF];
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+      wb[i] = scales(F == kGated && i >= 2 ? p.b2s : p.bs, p.lb, min(column(i) + r, p.n - 1), kb);
+#pragma unroll
+      for (int c = 0; c < 2 * S; ++c) b[i][c] = load(rb[i], c);
+    }
+    wa = scales(p.as, SSHDP_SCALE_ROWMAJOR, m0 + min(r, rows - 1), kb);
+#pragma unroll
+    for (int c = 0; c < 2 * S; ++c) a[c] = load(ra, c);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int sh = 8 * (2 * h + (q >> 1));
+        const u32x4_t &x = a[2 * s + h];
+        const uint32_t ea = (wa.w[s] >> sh) & 0xFFu;
+        const u32x4_t y[2] = {to_bf16((int)x[0], (int)x[1], ea), to_bf16((int)x[2], (int)x[3], ea)};
+#pragma unroll
+        for (int i = 0; i < NF; ++i) {
+          const u32x4_t &z = b[i][2 * s + h];
+          const uint32_t eb = (wb[i].w[s] >> sh) & 0xFFu;
+          acc[i] = mma_bf16(to_bf16((int)z[0], (int)z[1], eb), y[0], acc[i]);
+          acc[i] = mma_bf16(to_bf16((int)z[2], (int)z[3], eb), y[1], acc[i]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NF; ++i) part[wave][i][lane] = acc[i];
+  __syncthreads();
+  auto total = [&](int i) __attribute__((always_inline)) {
+    f32x4_t v = part[0][i][lane];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += part[w][i][lane];
+    return v;
+  };
+  p.m = rows;
+  const int64_t out = f.first + m0;
+  if constexpr (F == kGated) {
+    if (wave) return;
+    float h[8];
+    uint32_t m = 0;
+    const int64_t e = (out + r) * p.n + n0 + 4 * q;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const f32x4_t gate = total(c), up = total(2 + c);
+      if (g.gate && r < rows) {
+        *reinterpret_cast<uint2 *>(g.gate + e + 16 * c) = make_uint2(pk_bf16(gate[0], gate[1]), pk_bf16(gate[2], gate[3]));
+        *reinterpret_cast<uint2 *>(g.up + e + 16 * c) = make_uint2(pk_bf16(up[0], up[1]), pk_bf16(up[2], up[3]));
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        h[4 * c + k] = swiglu(gate[k], up[k]);
+        m = max(m, __float_as_uint(h[4 * c + k]) & 0x7FFFFFFFu);
+      }
+    }
+    if (!g.codes) return;
+    const auto x = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+    m = max(x[0], x[1]);
+    const auto y = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    const uint32_t sb = mx_scale_byte(max(y[0], y[1]));
+    if (r >= rows) return;
+    const float sf = mx_scale_float(sb);
+    *reinterpret_cast<uint32_t *>(g.codes + e) = mx_or_nan(mx_cvt4(h[0], h[1], h[2], h[3], sf), sb);
+    *reinterpret_cast<uint32_t *>(g.codes + e + 16) = mx_or_nan(mx_cvt4(h[4], h[5], h[6], h[7], sf), sb);
+    if (q == 0) g.scales[(out + r) * (p.n >> 5) + block] = (uint8_t)sb;
+  } else {
+    for (int i = wave; i < NF; i += W) {
+      f32x4_t v = total(i);
+      const int64_t n = column(i) + 4 * q, e = out * p.ld;
+      if (BF16) {
+        p.out = static_cast<uint16_t *>(g.p.out) + e;
+        if (g.addend16 && r < rows) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (n + k < p.n) v[k] += __uint_as_float((uint32_t)g.addend16[e + r * p.ld + n + k] << 16);
+        }
+        store_bf16(p, r, n, v);
+      } else {
+        if (g.p.addend) p.addend = g.p.addend + e;
+        store_f32(p, static_cast<float *>(g.p.out) + e, r, n, v);
+      }
+    }
+  }
 }
 
 template <class C, bool NN, Form F>
 hipError_t group_rows(const GemmGrouped &g, hipStream_t s) {
-  const int cols = tile_cols(g, C::TM), tn = (int)((g.p.n + cols - 1) / cols);
-  const dim3 grid((unsigned)tiles_of(g, C::TM)), block(C::NT);
+  const int cols = grouped_cols(g.form, C::TM), tn = (int)((g.p.n + cols - 1) / cols);
+  const dim3 grid((unsigned)grouped_tiles(g.form, g.groups, g.p.m, g.p.n, C::TM)), block(C::NT);
   auto launch = [&](auto sh) {
     constexpr bool SHORT = decltype(sh)::value;
-    if constexpr (F == kGated) {
-      hipLaunchKernelGGL((k_group8<C, NN, SHORT, F>), grid, block, 0, s, g, tn);
-    } else {
-      if (g.bf16) hipLaunchKernelGGL((k_group8<C, NN, SHORT, F>), grid, block, 0, s, g, tn);
-      else hipLaunchKernelGGL((k_group16<C, NN, SHORT>), grid, block, 0, s, g, tn);
-    }
+    if (g.bf16) hipLaunchKernelGGL((k_group8<C, NN, SHORT, F>), grid, block, 0, s, g, tn);
+    else if constexpr (C::TM == 128 && F == kWhole) hipLaunchKernelGGL((k_group16<C, NN, SHORT>), grid, block, 0, s, g, tn);
   };
   if (gemm_short(g.p.k)) launch(std::true_type{});
   else launch(std::false_type{});
   return hipGetLastError();
 }
 
-template <class C>
-hipError_t group_columns(const GemmGrouped &g, hipStream_t s) {
-  const int tm = (int)((g.p.m + C::TM - 1) / C::TM), tn = (int)((g.p.n + C::TN - 1) / C::TN);
-  // what the CUs hold at once: every XCD has its share whatever the number of tiles
-  hipLaunchKernelGGL((k_group_columns<C>), dim3(512), dim3(C::NT), 0, s, g, tm, tn);
+template <Form F, bool BF16>
+hipError_t group_few(const GemmGrouped &g, hipStream_t s) {
+  const int cols = grouped_cols(g.form, 16), blocks = (int)((g.p.n + cols - 1) / cols);
+  const dim3 grid((unsigned)grouped_tiles(g.form, g.groups, g.p.m, g.p.n, 16));
+  if (g.p.k <= 2048) hipLaunchKernelGGL((k_group_few<F, BF16, 4>), grid, dim3(256), 0, s, g, blocks);
+  else hipLaunchKernelGGL((k_group_few<F, BF16, 8>), grid, dim3(512), 0, s, g, blocks);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t gemm_grouped_tiles(const GemmGrouped &g) { return tiles_of(g, 128); }
-
 hipError_t launch_gemm_grouped(const GemmGrouped &g, hipStream_t s) {
-  const bool large = tile_of_rows(g) == 256;
-  switch (g.form) {
-    case kRowsNT: return large ? group_rows<T256, false, kWhole>(g, s) : group_rows<T128, false, kWhole>(g, s);
-    case kRowsNN: return large ? group_rows<T256, true, kWhole>(g, s) : group_rows<T128, true, kWhole>(g, s);
-    case kRowsGated: return large ? group_rows<T256, false, kGated>(g, s) : group_rows<T128, false, kGated>(g, s);
-    default: return group_columns<T128>(g, s);
+  if (g.form == kColumns) {
+    // what the CUs hold at once: every XCD has its share whatever the number of tiles
+    const int tm = (int)((g.p.m + 127) / 128), tn = (int)((g.p.n + 127) / 128);
+    hipLaunchKernelGGL((k_group_columns<T128>), dim3(512), dim3(T128::NT), 0, s, g, tm, tn);
+    return hipGetLastError();
   }
+  const int tile = grouped_tile(g.form, g.groups, g.p.m, g.p.n, g.p.k, g.bf16);
+  if (tile == 16) {
+    if (g.form == kRowsGated) return group_few<kGated, true>(g, s);
+    return g.bf16 ? group_few<kWhole, true>(g, s) : group_few<kWhole, false>(g, s);
+  }
+  const bool large = tile == 256;
+  if (g.form == kRowsGated) return large ? group_rows<T256, false, kGated>(g, s) : group_rows<T128, false, kGated>(g, s);
+  if (g.form == kRowsNN) return large ? group_rows<T256, true, kWhole>(g, s) : group_rows<T128, true, kWhole>(g, s);
+  return large ? group_rows<T256, false, kWhole>(g, s) : group_rows<T128, false, kWhole>(g, s);
 }
 
 }  // namespace sshdp

@@ -1,5 +1,6 @@
 // moe.h -- launchers of the expert layer's operators.
 #pragma once
+#include "grouped_shape.h"
 #include "internal.h"
 
 namespace sshdp {
@@ -29,7 +30,6 @@ hipError_t launch_swiglu_grad(const sshdp_swiglu_grad &a, hipStream_t s);
 
 // Products grouped by expert (k_gemm_grouped.hip).  rows: all of A's (ROWS_*), n and k as in
 // GemmMx, those of one expert's product.
-enum GroupForm { kRowsNT, kRowsNN, kRowsGated, kColumns };
 struct GemmGrouped {
   GroupForm form;
   bool bf16;                          // output type
@@ -41,7 +41,6 @@ struct GemmGrouped {
   const int32_t *offsets;             // NULL: one group of all rows
   int32_t groups;
 };
-int64_t gemm_grouped_tiles(const GemmGrouped &g);    // workgroups at most
 hipError_t launch_gemm_grouped(const GemmGrouped &g, hipStream_t s);
 
 }  // namespace sshdp

@@ -7,6 +7,7 @@ import pytest
 
 import mxfp8_weight_repack_amd as sh
 from gpu_util import say
+from grouped_sizes import SIZES
 from test_gpu_gemm_shapes import Operand
 
 torch = pytest.importorskip("torch")
@@ -122,6 +123,21 @@ def check(op, counts, n, k, dtype, lb="rowmajor", tail=0):
     assert bool(got[bad].isnan().all()) and torch.equal(got[~bad], ref.to(td)[~bad])
 
 
+@pytest.mark.parametrize("name,layout", [(n, lay) for n in SIZES if " gated " not in n
+                                         for lay in ("rowmajor", "tile32x4", "block32x32")
+                                         if " nn " not in n or lay == "block32x32"])
+def test_every_kernel_of_rows(name, layout):
+    """Edges that no tile divides; in the layouts that group rows and columns, the next ones those take."""
+    counts, n, k = SIZES[name]
+    words = name.split()
+    if layout != "rowmajor":
+        n = -(-n // 32) * 32
+    if layout == "tile32x4":
+        k = -(-k // 128) * 128
+    say(f"{name} {layout}: {counts} {n} x {k}")
+    check(words[1], counts, n, k, words[2], lb=layout)
+
+
 MANY = [0, 1, 0, 5, 33, 0, 0, 2] * 12 + [130]          # over 64 experts
 ROWS = [
     ([37], 96, 64, 0), ([1], 32, 32, 0), ([0, 1, 0], 64, 96, 3), ([0, 0], 64, 64, 5), ([5, 0, 16, 17, 1], 96, 544, 2),
@@ -213,7 +229,8 @@ def check_codes(codes, scales, h, eh):
 
 
 GATED = ROWS[:2] + ROWS[2:9] + [([1, 2, 0, 3] * 20, 96, 4256, 0), ([7, 1, 12], 64, 8192, 0), ([9, 2], 64, 8224, 0),
-                                ([40, 1], 32, 512, 4), ([700, 300], 704, 256, 9)]
+                                ([40, 1], 32, 512, 4), ([700, 300], 704, 256, 9)] + \
+    [(*s, 0) for name, s in SIZES.items() if " gated " in name]
 
 
 @pytest.mark.parametrize("layout", ["rowmajor", "tile32x4", "block32x32"])

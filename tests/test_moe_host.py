@@ -2,13 +2,17 @@
 touches the device), the sizes they ask for, and their gradients' formulas against differences."""
 
 import itertools
+import os
+import subprocess
 
 import numpy as np
 import pytest
 
 import mxfp8_weight_repack_amd as sh
 import moe_ref as M
+from grouped_sizes import SIZES
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 P = 1 << 20                                            # an aligned address that no refused call follows
 
 
@@ -255,3 +259,33 @@ def test_activation_gradient_formula_against_differences():
     # central differences of a function whose third derivative is under 1: off by h^2, and 1e-16 / h of rounding
     assert np.all(np.abs((f(g + h, u) - f(g - h, u)) / (2 * h) - dg) <= 1e-9 * (1 + np.abs(d * u)) * (1 + np.abs(g)))
     assert np.all(np.abs((f(g, u + h) - f(g, u - h)) / (2 * h) - du) <= 1e-9 * (1 + np.abs(d * g)) * (1 + np.abs(u)))
+
+
+# ------------------------------------------------------------------------------------------- the choice of the kernel
+
+def _choices(tmp_path, lines):
+    exe = str(tmp_path / "shapes")
+    subprocess.run(["g++", "-std=c++17", "-I", os.path.join(ROOT, "mxfp8_weight_repack_amd", "csrc"),
+                    os.path.join(ROOT, "tests", "host_grouped_shapes.cpp"), "-o", exe], check=True)
+    out = subprocess.run([exe], input="\n".join(lines), capture_output=True, text=True, check=True).stdout
+    return [r.rsplit(" ", 1) for r in out.splitlines()]
+
+
+def test_every_grouped_kernel_has_its_size(tmp_path):
+    """Each size of tests/grouped_sizes.py runs the kernel it is named after, and no drawn size runs another."""
+    def line(name, counts, n, k):
+        words = name.split()
+        return f"{words[1]} {len(counts)} {sum(counts)} {n} {k} {int(words[2] == 'bf16')}"
+    got = _choices(tmp_path, [line(n, *s) for n, s in SIZES.items()])
+    assert [g[0] for g in got] == list(SIZES)
+    rng = np.random.default_rng(0)
+    lines = []
+    for _ in range(4000):
+        form = str(rng.choice(["nt", "nn", "gated"]))
+        p, n, k = (int(2 ** rng.uniform(0, top)) for top in (20, 13, 14))
+        n, k = (-(-n // 32) * 32 if form != "nt" else n), -(-k // 32) * 32
+        lines.append(f"{form} {int(2 ** rng.uniform(0, 10))} {p} {n} {k} {int(form == 'gated' or rng.random() < 0.5)}")
+    names, tiles = zip(*_choices(tmp_path, lines))
+    assert set(names) <= set(SIZES)
+    # a launch has under 2^32 threads, of 512 at most
+    assert max(int(t) for t in tiles) < 1 << 23
