@@ -244,9 +244,10 @@ def _check(code, what):
 def _ptr(x):
     if x is None:
         return None
-    if isinstance(x, int):
+    try:
+        return x.data_ptr()
+    except AttributeError:
         return x
-    return x.data_ptr()
 
 
 def _stream(s):

@@ -34,13 +34,11 @@ __device__ __forceinline__ void put_rows(const sshdp_mx_out &o, const float (&v)
   if ((lane & 3) == 0) o.scales[e >> 5] = (uint8_t)sb;
 }
 
-__device__ __forceinline__ void put_column(const sshdp_mx_out &o, const float (&v)[32], int64_t e) {
-  if (!o.codes_t) return;
+// One column's 4 blocks by 4 lanes, from element e on.
+__device__ __forceinline__ void put_column(const sshdp_mx_out &o, const float (&v)[32], int64_t e, int blocks, int lane) {
   const MxColumn c = mx_column(v);
-  u32x4r_t *d = reinterpret_cast<u32x4r_t *>(o.codes_t + e);
-  d[0] = c.codes[0];
-  d[1] = c.codes[1];
-  o.scales_t[e >> 5] = (uint8_t)c.scale;
+  mx_store_column(c, o.codes_t + e, blocks, lane);
+  if ((lane & 3) < blocks) o.scales_t[(e >> 5) + (lane & 3)] = (uint8_t)c.scale;
 }
 
 // Along the rows alone: 8 elements a lane.
@@ -66,68 +64,75 @@ __global__ __launch_bounds__(256) void k_act_rows(sshdp_swiglu_grad a) {
 
 constexpr int kActRows = 128, kActCols = 64;         // tile of one workgroup
 
-// Columns too: a tile of the three inputs goes to LDS as it is; on the way a lane takes 8
-// elements of a row (4 lanes a block), afterwards a lane 32 rows of one column, from LDS, and
-// computes them again.
-__global__ __launch_bounds__(256) void k_act_tiles(sshdp_swiglu_grad a, int tiles_c) {
-  __shared__ __align__(16) uint16_t sm[3][kActRows][kActCols];
+// Columns too: a lane computes 8 elements of 4 rows and keeps the three results; one result
+// after the other goes through LDS, from which a lane takes 32 rows of one column.  (A column's
+// values computed anew from the inputs in LDS instead: 102 us for 26624 x 1408.)  LDS columns
+// are rotated by the row group, so the 4 groups that a wave reads at one step fall on
+// different banks.
+__global__ __launch_bounds__(256) void k_act_tiles(sshdp_swiglu_grad a, uint32_t tiles_c, uint32_t tiles) {
+  constexpr int NP = kActRows / 32;
+  __shared__ __align__(16) float sm[kActRows][kActCols];
   const int t = threadIdx.x;
-  const int64_t tr = blockIdx.x / tiles_c, r0 = tr * kActRows, c0 = (blockIdx.x - tr * tiles_c) * (int64_t)kActCols;
+  const uint32_t xcd = blockIdx.x & 7, pos = xcd * (tiles >> 3) + min(xcd, tiles & 7) + (blockIdx.x >> 3);
+  const int64_t r0 = pos / tiles_c * (int64_t)kActRows, c0 = pos % tiles_c * (int64_t)kActCols;
   const int64_t used = rows_in_use(a);
   if (r0 >= used) return;
   const int lc = (t & 7) * 8, lr = t >> 3;
   const bool in_c = c0 + lc < a.cols;
   const void *src[3] = {a.dh, a.gate, a.up};
-  Raw8<true> raw[kActRows / 32][3];
+  Raw8<true> raw[NP][3];
 #pragma unroll
-  for (int p = 0; p < kActRows / 32; ++p)
+  for (int p = 0; p < NP; ++p)
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       const int64_t r = r0 + lr + 32 * p;
       raw[p][k] = Raw8<true>{};
       if (in_c && r < used && src[k]) raw[p][k] = load8<true>(src[k], r * a.cols + c0 + lc);
     }
+  float v[3][NP][8];                                 // dgate, dup, h
 #pragma unroll
-  for (int p = 0; p < kActRows / 32; ++p) {
-    const int rr = lr + 32 * p;
-    float d[8], g[8], u[8], dg[8], du[8], h[8];
-#pragma unroll
-    for (int k = 0; k < 3; ++k) *reinterpret_cast<Raw8<true> *>(&sm[k][rr][lc]) = raw[p][k];
+  for (int p = 0; p < NP; ++p) {
+    float d[8], g[8], u[8];
     unpack8<true>(raw[p][0], d);
     unpack8<true>(raw[p][1], g);
     unpack8<true>(raw[p][2], u);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const Act r = act_grad(d[j], g[j], u[j]);
-      dg[j] = r.dg;
-      du[j] = r.du;
-      h[j] = r.h;
+      v[0][p][j] = r.dg;
+      v[1][p][j] = r.du;
+      v[2][p][j] = r.h;
     }
+    const int rr = lr + 32 * p;
     const int64_t e = (r0 + rr) * a.cols + c0 + lc;
     const bool in = in_c && r0 + rr < used;
-    put_rows(a.dgate, dg, e, in, t);
-    put_rows(a.dup, du, e, in, t);
-    put_rows(a.h, h, e, in, t);
+    put_rows(a.dgate, v[0][p], e, in, t);
+    put_rows(a.dup, v[1][p], e, in, t);
+    put_rows(a.h, v[2][p], e, in, t);
   }
-  __syncthreads();
+  const sshdp_mx_out *out[3] = {&a.dgate, &a.dup, &a.h};
   const int grp = t & 3, c = t >> 2;
-  const int64_t r = r0 + 32 * grp;
-  if (c0 + c >= a.cols || r >= used) return;
-  float dg[32], du[32], h[32];
+  const int64_t e = (c0 + c) * a.rows + r0;
+  const int blocks = (int)min<int64_t>(4, (used - r0 + 31) / 32);
+  bool first = true;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    float v[3];
+  for (int k = 0; k < 3; ++k) {
+    if (!out[k]->codes_t) continue;
+    if (!first) __syncthreads();                     // the one before has been read
+    first = false;
 #pragma unroll
-    for (int k = 0; k < 3; ++k) v[k] = __uint_as_float((uint32_t)sm[k][32 * grp + j][c] << 16);
-    const Act x = act_grad(v[0], v[1], v[2]);
-    dg[j] = x.dg;
-    du[j] = x.du;
-    h[j] = x.h;
+    for (int p = 0; p < NP; ++p) {
+      float4 *q = reinterpret_cast<float4 *>(&sm[lr + 32 * p][lc ^ (16 * p)]);
+      q[0] = make_float4(v[k][p][0], v[k][p][1], v[k][p][2], v[k][p][3]);
+      q[1] = make_float4(v[k][p][4], v[k][p][5], v[k][p][6], v[k][p][7]);
+    }
+    __syncthreads();
+    if (c0 + c >= a.cols) continue;
+    float x[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) x[j] = sm[32 * grp + j][c ^ (16 * grp)];
+    put_column(*out[k], x, e, blocks, t);
   }
-  const int64_t e = (c0 + c) * a.rows + r;
-  put_column(a.dgate, dg, e);
-  put_column(a.dup, du, e);
-  put_column(a.h, h, e);
 }
 
 }  // namespace
@@ -135,7 +140,7 @@ __global__ __launch_bounds__(256) void k_act_tiles(sshdp_swiglu_grad a, int tile
 hipError_t launch_swiglu_grad(const sshdp_swiglu_grad &a, hipStream_t s) {
   if (a.dgate.codes_t || a.dup.codes_t || a.h.codes_t) {
     const int64_t tc = (a.cols + kActCols - 1) / kActCols, tr = (a.rows + kActRows - 1) / kActRows;
-    hipLaunchKernelGGL(k_act_tiles, dim3((unsigned)(tr * tc)), dim3(256), 0, s, a, (int)tc);
+    hipLaunchKernelGGL(k_act_tiles, dim3((unsigned)(tr * tc)), dim3(256), 0, s, a, (uint32_t)tc, (uint32_t)(tr * tc));
   } else {
     const int64_t runs = a.rows * (a.cols / 8);
     hipLaunchKernelGGL(k_act_rows, dim3((unsigned)std::min<int64_t>((runs + 255) / 256, 1 << 20)), dim3(256), 0, s, a);

@@ -287,8 +287,8 @@ __global__ __launch_bounds__(256) void k_moe_tiles(sshdp_moe_gather a, uint32_t 
   if (!a.out.codes_t) return;
   __syncthreads();
   const int grp = t & 3, c = (t >> 2) * 2;
-  const int64_t r = r0 + 32 * grp;
-  if (c0 + c >= a.cols || r >= used) return;
+  if (c0 + c >= a.cols) return;
+  const int blocks = (int)min<int64_t>(4, (used - r0 + 31) / 32);
   const char *q = sm + (32 * grp * kMtCols + (c ^ (grp * ROT))) * ES;
   MxColumn o[2];
   if constexpr (BF16 && !WEIGHTED) {
@@ -320,11 +320,9 @@ __global__ __launch_bounds__(256) void k_moe_tiles(sshdp_moe_gather a, uint32_t 
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int64_t e = (c0 + c + h) * a.rows + r;
-    u32x4r_t *d = reinterpret_cast<u32x4r_t *>(a.out.codes_t + e);
-    __builtin_nontemporal_store(o[h].codes[0], d);
-    __builtin_nontemporal_store(o[h].codes[1], d + 1);
-    a.out.scales_t[e >> 5] = (uint8_t)o[h].scale;
+    const int64_t e = (c0 + c + h) * a.rows + r0;
+    mx_store_column(o[h], a.out.codes_t + e, blocks, t);
+    if (grp < blocks) a.out.scales_t[(e >> 5) + grp] = (uint8_t)o[h].scale;
   }
 }
 

@@ -101,4 +101,25 @@ __device__ __forceinline__ void mx_columns_bf16(const uint32_t (&x)[32], MxColum
   }
 }
 
+// A column's 128 rows of codes from the 4 lanes (aligned to 4) that hold its 4 blocks: lane l's
+// is block l.  Stored as they are, the lanes' 16 bytes lie 32 apart; exchanged within the four,
+// each store writes 64 bytes in a row (the gradients' 26624 x 1408 columns 18 us each against
+// 11).  `at`: block 0's place; `blocks`: how many of the 4 are stored.  Every lane of the four
+// must call it.
+__device__ __forceinline__ void mx_store_column(const MxColumn &c, uint8_t *at, int blocks, int lane) {
+  const int l = lane & 3;
+  u32x4r_t w[2];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    // quad_perm [0, 0, 1, 1] and [2, 2, 3, 3]: two lanes a block, one a half
+    const int a0 = __builtin_amdgcn_mov_dpp((int)c.codes[0][j], 0x50, 0xF, 0xF, true), a1 = __builtin_amdgcn_mov_dpp((int)c.codes[1][j], 0x50, 0xF, 0xF, true);
+    const int b0 = __builtin_amdgcn_mov_dpp((int)c.codes[0][j], 0xFA, 0xF, 0xF, true), b1 = __builtin_amdgcn_mov_dpp((int)c.codes[1][j], 0xFA, 0xF, 0xF, true);
+    w[0][j] = (uint32_t)(l & 1 ? a1 : a0);
+    w[1][j] = (uint32_t)(l & 1 ? b1 : b0);
+  }
+  u32x4r_t *d = reinterpret_cast<u32x4r_t *>(at + 16 * l);
+  if ((l >> 1) < blocks) __builtin_nontemporal_store(w[0], d);
+  if (2 + (l >> 1) < blocks) __builtin_nontemporal_store(w[1], d + 4);
+}
+
 }  // namespace sshdp
