@@ -64,53 +64,77 @@ __global__ __launch_bounds__(256) void k_act_rows(sshdp_swiglu_grad a) {
 
 constexpr int kActRows = 128, kActCols = 64;         // tile of one workgroup
 
-// Columns too: a lane computes 8 elements of 4 rows and keeps the three results; one result
-// after the other goes through LDS, from which a lane takes 32 rows of one column.  (A column's
-// values computed anew from the inputs in LDS instead: 102 us for 26624 x 1408.)  LDS columns
-// are rotated by the row group, so the 4 groups that a wave reads at one step fall on
-// different banks.
+// Columns too: a lane computes 16 elements of 2 rows, stores their codes (the scales of the two
+// in one store) and keeps the three results; one result after the other goes through LDS, from
+// which a lane takes 32 rows of one column.  LDS columns are rotated by the row group, so the 4
+// groups that a wave reads at one step fall on different banks.  Bound by the number of store
+// instructions as much as by their bytes: with 8 elements a lane and a store for each row's
+// scales 26624 x 1408 took 102-111 us.
 __global__ __launch_bounds__(256) void k_act_tiles(sshdp_swiglu_grad a, uint32_t tiles_c, uint32_t tiles) {
-  constexpr int NP = kActRows / 32;
+  constexpr int NP = kActRows / 64;
   __shared__ __align__(16) float sm[kActRows][kActCols];
   const int t = threadIdx.x;
   const uint32_t xcd = blockIdx.x & 7, pos = xcd * (tiles >> 3) + min(xcd, tiles & 7) + (blockIdx.x >> 3);
   const int64_t r0 = pos / tiles_c * (int64_t)kActRows, c0 = pos % tiles_c * (int64_t)kActCols;
   const int64_t used = rows_in_use(a);
   if (r0 >= used) return;
-  const int lc = (t & 7) * 8, lr = t >> 3;
+  const int lc = (t & 3) * 16, lr = t >> 2;
   const bool in_c = c0 + lc < a.cols;
   const void *src[3] = {a.dh, a.gate, a.up};
-  Raw8<true> raw[NP][3];
+  Raw8<true> raw[NP][3][2];
 #pragma unroll
   for (int p = 0; p < NP; ++p)
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-      const int64_t r = r0 + lr + 32 * p;
-      raw[p][k] = Raw8<true>{};
-      if (in_c && r < used && src[k]) raw[p][k] = load8<true>(src[k], r * a.cols + c0 + lc);
+      const int64_t r = r0 + lr + 64 * p;
+      raw[p][k][0] = raw[p][k][1] = Raw8<true>{};
+      if (in_c && r < used && src[k]) {
+        raw[p][k][0] = load8<true>(src[k], r * a.cols + c0 + lc);
+        raw[p][k][1] = load8<true>(src[k], r * a.cols + c0 + lc + 8);
+      }
     }
-  float v[3][NP][8];                                 // dgate, dup, h
+  const sshdp_mx_out *out[3] = {&a.dgate, &a.dup, &a.h};
+  float v[3][NP][16];                                // dgate, dup, h
+  uint32_t sbs[3] = {0, 0, 0};                       // lane p of 4: the scales of its row of pass p
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
-    float d[8], g[8], u[8];
-    unpack8<true>(raw[p][0], d);
-    unpack8<true>(raw[p][1], g);
-    unpack8<true>(raw[p][2], u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const Act r = act_grad(d[j], g[j], u[j]);
-      v[0][p][j] = r.dg;
-      v[1][p][j] = r.du;
-      v[2][p][j] = r.h;
+    for (int h = 0; h < 2; ++h) {
+      float d[8], g[8], u[8];
+      unpack8<true>(raw[p][0][h], d);
+      unpack8<true>(raw[p][1][h], g);
+      unpack8<true>(raw[p][2][h], u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const Act r = act_grad(d[j], g[j], u[j]);
+        v[0][p][8 * h + j] = r.dg;
+        v[1][p][8 * h + j] = r.du;
+        v[2][p][8 * h + j] = r.h;
+      }
     }
-    const int rr = lr + 32 * p;
+    const int rr = lr + 64 * p;
     const int64_t e = (r0 + rr) * a.cols + c0 + lc;
-    const bool in = in_c && r0 + rr < used;
-    put_rows(a.dgate, v[0][p], e, in, t);
-    put_rows(a.dup, v[1][p], e, in, t);
-    put_rows(a.h, v[2][p], e, in, t);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      if (!out[k]->codes) continue;
+      uint32_t sb;
+      const u32x4r_t x = mx_codes2(v[k][p], sb);
+      if (in_c && r0 + rr < used) __builtin_nontemporal_store(x, reinterpret_cast<u32x4r_t *>(out[k]->codes + e));
+      // the row's two scale bytes, in all of its 4 lanes
+      uint32_t q = sb << (8 * ((t & 3) >> 1));
+      q |= (uint32_t)__builtin_amdgcn_mov_dpp((int)q, 0x4E, 0xF, 0xF, true);      // quad_perm [2, 3, 0, 1]
+      if ((t & 3) == p) sbs[k] = q;
+    }
   }
-  const sshdp_mx_out *out[3] = {&a.dgate, &a.dup, &a.h};
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    typedef uint16_t u16u_t __attribute__((aligned(1)));
+    const int64_t r = r0 + lr + 64 * (t & 3);
+    if (!out[k]->codes || (t & 3) >= NP || r >= used) continue;
+    uint8_t *d = out[k]->scales + r * (a.cols >> 5) + (c0 >> 5);
+    if (c0 + 32 < a.cols) *reinterpret_cast<u16u_t *>(d) = (uint16_t)sbs[k];
+    else *d = (uint8_t)sbs[k];
+  }
   const int grp = t & 3, c = t >> 2;
   const int64_t e = (c0 + c) * a.rows + r0;
   const int blocks = (int)min<int64_t>(4, (used - r0 + 31) / 32);
@@ -122,9 +146,10 @@ __global__ __launch_bounds__(256) void k_act_tiles(sshdp_swiglu_grad a, uint32_t
     first = false;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-      float4 *q = reinterpret_cast<float4 *>(&sm[lr + 32 * p][lc ^ (16 * p)]);
-      q[0] = make_float4(v[k][p][0], v[k][p][1], v[k][p][2], v[k][p][3]);
-      q[1] = make_float4(v[k][p][4], v[k][p][5], v[k][p][6], v[k][p][7]);
+      const int rr = lr + 64 * p;
+      float4 *q = reinterpret_cast<float4 *>(&sm[rr][lc ^ (16 * (rr >> 5))]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = make_float4(v[k][p][4 * i], v[k][p][4 * i + 1], v[k][p][4 * i + 2], v[k][p][4 * i + 3]);
     }
     __syncthreads();
     if (c0 + c >= a.cols) continue;

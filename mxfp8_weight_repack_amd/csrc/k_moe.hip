@@ -221,7 +221,7 @@ __global__ __launch_bounds__(256) void k_moe_rows(sshdp_moe_gather a, uint32_t r
 }
 
 constexpr int kMtRows = 128, kMtCols = 128;          // tile of one workgroup
-constexpr int64_t kMtLeast = 1024;                   // fewer leave CUs without work
+constexpr int64_t kMtLeast = 512;                   // fewer leave CUs without work
 
 // Tiles, where there are enough of them or columns are wanted: the tile of k_quant_tiles (LDS
 // columns rotated by the row group, a lane two columns' 32 rows), its rows fetched by `source`,
@@ -229,60 +229,97 @@ constexpr int64_t kMtLeast = 1024;                   // fewer leave CUs without 
 // XCD i % 8 takes a contiguous eighth of the tiles column by column, so that what it reads of x
 // at one time, 128 columns of all tokens, stays in its L2 (26624 x 2048 bfloat16 of 4093 tokens,
 // rows tile by tile instead: both ways 46 against 31 us).
+// Along the rows a lane takes 16 elements, 16 codes a store, and keeps the scales of its rows'
+// four blocks until one store has them all: a store instruction's cost does not go by its bytes.
 template <bool BF16, bool WEIGHTED>
 __global__ __launch_bounds__(256) void k_moe_tiles(sshdp_moe_gather a, uint32_t tiles_r, uint32_t tiles) {
-  constexpr int ES = BF16 ? 2 : 4, ROT = BF16 ? 32 : 16, NP = kMtRows / 16;
+  constexpr int ES = BF16 ? 2 : 4, ROT = BF16 ? 32 : 16, NP = kMtRows / 32;
   __shared__ __align__(16) char sm[kMtRows * kMtCols * ES];
   __shared__ float sw[WEIGHTED ? kMtRows : 1];
   const int t = threadIdx.x;
   const uint32_t xcd = blockIdx.x & 7, pos = xcd * (tiles >> 3) + min(xcd, tiles & 7) + (blockIdx.x >> 3);
   const int64_t r0 = pos % tiles_r * (int64_t)kMtRows, c0 = pos / tiles_r * (int64_t)kMtCols;
-  const int lc = (t & 15) * 8, lr = t >> 4;
+  const int lc = (t & 7) * 16, lr = t >> 3;
   const bool in_c = c0 + lc < a.cols;
   int slot[NP];
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
-    const int64_t r = r0 + lr + 16 * p;
+    const int64_t r = r0 + lr + 32 * p;
     slot[p] = r < a.rows ? a.source[r] : -1;
   }
   const int64_t used = rows_in_use(a);
   if (r0 >= used) return;
-  Raw8<BF16> raw[NP];
+  Raw8<BF16> raw[NP][2];
   float w[NP];
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
-    const int token = r0 + lr + 16 * p < used ? token_of(a, slot[p]) : -1;
-    raw[p] = Raw8<BF16>{};
+    const int token = r0 + lr + 32 * p < used ? token_of(a, slot[p]) : -1;
+    raw[p][0] = raw[p][1] = Raw8<BF16>{};
     w[p] = 0.f;
     if (token >= 0) {
       if (WEIGHTED) w[p] = a.weights[slot[p]];
-      if (in_c) raw[p] = load8<BF16>(a.x, token * a.ld_x + c0 + lc);
+      if (in_c) {
+        raw[p][0] = load8<BF16>(a.x, token * a.ld_x + c0 + lc);
+        raw[p][1] = load8<BF16>(a.x, token * a.ld_x + c0 + lc + 8);
+      }
     }
   }
+  uint32_t sbs = 0;                                  // lane p of 8: the scales of its row of pass p
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
-    const int rr = lr + 16 * p;
+    const int rr = lr + 32 * p;
     if (a.out.codes_t) {
-      *reinterpret_cast<Raw8<BF16> *>(sm + (rr * kMtCols + (lc ^ ((rr >> 5) * ROT))) * ES) = raw[p];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<Raw8<BF16> *>(sm + (rr * kMtCols + ((lc + 8 * h) ^ (p * ROT))) * ES) = raw[p][h];
       if (WEIGHTED && lc == 0) sw[rr] = w[p];
     }
     const bool in = in_c && r0 + rr < used;
     const int64_t e = (r0 + rr) * a.cols + c0 + lc;
-    float v[8];
+    float v[16];
     if (WEIGHTED) {
-      unpack8<BF16>(raw[p], v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= w[p];
-      if (a.y && in) store8<BF16>(a.y, e, pack8<BF16>(v));
-    } else if (a.y && in) {
-      store8<BF16>(a.y, e, raw[p]);
+      for (int h = 0; h < 2; ++h) {
+        float x[8];
+        unpack8<BF16>(raw[p][h], x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[8 * h + j] = x[j] *= w[p];
+        if (a.y) raw[p][h] = pack8<BF16>(x);
+      }
+    }
+    if (a.y) {
+      if constexpr (BF16) {
+        u32x4r_t x[2];
+        mx_in_runs(raw[p][0].w, raw[p][1].w, t, x);
+        u32x4r_t *d = reinterpret_cast<u32x4r_t *>(static_cast<uint16_t *>(a.y) + e - (t & 3) * 16) + (t & 3);
+        const int64_t c = c0 + (lc & ~63);             // the four lanes' first column: a store is a block of 32
+        if (r0 + rr < used && c < a.cols) __builtin_nontemporal_store(x[0], d);
+        if (r0 + rr < used && c + 32 < a.cols) __builtin_nontemporal_store(x[1], d + 4);
+      } else if (in) {                               // ordinary stores: the L2 puts the lines together
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          reinterpret_cast<u32x4r_t *>(static_cast<float *>(a.y) + e)[k] = raw[p][k >> 1].w[k & 1];
+      }
     }
     if (!a.out.codes) continue;
     uint32_t sb;
-    const u32x2_t x = WEIGHTED ? mx_codes4(v, sb) : mx_codes4_raw<BF16>(raw[p], sb);
-    if (!in) continue;
-    __builtin_nontemporal_store(x, reinterpret_cast<u32x2_t *>(a.out.codes + e));
-    if ((t & 3) == 0) a.out.scales[e >> 5] = (uint8_t)sb;
+    const u32x4r_t x = WEIGHTED ? mx_codes2(v, sb) : mx_codes2_raw<BF16>(raw[p], sb);
+    if (in) __builtin_nontemporal_store(x, reinterpret_cast<u32x4r_t *>(a.out.codes + e));
+    // the row's four scale bytes in a word, in all of its 8 lanes
+    uint32_t q = sb << (8 * ((t & 7) >> 1));
+    q |= (uint32_t)__builtin_amdgcn_mov_dpp((int)q, 0x4E, 0xF, 0xF, true);        // quad_perm [2, 3, 0, 1]
+    q |= (uint32_t)__builtin_amdgcn_mov_dpp((int)q, 0x141, 0xF, 0xF, true);       // row_half_mirror
+    if ((t & 7) == p) sbs = q;
+  }
+  if (a.out.codes && (t & 7) < NP) {
+    typedef uint32_t u32u_t __attribute__((aligned(1)));
+    const int64_t r = r0 + lr + 32 * (t & 7);
+    uint8_t *d = a.out.scales + r * (a.cols >> 5) + (c0 >> 5);
+    const int n = (int)min<int64_t>(4, (a.cols - c0) >> 5);
+    if (r < used) {
+      if (n == 4) *reinterpret_cast<u32u_t *>(d) = sbs;
+      else for (int k = 0; k < n; ++k) d[k] = (uint8_t)(sbs >> (8 * k));
+    }
   }
   if (!a.out.codes_t) return;
   __syncthreads();

@@ -64,6 +64,49 @@ __device__ __forceinline__ u32x2_t mx_codes4_raw(const Raw8<BF16> &r, uint32_t &
   }
 }
 
+// 16 codes of a lane's 16 elements and its block's scale byte, 2 aligned lanes a block.  Every
+// lane of the wave must call it.
+__device__ __forceinline__ u32x4r_t mx_codes2(const float (&v)[16], uint32_t &sb) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) a = max(a, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  a = max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0xB1, 0xF, 0xF, true));      // quad_perm [1, 0, 3, 2]
+  sb = mx_scale_byte(a);
+  const float s = mx_scale_float(sb);
+  u32x4r_t c;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) c[j] = mx_or_nan(mx_cvt4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], s), sb);
+  return c;
+}
+
+// The same of 16 elements as loaded.
+template <bool BF16>
+__device__ __forceinline__ u32x4r_t mx_codes2_raw(const Raw8<BF16> (&r)[2], uint32_t &sb) {
+  if constexpr (BF16) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = mx_max_bf16(m, r[j >> 2].w[j & 3]);
+    uint32_t a = max(m << 16, m & 0xFFFF0000u);
+    a = max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0xB1, 0xF, 0xF, true));
+    sb = mx_scale_byte(a);
+    const float s = mx_scale_float(sb);
+    u32x4r_t c;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = mx_or_nan(mx_cvt4_bf16(r[j >> 1].w[2 * (j & 1)], r[j >> 1].w[2 * (j & 1) + 1], s), sb);
+    return c;
+  } else {
+    float v[16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float x[8];
+      unpack8<BF16>(r[h], x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[8 * h + j] = x[j];
+    }
+    return mx_codes2(v, sb);
+  }
+}
+
 // One block's 32 codes that a lane holds alone.
 struct MxColumn {
   u32x4r_t codes[2];
@@ -101,22 +144,27 @@ __device__ __forceinline__ void mx_columns_bf16(const uint32_t (&x)[32], MxColum
   }
 }
 
+// Two 16-byte chunks a lane, 32 bytes apart from lane to lane, exchanged within 4 aligned lanes
+// so that each of two stores writes 64 bytes in a row: store k takes the chunks of the lanes
+// 2 k and 2 k + 1, and chunk lane & 3 of them.  Every lane of the four must call it.
+__device__ __forceinline__ void mx_in_runs(const u32x4r_t &lo, const u32x4r_t &hi, int lane, u32x4r_t (&w)[2]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    // quad_perm [0, 0, 1, 1] and [2, 2, 3, 3]: two lanes a source, one a half
+    const int a0 = __builtin_amdgcn_mov_dpp((int)lo[j], 0x50, 0xF, 0xF, true), a1 = __builtin_amdgcn_mov_dpp((int)hi[j], 0x50, 0xF, 0xF, true);
+    const int b0 = __builtin_amdgcn_mov_dpp((int)lo[j], 0xFA, 0xF, 0xF, true), b1 = __builtin_amdgcn_mov_dpp((int)hi[j], 0xFA, 0xF, 0xF, true);
+    w[0][j] = (uint32_t)(lane & 1 ? a1 : a0);
+    w[1][j] = (uint32_t)(lane & 1 ? b1 : b0);
+  }
+}
+
 // A column's 128 rows of codes from the 4 lanes (aligned to 4) that hold its 4 blocks: lane l's
-// is block l.  Stored as they are, the lanes' 16 bytes lie 32 apart; exchanged within the four,
-// each store writes 64 bytes in a row (the gradients' 26624 x 1408 columns 18 us each against
-// 11).  `at`: block 0's place; `blocks`: how many of the 4 are stored.  Every lane of the four
-// must call it.
+// is block l (stored lane by lane the gradients' 26624 x 1408 columns took 18 us each, in runs
+// 11).  `at`: block 0's place; `blocks`: how many of the 4 are stored.
 __device__ __forceinline__ void mx_store_column(const MxColumn &c, uint8_t *at, int blocks, int lane) {
   const int l = lane & 3;
   u32x4r_t w[2];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    // quad_perm [0, 0, 1, 1] and [2, 2, 3, 3]: two lanes a block, one a half
-    const int a0 = __builtin_amdgcn_mov_dpp((int)c.codes[0][j], 0x50, 0xF, 0xF, true), a1 = __builtin_amdgcn_mov_dpp((int)c.codes[1][j], 0x50, 0xF, 0xF, true);
-    const int b0 = __builtin_amdgcn_mov_dpp((int)c.codes[0][j], 0xFA, 0xF, 0xF, true), b1 = __builtin_amdgcn_mov_dpp((int)c.codes[1][j], 0xFA, 0xF, 0xF, true);
-    w[0][j] = (uint32_t)(l & 1 ? a1 : a0);
-    w[1][j] = (uint32_t)(l & 1 ? b1 : b0);
-  }
+  mx_in_runs(c.codes[0], c.codes[1], l, w);
   u32x4r_t *d = reinterpret_cast<u32x4r_t *>(at + 16 * l);
   if ((l >> 1) < blocks) __builtin_nontemporal_store(w[0], d);
   if (2 + (l >> 1) < blocks) __builtin_nontemporal_store(w[1], d + 4);
