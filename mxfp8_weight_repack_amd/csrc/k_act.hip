@@ -67,15 +67,15 @@ constexpr int kActRows = 128, kActCols = 64;         // tile of one workgroup
 // Columns too: a lane computes 16 elements of 2 rows, stores their codes (the scales of the two
 // in one store) and keeps the three results; one result after the other goes through LDS, from
 // which a lane takes 32 rows of one column.  LDS columns are rotated by the row group, so the 4
-// groups that a wave reads at one step fall on different banks.  Bound by the number of store
+// groups that a wave reads at one step fall on different banks.  Tiles go along the rows, all
+// XCDs side by side: 26624 x 1408 97 us, each XCD in an eighth of the rows 107.  Bound by the number of store
 // instructions as much as by their bytes: with 8 elements a lane and a store for each row's
 // scales 26624 x 1408 took 102-111 us.
-__global__ __launch_bounds__(256) void k_act_tiles(sshdp_swiglu_grad a, uint32_t tiles_c, uint32_t tiles) {
+__global__ __launch_bounds__(256) void k_act_tiles(sshdp_swiglu_grad a, uint32_t tiles_c) {
   constexpr int NP = kActRows / 64;
   __shared__ __align__(16) float sm[kActRows][kActCols];
   const int t = threadIdx.x;
-  const uint32_t xcd = blockIdx.x & 7, pos = xcd * (tiles >> 3) + min(xcd, tiles & 7) + (blockIdx.x >> 3);
-  const int64_t r0 = pos / tiles_c * (int64_t)kActRows, c0 = pos % tiles_c * (int64_t)kActCols;
+  const int64_t r0 = blockIdx.x / tiles_c * (int64_t)kActRows, c0 = blockIdx.x % tiles_c * (int64_t)kActCols;
   const int64_t used = rows_in_use(a);
   if (r0 >= used) return;
   const int lc = (t & 3) * 16, lr = t >> 2;
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(256) void k_act_tiles(sshdp_swiglu_grad a, uint32_t
 hipError_t launch_swiglu_grad(const sshdp_swiglu_grad &a, hipStream_t s) {
   if (a.dgate.codes_t || a.dup.codes_t || a.h.codes_t) {
     const int64_t tc = (a.cols + kActCols - 1) / kActCols, tr = (a.rows + kActRows - 1) / kActRows;
-    hipLaunchKernelGGL(k_act_tiles, dim3((unsigned)(tr * tc)), dim3(256), 0, s, a, (uint32_t)tc, (uint32_t)(tr * tc));
+    hipLaunchKernelGGL(k_act_tiles, dim3((unsigned)(tr * tc)), dim3(256), 0, s, a, (uint32_t)tc);
   } else {
     const int64_t runs = a.rows * (a.cols / 8);
     hipLaunchKernelGGL(k_act_rows, dim3((unsigned)std::min<int64_t>((runs + 255) / 256, 1 << 20)), dim3(256), 0, s, a);

@@ -91,10 +91,15 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_place(const I *ids, int64_
     const int e = t % pitch, parts = kSortThreads / pitch;
     if (e < experts) {
       int all = 0, mine = 0;
-      for (int c = t / pitch; c < (int)gridDim.x; c += parts) {
-        const int v = counts[(int64_t)c * experts + e];
-        all += v;
-        if (c < (int)blockIdx.x) mine += v;
+      for (int c0 = t / pitch; c0 < (int)gridDim.x; c0 += 8 * parts) {
+        int v[8];                                     // in flight together
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c0 + i * parts < (int)gridDim.x ? counts[(int64_t)(c0 + i * parts) * experts + e] : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          all += v[i];
+          mine += c0 + i * parts < (int)blockIdx.x ? v[i] : 0;
+        }
       }
       atomicAdd(&total[e], all);
       atomicAdd(&before[e], mine);
@@ -293,8 +298,8 @@ __global__ __launch_bounds__(256) void k_moe_tiles(sshdp_moe_gather a, uint32_t 
         mx_in_runs(raw[p][0].w, raw[p][1].w, t, x);
         u32x4r_t *d = reinterpret_cast<u32x4r_t *>(static_cast<uint16_t *>(a.y) + e - (t & 3) * 16) + (t & 3);
         const int64_t c = c0 + (lc & ~63);             // the four lanes' first column: a store is a block of 32
-        if (r0 + rr < used && c < a.cols) __builtin_nontemporal_store(x[0], d);
-        if (r0 + rr < used && c + 32 < a.cols) __builtin_nontemporal_store(x[1], d + 4);
+        if (r0 + rr < used && c < a.cols) *d = x[0];            // (as nontemporal stores 32 us for 24)
+        if (r0 + rr < used && c + 32 < a.cols) d[4] = x[1];
       } else if (in) {                               // ordinary stores: the L2 puts the lines together
 #pragma unroll
         for (int k = 0; k < 4; ++k)
