@@ -7,11 +7,18 @@ namespace sshdp {
 // The sigmoid: off by at most (1.25 |x| + 6) 2^-24 of itself for x under 0 (the rounding of the
 // exponent x log2(e) and of log2(e) grow with x: 1.23 of them), 2^-21 over it; 0 from about -88
 // on, where it leaves float32's normal range.  Four instructions: a gated tile has 32 of them
-// a lane at its end.
-__device__ __forceinline__ float sigmoid(float x) {
+// a lane at its end, and its sums are not nearer than that.
+__device__ __forceinline__ float sigmoid_near(float x) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * -1.44269504f));
 }
 
-__device__ __forceinline__ float swiglu(float gate, float up) { return gate * sigmoid(gate) * up; }
+// The same within 2^-21 for any x: what the exponent's rounding and log2(e)'s leave out is
+// multiplied back in.  For where memory is what takes the time.
+__device__ __forceinline__ float sigmoid(float x) {
+  constexpr float L = 1.44269504f, l = 1.92596299e-8f;        // log2(e) and what float32 leaves of it
+  const float y = __builtin_amdgcn_fmed3f(-x, -88.f, 88.f), hi = y * L, lo = fmaf(y, l, fmaf(y, L, -hi));
+  const float e = __builtin_amdgcn_exp2f(hi);
+  return x < -87.f ? 0.f : __builtin_amdgcn_rcpf(1.f + fmaf(e * lo, 0.693147181f, e));
+}
 
 }  // namespace sshdp

@@ -154,7 +154,8 @@ __device__ __forceinline__ void finish_gated(const GemmGrouped &g, const GemmMx 
       uint32_t a = 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        h[k] = swiglu(acc[2 * b + (k >> 2)][j][k & 3], acc[HP + 2 * b + (k >> 2)][j][k & 3]);
+        const float gate = acc[2 * b + (k >> 2)][j][k & 3];
+        h[k] = gate * sigmoid_near(gate) * acc[HP + 2 * b + (k >> 2)][j][k & 3];
         a = max(a, __float_as_uint(h[k]) & 0x7FFFFFFFu);
       }
       const auto x = __builtin_amdgcn_permlane16_swap(a, a, false, false);   // the lanes 16 apart
@@ -577,7 +578,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        h[4 * c + k] = swiglu(gate[k], up[k]);
+        h[4 * c + k] = gate[k] * sigmoid(gate[k]) * up[k];
         m = max(m, __float_as_uint(h[4 * c + k]) & 0x7FFFFFFFu);
       }
     }
