@@ -496,9 +496,7 @@ __device__ __forceinline__ void store_part(const GemmMx &p, float *parts, int64_
 
 // A tile's sums over a wave group's steps, which must be at least one, by the 8-bit matrix
 // instruction.  Every load to LDS has landed when it returns; other waves may still read theirs.
-// EARLY: the second stage's loads go out before the first scales have come, which saves short
-// products one trip to memory.
-template <class C, bool NN, bool SHORT, bool EARLY = false, class L>
+template <class C, bool NN, bool SHORT, class L>
 __device__ __forceinline__ void sums8(const L &ld, char *smem, f32x4_t (&acc)[C::FP][C::FQ]) {
   const int lane = ld.lane, wave = ld.wave, wn = wave / C::WM, wm = wave % C::WM;
   const int r = lane & 15, g = lane >> 4;
@@ -577,19 +575,13 @@ __device__ __forceinline__ void sums8(const L &ld, char *smem, f32x4_t (&acc)[C:
   u32x4_t sw = ld.template scales<SHORT>(0);
   ld.load_p(smem, 0, 0);
   ld.load_q(smem, 0, 0);
-  if (!EARLY) put_scales(sw, 0);
+  put_scales(sw, 0);
 #pragma unroll
   for (int st = 1; st < C::NST; ++st) {
     ld.load_p(smem, st, min(st, nk - 1));
     ld.load_q(smem, st, min(st, nk - 1));
   }
-  if (EARLY) {
-    const u32x4_t first = sw;
-    if (!SHORT) sw = ld.template scales<false>(1);
-    put_scales(first, 0);
-  } else if (!SHORT) {
-    sw = ld.template scales<false>(1);
-  }
+  if (!SHORT) sw = ld.template scales<false>(1);
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(0) : "memory");
   __syncthreads();
 #pragma unroll
@@ -670,8 +662,9 @@ __device__ __forceinline__ void sums8(const L &ld, char *smem, f32x4_t (&acc)[C:
 // matrix instructions.  A half step is one 16-byte chunk per lane (64 k): its m-side fragments
 // stay converted while the n side's pass by, one converted (8 conversions) beside the previous
 // one's 2 x FQ matrix instructions.
-// `beside` issues BESIDE other loads behind the first two stages'; the first two steps do not
-// wait for them.
+// EARLY: the second stage's loads go out before the first scales have come, which saves a trip to
+// memory where ranges are short.  `beside` issues BESIDE other loads behind the first two stages';
+// the first two steps do not wait for them.
 template <class C, bool NN, bool SHORT, bool EARLY, int BESIDE, class L, class B>
 __device__ __forceinline__ void sums16(const L &ld, char *smem, f32x4_t (&acc)[C::FP][C::FQ], B beside) {
   const int lane = ld.lane, wave = ld.wave, wn = wave / C::WM, wm = wave % C::WM;

@@ -70,11 +70,11 @@ __device__ __forceinline__ bool find_piece(const int32_t *offsets, int groups, i
   return false;
 }
 
-// All pieces.
+// All pieces.  Experts whose rows overlap have more of them than an int counts.
 template <int PIECE>
-__device__ __forceinline__ int count_pieces(const int32_t *offsets, int groups, int rows) {
+__device__ __forceinline__ int64_t count_pieces(const int32_t *offsets, int groups, int rows) {
   const int lane = threadIdx.x & 63;
-  int total = 0;
+  int64_t total = 0;
   for (int e0 = 0; e0 < groups; e0 += 64) {
     int first, n;
     rows_of(offsets, groups, rows, e0 + lane, first, n);
@@ -88,7 +88,8 @@ __device__ __forceinline__ int count_pieces(const int32_t *offsets, int groups, 
 // XCD runs at once share an expert's panels.
 template <int TM>
 __device__ __forceinline__ bool find_tile(const GemmGrouped &g, int tiles_n, Found &f, int &tn) {
-  const int total = count_pieces<TM>(g.offsets, g.groups, (int)g.p.m) * tiles_n;
+  // the launch has a workgroup for every tile of offsets that do not run backwards
+  const int total = (int)min(count_pieces<TM>(g.offsets, g.groups, (int)g.p.m) * tiles_n, (int64_t)gridDim.x);
   const int id = blockIdx.x, q = total >> 3, rem = total & 7, x = id & 7;
   if (id >= total) return false;
   const int pos = x * q + min(x, rem) + (id >> 3);
