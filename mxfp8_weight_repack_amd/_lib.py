@@ -110,14 +110,14 @@ class MxMatrix(ctypes.Structure):
                 ("cols", ctypes.c_int64), ("layout", ctypes.c_int32), ("pad_", ctypes.c_int32)]
 
 
-class MxOut(ctypes.Structure):
-    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("codes_t", ctypes.c_void_p),
-                ("scales_t", ctypes.c_void_p)]
+def _mx_out(name):
+    """The fields of an sshdp_mx_out, laid flat in the struct that holds it (a call then fills one struct)."""
+    return [(f"{name}_{f}", ctypes.c_void_p) for f in ("codes", "scales", "codes_t", "scales_t")]
 
 
 class MoeGather(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("source", ctypes.c_void_p),
-                ("offsets", ctypes.c_void_p), ("y", ctypes.c_void_p), ("out", MxOut), ("tokens", ctypes.c_int64),
+                ("offsets", ctypes.c_void_p), ("y", ctypes.c_void_p), *_mx_out("out"), ("tokens", ctypes.c_int64),
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld_x", ctypes.c_int64),
                 ("top_k", ctypes.c_int32), ("experts", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("pad_", ctypes.c_int32)]
@@ -133,7 +133,7 @@ class MoeCombine(ctypes.Structure):
 class MoeCombineGrad(ctypes.Structure):
     _fields_ = [("dout", ctypes.c_void_p), ("y", ctypes.c_void_p), ("weights", ctypes.c_void_p),
                 ("place", ctypes.c_void_p), ("source", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
-                ("dy", ctypes.c_void_p), ("out", MxOut), ("dweights", ctypes.c_void_p), ("tokens", ctypes.c_int64),
+                ("dy", ctypes.c_void_p), *_mx_out("out"), ("dweights", ctypes.c_void_p), ("tokens", ctypes.c_int64),
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld_dout", ctypes.c_int64),
                 ("top_k", ctypes.c_int32), ("experts", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("pad_", ctypes.c_int32)]
@@ -141,8 +141,9 @@ class MoeCombineGrad(ctypes.Structure):
 
 class SwigluGrad(ctypes.Structure):
     _fields_ = [("dh", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("up", ctypes.c_void_p),
-                ("offsets", ctypes.c_void_p), ("dgate", MxOut), ("dup", MxOut), ("h", MxOut), ("rows", ctypes.c_int64),
-                ("cols", ctypes.c_int64), ("groups", ctypes.c_int32), ("pad_", ctypes.c_int32)]
+                ("offsets", ctypes.c_void_p), *_mx_out("dgate"), *_mx_out("dup"), *_mx_out("h"),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("groups", ctypes.c_int32),
+                ("pad_", ctypes.c_int32)]
 
 
 # every symbol include/sshdp.h declares, with its argument and return types
@@ -505,9 +506,7 @@ INDEX = {"int32": 0, "int64": 1}    # SSHDP_INDEX_*
 
 def mx_pair(codes=None, scales=None, codes_t=None, scales_t=None):
     """An MXFP8 output along rows (codes, scales) and/or along columns (codes_t, scales_t)."""
-    o = MxOut(_ptr(codes), _ptr(scales), _ptr(codes_t), _ptr(scales_t))
-    o._keep = (codes, scales, codes_t, scales_t)
-    return o
+    return codes, scales, codes_t, scales_t
 
 
 def moe_rows(tokens, top_k, experts, align=1):
@@ -535,7 +534,7 @@ def moe_gather_mxfp8(x, source, offsets, tokens, top_k, experts, rows, cols, dty
                      codes=None, scales=None, codes_t=None, scales_t=None, ld_x=None, stream=None):
     """Tokens to the experts' rows (y, in x's type) and/or their MXFP8 along rows and columns."""
     a = MoeGather(_ptr(x), _ptr(weights), _ptr(source), _ptr(offsets), _ptr(y),
-                  MxOut(_ptr(codes), _ptr(scales), _ptr(codes_t), _ptr(scales_t)), tokens, rows, cols,
+                  _ptr(codes), _ptr(scales), _ptr(codes_t), _ptr(scales_t), tokens, rows, cols,
                   cols if ld_x is None else ld_x, top_k, experts, DTYPE.get(dtype, -1), 0)
     _check(lib().sshdp_moe_gather_mxfp8(ctypes.byref(a), _stream(stream)), "sshdp_moe_gather_mxfp8")
 
@@ -552,7 +551,7 @@ def moe_combine_backward(dout, y, weights, place, source, offsets, tokens, top_k
                          stream=None):
     """The gradient of y, as dy and/or MXFP8 along rows and columns, and of the weights."""
     a = MoeCombineGrad(_ptr(dout), _ptr(y), _ptr(weights), _ptr(place), _ptr(source), _ptr(offsets), _ptr(dy),
-                       MxOut(_ptr(codes), _ptr(scales), _ptr(codes_t), _ptr(scales_t)), _ptr(dweights), tokens, rows,
+                       _ptr(codes), _ptr(scales), _ptr(codes_t), _ptr(scales_t), _ptr(dweights), tokens, rows,
                        cols, cols if ld_dout is None else ld_dout, top_k, experts, DTYPE.get(dtype, -1), 0)
     _check(lib().sshdp_moe_combine_backward(ctypes.byref(a), _stream(stream)), "sshdp_moe_combine_backward")
 
@@ -576,8 +575,8 @@ def gemm_mxfp8_swiglu(a, gate_w, up_w, codes=None, scales=None, offsets=None, gr
 
 def swiglu_backward_mxfp8(dh, gate, up, rows, cols, offsets=None, groups=1, dgate=None, dup=None, h=None, stream=None):
     """The gradients of gate and up, and h = silu(gate) * up again, as MXFP8 (mx_pair outputs, None for none)."""
-    a = SwigluGrad(_ptr(dh), _ptr(gate), _ptr(up), _ptr(offsets), dgate or MxOut(), dup or MxOut(), h or MxOut(), rows,
-                   cols, groups, 0)
+    none = (None,) * 4
+    a = SwigluGrad(*map(_ptr, (dh, gate, up, offsets, *(dgate or none), *(dup or none), *(h or none))), rows, cols, groups, 0)
     _check(lib().sshdp_swiglu_backward_mxfp8(ctypes.byref(a), _stream(stream)), "sshdp_swiglu_backward_mxfp8")
 
 
