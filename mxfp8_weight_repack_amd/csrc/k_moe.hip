@@ -19,7 +19,9 @@ constexpr int kSortOnce = 4096;                      // slots that one workgroup
 constexpr int kSortMostChunks = 256;
 
 // Slots a workgroup takes: all of up to 4096, else the fewest of a power of two from 1024 on
-// that leave at most 256 workgroups, each of which reads every other's counts.
+// that leave at most 256 workgroups, each of which reads every other's counts.  Bound by trips
+// to memory and barriers: 16 tokens of 6 choices 4.7 us in one launch; 16384 x 6 slots of 64
+// experts 2.5 + 6.2 us in two, of 1.6 MB (0.3 us at a copy's rate).
 int64_t sort_chunk(int64_t slots) {
   if (slots <= kSortOnce) return kSortOnce;
   int64_t c = kSortThreads;
@@ -175,8 +177,9 @@ __device__ __forceinline__ int64_t rows_in_use(const sshdp_moe_gather &a) {
 
 constexpr int kMrRuns = 4;                           // runs of 8 elements a lane has in flight
 
-// Along the rows: 8 elements a lane and 4 lanes a block, 1024 consecutive runs of all rows a
-// workgroup.  A run waits for its row's source and then for the token: four of them together.
+// y, and the codes along the rows if wanted: 8 elements a lane and 4 lanes a block, 1024
+// consecutive runs of all rows a workgroup.  A run waits for its row's source and then for the
+// token: four of them together.
 template <bool BF16, bool WEIGHTED>
 __global__ __launch_bounds__(256) void k_moe_rows(sshdp_moe_gather a, uint32_t runs_per_row) {
   const int64_t used = rows_in_use(a), first = blockIdx.x * (int64_t)(256 * kMrRuns), row0 = first / runs_per_row;
@@ -212,8 +215,8 @@ __global__ __launch_bounds__(256) void k_moe_rows(sshdp_moe_gather a, uint32_t r
       unpack8<BF16>(raw[u], v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= w[u];
-      if (a.y && in) store8<BF16>(a.y, e * 8, pack8<BF16>(v));
-    } else if (a.y && in) {
+      if (in) store8<BF16>(a.y, e * 8, pack8<BF16>(v));
+    } else if (in) {
       store8<BF16>(a.y, e * 8, raw[u]);
     }
     if (!a.out.codes) continue;
@@ -226,14 +229,19 @@ __global__ __launch_bounds__(256) void k_moe_rows(sshdp_moe_gather a, uint32_t r
 }
 
 constexpr int kMtRows = 128, kMtCols = 128;          // tile of one workgroup
-constexpr int64_t kMtLeast = 512;                   // fewer leave CUs without work
+// Runs only with y wanted, whose stores weigh more than a tile's few of the codes, and only where
+// tiles are few: 960 x 8192 (512 tiles) 7.0 us by runs and 6.9 by tiles, float32 13.3 and 17.6;
+// 960 x 2048 (128) 4.6 and 5.1, 6.2 and 8.2; 7680 x 2048 (960) 11.5 and 11.9, 30.6 and 31.1; 24558 x
+// 2048 36.9 and 34.2, 86 and 81.  Codes alone 960 x 8192 6.3 and 4.7, 96 x 2048 4.0 and 3.7.
+constexpr int64_t kMtLeast = 768;
 
-// Tiles, where there are enough of them or columns are wanted: the tile of k_quant_tiles (LDS
+// Tiles, wherever runs do not serve better: the tile of k_quant_tiles (LDS
 // columns rotated by the row group, a lane two columns' 32 rows), its rows fetched by `source`,
 // their weights beside them.  A token is read once for each of its choices, by rows far apart:
 // XCD i % 8 takes a contiguous eighth of the tiles column by column, so that what it reads of x
 // at one time, 128 columns of all tokens, stays in its L2 (26624 x 2048 bfloat16 of 4093 tokens,
-// rows tile by tile instead: both ways 46 against 31 us).
+// both ways 28 us, 5.3 TB/s of the 148 MB that pass the L2; with rows tile by tile, before stores
+// were as wide, 46 against 31).
 // Along the rows a lane takes 16 elements, 16 codes a store, and keeps the scales of its rows'
 // four blocks until one store has them all: a store instruction's cost does not go by its bytes.
 template <bool BF16, bool WEIGHTED>
@@ -298,7 +306,8 @@ __global__ __launch_bounds__(256) void k_moe_tiles(sshdp_moe_gather a, uint32_t 
         mx_in_runs(raw[p][0].w, raw[p][1].w, t, x);
         u32x4r_t *d = reinterpret_cast<u32x4r_t *>(static_cast<uint16_t *>(a.y) + e - (t & 3) * 16) + (t & 3);
         const int64_t c = c0 + (lc & ~63);             // the four lanes' first column: a store is a block of 32
-        if (r0 + rr < used && c < a.cols) *d = x[0];            // (as nontemporal stores 32 us for 24)
+        // ordinary stores: nontemporal ones made y alone 32 us instead of 24
+        if (r0 + rr < used && c < a.cols) *d = x[0];
         if (r0 + rr < used && c + 32 < a.cols) d[4] = x[1];
       } else if (in) {                               // ordinary stores: the L2 puts the lines together
 #pragma unroll
@@ -372,7 +381,8 @@ __global__ __launch_bounds__(256) void k_moe_tiles(sshdp_moe_gather a, uint32_t 
 
 constexpr int kCombineAt = 8;                        // choices whose rows are in flight together
 
-// 8 elements of a token a lane: its choices' rows are read together and added in order.
+// 8 elements of a token a lane: its choices' rows are read together and added in order.  Bound by
+// HBM: 8191 tokens of 6 choices, 2048 bfloat16 and a residual 48 us, 5.5 TB/s.
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_moe_combine(sshdp_moe_combine_args a, int runs_per_row) {
   const int64_t runs = a.tokens * runs_per_row;
@@ -416,7 +426,7 @@ __global__ __launch_bounds__(256) void k_moe_combine(sshdp_moe_combine_args a, i
 }
 
 // The weights' gradient: a wave per token, 512 columns at a time, its choices' rows in flight
-// together.
+// together (4093 tokens of 6 choices, 2048 bfloat16: 20 us, 5.9 TB/s; a row after the other 35).
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_moe_dweights(sshdp_moe_combine_grad a) {
   const int lane = threadIdx.x & 63;
@@ -490,7 +500,7 @@ hipError_t launch_moe_gather(const sshdp_moe_gather &a, hipStream_t s) {
   auto run = [&](auto bf16, auto weighted) {
     constexpr bool B = decltype(bf16)::value, W = decltype(weighted)::value;
     const int64_t tr = (a.rows + kMtRows - 1) / kMtRows, tiles = tr * ((a.cols + kMtCols - 1) / kMtCols);
-    if (a.out.codes_t || tiles >= kMtLeast) {
+    if (a.out.codes_t || !a.y || tiles >= kMtLeast) {
       hipLaunchKernelGGL((k_moe_tiles<B, W>), dim3((unsigned)tiles), dim3(256), 0, s, a, (uint32_t)tr, (uint32_t)tiles);
     } else {
       const int64_t runs = a.rows * (a.cols / 8), each = 256 * kMrRuns;

@@ -173,6 +173,28 @@ def test_gather(tokens, top_k, experts, cols, align, dtype):
                 assert torch.equal(c2, c) and torch.equal(s2, s) and torch.equal(y2, yd)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("weighted", [False, True])
+@pytest.mark.parametrize("tokens,cols", [(1, 32), (16, 96), (333, 2080), (2100, 2048)])
+def test_gather_of_any_set_of_outputs(tokens, cols, weighted, dtype):
+    """Each output alone, and with the others: one set of bits, whichever kernel makes it."""
+    rng = np.random.default_rng(tokens)
+    ids = rng.integers(-1, 8, (tokens, 3))
+    offsets, _, source, rows = sort(ids, tokens, 3, 8, 32)
+    x = dev(rng.standard_normal((tokens, cols)).astype(np.float32), dtype)
+    w = dev(rng.standard_normal((tokens, 3)).astype(np.float32)) if weighted else None
+    made = {}
+    for names in (("y",), ("codes", "scales"), ("y", "codes", "scales"), ("codes_t", "scales_t"),
+                  ("y", "codes", "scales", "codes_t", "scales_t")):
+        out = dict(y=torch.full((rows, cols), 7.0, dtype=x.dtype, device="cuda"), codes=buf(rows, cols),
+                   scales=buf(rows, cols // 32), codes_t=buf(cols, rows), scales_t=buf(cols, rows // 32))
+        sh.moe_gather_mxfp8(x, source, offsets, tokens, 3, 8, rows, cols, dtype=dtype, weights=w, stream=stream(),
+                            **{n: out[n] for n in names})
+        for n in names:
+            got = host(out[n]).view(np.uint32 if n == "y" else np.uint8)
+            np.testing.assert_array_equal(got, made.setdefault(n, got))
+
+
 @pytest.mark.parametrize("both", [False, True])
 def test_gather_of_non_finite_tokens(both):
     """NaN and infinity stay in their own rows' (and columns') blocks; dropped tokens' are never read."""
