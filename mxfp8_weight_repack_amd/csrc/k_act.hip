@@ -41,7 +41,8 @@ __device__ __forceinline__ void put_column(const sshdp_mx_out &o, const float (&
   if ((lane & 3) < blocks) o.scales_t[(e >> 5) + (lane & 3)] = (uint8_t)c.scale;
 }
 
-// Along the rows alone: 8 elements a lane.
+// Along the rows alone: 8 elements a lane.  Bound by HBM: dgate and dup of 24576 x 1408 42 us, 6.7
+// TB/s (by the tiles below 47; 6 x 704 2.9 and 4.4).
 __global__ __launch_bounds__(256) void k_act_rows(sshdp_swiglu_grad a) {
   const int64_t runs = rows_in_use(a) * (a.cols >> 3);   // a multiple of 4: a block's lanes leave together
   for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < runs; i += (int64_t)gridDim.x * 256) {
@@ -68,9 +69,9 @@ constexpr int kActRows = 128, kActCols = 64;         // tile of one workgroup
 // in one store) and keeps the three results; one result after the other goes through LDS, from
 // which a lane takes 32 rows of one column.  LDS columns are rotated by the row group, so the 4
 // groups that a wave reads at one step fall on different banks.  Tiles go along the rows, all
-// XCDs side by side: 26624 x 1408 97 us, each XCD in an eighth of the rows 107.  Bound by the number of store
-// instructions as much as by their bytes: with 8 elements a lane and a store for each row's
-// scales 26624 x 1408 took 102-111 us.
+// XCDs side by side: 26624 x 1408, all ten outputs, 95 to 97 us (79 back to
+// back, part of the inputs still in the last-level cache: 4.9 TB/s), each XCD in an eighth of the rows 107.  Bound by HBM and by the number of
+// store instructions: with 8 elements a lane and a store for each row's scales 102 to 111 us.
 __global__ __launch_bounds__(256) void k_act_tiles(sshdp_swiglu_grad a, uint32_t tiles_c) {
   constexpr int NP = kActRows / 64;
   __shared__ __align__(16) float sm[kActRows][kActCols];
