@@ -218,10 +218,11 @@ __device__ __forceinline__ void add_bf16(const GemmMx &p, const uint16_t *addend
 
 // A tile of an expert's rows, bfloat16 or codes out.  Bound by the wait for operands at each step and,
 // in 256-tiles, by what one workgroup a CU has nothing to hide behind: its first operands and its
-// end (7 us of the 36 of a gated tile with K 2048).  24558 slots of 64 experts, products from HBM:
-// gated 2 x 1408 x 2048 with both kept 228 us (283 GFLOP, 606 MB; matrix cores 37% busy), by
-// 128-tiles 245; input gradient 2048 x 1408 129 us (142 GFLOP, 311 MB; 37%).  Workgroups that stay
-// and walk the tiles lose to the hardware's dealing: 146 us for the gradient.
+// end (8 us of the 37 of a gated tile with K 2048).  24558 slots of 64 experts, operands from HBM:
+// gated 2 x 1408 x 2048 with both kept 220 to 228 us (283 GFLOP, 606 MB; matrix cores 37% busy),
+// by 128-tiles 245; input gradient, K 2048 and 1408 columns, 125 to 129 us (142 GFLOP, 311 MB;
+// 37%).  Workgroups that stay and walk the tiles lose to the hardware's dealing: 146 us for the
+// gradient.
 template <class C, bool NN, bool SHORT, Form F>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C::WPS))) void k_group8(GemmGrouped g, int tiles_n) {
   __shared__ __align__(1024) char smem[C::LDS];
