@@ -47,54 +47,55 @@ struct Found {
   int at;                                            // which of its pieces
 };
 
-// The experts' rows in pieces of PIECE, one expert after the other; false past the last
-// piece.  Every lane of the wave must call it, with the same `at`.
+// 64 experts' rows, one a lane, in pieces of PIECE, one expert after the other.
 template <int PIECE>
-__device__ __forceinline__ bool find_piece(const int32_t *offsets, int groups, int rows, int at, Found &f) {
-  const int lane = threadIdx.x & 63;
-  for (int e0 = 0; e0 < groups; e0 += 64) {
-    int first, n;
-    rows_of(offsets, groups, rows, e0 + lane, first, n);
-    const int mine = (n + PIECE - 1) / PIECE, upto = scan_lanes(mine);
-    const uint64_t past = __ballot(upto > at);
-    if (past) {
-      const int l = __builtin_ctzll(past);
-      f.e = e0 + l;
-      f.first = __builtin_amdgcn_readlane(first, l);
-      f.rows = __builtin_amdgcn_readlane(n, l);
-      f.at = at - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(mine, l));
-      return true;
-    }
-    at -= __builtin_amdgcn_readlane(upto, 63);
-  }
-  return false;
-}
+struct Pieces {
+  int e0, first, n, mine, upto;                      // upto: of the experts e0 to the lane's
 
-// All pieces.  Experts whose rows overlap have more of them than an int counts.
-template <int PIECE>
-__device__ __forceinline__ int64_t count_pieces(const int32_t *offsets, int groups, int rows) {
-  const int lane = threadIdx.x & 63;
-  int64_t total = 0;
-  for (int e0 = 0; e0 < groups; e0 += 64) {
-    int first, n;
-    rows_of(offsets, groups, rows, e0 + lane, first, n);
-    total += __builtin_amdgcn_readlane(scan_lanes((n + PIECE - 1) / PIECE), 63);
+  __device__ __forceinline__ Pieces(const int32_t *offsets, int groups, int rows, int e0_) : e0(e0_) {
+    rows_of(offsets, groups, rows, e0 + (threadIdx.x & 63), first, n);
+    mine = (n + PIECE - 1) / PIECE;
+    upto = scan_lanes(mine);
   }
-  return total;
-}
+  __device__ __forceinline__ int all() const { return __builtin_amdgcn_readlane(upto, 63); }
+  // Piece `at` of them, the same for every lane; false past the last one.
+  __device__ __forceinline__ bool find(int at, Found &f) const {
+    const uint64_t past = __ballot(upto > at);
+    if (!past) return false;
+    const int l = __builtin_ctzll(past);
+    f.e = e0 + l;
+    f.first = __builtin_amdgcn_readlane(first, l);
+    f.rows = __builtin_amdgcn_readlane(n, l);
+    f.at = at - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(mine, l));
+    return true;
+  }
+};
 
 // A workgroup's tile: XCD i % 8 takes one contiguous eighth of an order that goes through the
 // experts, and through each one's tiles in strips of 4 along its rows, so the workgroups an
 // XCD runs at once share an expert's panels.
 template <int TM>
 __device__ __forceinline__ bool find_tile(const GemmGrouped &g, int tiles_n, Found &f, int &tn) {
-  // the launch has a workgroup for every tile of offsets that do not run backwards
-  const int total = (int)min(count_pieces<TM>(g.offsets, g.groups, (int)g.p.m) * tiles_n, (int64_t)gridDim.x);
+  const int rows = (int)g.p.m;
+  const Pieces<TM> head(g.offsets, g.groups, rows, 0);  // up to 64 experts are read once
+  int64_t pieces = head.all();
+  for (int e0 = 64; e0 < g.groups; e0 += 64) pieces += Pieces<TM>(g.offsets, g.groups, rows, e0).all();
+  // the launch has a workgroup for every tile of offsets that do not run backwards; experts whose
+  // rows overlap have more pieces than an int counts
+  const int total = (int)min(pieces * tiles_n, (int64_t)gridDim.x);
   const int id = blockIdx.x, q = total >> 3, rem = total & 7, x = id & 7;
   if (id >= total) return false;
   const int pos = x * q + min(x, rem) + (id >> 3);
   // tiles_n tiles to each of an expert's row pieces, taken strip by strip
-  if (!find_piece<TM>(g.offsets, g.groups, (int)g.p.m, pos / tiles_n, f)) return false;
+  if (!head.find(pos / tiles_n, f)) {
+    int at = pos / tiles_n - head.all(), e0 = 64;
+    for (; e0 < g.groups; e0 += 64) {
+      const Pieces<TM> some(g.offsets, g.groups, rows, e0);
+      if (some.find(at, f)) break;
+      at -= some.all();
+    }
+    if (e0 >= g.groups) return false;
+  }
   const int tiles_m = (f.rows + TM - 1) / TM, in = pos - (pos / tiles_n - f.at) * tiles_n;
   const int strip = in / (4 * tiles_n), rest = in - strip * 4 * tiles_n, h = min(4, tiles_m - 4 * strip);
   tn = rest / h;
