@@ -235,23 +235,34 @@ constexpr int kMtRows = 128, kMtCols = 128;          // tile of one workgroup
 // 2048 36.9 and 34.2, 86 and 81.  Codes alone 960 x 8192 6.3 and 4.7, 96 x 2048 4.0 and 3.7.
 constexpr int64_t kMtLeast = 768;
 
+// Column tiles side by side that an XCD takes row by row: two, where there are results along the
+// rows, whose runs of memory are then twice as long, and where half the L2 holds that much of x.
+// 24558 rows of 4093 bfloat16 tokens x 2048, both ways, 26 us, a column tile at a time 29; of 8192
+// tokens 52 and 51, 16384 129 and 124.
+uint32_t moe_band(const sshdp_moe_gather &a) {
+  const int64_t x = a.tokens * 2 * kMtCols * (a.dtype == SSHDP_DTYPE_BF16 ? 2 : 4);
+  return (a.y || a.out.codes) && x <= 2 << 20 ? 2 : 1;
+}
+
 // Tiles, wherever runs do not serve better: the tile of k_quant_tiles (LDS
 // columns rotated by the row group, a lane two columns' 32 rows), its rows fetched by `source`,
 // their weights beside them.  A token is read once for each of its choices, by rows far apart:
-// XCD i % 8 takes a contiguous eighth of the tiles column by column, so that what it reads of x
-// at one time, 128 columns of all tokens, stays in its L2 (26624 x 2048 bfloat16 of 4093 tokens,
-// both ways 28 us, 5.3 TB/s of the 148 MB that pass the L2; with rows tile by tile, before stores
-// were as wide, 46 against 31).
+// XCD i % 8 takes a contiguous eighth of the tiles, one or two columns of them at a time, so that
+// what it reads of x meanwhile, 128 or 256 columns of all tokens, stays in its L2 (24558 x 2048
+// bfloat16 of 4093 tokens, both ways 26 us, 119 MB at 4.6 TB/s, nearly all of it writes; with rows
+// tile by tile, before stores were as wide, 46 against 31).
 // Along the rows a lane takes 16 elements, 16 codes a store, and keeps the scales of its rows'
 // four blocks until one store has them all: a store instruction's cost does not go by its bytes.
 template <bool BF16, bool WEIGHTED>
-__global__ __launch_bounds__(256) void k_moe_tiles(sshdp_moe_gather a, uint32_t tiles_r, uint32_t tiles) {
+__global__ __launch_bounds__(256) void k_moe_tiles(sshdp_moe_gather a, uint32_t tiles_r, uint32_t tiles,
+                                                   uint32_t band) {
   constexpr int ES = BF16 ? 2 : 4, ROT = BF16 ? 32 : 16, NP = kMtRows / 32;
   __shared__ __align__(16) char sm[kMtRows * kMtCols * ES];
   __shared__ float sw[WEIGHTED ? kMtRows : 1];
   const int t = threadIdx.x;
   const uint32_t xcd = blockIdx.x & 7, pos = xcd * (tiles >> 3) + min(xcd, tiles & 7) + (blockIdx.x >> 3);
-  const int64_t r0 = pos % tiles_r * (int64_t)kMtRows, c0 = pos / tiles_r * (int64_t)kMtCols;
+  const uint32_t b = pos / (tiles_r * band), in_b = pos - b * tiles_r * band, wide = min(band, tiles / tiles_r - b * band);
+  const int64_t r0 = in_b / wide * (int64_t)kMtRows, c0 = (b * band + in_b % wide) * (int64_t)kMtCols;
   const int lc = (t & 7) * 16, lr = t >> 3;
   const bool in_c = c0 + lc < a.cols;
   int slot[NP];
@@ -501,7 +512,8 @@ hipError_t launch_moe_gather(const sshdp_moe_gather &a, hipStream_t s) {
     constexpr bool B = decltype(bf16)::value, W = decltype(weighted)::value;
     const int64_t tr = (a.rows + kMtRows - 1) / kMtRows, tiles = tr * ((a.cols + kMtCols - 1) / kMtCols);
     if (a.out.codes_t || !a.y || tiles >= kMtLeast) {
-      hipLaunchKernelGGL((k_moe_tiles<B, W>), dim3((unsigned)tiles), dim3(256), 0, s, a, (uint32_t)tr, (uint32_t)tiles);
+      hipLaunchKernelGGL((k_moe_tiles<B, W>), dim3((unsigned)tiles), dim3(256), 0, s, a, (uint32_t)tr, (uint32_t)tiles,
+                         moe_band(a));
     } else {
       const int64_t runs = a.rows * (a.cols / 8), each = 256 * kMrRuns;
       hipLaunchKernelGGL((k_moe_rows<B, W>), dim3((unsigned)((runs + each - 1) / each)), dim3(256), 0, s, a,
