@@ -15,16 +15,20 @@ namespace {
 // --------------------------------------------------------------------- slots by expert
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
-constexpr int kSortOnce = 4096;                      // slots that one workgroup sorts alone
+constexpr int kSortOnce = 2048;                      // slots that one workgroup sorts alone
 constexpr int kSortMostChunks = 256;
 
-// Slots a workgroup takes: all of up to 4096, else the fewest of a power of two from 1024 on
-// that leave at most 256 workgroups, each of which reads every other's counts.  Bound by trips
-// to memory and barriers: 16 tokens of 6 choices 4.7 us in one launch; 16384 x 6 slots of 64
-// experts 2.5 + 6.2 us in two, of 1.6 MB (0.3 us at a copy's rate).
+// Slots a workgroup takes, a power of two from 1024 (one for each lane) on: all of up to 2048,
+// else the fewest that leave at most 256 workgroups, each of which reads every other's counts.
+// Bound by trips to memory and barriers.  Of 64 experts: 512 slots 4.1 us by one workgroup with
+// a slot a lane, 7.0 with four; 2048 slots 5.9 by one, 6.8 in two launches; 4096 8.7 and 6.9; 98286
+// 8.1 (2.6 + 6.2 traced), of 1.6 MB, 0.3 us at a copy's rate.
 int64_t sort_chunk(int64_t slots) {
-  if (slots <= kSortOnce) return kSortOnce;
   int64_t c = kSortThreads;
+  if (slots <= kSortOnce) {
+    while (c < slots) c *= 2;
+    return c;
+  }
   while ((slots + c - 1) / c > kSortMostChunks) c *= 2;
   return c;
 }

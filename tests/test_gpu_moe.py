@@ -80,6 +80,14 @@ def test_sort(tokens, top_k, experts, align, how):
             np.testing.assert_array_equal(host(g)[:w.size], w, err_msg=name)
 
 
+@pytest.mark.parametrize("slots", [1, 63, 64, 65, 1023, 1024, 1025, 2047, 2048, 2049])
+def test_sort_where_the_split_changes(slots):
+    ids = np.random.default_rng(slots).integers(-1, 40, (slots, 1))
+    got = sort(ids, slots, 1, 39, 32)
+    for g, w in zip(got, M.sort(ids, 39, 32, got[3])):
+        np.testing.assert_array_equal(host(g)[:len(w)], w)
+
+
 def test_sort_of_wide_ids_and_roomy_buffers():
     """64-bit ids whose low halves name experts are dropped; more rows than needed are filled with -1."""
     say("sort, wide ids")
