@@ -17,7 +17,7 @@ struct Act {
 };
 __device__ __forceinline__ Act act_grad(float dh, float g, float u) {
   const float s = sigmoid(g), silu = g * s;
-  return {dh * u * fmaf(silu, 1.f - s, s), dh * silu, silu * u};
+  return {dh * u * (s * fmaf(g, 1.f - s, 1.f)), dh * silu, silu * u};
 }
 
 // Rows in use, whatever the offsets hold.

@@ -28,7 +28,7 @@ def near(g):
 
 
 def formula(dh, gate, up):
-    """{name: (value, bound)} in float64.  dgate's factor s + silu (1 - s) has each s off by near, 1 - s by that and a
+    """{name: (value, bound)} in float64.  dgate's factor s (1 + gate (1 - s)) has each s off by near, 1 - s by that and a
     rounding, in terms no larger than s (1 + |gate|); then five more roundings."""
     d, g, u = (t.double() for t in (dh, gate, up))
     s = torch.special.expit(g)
