@@ -640,8 +640,8 @@ int sshdp_gemm_mxfp8_grouped(const sshdp_mx_matrix *a, const sshdp_mx_matrix *b,
  *   gate = A Bg_e^T,  up = A Bu_e^T,  h = silu(gate) * up,
  *   silu(x) = x / (1 + exp(-x)),  codes, scales = G(h) along the rows (ROWMAJOR).
  * The products are sshdp_gemm_mxfp8's of bfloat16 output; h is computed in float32
- * (within (1.25 |gate| + 8) 2^-24 of itself) from the sums, before they are rounded.  `gate` and `up`
- * (both or neither) receive the products in bfloat16, what the backward pass
+ * (within (1.25 |gate| + 8) 2^-24 of itself) from the sums, before they are rounded.
+ * `gate` and `up` (both or neither) receive the products in bfloat16, what the backward pass
  * needs; codes and scales may be left out then.  All outputs are dense, A.rows x N,
  * N = gate_w.rows / groups a multiple of 32; gate_w and up_w have the same shape
  * and layout.  The rest is as in sshdp_gemm_mxfp8_grouped with SSHDP_GEMM_NT. */
@@ -653,10 +653,10 @@ int sshdp_gemm_mxfp8_swiglu(const sshdp_mx_matrix *a, const sshdp_mx_matrix *gat
  * sshdp_gemm_mxfp8_swiglu leaves them) and dh, the gradient of h,
  *   s = 1 / (1 + exp(-gate)):  dgate = dh * up * s * (1 + gate * (1 - s)),
  *   dup = dh * gate * s,  and h = gate * s * up once more,
- * each in float32 (with s within (1.25 |gate| + 8) 2^-24 of itself) and then G along the rows, along the columns (pitch `rows`, a multiple
- * of 32 rows; zeros past a block's last row in use), or both: the operands of the two
- * input gradients, of the weight gradients, and h along the tokens for the next
- * projection's.  dh, gate and up are dense rows x cols.  Rows from offsets[groups]
+ * each in float32 (with s within (1.25 |gate| + 8) 2^-24 of itself) and then G along
+ * the rows, along the columns (pitch `rows`, a multiple of 32 rows; zeros past a
+ * block's last row in use), or both: the operands of the two input gradients, of the
+ * weight gradients, and h along the tokens for the next projection's.  dh, gate and up are dense rows x cols.  Rows from offsets[groups]
  * on (offsets NULL: none) are neither read nor written.  Without dgate and dup, dh is
  * not read and may be NULL: the activation alone, of products kept in bfloat16.
  * s is 0 for gate under about -88.

@@ -69,9 +69,11 @@ constexpr int kActRows = 128, kActCols = 64;         // tile of one workgroup
 // in one store) and keeps the three results; one result after the other goes through LDS, from
 // which a lane takes 32 rows of one column.  LDS columns are rotated by the row group, so the 4
 // groups that a wave reads at one step fall on different banks.  Tiles go along the rows, all
-// XCDs side by side: 26624 x 1408, all ten outputs, 95 to 97 us (79 back to
-// back, part of the inputs still in the last-level cache: 4.9 TB/s), each XCD in an eighth of the rows 107.  Bound by HBM and by the number of
-// store instructions: with 8 elements a lane and a store for each row's scales 102 to 111 us.
+// XCDs side by side: 24558 x 1408, all ten outputs, 95 to 97 us, 4.0 TB/s (79 back to back, part
+// of the inputs still in the last-level cache), each XCD in an eighth of the rows 107; two or four
+// neighbouring tiles on an XCD, and ordinary stores in place of nontemporal ones, change nothing.
+// Bound by HBM and by the number of store instructions: with 8 elements a lane and a store for
+// each row's scales 102 to 111 us.
 __global__ __launch_bounds__(256) void k_act_tiles(sshdp_swiglu_grad a, uint32_t tiles_c) {
   constexpr int NP = kActRows / 64;
   __shared__ __align__(16) float sm[kActRows][kActCols];
