@@ -248,7 +248,9 @@ def _ptr(x):
     try:
         return x.data_ptr()
     except AttributeError:
-        return x
+        if isinstance(x, int):
+            return x
+        raise                                          # ctypes would take bytes, strings and arrays as host addresses
 
 
 def _stream(s):
