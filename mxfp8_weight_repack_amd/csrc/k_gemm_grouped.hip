@@ -468,9 +468,13 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
 // B (gated: 32 of each matrix): its W waves share K, a wave has 4 steps of all of them in
 // flight at once, straight from memory to registers, and its sums meet the others' in LDS.
 // The products are float32 sums whatever the output: the conversions that takes cost nothing
-// beside the reads.  16 tokens of 6 choices, 64 experts, gated 2 x 1408 x 2048: 49 to 51 us for
+// beside the reads.  For bfloat16 output (and gated), where any scale is allowed, rows with elements
+// that bfloat16 does not hold exactly are multiplied as codes, as tiles multiply all.  16 tokens of 6 choices, 64 experts, gated 2 x 1408 x 2048: 49 to 51 us for
 // the 302 MB of the 50 experts in use, 6 TB/s.
 constexpr int kFewSteps = 4, kFewFrags = 4;
+// Scale bytes under which every code is a normal bfloat16 number: 2^-9 2^(10 - 127) = 2^-126 and
+// 1.75 2^8 2^(246 - 127) < 2^128.
+constexpr uint32_t kBf16Least = 10, kBf16Most = 246;
 
 template <Form F, bool BF16, int W>
 __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_group_few(GemmGrouped g, int blocks_n) {
@@ -504,13 +508,25 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     const int64_t n = column(i), left = max(min<int64_t>(p.n - n, 16), (int64_t)0);
     rb[i] = resource((F == kGated && i >= 2 ? p.b2 : p.b) + (left ? n * p.k : 0), left);
   }
-  // word j: a row's blocks kb + 4 j .. + 3, zeros past the end
+  // word j: a row's blocks kb + 4 j .. + 3, ones (beside codes of zero) past the end
   struct Words {
     uint32_t w[S];
   };
+  auto row_scales = [&](const uint8_t *s, int layout, int64_t row) __attribute__((always_inline)) {
+    if (layout == SSHDP_SCALE_TILE32X4) return s + (row >> 5) * (KB >> 2) * 128 + (row & 31) * 4;
+    return s + (layout == SSHDP_SCALE_ROWMAJOR ? row : row >> 5) * KB;
+  };
+  auto word = [&](const uint8_t *s, bool tile, int at) __attribute__((always_inline)) {
+    const int n = min(KB - at, 4);
+    const uint8_t *b = s + (tile ? (at >> 2) * 128 : at);
+    uint32_t v = 0x7F7F7F7Fu;
+    if (n == 4) v = *reinterpret_cast<const u32u_t *>(b);
+    else for (int i = 0; i < n; ++i) v ^= (uint32_t)(b[i] ^ 0x7F) << (8 * i);
+    return v;
+  };
   auto scales = [&](const uint8_t *s, int layout, int64_t row, int kb) __attribute__((always_inline)) {
     const bool tile = layout == SSHDP_SCALE_TILE32X4;
-    s += tile ? (row >> 5) * (KB >> 2) * 128 + (row & 31) * 4 : (layout == SSHDP_SCALE_ROWMAJOR ? row : row >> 5) * KB;
+    s = row_scales(s, layout, row);
     Words v{};
     if (kb + 4 * S <= KB && !tile) {
       const u32x4_t x = *reinterpret_cast<const u32x4u_t *>(s + kb);
@@ -518,51 +534,118 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
       for (int j = 0; j < S; ++j) v.w[j] = x[j];
     } else {
 #pragma unroll
-      for (int j = 0; j < S; ++j) {
-        const int at = kb + 4 * j, n = min(KB - at, 4);
-        const uint8_t *b = s + (tile ? (at >> 2) * 128 : at);
-        if (n == 4) v.w[j] = *reinterpret_cast<const u32u_t *>(b);
-        else for (int i = 0; i < n; ++i) v.w[j] |= (uint32_t)b[i] << (8 * i);
-      }
+      for (int j = 0; j < S; ++j) v.w[j] = word(s, tile, kb + 4 * j);
     }
     return v;
   };
+  auto b_row = [&](int i) __attribute__((always_inline)) { return min(column(i) + r, p.n - 1); };
+  auto b_scales = [&](int i) __attribute__((always_inline)) { return F == kGated && i >= 2 ? p.b2s : p.bs; };
+  const int64_t a_row = m0 + min(r, rows - 1);
   f32x4_t acc[NF];
 #pragma unroll
   for (int i = 0; i < NF; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  // The byte of the lane's chunk in half h of a step: its block is 2 h + q / 2.
+  auto byte = [&](uint32_t w, int h) __attribute__((always_inline)) { return (w >> (8 * (2 * h + (q >> 1)))) & 0xFFu; };
+  auto multiply = [&](const u32x4_t &x, uint32_t ea, const u32x4_t (&z)[NF], const uint32_t (&eb)[NF]) __attribute__((always_inline)) {
+    const u32x4_t y[2] = {to_bf16((int)x[0], (int)x[1], ea), to_bf16((int)x[2], (int)x[3], ea)};
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+      acc[i] = mma_bf16(to_bf16((int)z[i][0], (int)z[i][1], eb[i]), y[0], acc[i]);
+      acc[i] = mma_bf16(to_bf16((int)z[i][2], (int)z[i][3], eb[i]), y[1], acc[i]);
+    }
+  };
+  auto load = [&](__amdgpu_buffer_rsrc_t rs, int c, int from) __attribute__((always_inline)) {
+    const int k0 = from * 32 + 16 * q, left = (int)p.k - k0, voff = r * (int)p.k + k0;
+    return __builtin_bit_cast(u32x4_t,
+                              __builtin_amdgcn_raw_buffer_load_b128(rs, 64 * c < left ? voff + 64 * c : INT32_MAX - 15, 0, 0));
+  };
+  uint32_t lo = 255, hi = 0;                         // of the scale bytes of chunks that are not all zeros
+  auto seen = [&](const u32x4_t &c, uint32_t e) __attribute__((always_inline)) {
+    if (!BF16) return;
+    e = (c[0] | c[1] | c[2] | c[3]) & 0x7F7F7F7Fu ? e : 127;
+    lo = min(lo, e);
+    hi = max(hi, e);
+  };
   for (int kb = 4 * S * wave; kb < KB; kb += 4 * S * W) {
-    const int k0 = kb * 32 + 16 * q, left = (int)p.k - k0, voff = r * (int)p.k + k0;
-    auto load = [&](__amdgpu_buffer_rsrc_t rs, int c) __attribute__((always_inline)) {
-      return __builtin_bit_cast(u32x4_t,
-                                __builtin_amdgcn_raw_buffer_load_b128(rs, 64 * c < left ? voff + 64 * c : INT32_MAX - 15, 0, 0));
-    };
     u32x4_t a[2 * S], b[NF][2 * S];
     Words wa, wb[NF];
 #pragma unroll
     for (int i = 0; i < NF; ++i) {
-      wb[i] = scales(F == kGated && i >= 2 ? p.b2s : p.bs, p.lb, min(column(i) + r, p.n - 1), kb);
+      wb[i] = scales(b_scales(i), p.lb, b_row(i), kb);
 #pragma unroll
-      for (int c = 0; c < 2 * S; ++c) b[i][c] = load(rb[i], c);
+      for (int c = 0; c < 2 * S; ++c) b[i][c] = load(rb[i], c, kb);
     }
-    wa = scales(p.as, SSHDP_SCALE_ROWMAJOR, m0 + min(r, rows - 1), kb);
+    wa = scales(p.as, SSHDP_SCALE_ROWMAJOR, a_row, kb);
 #pragma unroll
-    for (int c = 0; c < 2 * S; ++c) a[c] = load(ra, c);
+    for (int c = 0; c < 2 * S; ++c) a[c] = load(ra, c, kb);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int s = 0; s < S; ++s) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int sh = 8 * (2 * h + (q >> 1));
-        const u32x4_t &x = a[2 * s + h];
-        const uint32_t ea = (wa.w[s] >> sh) & 0xFFu;
-        const u32x4_t y[2] = {to_bf16((int)x[0], (int)x[1], ea), to_bf16((int)x[2], (int)x[3], ea)};
+        u32x4_t z[NF];
+        uint32_t eb[NF], ea = byte(wa.w[s], h);
+        seen(a[2 * s + h], ea);
 #pragma unroll
         for (int i = 0; i < NF; ++i) {
-          const u32x4_t &z = b[i][2 * s + h];
-          const uint32_t eb = (wb[i].w[s] >> sh) & 0xFFu;
-          acc[i] = mma_bf16(to_bf16((int)z[0], (int)z[1], eb), y[0], acc[i]);
-          acc[i] = mma_bf16(to_bf16((int)z[2], (int)z[3], eb), y[1], acc[i]);
+          z[i] = b[i][2 * s + h];
+          eb[i] = byte(wb[i].w[s], h);
+          seen(z[i], eb[i]);
         }
+        multiply(a[2 * s + h], ea, z, eb);
+      }
+    }
+  }
+  if (BF16 && __any(lo < kBf16Least || hi > kBf16Most)) {
+    // Some of the wave's elements are outside bfloat16's range, or NaN: its steps once more, each
+    // multiplied as codes too, which the 8-bit instruction takes under every scale.  The rows of A
+    // and of B with such elements take those sums, the others come out as they were.
+#pragma unroll
+    for (int i = 0; i < NF; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int kb = 4 * S * wave; kb < KB; kb += 4 * S * W) {
+      for (int at = kb; at < min(kb + 4 * S, KB); at += 4) {
+        u32x4_t x[2], z[2][NF];
+        uint32_t xw = word(row_scales(p.as, SSHDP_SCALE_ROWMAJOR, a_row), false, at), zw[NF];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) x[h] = load(ra, h, at);
+#pragma unroll
+        for (int i = 0; i < NF; ++i) {
+          zw[i] = word(row_scales(b_scales(i), p.lb, b_row(i)), p.lb == SSHDP_SCALE_TILE32X4, at);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) z[h][i] = load(rb[i], h, at);
+        }
+        // whether a chunk has such an element; then the rows of the 16 that have one, a bit each
+        auto beyond = [&](const u32x4_t &c, uint32_t e) __attribute__((always_inline)) {
+          return ((c[0] | c[1] | c[2] | c[3]) & 0x7F7F7F7Fu) && (e < kBf16Least || (e > kBf16Most && e != 255));
+        };
+        auto rows_of_lanes = [](bool any) __attribute__((always_inline)) {
+          const uint64_t v = __ballot(any);
+          const uint32_t o = (uint32_t)v | (uint32_t)(v >> 32);
+          return (o | o >> 16) & 0xFFFFu;
+        };
+        auto codes = [](const u32x4_t &u, const u32x4_t &v) __attribute__((always_inline)) {
+          return i32x8_t{(int)u[0], (int)u[1], (int)u[2], (int)u[3], (int)v[0], (int)v[1], (int)v[2], (int)v[3]};
+        };
+        const uint32_t of_a = rows_of_lanes(beyond(x[0], byte(xw, 0)) || beyond(x[1], byte(xw, 1)));
+        uint32_t of_b[NF];
+        f32x4_t any[NF];
+#pragma unroll
+        for (int i = 0; i < NF; ++i) {
+          of_b[i] = rows_of_lanes(beyond(z[0][i], byte(zw[i], 0)) || beyond(z[1][i], byte(zw[i], 1)));
+          any[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes(z[0][i], z[1][i]), codes(x[0], x[1]), acc[i], 0, 0, 0,
+                                                                    (int)(zw[i] >> (8 * q)), 0, (int)(xw >> (8 * q)));
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t eb[NF];
+#pragma unroll
+          for (int i = 0; i < NF; ++i) eb[i] = byte(zw[i], h);
+          multiply(x[h], byte(xw, h), z[h], eb);
+        }
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[i][k] = (of_a >> r | of_b[i] >> (4 * q + k)) & 1 ? any[i][k] : acc[i][k];
       }
     }
   }
