@@ -640,7 +640,8 @@ int sshdp_gemm_mxfp8_grouped(const sshdp_mx_matrix *a, const sshdp_mx_matrix *b,
  *   gate = A Bg_e^T,  up = A Bu_e^T,  h = silu(gate) * up,
  *   silu(x) = x / (1 + exp(-x)),  codes, scales = G(h) along the rows (ROWMAJOR).
  * The products are sshdp_gemm_mxfp8's of bfloat16 output; h is computed in float32
- * (within (1.25 |gate| + 8) 2^-24 of itself) from the sums, before they are rounded.
+ * (within (1.25 |gate| + 8) 2^-24 of itself; for gates under -87.336, whose sigmoid is
+ * no normal float32 number, within 2^-126 |gate up|) from the sums, before they are rounded.
  * `gate` and `up` (both or neither) receive the products in bfloat16, what the backward pass
  * needs; codes and scales may be left out then.  All outputs are dense, A.rows x N,
  * N = gate_w.rows / groups a multiple of 32; gate_w and up_w have the same shape
@@ -659,7 +660,7 @@ int sshdp_gemm_mxfp8_swiglu(const sshdp_mx_matrix *a, const sshdp_mx_matrix *gat
  * weight gradients, and h along the tokens for the next projection's.  dh, gate and up are dense rows x cols.  Rows from offsets[groups]
  * on (offsets NULL: none) are neither read nor written.  Without dgate and dup, dh is
  * not read and may be NULL: the activation alone, of products kept in bfloat16.
- * s is 0 for gate under about -88.
+ * s is 0 for gates under -87.336, where it is no normal float32 number.
  * Errors: ARG (null gate or up, dh missing, no output, half a pair, negative size,
  * groups < 1 with offsets), SCHEMA (cols not a multiple of 32, rows not one with an
  * output along columns, an edge over 2^30, groups over 1024), ALIGN (all but the
