@@ -1,6 +1,7 @@
 // mx_encode.h -- G of values in registers by the scaled conversions of gfx950, which divide by the
-// scale on the way (one instruction for two codes; compared with ldexp and the plain conversion
-// on every bfloat16 and 2^24 float32 values under each of the 255 scales: the same codes).
+// scale on the way (one instruction for two codes; tested against the codes' definition for every
+// bfloat16 value under each of the 248 scales that a block may have, and for float32 values at,
+// beside and between the rounding borders under each).
 #pragma once
 #include <hip/hip_runtime.h>
 

@@ -1,5 +1,5 @@
-"""The gated activation where its exponential matters, in every kernel that computes it: gates far out on both sides.
-Products are exact sums, so the gates are known to the bit."""
+"""The gated activation where its exponential matters, in every kernel that computes it: gates far out on both sides, and
+many gates whose results lie next to codes' rounding borders.  Products are exact sums, so the gates are known to the bit."""
 
 import pytest
 
@@ -91,3 +91,60 @@ def test_far_gates(name):
     h = g * torch.special.expit(g) * u
     under = torch.where(g < CUT, 2.0 ** -126 * g.abs() * u, 0.0)
     check_codes(codes, scales, h.contiguous(), h.abs() * near(g) * (g >= CUT) + under)
+
+
+@pytest.mark.parametrize("name", GATE_SIZES)
+def test_gates_of_many_sizes(name):
+    """Gates -88 to -20 and ups 0.5 to 8, both from a row's part and a column's: of many values many lie next to a code's
+    rounding border, and none may leave it further than stated."""
+    say(f"{name}, many gates")
+    counts, k = GATE_SIZES[name]
+    n, e, rows = GATE_COLUMNS, len(counts), sum(counts)
+    r = torch.Generator(device="cuda").manual_seed(k + rows)
+    pick = lambda top, size: torch.randint(0, top, (size,), generator=r, device="cuda")   # noqa: E731
+    # gate -(c + d), quarters; neighbouring columns' are alike, so few of a block's values vanish beside its largest
+    c, d = 20 + torch.sort(pick(36 * 4, n)).values / 4.0, pick(31 * 4, rows) / 4.0
+    a, gv, uv = torch.zeros(rows, k, device="cuda"), torch.zeros(n, k, device="cuda"), torch.zeros(n, k, device="cuda")
+    a[:, :8] = 1                                       # the columns' part: c's digits times one
+    gv[:, 8:16] = -1                                   # the rows' part
+    for j in range(8):                                 # 32 .. 1/4
+        p = 2.0 ** (5 - j)
+        gv[:, j] = -p * (torch.floor(c / p) % 2)
+        a[:, 8 + j] = p * (torch.floor(d / p) % 2)
+    a[:, 16], a[:, 24] = 1, 1 + pick(8, rows) / 8.0
+    uv[:, 16], uv[:, 24] = 0.5 + pick(8, n) / 16.0, (1 + pick(8, n) / 8.0) * 2
+    g = -(c.double().unsqueeze(0) + d.double().unsqueeze(1))
+    u = uv[:, 16].double().unsqueeze(0) + a[:, 24].double().unsqueeze(1) * uv[:, 24].double().unsqueeze(0)
+    bank = lambda t: t.repeat(e, 1)                    # noqa: E731
+    codes, scales, gate, up = call(mx(a), mx(bank(gv)), mx(bank(uv)), counts, n)
+    assert torch.equal(gate, g.bfloat16()) and torch.equal(up, u.bfloat16())
+    h = g * torch.special.expit(g) * u
+    check_codes(codes, scales, h, h.abs() * near(g))
+
+
+def test_gradient_within_its_own_bound():
+    """4 million gates of -87 to 30 in the activation's gradient: the sigmoid to 2^-21 and the products behind it, which
+    codes next to a rounding border tell from a sigmoid whose error grows with the gate."""
+    say("swiglu gradient, many gates")
+    r = torch.Generator(device="cuda").manual_seed(11)
+    rows, cols = 2048, 2048
+    gate = (torch.rand(rows, cols, generator=r, device="cuda") * 117 - 87).bfloat16()
+    up, dh = ((torch.rand(rows, cols, generator=r, device="cuda") + 0.5).bfloat16() for _ in range(2))
+    # blocks of like gates along both directions, so that most values are far above their block's smallest code
+    gate = torch.sort(gate.view(-1)).values.view(rows // 32, cols // 32, 32, 32).permute(0, 2, 1, 3).reshape(rows, cols).contiguous()
+    out = {}
+    for name in ("dgate", "dup", "h"):
+        out[name] = [torch.zeros(*s, dtype=torch.uint8, device="cuda") for s in
+                     ((rows, cols), (rows, cols // 32), (cols, rows), (cols, rows // 32))]
+    sh.swiglu_backward_mxfp8(dh, gate, up, rows, cols, **{k: sh.mx_pair(*v) for k, v in out.items()}, stream=stream())
+    d, g, u = dh.double(), gate.double(), up.double()
+    s = torch.special.expit(g)
+    # dup, h: the sigmoid and two products.  dgate: s in two places, 1 - s and the sum rounded, terms no larger than
+    # s (1 + |g|), then two products.
+    one, both = 2.0 ** -21 + 2 * 2.0 ** -24, 2 * 2.0 ** -21 + 4 * 2.0 ** -24
+    ref = {"dgate": (d * u * s * (1 + g * (1 - s)), both * d * u * s * (1 + g.abs())),
+           "dup": (d * g * s, one * (d * g * s).abs()), "h": (g * s * u, one * (g * s * u).abs())}
+    for name, (v, e) in ref.items():
+        t = out[name]
+        check_codes(t[0], t[1], v, e + 2.0 ** -148)
+        check_codes(t[2], t[3], v.t().contiguous(), e.t().contiguous() + 2.0 ** -148)
