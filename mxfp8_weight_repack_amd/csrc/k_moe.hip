@@ -68,6 +68,14 @@ __device__ __forceinline__ uint64_t same_key(int key, int bits) {
   return m;
 }
 
+// Between LDS accesses of lanes of one wave to what other lanes of it read or wrote: the compiler
+// keeps their order.  No instruction comes of it, a wave's LDS accesses are done in order.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // A workgroup places its chunk's slots: a wave takes consecutive ones, counts its slots of
 // each expert 64 at a time (a lane's rank among the 64 is the number of lower lanes with its
 // expert), the waves' counts become first rows, and the same passes over the slots hand the
@@ -90,6 +98,7 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_place(const I *ids, int64_
     const int e = expert_of(ids, s0 + i + lane, slots, experts);
     const uint64_t m = same_key(e, bits);
     if (e < experts && !(m & lower)) next[wave][e] += __popcll(m);
+    wave_order();
   }
   if (counts) {
     // all chunks' counts, and those of the chunks before this one
@@ -154,7 +163,9 @@ __global__ __launch_bounds__(kSortThreads) void k_moe_place(const I *ids, int64_
       source[at] = (int)s;
     }
     // the lanes of one expert have read its next row before their first one moves it
+    wave_order();
     if (e < experts && !(m & lower)) next[wave][e] = at + __popcll(m);
+    wave_order();
     if (s < slots) place[s] = at;
   }
   if (blockIdx.x == 0)
