@@ -122,9 +122,22 @@ def test_gates_of_many_sizes(name):
     check_codes(codes, scales, h, h.abs() * near(g))
 
 
+def gradient_with_bounds(d, g, u):
+    """{output: (float64 value, bound)}: the sigmoid s to 2^-21, other roundings 2^-24 each.  dup, h: s and two products.
+    dgate = d u (s f), f = 1 + g (1 - s): s, three products and f's sum relative to the result; 1 - s is off by s's own error
+    and its rounding, which is by no more than s."""
+    s, eps = torch.special.expit(g), 2.0 ** -24
+    f = 1 + g * (1 - s)
+    one = 2.0 ** -21 + 2 * eps
+    return {"dgate": (d * u * s * f, (d * u * s).abs() * ((2.0 ** -21 + 4 * eps) * f.abs() +
+                                                          g.abs() * (2.0 ** -21 * s + s.clamp_max(eps)))),
+            "dup": (d * g * s, one * (d * g * s).abs()), "h": (g * s * u, one * (g * s * u).abs())}
+
+
 def test_gradient_within_its_own_bound():
     """4 million gates of -87 to 30 in the activation's gradient: the sigmoid to 2^-21 and the products behind it, which
-    codes next to a rounding border tell from a sigmoid whose error grows with the gate."""
+    codes next to a rounding border tell from a sigmoid whose error grows with the gate (dgate's, whose factors have the
+    most bits)."""
     say("swiglu gradient, many gates")
     r = torch.Generator(device="cuda").manual_seed(11)
     rows, cols = 2048, 2048
@@ -138,12 +151,7 @@ def test_gradient_within_its_own_bound():
                      ((rows, cols), (rows, cols // 32), (cols, rows), (cols, rows // 32))]
     sh.swiglu_backward_mxfp8(dh, gate, up, rows, cols, **{k: sh.mx_pair(*v) for k, v in out.items()}, stream=stream())
     d, g, u = dh.double(), gate.double(), up.double()
-    s = torch.special.expit(g)
-    # dup, h: the sigmoid and two products.  dgate: s in two places, 1 - s and the sum rounded, terms no larger than
-    # s (1 + |g|), then two products.
-    one, both = 2.0 ** -21 + 2 * 2.0 ** -24, 2 * 2.0 ** -21 + 4 * 2.0 ** -24
-    ref = {"dgate": (d * u * s * (1 + g * (1 - s)), both * d * u * s * (1 + g.abs())),
-           "dup": (d * g * s, one * (d * g * s).abs()), "h": (g * s * u, one * (g * s * u).abs())}
+    ref = gradient_with_bounds(d, g, u)
     for name, (v, e) in ref.items():
         t = out[name]
         check_codes(t[0], t[1], v, e + 2.0 ** -148)
