@@ -546,6 +546,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
   for (int i = 0; i < NF; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   // The byte of the lane's chunk in half h of a step: its block is 2 h + q / 2.
   auto byte = [&](uint32_t w, int h) __attribute__((always_inline)) { return (w >> (8 * (2 * h + (q >> 1)))) & 0xFFu; };
+  auto any_code = [](const u32x4_t &c) __attribute__((always_inline)) { return (c[0] | c[1] | c[2] | c[3]) & 0x7F7F7F7Fu; };
   auto multiply = [&](const u32x4_t &x, uint32_t ea, const u32x4_t (&z)[NF], const uint32_t (&eb)[NF]) __attribute__((always_inline)) {
     const u32x4_t y[2] = {to_bf16((int)x[0], (int)x[1], ea), to_bf16((int)x[2], (int)x[3], ea)};
 #pragma unroll
@@ -559,13 +560,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     return __builtin_bit_cast(u32x4_t,
                               __builtin_amdgcn_raw_buffer_load_b128(rs, 64 * c < left ? voff + 64 * c : INT32_MAX - 15, 0, 0));
   };
-  uint32_t lo = 255, hi = 0;                         // of the scale bytes of chunks that are not all zeros
-  auto seen = [&](const u32x4_t &c, uint32_t e) __attribute__((always_inline)) {
-    if (!BF16) return;
-    e = (c[0] | c[1] | c[2] | c[3]) & 0x7F7F7F7Fu ? e : 127;
-    lo = min(lo, e);
-    hi = max(hi, e);
-  };
+  uint32_t small = 0;                                // codes of elements under bfloat16's normal numbers
   for (int kb = 4 * S * wave; kb < KB; kb += 4 * S * W) {
     u32x4_t a[2 * S], b[NF][2 * S];
     Words wa, wb[NF];
@@ -579,24 +574,39 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
 #pragma unroll
     for (int c = 0; c < 2 * S; ++c) a[c] = load(ra, c, kb);
     __builtin_amdgcn_sched_barrier(0);
+    uint32_t least = 255;                            // of the scale bytes
 #pragma unroll
     for (int s = 0; s < S; ++s) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         u32x4_t z[NF];
         uint32_t eb[NF], ea = byte(wa.w[s], h);
-        seen(a[2 * s + h], ea);
+        least = min(least, ea);
 #pragma unroll
         for (int i = 0; i < NF; ++i) {
           z[i] = b[i][2 * s + h];
           eb[i] = byte(wb[i].w[s], h);
-          seen(z[i], eb[i]);
+          least = min(least, eb[i]);
         }
         multiply(a[2 * s + h], ea, z, eb);
       }
     }
+    if (BF16 && __any(least < kBf16Least)) {         // blocks of zeros, as a rule
+#pragma unroll
+      for (int c = 0; c < 2 * S; ++c) {
+        small |= byte(wa.w[c >> 1], c & 1) < kBf16Least ? any_code(a[c]) : 0;
+#pragma unroll
+        for (int i = 0; i < NF; ++i) small |= byte(wb[i].w[c >> 1], c & 1) < kBf16Least ? any_code(b[i][c]) : 0;
+      }
+    }
   }
-  if (BF16 && __any(lo < kBf16Least || hi > kBf16Most)) {
+  // an element from 2^128 on makes sums infinite or NaN
+  uint32_t most = small ? 0x7F800000u : 0;
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) most = max(most, __float_as_uint(acc[i][k]) & 0x7FFFFFFFu);
+  if (BF16 && __any(most >= 0x7F800000u)) {
     // Some of the wave's elements are outside bfloat16's range, or NaN: its steps once more, each
     // multiplied as codes too, which the 8-bit instruction takes under every scale.  The rows of A
     // and of B with such elements take those sums, the others come out as they were.
@@ -616,7 +626,7 @@ __global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2, 2))) 
         }
         // whether a chunk has such an element; then the rows of the 16 that have one, a bit each
         auto beyond = [&](const u32x4_t &c, uint32_t e) __attribute__((always_inline)) {
-          return ((c[0] | c[1] | c[2] | c[3]) & 0x7F7F7F7Fu) && (e < kBf16Least || (e > kBf16Most && e != 255));
+          return any_code(c) && (e < kBf16Least || (e > kBf16Most && e != 255));
         };
         auto rows_of_lanes = [](bool any) __attribute__((always_inline)) {
           const uint64_t v = __ballot(any);
