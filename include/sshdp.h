@@ -616,9 +616,12 @@ int sshdp_moe_combine_backward(const sshdp_moe_combine_grad *args, void *stream)
  *     transposed operands of the two sides (codes_t, scales_t), the sorted rows
  *     along their columns; offsets must be multiples of 32.  An expert without rows
  *     gets its addend, or zeros.
- * Types and arithmetic are those of sshdp_gemm_mxfp8.  A's scales (TN: both) are
- * ROWMAJOR, B's in any layout.  `addend` (NULL for none) has out's type, shape and
- * ld, and may be out; for bfloat16 it is added in float32 ahead of the rounding.
+ * Types and arithmetic are those of sshdp_gemm_mxfp8, except that NT with few rows an
+ * expert (a rule on the sizes) has float32 sums for bfloat16 output too: a row's
+ * bfloat16 result may differ between batches of different sizes, by the 8-bit
+ * products' cut.  A's scales (TN: both) are ROWMAJOR, B's in any layout.  `addend`
+ * (NULL for none) has out's type, shape and ld, and may be out; for bfloat16 it is
+ * added in float32 ahead of the rounding.
  * `offsets`, groups + 1 device integers, may be NULL with one group, which then
  * has all rows.  Rows outside every expert's (behind the last one) are neither
  * read nor written; offsets that run backwards or past the rows make the call
@@ -639,7 +642,12 @@ int sshdp_gemm_mxfp8_grouped(const sshdp_mx_matrix *a, const sshdp_mx_matrix *b,
  * activation and G in one pass:
  *   gate = A Bg_e^T,  up = A Bu_e^T,  h = silu(gate) * up,
  *   silu(x) = x / (1 + exp(-x)),  codes, scales = G(h) along the rows (ROWMAJOR).
- * The products are sshdp_gemm_mxfp8's of bfloat16 output; h is computed in float32
+ * The products are sshdp_gemm_mxfp8's of bfloat16 output, every code under every scale:
+ * each 8 consecutive k's are cut off at 2^-14 of the binade of their largest (few rows
+ * an expert, a rule on the sizes: float32 sums, so a row's results may differ between
+ * batches of different sizes by that cut).  Of normal operands with K = 2048 it moves
+ * one code of h in 600, and one scale in 40000, that lies next to a rounding border;
+ * there is no form with float32 sums for every size.  h is computed in float32
  * (within (1.25 |gate| + 8) 2^-24 of itself; for gates under -87.336, whose sigmoid is
  * no normal float32 number, within 2^-126 |gate up|) from the sums, before they are rounded.
  * `gate` and `up` (both or neither) receive the products in bfloat16, what the backward pass

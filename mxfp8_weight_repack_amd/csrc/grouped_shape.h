@@ -26,10 +26,14 @@ inline int grouped_cols(GroupForm form, int tile) {
 
 // 16: the kernel of a few rows an expert; else the tile's edge.  The candidate with the least
 // modelled time in microseconds.  The tiles' constants were fitted to 216 sizes of 1, 8 and 64
-// experts, 512 .. 24576 rows, 704 x 512 .. 2048 x 4096, operands from HBM: what it picks takes
-// 1.2% more than the better of the two on average and 1.26 times at worst (always 128: 6.4% and
-// 1.36 times).  Few rows against 128-tiles at 216 sizes of 4 .. 1024 rows, 320 x 1024 .. 2048 x
-// 4096: 1.7% and 1.36 times (products of 9 us).
+// experts, 512 .. 24576 rows dealt evenly, 704 x 512 .. 2048 x 4096, operands from HBM: there what it
+// picks takes 1.2% more than the better of the two on average and 1.26 times at worst (always 128:
+// 6.4% and 1.36 times).  Few rows against 128-tiles at 216 sizes of 4 .. 1024 rows, 320 x 1024 ..
+// 2048 x 4096: 1.7% and 1.36 times (products of 9 us).  At 90 other sizes (2 to 128 experts, 33 ..
+// 24576 rows, n and k 320 .. 4096), rows dealt evenly, as a router with favourites deals them, and
+// with most of them at a few experts: between the tiles 1.1, 0.4 and 0.6% on average and 1.29 times at
+// worst (always 128: 4% and 1.39 times); where few rows come into question (17 sizes) 8% and 1.7
+// times, with K under 512, of which one wave of the few rows' four has all the work.
 //   few rows:  each piece reads its expert's B, at 5.5 TB/s, in no less than 3 us a round (64
 //              experts, gated 1408 x 2048: 96 rows 51 us, 128-tiles 54; 768 rows 91 and 83; one
 //              expert of 16 rows 9.4 and 14.3);

@@ -220,10 +220,13 @@ __device__ __forceinline__ void add_bf16(const GemmMx &p, const uint16_t *addend
 // A tile of an expert's rows, bfloat16 or codes out.  Bound by the wait for operands at each step and,
 // in 256-tiles, by what one workgroup a CU has nothing to hide behind: its first operands and its
 // end (8 us of the 37 of a gated tile with K 2048).  24558 slots of 64 experts, operands from HBM:
-// gated 2 x 1408 x 2048 with both kept 220 to 228 us (283 GFLOP, 606 MB; matrix cores 37% busy),
-// by 128-tiles 245; input gradient, K 2048 and 1408 columns, 125 to 129 us (142 GFLOP, 311 MB;
-// 37%).  Workgroups that stay and walk the tiles lose to the hardware's dealing: 146 us for the
-// gradient.
+// gated 2 x 1408 x 2048 with both kept 218 to 229 us (283 GFLOP, 606 MB; matrix cores 37% busy),
+// by 128-tiles 245; input gradient, K 2048 and 1408 columns, 124 to 131 us (142 GFLOP, 311 MB; 37%).
+// Workgroups that stay and walk the tiles lose to the hardware's dealing: 146 us for the gradient.
+// The 8-bit instruction's cut is a choice: with float32 sums the gated pair takes 1.3 times as long
+// (351 against 266 us after a write through the caches).  Of 37 million codes of h 59000 then move
+// over a rounding border no more, and h is no nearer: 2.65e-2 of itself from its value with
+// either, which is G's own rounding.
 template <class C, bool NN, bool SHORT, Form F>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C::WPS))) void k_group8(GemmGrouped g, int tiles_n) {
   __shared__ __align__(1024) char smem[C::LDS];
@@ -469,8 +472,10 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(C::WPS, C
 // flight at once, straight from memory to registers, and its sums meet the others' in LDS.
 // The products are float32 sums whatever the output: the conversions that takes cost nothing
 // beside the reads.  For bfloat16 output (and gated), where any scale is allowed, rows with elements
-// that bfloat16 does not hold exactly are multiplied as codes, as tiles multiply all.  16 tokens of 6 choices, 64 experts, gated 2 x 1408 x 2048: 49 to 51 us for
-// the 302 MB of the 50 experts in use, 6 TB/s.
+// that bfloat16 does not hold exactly are multiplied as codes, as tiles multiply all.  Looking for
+// them takes 0.1 to 0.3 us; a wave that has some goes over its operands again (two experts of 16
+// rows, all such: 20 us instead of 13.5).  16 tokens of 6 choices, 64 experts, gated 2 x 1408 x
+// 2048: 47 to 52 us for the 302 MB of the 50 experts in use, 5.8 to 6.4 TB/s.
 constexpr int kFewSteps = 4, kFewFrags = 4;
 // Scale bytes under which every code is a normal bfloat16 number: 2^-9 2^(10 - 127) = 2^-126 and
 // 1.75 2^8 2^(246 - 127) < 2^128.
