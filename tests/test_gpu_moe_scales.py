@@ -98,6 +98,27 @@ def test_gated_pair_of_elements_of_any_size(name, bytes_):
     check_codes(codes, scales, h, h.abs() * (1.25 * gate.abs() + 8) * 2.0 ** -24 * (gate >= -87.336) + under)
 
 
+@pytest.mark.parametrize("layout", ["tile32x4", "block32x32"])
+@pytest.mark.parametrize("way", [WAYS[0], WAYS[2]], ids=str)
+@pytest.mark.parametrize("counts,n,k", [([3, 0, 17, 1], 96, 640), ([5, 20], 64, 4352), ([40], 32, 128)])
+def test_few_rows_by_banks_in_every_layout(counts, n, k, way, layout):
+    """The second pass finds a step's scales where each layout has them."""
+    say(f"few rows {counts} {n} x {k} {layout}, scale bytes {way}")
+    extreme, ordinary, other = way
+    e = len(counts)
+    a, b = Operand(sum(counts), k, "rowmajor", 1), Operand(e * n, k, layout, 2)
+    for x, y in ((a, b), (b, a)):
+        if extreme < 10:
+            g = torch.Generator(device="cuda").manual_seed(3)
+            x.codes = torch.randint(0, 8, x.codes.shape, generator=g, device="cuda", dtype=torch.uint8)
+        y.blocks[:] = other
+        spread(x, extreme, ordinary)
+        remake(y)
+        ref = reference(a, b, counts, "nt")
+        assert bool((ref.abs() < 2.0 ** 127).all())
+        assert torch.equal(run(a, b, counts, "nt", "bf16"), ref.to(torch.bfloat16))
+
+
 @pytest.mark.parametrize("name", ["few nt bf16 4", "few nt bf16 8"])
 def test_ordinary_rows_keep_their_bits(name):
     """Elements of any size in one row, or in one column's weights, change no bit of another's result."""
